@@ -85,7 +85,7 @@ def draw(rng):
     elif rng.random() < 0.6:  # single tokens, or the few that a draft proposes
         q_len = rng.choice((1, 1, 1, rng.randint(2, 8)))
         B = _log_int(rng, 1, 64)
-        ctx = _log_int(rng, 1, min(262144, (1 << 30) // (B * Hkv * D)))
+        ctx = _log_int(rng, 1, min(262144, 960_000_000 // (B * Hkv * D)))
         window = rng.choice((0, 0, 0, 1 + ctx // 3))
     else:  # chunks of a prompt
         q_len = _log_int(rng, 16, 2048)
