@@ -55,7 +55,9 @@ typedef enum {
   MOE_ERR_CUDA = -6,            /* a CUDA runtime/driver call failed                   */
   MOE_ERR_DEVICE_TIMEOUT = -7,  /* device: a pipeline wait hit its time limit         */
   MOE_ERR_BAD_MAPPING = -8,     /* device: token_lora_mapping outside [-1, A)         */
-  MOE_ERR_BAD_EXPERT_ID = -9    /* device: a topk id outside [-1, E)                  */
+  MOE_ERR_BAD_EXPERT_ID = -9,   /* device: a topk id outside [-1, E)                  */
+  MOE_ERR_BAD_PAGE = -10,       /* device: a block table entry outside the cache      */
+  MOE_ERR_BAD_POSITION = -11    /* device: a position outside the table or below 0    */
 } moe_status_t;
 
 /* Supported limits (larger values return MOE_ERR_UNSUPPORTED). */
@@ -446,6 +448,177 @@ int moe_lora_forward(const moe_lora_args_t* args, moe_stream_t stream);
  * last call using ``workspace`` left (MOE_OK or a negative device code), or
  * MOE_ERR_CUDA if the synchronisation or the copy failed. */
 int moe_read_device_status(const void* workspace, moe_stream_t stream);
+
+/* ===========================================================================
+ * The attention half of a decoder layer: rotary positions, a paged cache of
+ * 8-bit keys and values, and attention over it.  The pages have no
+ * counterpart to these entry points; they serve the layer that runs directly
+ * before the routed MoE.
+ *
+ * Element types of q, k, v and out (moe_*_args_t.dtype).  Strides of these
+ * tensors are in elements and may be any that keep the last axis contiguous.
+ * status: device int32[4] or NULL.  A kernel that meets a bad table entry or
+ * position writes its code there if the word is 0 and goes on as each entry
+ * point says; a clean call writes nothing.  The caller zeroes it before use.
+ * ======================================================================== */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F16 1
+#define MOE_DTYPE_F32 2
+
+/* ---------------------------------------------------------------------------
+ * moe_rope -- rotary positions of q and, in the same launch, k.
+ *
+ * For each pair (u, w) of a head, its frequency i < rotary_dim / 2 and its
+ * token's position p, in float32:
+ *   u' = u C[p,i] - w S[p,i],   w' = w C[p,i] + u S[p,i],
+ * C = cos_sin[p, 0:R/2], S = cos_sin[p, R/2:R], R = rotary_dim.  Pairs are
+ * (x_i, x_{i + R/2}) (interleaved = 0) or (x_{2i}, x_{2i+1}).  Columns from R
+ * on are copied.  inverse != 0 uses -S: the transposed rotation, which is the
+ * gradient of the forward (a factor on C and S included).
+ *
+ *   q, q_out [N, Hq, D], k, k_out [N, Hk, D] (Hk = 0: none) of ``dtype``;
+ *     an output may be its own input.
+ *   positions [N] int32; one outside [0, num_positions) leaves its token's
+ *     heads unturned and reports MOE_ERR_BAD_POSITION.
+ *   cos_sin [num_positions, rotary_dim] float32, 16-byte aligned.
+ * Limits: 1 <= D <= 1024, rotary_dim even, 2 <= rotary_dim <= D, D even.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;           /* sizeof(moe_rope_args_t) */
+  int dtype;
+  const void* q;
+  void* q_out;
+  const void* k;
+  void* k_out;
+  int64_t q_stride_token, q_stride_head, q_out_stride_token, q_out_stride_head;
+  int64_t k_stride_token, k_stride_head, k_out_stride_token, k_out_stride_head;
+  const int32_t* positions;
+  const float* cos_sin;
+  int32_t* status;
+  int N, Hq, Hk, D, rotary_dim, num_positions, interleaved, inverse;
+} moe_rope_args_t;
+int moe_rope(const moe_rope_args_t* args, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged cache of float8 e4m3 codes (max 448, 0x7F / 0xFF are NaN).
+ *
+ * Page g holds page_size tokens of kv_heads heads of head_dim codes; the code
+ * of (page, head, token, d) is at page * stride_page + head * stride_head +
+ * token * stride_token + d bytes, so both orders of heads and tokens in a page
+ * fit.  k_scale, v_scale [num_pages, kv_heads] float32: the value is code *
+ * scale.  Token j of a sequence is at (block_table[j / page_size], j %
+ * page_size).  Codes past a sequence's last token and table entries past its
+ * last page are never used and may hold anything.
+ * Limits: head_dim a multiple of 16, at most 128; page_size a multiple of 8,
+ * at most 256; strides multiples of 16 and the bases 16-byte aligned
+ * (MOE_ERR_ALIGN); kv_heads <= 1024.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t k_stride_page, k_stride_head, k_stride_token;
+  int64_t v_stride_page, v_stride_head, v_stride_token;
+  int num_pages, kv_heads, page_size, head_dim;
+} moe_kv_cache_t;
+
+/* ---------------------------------------------------------------------------
+ * moe_kv_append -- new tokens' keys, rotated on the way, and values into the
+ * cache; optionally the queries' rotation in the same launch.
+ *
+ * Sequence b has the new tokens [cu_q[b], cu_q[b+1]) (cu_q NULL: token b, N =
+ * B); they become its last ones: seq_lens[b] counts them.  For each (page,
+ * head) that they touch, with amax their largest magnitude there in float32
+ * after the rotation: s = the smallest power of two, at least 2^-42, with
+ * amax <= 448 s; the scale becomes max(s, the scale it had) if the page holds
+ * earlier tokens of the sequence, else s.  Earlier codes are multiplied by
+ * old scale / new scale and the new ones are e4m3(x / scale), nearest with
+ * ties to even.  Infinities become +-448 under the largest scale, NaN the NaN
+ * code; neither is counted in amax but infinity.
+ *
+ *   k, v [N, kv_heads, head_dim] of ``dtype`` (bf16 or f16).
+ *   q, q_out [N, Hq, head_dim] or NULL with Hq = 0: rotated as k is.  An
+ *     output may be its own input.  Rows from cu_q[B] on are not written.
+ *   block_table [B, table_width], seq_lens [B], cu_q [B + 1] int32.
+ *   positions [N] int32 or NULL: the angle's position of each token, where it
+ *     is not the token's place in its sequence.
+ *   cos_sin as in moe_rope, or NULL with rotary_dim = 0: no rotation.
+ *   max_q_len: at least the most new tokens of one sequence (1 if cu_q is
+ *     NULL); more are not appended.
+ * A page that two sequences of a call append to is not allowed.  A table
+ * entry outside [0, num_pages), or a page past table_width, drops its tokens
+ * and reports MOE_ERR_BAD_PAGE; a sequence with more new tokens than
+ * seq_lens drops those before its start, and a position outside the table
+ * leaves its token unturned: both report MOE_ERR_BAD_POSITION.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;           /* sizeof(moe_kv_append_args_t) */
+  int dtype;
+  moe_kv_cache_t cache;
+  const void* k;
+  const void* v;
+  int64_t k_stride_token, k_stride_head, v_stride_token, v_stride_head;
+  const void* q;
+  void* q_out;
+  int64_t q_stride_token, q_stride_head, q_out_stride_token, q_out_stride_head;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  const int32_t* positions;
+  const float* cos_sin;
+  int32_t* status;
+  int N, B, Hq, table_width, max_q_len, rotary_dim, num_positions, interleaved;
+} moe_kv_append_args_t;
+int moe_kv_append(const moe_kv_append_args_t* args, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_paged_attention -- causal attention of new tokens over the cache, their
+ * own keys included (append first).
+ *
+ * Row t of sequence b is at position i = seq_lens[b] - q_len[b] + t and sees
+ * the keys j with j <= i and, if window > 0, j > i - window.  For query head
+ * h and key head h / (Hq / kv_heads):
+ *   S_j = scale * k_scale * (q . k_j),  out = sum_j softmax(S)_j v_scale v_j,
+ *   lse = log sum_j exp(S_j),
+ * with float32 sums.  A row that sees no key gives out = 0, lse = -infinity.
+ * Keys that a row does not see do not touch it, whatever their codes are.
+ *
+ *   q, out [N, Hq, head_dim] of ``dtype`` (bf16 or f16), 16-byte aligned with
+ *     strides that are multiples of 8 elements; Hq a multiple of kv_heads.
+ *   lse [N, Hq] float32 or NULL.
+ *   block_table, seq_lens, cu_q: as in moe_kv_append.  Rows from cu_q[B] on
+ *     are not written.
+ *   max_q_len, max_seq_len: at least the largest of the call; they size the
+ *     launch (rows past max_q_len are not computed).
+ *   workspace: moe_paged_attention_workspace_size() bytes, 256-byte aligned,
+ *     zero-filled once before its first use; calls leave it ready for the
+ *     next.  Calls that overlap on the GPU must not share one.
+ *   wait_timeout_ms: limit of every device-side wait (0 = 2000 ms); a wait
+ *     that runs out reports MOE_ERR_DEVICE_TIMEOUT, the output is then garbage.
+ * A table entry outside [0, num_pages) reports MOE_ERR_BAD_PAGE and its keys
+ * are left out.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;           /* sizeof(moe_paged_attention_args_t) */
+  int dtype;
+  moe_kv_cache_t cache;
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_stride_token, q_stride_head, out_stride_token, out_stride_head;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  int32_t* status;
+  void* workspace;
+  size_t workspace_bytes;
+  int N, B, Hq, table_width, max_q_len, max_seq_len, window, wait_timeout_ms;
+  float scale;
+  uint32_t debug_flags;           /* 0 */
+} moe_paged_attention_args_t;
+size_t moe_paged_attention_workspace_size(void);
+int moe_paged_attention(const moe_paged_attention_args_t* args, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -29,6 +29,8 @@ MOE_ERR_CUDA = -6
 MOE_ERR_DEVICE_TIMEOUT = -7
 MOE_ERR_BAD_MAPPING = -8
 MOE_ERR_BAD_EXPERT_ID = -9
+MOE_ERR_BAD_PAGE = -10
+MOE_ERR_BAD_POSITION = -11
 MOE_NUM_STAGE_EVENTS = 8
 MOE_WEIGHTS_BF16 = 0
 MOE_WEIGHTS_FP8_E4M3_B128 = 1
@@ -44,7 +46,8 @@ EXPORTED_SYMBOLS = [
     "moe_status_string", "moe_lora_abi_version", "moe_route_topk", "moe_permute_workspace_size",
     "moe_permute", "moe_lora_workspace_plan", "moe_lora_workspace_size", "moe_lora_forward",
     "moe_read_device_status", "moe_permute_noalloc", "moe_per_token_group_quant_fp8",
-    "moe_lora_workspace_size_ex",
+    "moe_lora_workspace_size_ex", "moe_rope", "moe_kv_append", "moe_paged_attention_workspace_size",
+    "moe_paged_attention",
 ]
 
 
@@ -132,6 +135,11 @@ def lib() -> ctypes.CDLL:
         L.moe_per_token_group_quant_fp8.argtypes = [vp, i32, i32, i32, vp, i32, vp, vp, vp]
         L.moe_lora_workspace_size_ex.restype = sz
         L.moe_lora_workspace_size_ex.argtypes = [i32] * 8
+        for fn in (L.moe_rope, L.moe_kv_append, L.moe_paged_attention):
+            fn.restype = i32
+            fn.argtypes = [ctypes.c_char_p, vp]     # the argument struct's bytes, stream
+        L.moe_paged_attention_workspace_size.restype = sz
+        L.moe_paged_attention_workspace_size.argtypes = []
         _lib = L
     return _lib
 
@@ -425,3 +433,7 @@ class MoeLoraLayer:
 
     def device_status(self, stream=None) -> int:
         return moe_read_device_status(self._ws, stream)
+
+
+from .attention import (MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32, KvAppendArgs, KvCache,  # noqa: E402
+                        PagedAttentionArgs, PagedKVCache, RopeArgs, moe_rope, rope_frequencies, rope_table)

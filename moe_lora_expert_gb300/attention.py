@@ -1,0 +1,369 @@
+"""Rotary positions, the paged 8-bit cache and attention over it.
+
+The attention half of a decoder layer, for serving next to ``MoeLoraLayer``:
+
+    cos_sin = rope_table(131072, 128, scaling={"kind": "yarn", "factor": 4.0, "original": 32768})
+    cache = PagedKVCache.create(num_pages=4096, kv_heads=4, page_size=64, head_dim=128)
+    q = cache.append(k, v, block_table, seq_lens, q=q, cos_sin=cos_sin)    # k and q rotated on the way
+    out = cache.attend(q, block_table, seq_lens)                           # one new token a sequence
+
+Argument marshalling only, as in the package's other bindings: every step runs
+in the library's kernels, PyTorch supplies memory and streams.  The arguments
+of a call are packed into the C struct's bytes in one go, since the host's
+share of a decode step counts.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import struct
+from typing import Dict, Optional
+
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F16 = 1
+MOE_DTYPE_F32 = 2
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_int),
+                *[(n, ctypes.c_void_p) for n in ("q", "q_out", "k", "k_out")],
+                *[(n, ctypes.c_int64) for n in (
+                    "q_stride_token", "q_stride_head", "q_out_stride_token", "q_out_stride_head",
+                    "k_stride_token", "k_stride_head", "k_out_stride_token", "k_out_stride_head")],
+                *[(n, ctypes.c_void_p) for n in ("positions", "cos_sin", "status")],
+                *[(n, ctypes.c_int) for n in ("N", "Hq", "Hk", "D", "rotary_dim", "num_positions",
+                                              "interleaved", "inverse")]]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [*[(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")],
+                *[(n, ctypes.c_int64) for n in ("k_stride_page", "k_stride_head", "k_stride_token",
+                                                "v_stride_page", "v_stride_head", "v_stride_token")],
+                *[(n, ctypes.c_int) for n in ("num_pages", "kv_heads", "page_size", "head_dim")]]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_int), ("cache", KvCache),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                *[(n, ctypes.c_int64) for n in ("k_stride_token", "k_stride_head", "v_stride_token",
+                                                "v_stride_head")],
+                ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                *[(n, ctypes.c_int64) for n in ("q_stride_token", "q_stride_head", "q_out_stride_token",
+                                                "q_out_stride_head")],
+                *[(n, ctypes.c_void_p) for n in ("block_table", "seq_lens", "cu_q", "positions",
+                                                 "cos_sin", "status")],
+                *[(n, ctypes.c_int) for n in ("N", "B", "Hq", "table_width", "max_q_len", "rotary_dim",
+                                              "num_positions", "interleaved")]]
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_int), ("cache", KvCache),
+                *[(n, ctypes.c_void_p) for n in ("q", "out", "lse")],
+                *[(n, ctypes.c_int64) for n in ("q_stride_token", "q_stride_head", "out_stride_token",
+                                                "out_stride_head")],
+                *[(n, ctypes.c_void_p) for n in ("block_table", "seq_lens", "cu_q", "status", "workspace")],
+                ("workspace_bytes", ctypes.c_size_t),
+                *[(n, ctypes.c_int) for n in ("N", "B", "Hq", "table_width", "max_q_len", "max_seq_len",
+                                              "window", "wait_timeout_ms")],
+                ("scale", ctypes.c_float), ("debug_flags", ctypes.c_uint32)]
+
+
+# The same layouts as bytes (64-bit pointers; the structs have no padding but
+# where every 8-byte field is aligned already).
+_ROPE = struct.Struct("=Ii4Q8q3Q8i")
+_CACHE = struct.Struct("=4Q6q4i")
+_HEAD = struct.Struct("=Ii")
+_APPEND = struct.Struct("=2Q4q2Q4q6Q8i")
+_ATTEND = struct.Struct("=3Q4q6Q8ifI")
+
+_codes = None
+
+
+def _dtype_code(dtype, name):
+    global _codes
+    if _codes is None:
+        import torch
+        _codes = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16,
+                  torch.float32: MOE_DTYPE_F32}
+    code = _codes.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or (moe_rope) float32, got {dtype}")
+    return code
+
+
+def _stream(stream, index):
+    import torch
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output of a call on ``stream``: its memory belongs to that stream."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _int32(t, shape, name):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _heads(t, N, D, dtype, name):
+    """(pointer, token stride, head stride, heads) of a [N, H, D] tensor."""
+    if t.dim() != 3 or t.shape[0] != N or t.shape[2] != D:
+        raise ValueError(f"{name} must have shape [{N}, heads, {D}], got {tuple(t.shape)}")
+    if t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must be contiguous along the head dimension")
+    return t.data_ptr(), st, sh, t.shape[1]
+
+
+def _table(cos_sin):
+    import torch
+    if (cos_sin.dtype != torch.float32 or not cos_sin.is_cuda or cos_sin.dim() != 2
+            or not cos_sin.is_contiguous()):
+        raise ValueError("cos_sin must be a contiguous float32 CUDA tensor [positions, rotary_dim]")
+    return cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
+
+
+# ----------------------------------------------------------------------------
+# Angles
+# ----------------------------------------------------------------------------
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[Dict] = None):
+    """(angle per position of each pair: list of rotary_dim / 2 floats, factor
+    on cos and sin).  ``scaling``, for contexts past the trained ones:
+
+    {"kind": "linear", "factor": s}     every angle / s
+    {"kind": "ntk", "factor": s}        base * s^(R / (R - 2)): the slowest angle / s, the fastest kept
+    {"kind": "yarn", "factor": s, "original": trained length, "beta_fast": 32, "beta_slow": 1,
+     "mscale": None}                    angles that turn more than beta_fast times in the trained
+                                        length kept, those under beta_slow / s, a ramp between;
+                                        cos and sin times mscale (0.1 ln s + 1)
+    {"kind": "llama3", "factor": s, "original": trained length, "low": 1, "high": 4}
+                                        wavelengths under original / high kept, those over
+                                        original / low divided by s, a blend between
+    """
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and at least 2")
+    R, sc = rotary_dim, dict(scaling or {"kind": "none"})
+    kind = sc.pop("kind")
+    factor = float(sc.pop("factor", 1.0))
+    if not factor > 0:
+        raise ValueError("factor must be positive")
+    mscale = 1.0
+    if kind == "ntk" and R > 2:
+        base = base * factor ** (R / (R - 2.0))
+    f = [base ** (-2.0 * i / R) for i in range(R // 2)]
+    if kind == "linear":
+        f = [x / factor for x in f]
+    elif kind == "yarn":
+        original = float(sc.pop("original"))
+        fast, slow = float(sc.pop("beta_fast", 32.0)), float(sc.pop("beta_slow", 1.0))
+        pair = lambda turns: R * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), R - 1)
+        ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(R // 2)]
+        f = [x * (1 - r) + x / factor * r for x, r in zip(f, ramp)]
+        given = sc.pop("mscale", None)
+        mscale = float(given) if given is not None else (0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0)
+    elif kind == "llama3":
+        original = float(sc.pop("original"))
+        low, high = float(sc.pop("low", 1.0)), float(sc.pop("high", 4.0))
+        blend = [min(max((original * x / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for x in f]
+        f = [x / factor * (1 - b) + x * b for x, b in zip(f, blend)]
+    elif kind not in ("none", "ntk"):
+        raise ValueError(f"unknown scaling kind {kind!r}")
+    if sc:
+        raise ValueError(f"unknown scaling arguments {sorted(sc)} for kind {kind!r}")
+    return f, mscale
+
+
+def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0,
+               scaling: Optional[Dict] = None, device=None):
+    """float32 [max_positions, rotary_dim]: cosines, then sines, of each
+    position's angles, computed in float64.  Made once, at load time."""
+    import torch
+    f, mscale = rope_frequencies(rotary_dim, base, scaling)
+    at = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None]
+    at = at * torch.tensor(f, dtype=torch.float64, device=device)
+    return torch.cat([at.cos() * mscale, at.sin() * mscale], dim=1).float()
+
+
+def moe_rope(q, positions, cos_sin, k=None, interleaved=False, inverse=False, q_out=None, k_out=None,
+             status=None, stream=None):
+    """q [N, Hq, D] (and k [N, Hk, D]) rotated by ``positions`` int32 [N]; the
+    columns past the table's rotary_dim are copied.  Returns q_out, or (q_out,
+    k_out); pass the inputs as outputs to rotate in place.  ``inverse``: the
+    gradient of the forward for an upstream gradient in q's place."""
+    from . import _check, lib
+    N, Hq, D = q.shape
+    dtype = q.dtype
+    code = _dtype_code(dtype, "q")
+    if q_out is None:
+        q_out = _empty((N, Hq, D), dtype, q.device, stream)
+    qp, q0, q1, _ = _heads(q, N, D, dtype, "q")
+    op, o0, o1, ho = _heads(q_out, N, D, dtype, "q_out")
+    kp = kop = k0 = k1 = ko0 = ko1 = Hk = hko = 0
+    if k is not None:
+        if k_out is None:
+            k_out = _empty(k.shape, dtype, q.device, stream)
+        kp, k0, k1, Hk = _heads(k, N, D, dtype, "k")
+        kop, ko0, ko1, hko = _heads(k_out, N, D, dtype, "k_out")
+    if ho != Hq or hko != Hk:
+        raise ValueError("an output must have its input's heads")
+    tp, rows, R = _table(cos_sin)
+    args = _ROPE.pack(_ROPE.size, code, qp, op, kp, kop, q0, q1, o0, o1, k0, k1, ko0, ko1,
+                      _int32(positions, (N,), "positions"), tp,
+                      0 if status is None else _int32(status, (4,), "status"),
+                      N, Hq, Hk, D, R, rows, bool(interleaved), bool(inverse))
+    _check(lib().moe_rope(args, _stream(stream, q.device.index)), "moe_rope")
+    return q_out if k is None else (q_out, k_out)
+
+
+class PagedKVCache:
+    """A paged cache of e4m3 codes with one float32 scale for each (page, head).
+
+    k, v: uint8 or float8_e4m3fn [num_pages, kv_heads, page_size, head_dim], of
+    any strides that keep the last axis contiguous (so a buffer that holds
+    [num_pages, page_size, kv_heads, head_dim] goes in as its transpose);
+    k_scale, v_scale: float32 [num_pages, kv_heads].  Token j of a sequence is
+    at (block_table[b, j // page_size], j % page_size).
+    """
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        fp8 = (torch.uint8, torch.float8_e4m3fn)
+        for t, name in ((k, "k"), (v, "v")):
+            if t.dtype not in fp8 or not t.is_cuda or t.dim() != 4 or t.shape != k.shape or t.stride(3) != 1:
+                raise ValueError(f"{name}: uint8 or float8_e4m3fn CUDA [pages, kv_heads, page_size, head_dim], "
+                                 "contiguous along the last axis, k and v alike")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.dtype != torch.float32 or not t.is_cuda or t.shape != k.shape[:2] or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 CUDA tensor {tuple(k.shape[:2])}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.device = k.device
+        self.status = torch.zeros(4, dtype=torch.int32, device=k.device)
+        self._status_ptr = self.status.data_ptr()
+        self._bytes = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                  *k.stride()[:3], *v.stride()[:3], *k.shape)
+        self._workspaces = {}
+
+    @classmethod
+    def create(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, tokens_first=False,
+               device="cuda"):
+        """An empty cache; ``tokens_first``: [page_size, kv_heads] inside a page."""
+        import torch
+        shape = (num_pages, page_size, kv_heads, head_dim) if tokens_first else (
+            num_pages, kv_heads, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2))
+        if tokens_first:
+            k, v = k.transpose(1, 2), v.transpose(1, 2)
+        ks, vs = (torch.ones((num_pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+    def workspace(self, stream_handle: int):
+        """Scratch of one stream's calls (calls on two streams may overlap)."""
+        ws = self._workspaces.get(stream_handle)
+        if ws is None:
+            import torch
+            from . import lib
+            n = int(lib().moe_paged_attention_workspace_size())
+            t = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            torch.cuda.current_stream(self.device).synchronize()   # the zeros come before any stream's use
+            ws = self._workspaces[stream_handle] = (t.data_ptr(), n, t)
+        return ws
+
+    def _batch(self, N, block_table, seq_lens, cu_q, max_q_len):
+        B = seq_lens.shape[0]
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [sequences, pages]")
+        width = block_table.shape[1]
+        bt = _int32(block_table, (B, width), "block_table")
+        sl = _int32(seq_lens, (B,), "seq_lens")
+        if cu_q is None:
+            if N != B:
+                raise ValueError("without cu_q there is one new token for each sequence")
+            return B, width, bt, sl, 0, 1
+        return B, width, bt, sl, _int32(cu_q, (B + 1,), "cu_q"), N if max_q_len is None else max_q_len
+
+    def append(self, k, v, block_table, seq_lens, cu_q=None, max_q_len=None, q=None, cos_sin=None,
+               interleaved=False, positions=None, q_out=None, stream=None):
+        """The new tokens' k (rotated by ``cos_sin``) and v, [N, kv_heads,
+        head_dim], go into the pages of their sequences: tokens [cu_q[b],
+        cu_q[b + 1]) (one each without cu_q) end at seq_lens[b].  ``q`` [N, Hq,
+        head_dim] is rotated in the same launch and returned."""
+        from . import _check, lib
+        N, D = k.shape[0], self.head_dim
+        dtype = k.dtype
+        kp, k0, k1, hk = _heads(k, N, D, dtype, "k")
+        vp, v0, v1, hv = _heads(v, N, D, dtype, "v")
+        if hk != self.kv_heads or hv != hk:
+            raise ValueError(f"k and v must have the cache's {self.kv_heads} heads")
+        qp = q0 = q1 = op = o0 = o1 = Hq = 0
+        if q is not None:
+            if q_out is None:
+                q_out = _empty(q.shape, dtype, q.device, stream)
+            qp, q0, q1, Hq = _heads(q, N, D, dtype, "q")
+            op, o0, o1, ho = _heads(q_out, N, D, dtype, "q_out")
+            if ho != Hq:
+                raise ValueError("q_out must have q's heads")
+        B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
+        tp, rows, R = (0, 0, 0) if cos_sin is None else _table(cos_sin)
+        args = b"".join((_HEAD.pack(_HEAD.size + _CACHE.size + _APPEND.size, _dtype_code(dtype, "k")), self._bytes,
+                         _APPEND.pack(kp, vp, k0, k1, v0, v1, qp, op, q0, q1, o0, o1, bt, sl, cu,
+                                      0 if positions is None else _int32(positions, (N,), "positions"), tp,
+                                      self._status_ptr, N, B, Hq, width, longest, R, rows,
+                                      bool(interleaved))))
+        _check(lib().moe_kv_append(args, _stream(stream, self.device.index)), "moe_kv_append")
+        return q_out
+
+    def attend(self, q, block_table, seq_lens, cu_q=None, max_q_len=None, max_seq_len=None, scale=None,
+               window=0, out=None, return_lse=False, lse=None, wait_timeout_ms=0, stream=None):
+        """Causal attention of q [N, Hq, head_dim] over the cache: rows as in
+        ``append``, whose keys have to be in the cache already.  ``window``:
+        how many keys a row sees, its own included (0: all).  ``max_q_len``,
+        ``max_seq_len``: host-side bounds that size the launch (by default N
+        and the block table's width).  Returns out, or (out, lse float32 [N,
+        Hq]) with ``return_lse`` or a given ``lse``."""
+        import torch
+        from . import _check, lib
+        N, Hq, D = q.shape
+        dtype = q.dtype
+        if out is None:
+            out = _empty((N, Hq, D), dtype, q.device, stream)
+        if lse is not None:
+            if lse.dtype != torch.float32 or lse.shape != (N, Hq) or not lse.is_contiguous() or not lse.is_cuda:
+                raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{N}, {Hq}]")
+        elif return_lse:
+            lse = _empty((N, Hq), torch.float32, q.device, stream)
+        qp, q0, q1, _ = _heads(q, N, self.head_dim, dtype, "q")
+        op, o0, o1, ho = _heads(out, N, self.head_dim, dtype, "out")
+        if ho != Hq:
+            raise ValueError("out must have q's heads")
+        B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
+        handle = _stream(stream, self.device.index)
+        ws = self.workspace(handle)
+        args = b"".join((_HEAD.pack(_HEAD.size + _CACHE.size + _ATTEND.size, _dtype_code(dtype, "q")), self._bytes,
+                         _ATTEND.pack(qp, op, 0 if lse is None else lse.data_ptr(), q0, q1, o0, o1, bt, sl, cu,
+                                      self._status_ptr, ws[0], ws[1], N, B, Hq, width, longest,
+                                      width * self.page_size if max_seq_len is None else max_seq_len, window,
+                                      wait_timeout_ms, D ** -0.5 if scale is None else scale, 0)))
+        _check(lib().moe_paged_attention(args, handle), "moe_paged_attention")
+        return out if lse is None else (out, lse)
+
+    def device_status(self) -> int:
+        """The first problem that a call met on the device since the last
+        reading (MOE_OK: none); waits for the device's work and clears it."""
+        code = int(self.status[0].item())
+        if code:
+            self.status.zero_()
+        return code

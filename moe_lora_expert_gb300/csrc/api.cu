@@ -255,6 +255,8 @@ const char* moe_status_string(int status) {
     case MOE_ERR_DEVICE_TIMEOUT: return "MOE_ERR_DEVICE_TIMEOUT: a device pipeline wait timed out";
     case MOE_ERR_BAD_MAPPING: return "MOE_ERR_BAD_MAPPING: token_lora_mapping outside [-1, A)";
     case MOE_ERR_BAD_EXPERT_ID: return "MOE_ERR_BAD_EXPERT_ID: a topk id outside [-1, E)";
+    case MOE_ERR_BAD_PAGE: return "MOE_ERR_BAD_PAGE: a block table entry outside the cache";
+    case MOE_ERR_BAD_POSITION: return "MOE_ERR_BAD_POSITION: a position outside the table or below 0";
     default: return "unknown moe status";
   }
 }

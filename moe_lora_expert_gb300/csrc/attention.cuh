@@ -1,0 +1,156 @@
+// What the kernels of the attention half share: element types, the rotation of
+// one stretch of a head, float8 e4m3 conversions, and the launch interfaces of
+// rope.cu, kv_append.cu and paged_attention.cu.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moe_lora.h"
+
+namespace moe {
+
+// ---------------------------------------------------------------- elements
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+
+// N elements (N * sizeof(T) bytes, aligned to min(16, that)) to and from float32.
+template <typename T, int N>
+struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Pack {
+  T v[N];
+};
+template <typename T, int N>
+__device__ __forceinline__ void load_f32(const T* p, float (&x)[N]) {
+  const Pack<T, N> r = *reinterpret_cast<const Pack<T, N>*>(p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = to_f32(r.v[i]);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_f32(T* p, const float (&x)[N]) {
+  Pack<T, N> r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) r.v[i] = from_f32<T>(x[i]);
+  *reinterpret_cast<Pack<T, N>*>(p) = r;
+}
+
+// -------------------------------------------------------------------- e4m3
+// Two e4m3 codes (low byte first) to two float16 values, exact; NaN codes give NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(codes));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint16_t codes) {
+  const uint32_t h = e4m3x2_to_f16x2(codes);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Two float32 values to e4m3 codes (first in the low byte): nearest, ties to
+// even, magnitudes past 448 give 448, NaN stays NaN.
+__device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float first, float second) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(second), "f"(first));
+  return r;
+}
+
+// ---------------------------------------------------------------- rotation
+// A head is cut into D / 2V stretches of 2V elements that one thread handles.
+// Stretch c of the rotated part holds the pairs of frequencies [Vc, Vc + V):
+// two runs of V elements R/2 apart (half layout) or one run of 2V elements
+// (interleaved).  Past the rotated part a stretch is one run of 2V elements.
+// V divides R/2, and 2V divides D.
+template <int V>
+struct Stretch {
+  int a, b;       // first elements of the two runs
+  bool turned;    // in the rotated part
+  __device__ __forceinline__ Stretch(int c, int R, bool interleaved) {
+    turned = 2 * V * c < R;
+    const bool split = turned && !interleaved;
+    a = split ? V * c : 2 * V * c;
+    b = split ? R / 2 + V * c : a + V;
+  }
+};
+
+// cos and sin of frequencies [Vc, Vc + V) from a table row (R/2 cosines, then R/2 sines).
+template <int V>
+__device__ __forceinline__ void load_cos_sin(const float* row, int c, int R, float (&cs)[V], float (&sn)[V]) {
+  load_f32<float, V>(row + V * c, cs);
+  load_f32<float, V>(row + R / 2 + V * c, sn);
+}
+
+// (u, w) -> (u cos - w sin, w cos + u sin) for each pair, in float32.  In the
+// interleaved layout the 2V elements (a, b) hold the pairs side by side.
+template <int V>
+__device__ __forceinline__ void rotate(float (&a)[V], float (&b)[V], const float (&cs)[V], const float (&sn)[V],
+                                       bool interleaved) {
+  if (!interleaved || V == 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float u = a[i], w = b[i];
+      a[i] = u * cs[i] - w * sn[i];
+      b[i] = w * cs[i] + u * sn[i];
+    }
+  } else if constexpr (V > 1) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float u = a[2 * i], w = a[2 * i + 1];
+      a[2 * i] = u * cs[i] - w * sn[i];
+      a[2 * i + 1] = w * cs[i] + u * sn[i];
+      const float x = b[2 * i], y = b[2 * i + 1];
+      b[2 * i] = x * cs[V / 2 + i] - y * sn[V / 2 + i];
+      b[2 * i + 1] = y * cs[V / 2 + i] + x * sn[V / 2 + i];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launch
+// One operand of a rotation: [N, H, D] with strides in elements.
+struct RopeTensor {
+  const void* in;
+  void* out;
+  int64_t in_token, in_head, out_token, out_head;
+  int heads;
+};
+struct RopeParams {
+  RopeTensor q, k;
+  const int32_t* positions;
+  const float* cos_sin;
+  int32_t* status;
+  int N, D, R, num_positions, interleaved, inverse;
+};
+cudaError_t launch_rope(const RopeParams& p, int dtype, int V, cudaStream_t s);
+
+struct KvAppendParams {
+  moe_kv_cache_t cache;
+  const void *k, *v;
+  int64_t k_token, k_head, v_token, v_head;
+  RopeTensor q;                 // heads 0: none
+  const int32_t *block_table, *seq_lens, *cu_q, *positions;
+  const float* cos_sin;
+  int32_t* status;
+  int N, B, table_width, R, num_positions, interleaved;
+  int slots;                    // pages that one sequence's new tokens can touch
+};
+cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, int V, cudaStream_t s);
+
+struct AttentionParams {
+  moe_kv_cache_t cache;
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_token, q_head, out_token, out_head;
+  const int32_t *block_table, *seq_lens, *cu_q;
+  int32_t* status;
+  int N, B, Hq, table_width, max_q_len;
+  int window;                   // keys a row sees, itself included; 0 = all before it
+  float scale;
+};
+cudaError_t launch_paged_attention(const AttentionParams& p, int dtype, cudaStream_t s);
+
+}  // namespace moe
