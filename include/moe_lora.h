@@ -615,8 +615,12 @@ typedef struct {
   size_t workspace_bytes;
   int N, B, Hq, table_width, max_q_len, max_seq_len, window, wait_timeout_ms;
   float scale;
-  uint32_t debug_flags;           /* 0 */
+  uint32_t debug_flags;           /* 0 in normal use; see MOE_DEBUG_STALL_ATTENTION */
 } moe_paged_attention_args_t;
+/* Test-only flag: no key tile is loaded, so the waits for them run out after
+ * wait_timeout_ms; the call then reports MOE_ERR_DEVICE_TIMEOUT and its output
+ * is garbage, but the workspace is ready for the next call. */
+#define MOE_DEBUG_STALL_ATTENTION 4u
 size_t moe_paged_attention_workspace_size(void);
 int moe_paged_attention(const moe_paged_attention_args_t* args, moe_stream_t stream);
 

@@ -435,5 +435,5 @@ class MoeLoraLayer:
         return moe_read_device_status(self._ws, stream)
 
 
-from .attention import (MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32, KvAppendArgs, KvCache,  # noqa: E402
-                        PagedAttentionArgs, PagedKVCache, RopeArgs, moe_rope, rope_frequencies, rope_table)
+from .attention import (MOE_DEBUG_STALL_ATTENTION, MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32,  # noqa: E402
+                        KvAppendArgs, KvCache, PagedAttentionArgs, PagedKVCache, RopeArgs, moe_rope, rope_frequencies, rope_table)

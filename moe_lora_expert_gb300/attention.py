@@ -22,6 +22,7 @@ from typing import Dict, Optional
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F16 = 1
 MOE_DTYPE_F32 = 2
+MOE_DEBUG_STALL_ATTENTION = 4
 
 
 class RopeArgs(ctypes.Structure):
@@ -327,7 +328,7 @@ class PagedKVCache:
         return q_out
 
     def attend(self, q, block_table, seq_lens, cu_q=None, max_q_len=None, max_seq_len=None, scale=None,
-               window=0, out=None, return_lse=False, lse=None, wait_timeout_ms=0, stream=None):
+               window=0, out=None, return_lse=False, lse=None, wait_timeout_ms=0, debug_flags=0, stream=None):
         """Causal attention of q [N, Hq, head_dim] over the cache: rows as in
         ``append``, whose keys have to be in the cache already.  ``window``:
         how many keys a row sees, its own included (0: all).  ``max_q_len``,
@@ -356,7 +357,7 @@ class PagedKVCache:
                          _ATTEND.pack(qp, op, 0 if lse is None else lse.data_ptr(), q0, q1, o0, o1, bt, sl, cu,
                                       self._status_ptr, ws[0], ws[1], N, B, Hq, width, longest,
                                       width * self.page_size if max_seq_len is None else max_seq_len, window,
-                                      wait_timeout_ms, D ** -0.5 if scale is None else scale, 0)))
+                                      wait_timeout_ms, D ** -0.5 if scale is None else scale, debug_flags)))
         _check(lib().moe_paged_attention(args, handle), "moe_paged_attention")
         return out if lse is None else (out, lse)
 

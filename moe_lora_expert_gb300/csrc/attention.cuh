@@ -51,6 +51,18 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint16_t codes) {
   const uint32_t h = e4m3x2_to_f16x2(codes);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
+// 2^x, to 2 units in the last place; 2^-infinity is 0.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two float32 values to float16, first in the low half.
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float first, float second) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(second), "f"(first));
+  return r;
+}
 // Two float32 values to e4m3 codes (first in the low byte): nearest, ties to
 // even, magnitudes past 448 give 448, NaN stays NaN.
 __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float first, float second) {
@@ -139,6 +151,9 @@ struct KvAppendParams {
 };
 cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, int V, cudaStream_t s);
 
+// Attention.  A "row" is one (new token, query head) of a key head's group:
+// row r of sequence b and key head h is token r / group, query head h * group
+// + r % group.
 struct AttentionParams {
   moe_kv_cache_t cache;
   const void* q;
@@ -147,10 +162,15 @@ struct AttentionParams {
   int64_t q_token, q_head, out_token, out_head;
   const int32_t *block_table, *seq_lens, *cu_q;
   int32_t* status;
-  int N, B, Hq, table_width, max_q_len;
+  int N, B, Hq, table_width, max_q_len, max_seq_len;
   int window;                   // keys a row sees, itself included; 0 = all before it
   float scale;
+  void* workspace;
+  uint64_t wait_limit_ns;
+  uint32_t debug_flags;
 };
 cudaError_t launch_paged_attention(const AttentionParams& p, int dtype, cudaStream_t s);
+size_t decode_attention_workspace_bytes();
+int launch_decode_attention(const AttentionParams& p, int dtype, cudaStream_t s);   // a moe_status_t
 
 }  // namespace moe

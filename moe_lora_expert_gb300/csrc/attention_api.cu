@@ -124,7 +124,7 @@ int moe_kv_append(const moe_kv_append_args_t* a, moe_stream_t stream) {
   return done(moe::launch_kv_append(p, a->dtype, V, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t moe_paged_attention_workspace_size(void) { return 256; }
+size_t moe_paged_attention_workspace_size(void) { return moe::decode_attention_workspace_bytes(); }
 
 int moe_paged_attention(const moe_paged_attention_args_t* a, moe_stream_t stream) {
   if (a == nullptr) return MOE_ERR_NULL;
@@ -137,7 +137,7 @@ int moe_paged_attention(const moe_paged_attention_args_t* a, moe_stream_t stream
   const moe_kv_cache_t& c = a->cache;
   if (a->Hq <= 0 || a->Hq % c.kv_heads != 0 || a->max_seq_len < 0 || a->window < 0 || a->wait_timeout_ms < 0)
     return MOE_ERR_SHAPE;
-  if (a->Hq > 65536 || a->debug_flags != 0) return MOE_ERR_UNSUPPORTED;
+  if (a->Hq > 65536 || (a->debug_flags & ~MOE_DEBUG_STALL_ATTENTION) != 0) return MOE_ERR_UNSUPPORTED;
   if (a->N == 0 || a->B == 0 || a->max_q_len == 0) return MOE_OK;
   if (a->q == nullptr || a->out == nullptr) return MOE_ERR_NULL;
   const int64_t strides[4] = {a->q_stride_token, a->q_stride_head, a->out_stride_token, a->out_stride_head};
@@ -156,8 +156,13 @@ int moe_paged_attention(const moe_paged_attention_args_t* a, moe_stream_t stream
   p.N = a->N, p.B = a->B, p.Hq = a->Hq, p.table_width = a->table_width;
   p.max_q_len = a->cu_q == nullptr ? 1 : a->max_q_len < a->N ? a->max_q_len : a->N;
   p.window = a->window;
+  p.max_seq_len = a->max_seq_len;
   p.scale = a->scale;
+  p.workspace = a->workspace;
+  p.wait_limit_ns = 1000000ull * static_cast<uint64_t>(a->wait_timeout_ms > 0 ? a->wait_timeout_ms : 2000);
+  p.debug_flags = a->debug_flags;
   (void)cudaGetLastError();
+  if (p.max_q_len * (a->Hq / c.kv_heads) <= 256) return moe::launch_decode_attention(p, a->dtype, reinterpret_cast<cudaStream_t>(stream));
   return done(moe::launch_paged_attention(p, a->dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -1,0 +1,763 @@
+// Attention of a few new tokens over the paged cache: decode, and the few
+// tokens a draft proposes.
+//
+// Each key head's rows (new tokens x query heads of its group) are cut into
+// tiles of 16 and the keys into tiles of 64.  All (row tile, key tile) pairs
+// of the call form one line, which the CTAs of the grid share in equal
+// stretches whatever the sequences' lengths are; a row tile whose keys lie in
+// several stretches is joined by the CTA that finishes it last.
+//
+// Mathematics.  With t_j = log2(e) scale k_scale (q . k_j) the weights are
+//   w_j = 2^(t_j + log2(v_scale) - m),  m the running maximum of that exponent,
+//   out = sum_j w_j code_j / sum_j (w_j / v_scale),
+// so w_j is what multiplies the codes: it is at most 2^8 in float16 whatever
+// the pages' scales are, and both sums stay in float32.  Codes enter the
+// tensor cores as float16, which holds each exactly; so does q (bf16 rows are
+// first scaled by a power of two), and the scores are exact products.
+//
+// What bounds it.  One pass over the cache's bytes.  The tensor work of 16
+// rows is far below even mma.sync's rate (a 64-key tile needs 64 m16n8k16 per
+// 16 KB), so fragments go straight from shared memory to registers: a
+// tcgen05 tile would be 128 keys high and need its codes converted and written
+// back to shared memory first.
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "attention.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kKeys = 64;                 // keys of a tile
+constexpr int kRows = 16;                 // rows of a row tile
+constexpr int kStages = 4;
+constexpr int kWarps = 4;                 // consumers, 16 keys of a tile each
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kCtasPerSm = 3;
+constexpr int kMaxCtas = 640;
+constexpr int kMaxEntries = 512;          // (sequence, row tile) pairs of one launch
+constexpr int kJoin = 8;                  // pieces that are joined at a time
+constexpr int kPitch = 128;               // bytes of a key in shared memory
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;             // a maximum may rise by 2^8 before the sums are rescaled
+
+struct alignas(16) Group {                // 8 keys of a tile, which lie in one page
+  float k;                                // log2(e) * scale * k_scale
+  float lv;                               // log2(v_scale)
+  float inv_v;                            // 1 / v_scale
+  int valid;
+};
+
+struct Shared {
+  Group group[kStages][8];
+  uint64_t full[kStages], empty[kStages];
+  int prefix[kMaxEntries + 1];            // key tiles before each entry
+  int begin[kMaxEntries];                 // first key that some row of each entry sees
+  int end[kMaxEntries];                   // end of the keys that some row of it sees
+  float m[kWarps][kRows], l[kWarps][kRows];
+  int total, abort_flag, last, issued;
+};
+constexpr int kStageBytes = 2 * kKeys * kPitch;
+constexpr int kSmemBytes = kStages * kStageBytes + static_cast<int>(sizeof(Shared)) + 1024;
+
+// Partial sums of a row tile: [slot][row][128] and (m, l) [slot][row][2];
+// counters [2][slots].
+constexpr int kSlots = 2 * kMaxCtas;
+constexpr size_t kPartialBytes = static_cast<size_t>(kSlots) * kRows * 128 * 4;
+constexpr size_t kMlBytes = static_cast<size_t>(kSlots) * kRows * 2 * 4;
+constexpr size_t kCounterBytes = static_cast<size_t>(kSlots) * 2 * 4;
+
+struct Launch {
+  AttentionParams a;
+  int b0, B, row_tiles;                   // sequences [b0, b0 + B), row tiles of each
+  int box;                                // keys of one TMA box: gcd(page_size, 64)
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The rows of entry e (a sequence and a row tile of it).
+struct Entry {
+  int b, q_first, q_len, len, row0, rows;
+  __device__ __forceinline__ Entry(const Launch& p, int e, int group) {
+    b = p.b0 + e / p.row_tiles;
+    row0 = (e % p.row_tiles) * kRows;
+    q_first = p.a.cu_q == nullptr ? b : p.a.cu_q[b];
+    q_len = p.a.cu_q == nullptr ? 1 : p.a.cu_q[b + 1] - q_first;
+    len = p.a.seq_lens[b];
+    const int n = min(min(q_len, p.a.max_q_len), p.a.N - q_first);
+    rows = max(0, min(kRows, n * group - row0));
+  }
+  __device__ __forceinline__ int position(int row, int group) const { return len - q_len + (row0 + row) / group; }
+};
+
+// Where tile x of the line lies.
+struct Place {
+  int e, head, tile, count;
+  __device__ __forceinline__ Place(const Shared& s, int entries, int kv_heads, int x) {
+    int lo = 0, hi = entries;              // the last entry with prefix * heads <= x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.prefix[mid] * kv_heads <= x) lo = mid; else hi = mid;
+    }
+    e = lo;
+    count = s.prefix[e + 1] - s.prefix[e];
+    const int in = x - s.prefix[e] * kv_heads;
+    head = in / count;
+    tile = in - head * count;
+  }
+};
+
+// Removes the NaN codes of a word and remembers that there were some.
+__device__ __forceinline__ uint32_t drop_nan(uint32_t w, uint32_t& seen) {
+  const uint32_t nan = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  seen |= nan;
+  return w & ~nan;
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const Launch p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* const stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  Shared& s = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes);
+  const AttentionParams& a = p.a;
+  const moe_kv_cache_t& ca = a.cache;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.Hq / ca.kv_heads, entries = p.B * p.row_tiles;
+  constexpr int kWords = DP / 16;          // 4-code words of a key in one thread: K steps
+  constexpr int kTiles = DP / 8;           // output tiles of 8 columns
+
+  if (tid == 0) {
+    tma_prefetch_map(&k_map);
+    tma_prefetch_map(&v_map);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], kWarps);
+    }
+    s.abort_flag = 0;
+    s.issued = 0;
+    fence_mbarrier_init();
+  }
+  pdl_wait();
+
+  // The line: each entry's key tiles, one at least so that someone writes its rows.
+  const int64_t most = static_cast<int64_t>(a.table_width) * ca.page_size;
+  for (int e = tid; e < entries; e += kThreads) {
+    const Entry en(p, e, group);
+    int n = 0, lo = 0, hi = 0;
+    if (en.rows > 0) {
+      const int pos0 = en.position(0, group), pos1 = en.position(en.rows - 1, group);
+      lo = a.window > 0 && pos0 >= a.window ? pos0 + 1 - a.window : 0;
+      hi = max(0, pos1 + 1);
+      if (hi > most) {
+        hi = static_cast<int>(most);
+        set_status(a.status, MOE_ERR_BAD_PAGE);
+      }
+      n = max(1, (hi + kKeys - 1) / kKeys - lo / kKeys);
+    }
+    s.prefix[e + 1] = n;
+    s.begin[e] = lo;
+    s.end[e] = hi;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int per = (entries + 31) / 32, from = min(lane * per, entries), to = min(from + per, entries);
+    int sum = 0;
+    for (int e = from; e < to; ++e) sum += s.prefix[e + 1];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int run = incl - sum;
+    for (int e = from; e < to; ++e) {
+      run += s.prefix[e + 1];
+      s.prefix[e + 1] = run;
+    }
+    if (lane == 0) s.prefix[0] = 0;
+    if (lane == 31) s.total = incl * ca.kv_heads;
+  }
+  __syncthreads();
+  const int total = s.total, ctas = min(static_cast<int>(gridDim.x), total);   // with fewer tiles than CTAs, one each
+  auto begin_of = [&](int cta) { return static_cast<int>(static_cast<int64_t>(total) * cta / ctas); };
+  const bool idle = static_cast<int>(blockIdx.x) >= ctas;
+  const int x0 = idle ? 0 : begin_of(blockIdx.x), x1 = idle ? 0 : begin_of(blockIdx.x + 1);
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (*static_cast<volatile int*>(&s.abort_flag)) return;
+    if (!mbar_wait(bar, parity, a.wait_limit_ns)) {
+      set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+      *static_cast<volatile int*>(&s.abort_flag) = 1;
+    }
+  };
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    // Four tiles at a time, a lane for each group of 8 keys: its page from
+    // the block table, then that page's scales; both are fetched ahead of the
+    // tiles that use them.
+    struct Ahead {
+      int page, off, head;
+      float ks, vs;
+    };
+    const int sub = lane & 7;
+    auto find = [&](int k) {
+      Ahead f = {-1, 0, 0, 0.f, 0.f};
+      const int x = x0 + k + (lane >> 3);
+      if (x < x1) {
+        const Place at(s, entries, ca.kv_heads, x);
+        const int key = (s.begin[at.e] / kKeys + at.tile) * kKeys + 8 * sub;
+        const int page_at = key / ca.page_size;
+        f.off = key - page_at * ca.page_size;
+        f.head = at.head;
+        // boxes that no row sees are not looked up: their pages may be gone
+        if (key < s.end[at.e] && (key & ~(p.box - 1)) + p.box > s.begin[at.e]) {
+          f.page = a.block_table[static_cast<int64_t>(p.b0 + at.e / p.row_tiles) * a.table_width + page_at];
+          if (f.page < 0 || f.page >= ca.num_pages) {
+            f.page = -1;
+            set_status(a.status, MOE_ERR_BAD_PAGE);
+          }
+        }
+      }
+      return f;
+    };
+    auto scales = [&](Ahead& f) {
+      if (f.page >= 0) {
+        const int64_t i = static_cast<int64_t>(f.page) * ca.kv_heads + f.head;
+        f.ks = ca.k_scale[i];
+        f.vs = ca.v_scale[i];
+      }
+    };
+    Ahead now = find(0), next = find(4);
+    scales(now);
+    const bool stalled = (a.debug_flags & MOE_DEBUG_STALL_ATTENTION) != 0;   // a failure for the tests: no tile arrives
+    for (int k = 0; x0 + k < x1 && !stalled; k += 4) {
+      scales(next);
+      const Ahead later = find(k + 8);
+      Group g;
+      g.k = now.ks * a.scale * kLog2e;
+      const float vs = fmaxf(now.vs, 5.421010862427522e-20f);   // 2^-64: a zero scale gives zero values
+      g.lv = log2f(vs);
+      g.inv_v = 1.f / vs;
+      g.valid = now.page >= 0;
+      const bool issues = g.valid && (8 * sub) % p.box == 0;
+      const unsigned boxes = __ballot_sync(0xffffffffu, issues);
+      for (int i = 0; i < 4 && x0 + k + i < x1; ++i) {
+        const int st = (k + i) % kStages, fill = (k + i) / kStages;
+        if (fill > 0) wait(&s.empty[st], (fill - 1) & 1);
+        if ((lane >> 3) == i) s.group[st][sub] = g;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&s.full[st], __popc((boxes >> (8 * i)) & 0xFF) * p.box * kPitch * 2);
+          s.issued = k + i + 1;
+        }
+        __syncwarp();
+        if ((lane >> 3) == i && issues) {
+          const uint32_t dst = smem_u32(stages + st * kStageBytes) + 8 * sub * kPitch;
+          tma_load_4d(dst, &k_map, &s.full[st], now.off, now.head, now.page);
+          tma_load_4d(dst + kKeys * kPitch, &v_map, &s.full[st], now.off, now.head, now.page);
+        }
+      }
+      now = next;
+      next = later;
+    }
+  } else {
+    // ----------------------------------------------------------- consumers
+    const int g = lane >> 2, c = lane & 3;
+    int fill = 0;                          // tiles consumed so far
+    for (int x = x0; x < x1;) {
+      const Place at(s, entries, ca.kv_heads, x);
+      const Entry en(p, at.e, group);
+      const int n = min(at.count - at.tile, x1 - x);
+      const int first_tile = s.begin[at.e] / kKeys + at.tile;
+      int pos[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = g + 8 * i;
+        pos[i] = r < en.rows ? en.position(r, group) : -1;
+      }
+      const int pos_min = en.position(0, group), pos_max = en.position(en.rows - 1, group);
+      const int end = s.end[at.e];
+
+      // Q as the A operand: K step i, column pair (0, 1) in a0 / a1 and (2, 3)
+      // in a2 / a3 are columns DP/4 * c + 4 i + (0..3), the order in which a
+      // thread reads the codes of a key.
+      uint32_t qf[kWords][4];
+      float row_scale[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = g + 8 * i;
+        float q[DP / 4];
+        const int row = en.row0 + r, tok = en.q_first + row / group, h = at.head * group + row % group;
+        const T* src = static_cast<const T*>(a.q) + tok * a.q_token + h * a.q_head;
+        float amax = 0.f;
+#pragma unroll
+        for (int d = 0; d < DP / 4; d += 8) {
+          const int col = DP / 4 * c + d;
+          float v[8] = {};
+          if (r < en.rows && col < ca.head_dim) load_f32<T, 8>(src + col, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            q[d + j] = v[j];
+            amax = fmaxf(amax, fabsf(v[j]));
+          }
+        }
+        row_scale[i] = 1.f;
+        if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          // a power of two that brings the row's largest value into [1, 2)
+          const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+          if (ex > -120 && ex < 120) {
+            row_scale[i] = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+            const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+#pragma unroll
+            for (int d = 0; d < DP / 4; ++d) q[d] *= inv;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          qf[w][i] = f32x2_to_f16x2(q[4 * w], q[4 * w + 1]);
+          qf[w][2 + i] = f32x2_to_f16x2(q[4 * w + 2], q[4 * w + 3]);
+        }
+      }
+
+      float o[kTiles][4];
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+      for (int i = 0; i < n; ++i, ++fill) {
+        const int st = fill % kStages;
+        wait(&s.full[st], (fill / kStages) & 1);
+        const int key0 = (first_tile + i) * kKeys + 16 * warp;
+        const uint8_t* kt = stages + st * kStageBytes + 16 * warp * kPitch;
+        const uint8_t* vt = kt + kKeys * kPitch;
+        const Group g0 = s.group[st][2 * warp], g1 = s.group[st][2 * warp + 1];
+        const bool some = key0 < end && (a.window == 0 || key0 + 15 > pos_min - a.window) && (g0.valid || g1.valid);
+        if (some) {
+          // S = Q K^T for 16 keys
+          float sc[2][4] = {};
+          uint4 kw[2][DP / 64];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t* row = kt + (8 * h + g) * kPitch;
+#pragma unroll
+            for (int u = 0; u < DP / 64; ++u)
+              kw[h][u] = *reinterpret_cast<const uint4*>(row + (((DP / 64) * c + u) ^ g) * 16);
+          }
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4& u = kw[h][w / 4];
+              const uint32_t word = (w & 3) == 0 ? u.x : (w & 3) == 1 ? u.y : (w & 3) == 2 ? u.z : u.w;
+              mma_f16(sc[h], qf[w], e4m3x2_to_f16x2(word & 0xFFFF), e4m3x2_to_f16x2(word >> 16));
+            }
+          }
+          // exponents of the weights
+          float top[2] = {-INFINITY, -INFINITY};
+          const bool whole = key0 + 15 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) && g0.valid && g1.valid;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const Group& gr = h == 0 ? g0 : g1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float y = fmaf(sc[h][j], gr.k * row_scale[j >> 1], gr.lv);
+              if (!whole) {
+                const int key = key0 + 8 * h + 2 * c + (j & 1), ps = pos[j >> 1];
+                if (!gr.valid || key > ps || (a.window > 0 && key <= ps - a.window)) y = -INFINITY;
+              }
+              sc[h][j] = y;
+              top[j >> 1] = fmaxf(top[j >> 1], y);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+          }
+          const bool raise = top[0] > m[0] + kSlack || top[1] > m[1] + kSlack;
+          if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float now = fmaxf(m[r], top[r]);
+              const float keep = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - now);
+              m[r] = now;
+              l[r] *= keep;
+#pragma unroll
+              for (int j = 0; j < kTiles; ++j) {
+                o[j][2 * r] *= keep;
+                o[j][2 * r + 1] *= keep;
+              }
+            }
+          }
+          uint32_t pf[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const Group& gr = h == 0 ? g0 : g1;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float base = m[r] == -INFINITY ? 0.f : m[r];
+              const float w0 = fast_exp2(sc[h][2 * r] - base), w1 = fast_exp2(sc[h][2 * r + 1] - base);
+              l[r] = fmaf(w0 + w1, gr.inv_v, l[r]);
+              pf[2 * h + r] = f32x2_to_f16x2(w0, w1);
+            }
+          }
+          // O += P V: a thread reads DP / 8 columns of four keys; column j of
+          // them is output tile j
+          uint32_t vw[4][kTiles / 4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int key = 8 * (h >> 1) + 2 * c + (h & 1);
+            if constexpr (DP == 128) {
+              const uint4 u = *reinterpret_cast<const uint4*>(vt + key * kPitch + ((g ^ (key & 7)) * 16));
+              vw[h][0] = u.x, vw[h][1] = u.y, vw[h][2] = u.z, vw[h][3] = u.w;
+            } else {
+              const uint2 u = *reinterpret_cast<const uint2*>(vt + key * kPitch + (((g >> 1) ^ (key & 7)) * 16) + 8 * (g & 1));
+              vw[h][0] = u.x, vw[h][1] = u.y;
+            }
+          }
+          uint32_t nan = 0;
+          if (!whole) {                    // a weight of zero times a NaN code would be NaN
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+              for (int w = 0; w < kTiles / 4; ++w) vw[h][w] = drop_nan(vw[h][w], nan);
+          }
+#pragma unroll
+          for (int w = 0; w < kTiles / 4; ++w) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t sel = half == 0 ? 0x5140 : 0x7362;
+              const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], sel), hi = __byte_perm(vw[2][w], vw[3][w], sel);
+              const int j = 4 * w + 2 * half;
+              mma_f16(o[j], pf, e4m3x2_to_f16x2(lo & 0xFFFF), e4m3x2_to_f16x2(hi & 0xFFFF));
+              mma_f16(o[j + 1], pf, e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi >> 16));
+            }
+          }
+          if (!whole && __any_sync(0xffffffffu, nan != 0)) {
+            // NaN codes of a partly hidden tile reach the rows that see them
+            for (int k = 0; k < 16; ++k) {
+              const int key = key0 + k;
+              const bool ok = (k < 8 ? g0 : g1).valid != 0;
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                if (!ok || key > pos[r] || (a.window > 0 && key <= pos[r] - a.window)) continue;
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    const int col = (DP / 8) * (2 * c + z) + j;
+                    const uint8_t code = vt[k * kPitch + (((col >> 4) ^ (k & 7)) * 16) + (col & 15)];
+                    if ((code & 0x7F) == 0x7F) o[j][2 * r + z] = __uint_as_float(0x7FC00000u);
+                  }
+              }
+            }
+          }
+        }
+        if (i + 1 < n) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.empty[st]);
+        }
+      }
+
+      // Join the four warps: the last tile's stage is the scratch.
+      const int st = (fill - 1) % kStages;
+      float* scratch = reinterpret_cast<float*>(stages + st * kStageBytes);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (c == 0) {
+          s.m[warp][g + 8 * r] = m[r];
+          s.l[warp][g + 8 * r] = l[r];
+        }
+      }
+      named_barrier_sync(1, 32 * kWarps);
+      float M[2], L[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        M[r] = -INFINITY;
+        L[r] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M[r] = fmaxf(M[r], s.m[w][g + 8 * r]);
+        const float base = M[r] == -INFINITY ? 0.f : M[r];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) L[r] += s.l[w][g + 8 * r] * fast_exp2(s.m[w][g + 8 * r] - base);
+        const float keep = fast_exp2(m[r] - base);
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          o[j][2 * r] *= keep;
+          o[j][2 * r + 1] *= keep;
+        }
+      }
+      auto put = [&](float* to) {
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) to[(4 * j + z) * 32 + lane] = o[j][z];
+      };
+      auto add = [&](const float* from) {
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) o[j][z] += from[(4 * j + z) * 32 + lane];
+      };
+      if (warp >= 2) put(scratch + (warp - 2) * 2048);
+      named_barrier_sync(1, 32 * kWarps);
+      if (warp < 2) add(scratch + warp * 2048);
+      named_barrier_sync(1, 32 * kWarps);
+      if (warp == 1) put(scratch);
+      named_barrier_sync(1, 32 * kWarps);
+      if (warp == 0) add(scratch);
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.empty[st]);
+
+      const bool begun_before = at.tile > 0, goes_on = at.tile + n < at.count;
+      const bool split = begun_before || goes_on;
+      float* parts = static_cast<float*>(a.workspace);
+      float* ml = parts + kPartialBytes / 4;
+      int* counters = reinterpret_cast<int*>(ml + kMlBytes / 4);
+
+      // A thread of warp 0 holds, for rows g and g + 8, columns [DP/4 c, DP/4 c + DP/4).
+      if (warp == 0) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = g + 8 * r;
+          if (row >= en.rows) continue;
+          if (!split) {
+            const float inv = L[r] == 0.f ? 0.f : 1.f / L[r];
+            const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
+            T* dst = static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head;
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+              for (int j = 0; j < kTiles; j += 8) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = o[j + k][2 * r + z] * inv;
+                const int col = (DP / 8) * (2 * c + z) + j;
+                if (col < ca.head_dim) store_f32<T, 8>(dst + col, v);
+              }
+            if (c == 0 && a.lse != nullptr)
+              a.lse[static_cast<int64_t>(tok) * a.Hq + h] = L[r] == 0.f ? -INFINITY : (M[r] + log2f(L[r])) * kLn2;
+          } else {
+            const int slot = 2 * blockIdx.x + (begun_before ? 0 : 1);
+            float* dst = parts + (static_cast<size_t>(slot) * kRows + row) * 128;
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+              for (int j = 0; j < kTiles; j += 4) {
+                const float v[4] = {o[j][2 * r + z], o[j + 1][2 * r + z], o[j + 2][2 * r + z], o[j + 3][2 * r + z]};
+                store_f32<float, 4>(dst + (DP / 8) * (2 * c + z) + j, v);
+              }
+            if (c == 0) *reinterpret_cast<float2*>(ml + (static_cast<size_t>(slot) * kRows + row) * 2) = make_float2(M[r], L[r]);
+          }
+        }
+      }
+
+      if (split) {
+        // Pieces of this row tile: CTAs [cta0, cta1], joined eight at a time
+        // by whoever finishes last among them, then those results likewise.
+        const int u0 = x - at.tile, u1 = u0 + at.count;      // its stretch of the line
+        auto cta_of = [&](int y) {                            // the CTA that holds tile y
+          int cta = static_cast<int>(static_cast<int64_t>(y) * ctas / total);
+          while (cta + 1 < ctas && begin_of(cta + 1) <= y) ++cta;
+          while (begin_of(cta) > y) --cta;
+          return cta;
+        };
+        const int cta0 = cta_of(u0), cta1 = cta_of(u1 - 1), pieces = cta1 - cta0 + 1;
+        auto slot_of = [&](int piece) { return 2 * (cta0 + piece) + (piece == 0 ? 1 : 0); };
+        const int mine = static_cast<int>(blockIdx.x) - cta0;
+        int step = 1, from = mine / kJoin * kJoin, count = min(kJoin, pieces - from);
+        for (int level = 0;; ++level) {
+          __threadfence();
+          named_barrier_sync(1, 32 * kWarps);
+          if (tid == 0) {
+            int* counter = counters + level * kSlots + slot_of(from);
+            const bool last = atomicAdd(counter, 1) == count - 1;
+            if (last) *counter = 0;                           // ready for the next call
+            s.last = last;
+          }
+          named_barrier_sync(1, 32 * kWarps);
+          const bool last = s.last != 0;
+          named_barrier_sync(1, 32 * kWarps);
+          if (!last) break;
+          __threadfence();
+          const bool finish = count == pieces || level == 1;
+          // thread: 4 columns of rows tid / 32, + 4, ...
+          const int col = 4 * lane;
+          for (int row = warp; row < en.rows; row += kWarps) {
+            float Mx = -INFINITY, Lx = 0.f, acc[4] = {};
+            for (int i = 0; i < count; i += 8) {
+              float4 v[8];
+              float2 z[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                if (i + k >= count) {
+                  z[k] = make_float2(-INFINITY, 0.f);
+                  v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  continue;
+                }
+                const size_t at_row = static_cast<size_t>(slot_of(from + (i + k) * step)) * kRows + row;
+                z[k] = __ldcg(reinterpret_cast<const float2*>(ml + at_row * 2));
+                v[k] = col < DP ? __ldcg(reinterpret_cast<const float4*>(parts + at_row * 128 + col)) : make_float4(0, 0, 0, 0);
+              }
+              float now = Mx;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) now = fmaxf(now, z[k].x);
+              const float base = now == -INFINITY ? 0.f : now, keep = fast_exp2(Mx - base);
+              Lx *= keep;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) acc[q] *= keep;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float e = fast_exp2(z[k].x - base);
+                Lx = fmaf(z[k].y, e, Lx);
+                acc[0] = fmaf(v[k].x, e, acc[0]);
+                acc[1] = fmaf(v[k].y, e, acc[1]);
+                acc[2] = fmaf(v[k].z, e, acc[2]);
+                acc[3] = fmaf(v[k].w, e, acc[3]);
+              }
+              Mx = now;
+            }
+            if (finish) {
+              const float inv = Lx == 0.f ? 0.f : 1.f / Lx;
+              const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) acc[q] *= inv;
+              if (col < ca.head_dim) store_f32<T, 4>(static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head + col, acc);
+              if (lane == 0 && a.lse != nullptr)
+                a.lse[static_cast<int64_t>(tok) * a.Hq + h] = Lx == 0.f ? -INFINITY : (Mx + log2f(Lx)) * kLn2;
+            } else {
+              const size_t at_row = static_cast<size_t>(slot_of(from)) * kRows + row;
+              __syncwarp();
+              if (col < DP) store_f32<float, 4>(parts + at_row * 128 + col, acc);
+              if (lane == 0) *reinterpret_cast<float2*>(ml + at_row * 2) = make_float2(Mx, Lx);
+            }
+          }
+          if (finish) break;
+          step = kJoin;
+          from = 0;
+          count = (pieces + kJoin - 1) / kJoin;
+        }
+      }
+      x += n;
+    }
+  }
+
+  // Nothing of this CTA is in flight when it ends: the consumers have waited
+  // for every tile, unless a wait ran out.
+  __syncthreads();
+  if (tid == 0 && s.abort_flag) {
+    const int from = s.issued > kStages ? s.issued - kStages : 0;
+    for (int k = from; k < s.issued; ++k) mbar_wait(&s.full[k % kStages], (k / kStages) & 1, a.wait_limit_ns);
+  }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+}  // namespace
+
+// Keys or values of the cache as {head_dim, page_size, kv_heads, num_pages}
+// bytes; a box is ``rows`` tokens of one page and head, 128 bytes each (zeros
+// past head_dim), with the 128-byte swizzle.
+bool encode_cache_map(CUtensorMap* map, const moe_kv_cache_t& c, bool values, int rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.kv_heads), static_cast<cuuint64_t>(c.num_pages > 0 ? c.num_pages : 1)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(values ? c.v_stride_token : c.k_stride_token),
+                                 static_cast<cuuint64_t>(values ? c.v_stride_head : c.k_stride_head),
+                                 static_cast<cuuint64_t>(values ? c.v_stride_page : c.k_stride_page)};
+  const cuuint32_t box[4] = {128, static_cast<cuuint32_t>(rows), 1, 1}, step[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, values ? c.v : c.k, dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t decode_attention_workspace_bytes() { return kPartialBytes + kMlBytes + kCounterBytes; }
+
+namespace {
+
+template <typename T, int DP>
+int launch(const AttentionParams& a, cudaStream_t stream) {
+  CUtensorMap k_map, v_map;
+  Launch p = {};
+  p.a = a;
+  p.box = gcd(a.cache.page_size, kKeys);
+  if (!encode_cache_map(&k_map, a.cache, false, p.box) || !encode_cache_map(&v_map, a.cache, true, p.box)) return MOE_ERR_CUDA;
+  auto kernel = decode_attention_kernel<T, DP>;
+  if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmemBytes) != cudaSuccess) return MOE_ERR_CUDA;
+  const int sms = sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  const int group = a.Hq / a.cache.kv_heads;
+  const int64_t row_tiles = (static_cast<int64_t>(a.max_q_len) * group + kRows - 1) / kRows;
+  const int64_t line = (static_cast<int64_t>(a.table_width) * a.cache.page_size / kKeys + 1) * kMaxEntries * a.cache.kv_heads;
+  if (row_tiles > kMaxEntries || line > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  p.row_tiles = static_cast<int>(row_tiles);
+  const int per_launch = kMaxEntries / p.row_tiles;
+  const int64_t longest = a.max_seq_len > 0 ? a.max_seq_len : 1;
+  for (p.b0 = 0; p.b0 < a.B; p.b0 += per_launch) {
+    p.B = a.B - p.b0 < per_launch ? a.B - p.b0 : per_launch;
+    // no more CTAs than key tiles there can be
+    const int64_t tiles = (longest + kKeys - 1) / kKeys * p.B * p.row_tiles * a.cache.kv_heads;
+    int64_t grid = static_cast<int64_t>(sms) * kCtasPerSm;
+    if (grid > kMaxCtas) grid = kMaxCtas;
+    if (grid > tiles) grid = tiles;
+    if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, stream, k_map, v_map, p) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+int launch_decode_attention(const AttentionParams& p, int dtype, cudaStream_t s) {
+  if (dtype == MOE_DTYPE_F16) return p.cache.head_dim <= 64 ? launch<__half, 64>(p, s) : launch<__half, 128>(p, s);
+  return p.cache.head_dim <= 64 ? launch<__nv_bfloat16, 64>(p, s) : launch<__nv_bfloat16, 128>(p, s);
+}
+
+}  // namespace moe

@@ -415,6 +415,44 @@ def test_attention_bad_pages_are_left_out():
         assert batch.cache.device_status() == m.MOE_ERR_BAD_PAGE
 
 
+@pytest.mark.parametrize("new,P", [([1, 1], 16), ([3, 2], 8), ([40, 1], 16), ([150, 3], 64)])
+def test_attention_pages_before_the_window_may_be_gone(new, P):
+    """Entries of pages that no row sees any more are never looked up."""
+    rng = np.random.default_rng(15)
+    window, lens = 45, [400, 331]
+    batch = Batch(rng, new, lens, 2, P, 64, std=0.5)
+    q = rounded(rng, (sum(new), 4, 64), "bfloat16")
+    whole = batch.table.copy()
+    for b, (n, e) in enumerate(zip(new, lens)):
+        batch.table[b, :(e - n + 1 - window) // P] = -1
+    batch.dev["block_table"].copy_(tensor(batch.table, "int32"))
+    check_attention(batch, q, "bfloat16", window=window, decode=max(new) == 1, tables=whole)
+    assert batch.cache.device_status() == m.MOE_OK
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 33]])
+def test_attention_timeout_is_reported(new):
+    """With no key tile arriving the waits run out, the status says so, and
+    the next call on the same workspace is right."""
+    rng = np.random.default_rng(16)
+    batch = Batch(rng, new, [300, 100], 2, 16, 128, std=0.5)
+    q = rounded(rng, (sum(new), 4, 128), "bfloat16")
+    decode = max(new) == 1
+    batch.cache.attend(tensor(q, "bfloat16"), **batch.dev, cu_q=None if decode else batch.cu_dev, max_q_len=max(new),
+                       wait_timeout_ms=5, debug_flags=m.MOE_DEBUG_STALL_ATTENTION)
+    assert batch.cache.device_status() == m.MOE_ERR_DEVICE_TIMEOUT
+    check_attention(batch, q, "bfloat16", decode=decode)
+    assert batch.cache.device_status() == m.MOE_OK
+
+
+def test_attention_many_sequences():
+    """More sequences than one launch's list, empty and short ones among them."""
+    rng = np.random.default_rng(17)
+    lens = [int(x) for x in rng.integers(0, 40, 700)]
+    batch = Batch(rng, [1] * 700, lens, 1, 8, 16, std=0.5)
+    check_attention(batch, rounded(rng, (700, 2, 16), "bfloat16"), "bfloat16", decode=True)
+
+
 def test_attention_repeats_bit_for_bit_and_on_streams():
     """Twice the same bits; on two streams at once, each its own workspace."""
     torch = torch_mod()
