@@ -47,6 +47,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(codes));
   return r;
 }
+// The four codes of a word: the lower two to ``lo``, the upper two to ``hi``.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t word, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(word));
+}
 __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint16_t codes) {
   const uint32_t h = e4m3x2_to_f16x2(codes);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));

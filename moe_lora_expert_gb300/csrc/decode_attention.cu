@@ -33,9 +33,10 @@ namespace {
 
 constexpr int kKeys = 64;                 // keys of a tile
 constexpr int kRows = 16;                 // rows of a row tile
-constexpr int kStages = 4;
-constexpr int kWarps = 4;                 // consumers, 16 keys of a tile each
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 4;                 // 16 keys of a tile each
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRing = 3;                  // tiles in a warp's ring
+constexpr int kBatch = 16;                // tiles whose pages are looked up at once
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxCtas = 640;
 constexpr int kMaxEntries = 512;          // (sequence, row tile) pairs of one launch
@@ -53,16 +54,17 @@ struct alignas(16) Group {                // 8 keys of a tile, which lie in one 
 };
 
 struct Shared {
-  Group group[kStages][8];
-  uint64_t full[kStages], empty[kStages];
+  Group group[kWarps][kRing][2];
+  uint64_t full[kWarps][kRing];
   int prefix[kMaxEntries + 1];            // key tiles before each entry
   int begin[kMaxEntries];                 // first key that some row of each entry sees
   int end[kMaxEntries];                   // end of the keys that some row of it sees
   float m[kWarps][kRows], l[kWarps][kRows];
-  int total, abort_flag, last, issued;
+  int total, abort_flag, last;
 };
-constexpr int kStageBytes = 2 * kKeys * kPitch;
-constexpr int kSmemBytes = kStages * kStageBytes + static_cast<int>(sizeof(Shared)) + 1024;
+constexpr int kSlotBytes = 2 * 16 * kPitch;
+constexpr int kScratchBytes = 2 * kRows * 128 * 4;            // two warps' sums
+constexpr int kSmemBytes = kWarps * kRing * kSlotBytes + kScratchBytes + static_cast<int>(sizeof(Shared)) + 1024;
 
 // Partial sums of a row tile: [slot][row][128] and (m, l) [slot][row][2];
 // counters [2][slots].
@@ -74,7 +76,7 @@ constexpr size_t kCounterBytes = static_cast<size_t>(kSlots) * 2 * 4;
 struct Launch {
   AttentionParams a;
   int b0, B, row_tiles;                   // sequences [b0, b0 + B), row tiles of each
-  int box;                                // keys of one TMA box: gcd(page_size, 64)
+  int box;                                // keys of one TMA box: gcd(page_size, 16)
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -134,8 +136,9 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const Launch p) {
   extern __shared__ uint8_t raw[];
-  uint8_t* const stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  Shared& s = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes);
+  uint8_t* const rings = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  float* const scratch = reinterpret_cast<float*>(rings + kWarps * kRing * kSlotBytes);
+  Shared& s = *reinterpret_cast<Shared*>(reinterpret_cast<uint8_t*>(scratch) + kScratchBytes);
   const AttentionParams& a = p.a;
   const moe_kv_cache_t& ca = a.cache;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -146,12 +149,9 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   if (tid == 0) {
     tma_prefetch_map(&k_map);
     tma_prefetch_map(&v_map);
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], kWarps);
-    }
+    for (int w = 0; w < kWarps; ++w)
+      for (int i = 0; i < kRing; ++i) mbar_init(&s.full[w][i], 1);
     s.abort_flag = 0;
-    s.issued = 0;
     fence_mbarrier_init();
   }
   pdl_wait();
@@ -201,87 +201,73 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   const int x0 = idle ? 0 : begin_of(blockIdx.x), x1 = idle ? 0 : begin_of(blockIdx.x + 1);
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (*static_cast<volatile int*>(&s.abort_flag)) return;
+    if (mbar_try_wait(smem_u32(bar), parity) || *static_cast<volatile int*>(&s.abort_flag)) return;
     if (!mbar_wait(bar, parity, a.wait_limit_ns)) {
       set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
       *static_cast<volatile int*>(&s.abort_flag) = 1;
     }
   };
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer
-    // Four tiles at a time, a lane for each group of 8 keys: its page from
-    // the block table, then that page's scales; both are fetched ahead of the
-    // tiles that use them.
-    struct Ahead {
-      int page, off, head;
-      float ks, vs;
-    };
-    const int sub = lane & 7;
-    auto find = [&](int k) {
-      Ahead f = {-1, 0, 0, 0.f, 0.f};
-      const int x = x0 + k + (lane >> 3);
-      if (x < x1) {
-        const Place at(s, entries, ca.kv_heads, x);
-        const int key = (s.begin[at.e] / kKeys + at.tile) * kKeys + 8 * sub;
+  // Each warp streams its own 16 keys of every tile through a ring of its own:
+  // it issues the copies three tiles ahead, and no warp waits for another.
+  // Two lanes stand for a tile, one for each group of 8 keys; the 32 lanes
+  // look up the pages and scales of 16 tiles at once, a batch ahead.
+  struct Ahead {
+    int page, off, head;
+    Group g;
+  };
+  const int steps = x1 - x0;
+  auto find = [&](int batch) {
+    Ahead f = {-1, 0, 0, {0.f, 0.f, 0.f, 0}};
+    const int k = batch * kBatch + (lane >> 1);
+    if (k < steps) {
+      const Place at(s, entries, ca.kv_heads, x0 + k);
+      const int key = (s.begin[at.e] / kKeys + at.tile) * kKeys + 16 * warp + 8 * (lane & 1);
+      // boxes that no row sees are not looked up: their pages may be gone
+      if (key < s.end[at.e] && (key & ~(p.box - 1)) + p.box > s.begin[at.e]) {
         const int page_at = key / ca.page_size;
         f.off = key - page_at * ca.page_size;
         f.head = at.head;
-        // boxes that no row sees are not looked up: their pages may be gone
-        if (key < s.end[at.e] && (key & ~(p.box - 1)) + p.box > s.begin[at.e]) {
-          f.page = a.block_table[static_cast<int64_t>(p.b0 + at.e / p.row_tiles) * a.table_width + page_at];
-          if (f.page < 0 || f.page >= ca.num_pages) {
-            f.page = -1;
-            set_status(a.status, MOE_ERR_BAD_PAGE);
-          }
+        f.page = a.block_table[static_cast<int64_t>(p.b0 + at.e / p.row_tiles) * a.table_width + page_at];
+        if (f.page < 0 || f.page >= ca.num_pages) {
+          f.page = -1;
+          set_status(a.status, MOE_ERR_BAD_PAGE);
+        } else {
+          const int64_t i = static_cast<int64_t>(f.page) * ca.kv_heads + f.head;
+          const float vs = fmaxf(ca.v_scale[i], 5.421010862427522e-20f);   // 2^-64: a zero scale gives zero values
+          f.g = {ca.k_scale[i] * a.scale * kLog2e, log2f(vs), 1.f / vs, 1};
         }
       }
-      return f;
-    };
-    auto scales = [&](Ahead& f) {
-      if (f.page >= 0) {
-        const int64_t i = static_cast<int64_t>(f.page) * ca.kv_heads + f.head;
-        f.ks = ca.k_scale[i];
-        f.vs = ca.v_scale[i];
-      }
-    };
-    Ahead now = find(0), next = find(4);
-    scales(now);
-    const bool stalled = (a.debug_flags & MOE_DEBUG_STALL_ATTENTION) != 0;   // a failure for the tests: no tile arrives
-    for (int k = 0; x0 + k < x1 && !stalled; k += 4) {
-      scales(next);
-      const Ahead later = find(k + 8);
-      Group g;
-      g.k = now.ks * a.scale * kLog2e;
-      const float vs = fmaxf(now.vs, 5.421010862427522e-20f);   // 2^-64: a zero scale gives zero values
-      g.lv = log2f(vs);
-      g.inv_v = 1.f / vs;
-      g.valid = now.page >= 0;
-      const bool issues = g.valid && (8 * sub) % p.box == 0;
-      const unsigned boxes = __ballot_sync(0xffffffffu, issues);
-      for (int i = 0; i < 4 && x0 + k + i < x1; ++i) {
-        const int st = (k + i) % kStages, fill = (k + i) / kStages;
-        if (fill > 0) wait(&s.empty[st], (fill - 1) & 1);
-        if ((lane >> 3) == i) s.group[st][sub] = g;
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&s.full[st], __popc((boxes >> (8 * i)) & 0xFF) * p.box * kPitch * 2);
-          s.issued = k + i + 1;
-        }
-        __syncwarp();
-        if ((lane >> 3) == i && issues) {
-          const uint32_t dst = smem_u32(stages + st * kStageBytes) + 8 * sub * kPitch;
-          tma_load_4d(dst, &k_map, &s.full[st], now.off, now.head, now.page);
-          tma_load_4d(dst + kKeys * kPitch, &v_map, &s.full[st], now.off, now.head, now.page);
-        }
-      }
-      now = next;
-      next = later;
     }
-  } else {
-    // ----------------------------------------------------------- consumers
+    return f;
+  };
+  Ahead now = find(0), next = find(1);
+  int issued = 0;
+  const bool stalled = (a.debug_flags & MOE_DEBUG_STALL_ATTENTION) != 0;   // a failure for the tests: no tile arrives
+  auto issue = [&]() {
+    if (issued >= steps || stalled) return;
+    const int in = issued % kBatch, slot = issued % kRing;
+    if (in == 0 && issued > 0) {
+      now = next;
+      next = find(issued / kBatch + 1);
+    }
+    const bool mine = (lane >> 1) == in, issues = mine && now.page >= 0 && (now.off & (p.box - 1)) == 0;
+    const unsigned boxes = __ballot_sync(0xffffffffu, issues);
+    if (mine) s.group[warp][slot][lane & 1] = now.g;
+    if (lane == 0) mbar_arrive_expect_tx(&s.full[warp][slot], __popc(boxes) * p.box * kPitch * 2);
+    __syncwarp();
+    if (issues) {
+      const uint32_t dst = smem_u32(rings + (warp * kRing + slot) * kSlotBytes) + 8 * (lane & 1) * kPitch;
+      tma_load_4d(dst, &k_map, &s.full[warp][slot], now.off, now.head, now.page);
+      tma_load_4d(dst + 16 * kPitch, &v_map, &s.full[warp][slot], now.off, now.head, now.page);
+    }
+    ++issued;
+  };
+  for (int i = 0; i < kRing; ++i) issue();
+
+  {
     const int g = lane >> 2, c = lane & 3;
-    int fill = 0;                          // tiles consumed so far
+    int taken = 0;                         // tiles consumed so far
     for (int x = x0; x < x1;) {
       const Place at(s, entries, ca.kv_heads, x);
       const Entry en(p, at.e, group);
@@ -342,15 +328,15 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       float o[kTiles][4];
 #pragma unroll
       for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float m[2] = {-INFINITY, -INFINITY}, base[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};   // base: m, or 0 while there is none
 
-      for (int i = 0; i < n; ++i, ++fill) {
-        const int st = fill % kStages;
-        wait(&s.full[st], (fill / kStages) & 1);
+      for (int i = 0; i < n; ++i, ++taken) {
+        const int slot = taken % kRing;
+        wait(&s.full[warp][slot], (taken / kRing) & 1);
         const int key0 = (first_tile + i) * kKeys + 16 * warp;
-        const uint8_t* kt = stages + st * kStageBytes + 16 * warp * kPitch;
-        const uint8_t* vt = kt + kKeys * kPitch;
-        const Group g0 = s.group[st][2 * warp], g1 = s.group[st][2 * warp + 1];
+        const uint8_t* kt = rings + (warp * kRing + slot) * kSlotBytes;
+        const uint8_t* vt = kt + 16 * kPitch;
+        const Group g0 = s.group[warp][slot][0], g1 = s.group[warp][slot][1];
         const bool some = key0 < end && (a.window == 0 || key0 + 15 > pos_min - a.window) && (g0.valid || g1.valid);
         if (some) {
           // S = Q K^T for 16 keys
@@ -369,7 +355,9 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             for (int h = 0; h < 2; ++h) {
               const uint4& u = kw[h][w / 4];
               const uint32_t word = (w & 3) == 0 ? u.x : (w & 3) == 1 ? u.y : (w & 3) == 2 ? u.z : u.w;
-              mma_f16(sc[h], qf[w], e4m3x2_to_f16x2(word & 0xFFFF), e4m3x2_to_f16x2(word >> 16));
+              uint32_t b0, b1;
+              e4m3x4_to_f16x4(word, b0, b1);
+              mma_f16(sc[h], qf[w], b0, b1);
             }
           }
           // exponents of the weights
@@ -401,6 +389,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
               const float now = fmaxf(m[r], top[r]);
               const float keep = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - now);
               m[r] = now;
+              base[r] = now == -INFINITY ? 0.f : now;
               l[r] *= keep;
 #pragma unroll
               for (int j = 0; j < kTiles; ++j) {
@@ -415,8 +404,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             const Group& gr = h == 0 ? g0 : g1;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const float base = m[r] == -INFINITY ? 0.f : m[r];
-              const float w0 = fast_exp2(sc[h][2 * r] - base), w1 = fast_exp2(sc[h][2 * r + 1] - base);
+              const float w0 = fast_exp2(sc[h][2 * r] - base[r]), w1 = fast_exp2(sc[h][2 * r + 1] - base[r]);
               l[r] = fmaf(w0 + w1, gr.inv_v, l[r]);
               pf[2 * h + r] = f32x2_to_f16x2(w0, w1);
             }
@@ -449,8 +437,11 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
               const uint32_t sel = half == 0 ? 0x5140 : 0x7362;
               const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], sel), hi = __byte_perm(vw[2][w], vw[3][w], sel);
               const int j = 4 * w + 2 * half;
-              mma_f16(o[j], pf, e4m3x2_to_f16x2(lo & 0xFFFF), e4m3x2_to_f16x2(hi & 0xFFFF));
-              mma_f16(o[j + 1], pf, e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi >> 16));
+              uint32_t l0, l1, h0, h1;
+              e4m3x4_to_f16x4(lo, l0, l1);
+              e4m3x4_to_f16x4(hi, h0, h1);
+              mma_f16(o[j], pf, l0, h0);
+              mma_f16(o[j + 1], pf, l1, h1);
             }
           }
           if (!whole && __any_sync(0xffffffffu, nan != 0)) {
@@ -473,15 +464,11 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             }
           }
         }
-        if (i + 1 < n) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.empty[st]);
-        }
+        __syncwarp();                      // every lane has read the slot
+        issue();
       }
 
-      // Join the four warps: the last tile's stage is the scratch.
-      const int st = (fill - 1) % kStages;
-      float* scratch = reinterpret_cast<float*>(stages + st * kStageBytes);
+      // Join the four warps.
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -491,7 +478,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
           s.l[warp][g + 8 * r] = l[r];
         }
       }
-      named_barrier_sync(1, 32 * kWarps);
+      __syncthreads();
       float M[2], L[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -499,10 +486,10 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         L[r] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M[r] = fmaxf(M[r], s.m[w][g + 8 * r]);
-        const float base = M[r] == -INFINITY ? 0.f : M[r];
+        const float ref = M[r] == -INFINITY ? 0.f : M[r];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) L[r] += s.l[w][g + 8 * r] * fast_exp2(s.m[w][g + 8 * r] - base);
-        const float keep = fast_exp2(m[r] - base);
+        for (int w = 0; w < kWarps; ++w) L[r] += s.l[w][g + 8 * r] * fast_exp2(s.m[w][g + 8 * r] - ref);
+        const float keep = fast_exp2(m[r] - ref);
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) {
           o[j][2 * r] *= keep;
@@ -522,16 +509,12 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
           for (int z = 0; z < 4; ++z) o[j][z] += from[(4 * j + z) * 32 + lane];
       };
       if (warp >= 2) put(scratch + (warp - 2) * 2048);
-      named_barrier_sync(1, 32 * kWarps);
+      __syncthreads();
       if (warp < 2) add(scratch + warp * 2048);
-      named_barrier_sync(1, 32 * kWarps);
+      __syncthreads();
       if (warp == 1) put(scratch);
-      named_barrier_sync(1, 32 * kWarps);
+      __syncthreads();
       if (warp == 0) add(scratch);
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.empty[st]);
-
       const bool begun_before = at.tile > 0, goes_on = at.tile + n < at.count;
       const bool split = begun_before || goes_on;
       float* parts = static_cast<float*>(a.workspace);
@@ -591,16 +574,16 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         int step = 1, from = mine / kJoin * kJoin, count = min(kJoin, pieces - from);
         for (int level = 0;; ++level) {
           __threadfence();
-          named_barrier_sync(1, 32 * kWarps);
+          __syncthreads();
           if (tid == 0) {
             int* counter = counters + level * kSlots + slot_of(from);
             const bool last = atomicAdd(counter, 1) == count - 1;
             if (last) *counter = 0;                           // ready for the next call
             s.last = last;
           }
-          named_barrier_sync(1, 32 * kWarps);
+          __syncthreads();
           const bool last = s.last != 0;
-          named_barrier_sync(1, 32 * kWarps);
+          __syncthreads();
           if (!last) break;
           __threadfence();
           const bool finish = count == pieces || level == 1;
@@ -665,12 +648,10 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     }
   }
 
-  // Nothing of this CTA is in flight when it ends: the consumers have waited
-  // for every tile, unless a wait ran out.
-  __syncthreads();
-  if (tid == 0 && s.abort_flag) {
-    const int from = s.issued > kStages ? s.issued - kStages : 0;
-    for (int k = from; k < s.issued; ++k) mbar_wait(&s.full[k % kStages], (k / kStages) & 1, a.wait_limit_ns);
+  // Nothing of this warp is in flight when it ends: it has waited for every
+  // tile, unless a wait ran out.
+  if (*static_cast<volatile int*>(&s.abort_flag)) {
+    for (int k = max(0, issued - kRing); k < issued; ++k) mbar_wait(&s.full[warp][k % kRing], (k / kRing) & 1, a.wait_limit_ns);
   }
 }
 
@@ -727,7 +708,7 @@ int launch(const AttentionParams& a, cudaStream_t stream) {
   CUtensorMap k_map, v_map;
   Launch p = {};
   p.a = a;
-  p.box = gcd(a.cache.page_size, kKeys);
+  p.box = gcd(a.cache.page_size, 16);
   if (!encode_cache_map(&k_map, a.cache, false, p.box) || !encode_cache_map(&v_map, a.cache, true, p.box)) return MOE_ERR_CUDA;
   auto kernel = decode_attention_kernel<T, DP>;
   if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmemBytes) != cudaSuccess) return MOE_ERR_CUDA;
