@@ -16,8 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoelora.so")
 SOURCES = ["api.cu", "routing.cu", "lora_shrink.cu", "expert_gemm.cu", "fp8_gemm.cu", "permute_noalloc.cu",
-           "attention_api.cu", "rope.cu", "kv_append.cu", "paged_attention.cu",
-           "decode_attention.cu"]
+           "attention_api.cu", "rope.cu", "kv_append.cu",
+           "decode_attention.cu", "prefill_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

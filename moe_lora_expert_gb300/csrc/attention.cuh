@@ -3,6 +3,7 @@
 // rope.cu, kv_append.cu and paged_attention.cu.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -178,7 +179,8 @@ struct AttentionParams {
   uint64_t wait_limit_ns;
   uint32_t debug_flags;
 };
-cudaError_t launch_paged_attention(const AttentionParams& p, int dtype, cudaStream_t s);
+bool encode_cache_map(CUtensorMap* map, const moe_kv_cache_t& c, bool values, int rows);
+int launch_prefill_attention(const AttentionParams& p, int dtype, cudaStream_t s);  // a moe_status_t
 size_t decode_attention_workspace_bytes();
 int launch_decode_attention(const AttentionParams& p, int dtype, cudaStream_t s);   // a moe_status_t
 

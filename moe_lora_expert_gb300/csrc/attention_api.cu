@@ -162,8 +162,9 @@ int moe_paged_attention(const moe_paged_attention_args_t* a, moe_stream_t stream
   p.wait_limit_ns = 1000000ull * static_cast<uint64_t>(a->wait_timeout_ms > 0 ? a->wait_timeout_ms : 2000);
   p.debug_flags = a->debug_flags;
   (void)cudaGetLastError();
-  if (p.max_q_len * (a->Hq / c.kv_heads) <= 256) return moe::launch_decode_attention(p, a->dtype, reinterpret_cast<cudaStream_t>(stream));
-  return done(moe::launch_paged_attention(p, a->dtype, reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
+  return p.max_q_len * static_cast<int64_t>(a->Hq / c.kv_heads) <= 64 ? moe::launch_decode_attention(p, a->dtype, st_)
+                                                                     : moe::launch_prefill_attention(p, a->dtype, st_);
 }
 
 }  // extern "C"

@@ -246,6 +246,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   const bool stalled = (a.debug_flags & MOE_DEBUG_STALL_ATTENTION) != 0;   // a failure for the tests: no tile arrives
   auto issue = [&]() {
     if (issued >= steps || stalled) return;
+    if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&s.abort_flag))) return;   // a slot that was not filled is not filled again
     const int in = issued % kBatch, slot = issued % kRing;
     if (in == 0 && issued > 0) {
       now = next;
