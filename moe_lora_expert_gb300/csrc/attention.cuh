@@ -180,6 +180,9 @@ struct AttentionParams {
   uint32_t debug_flags;
 };
 bool encode_cache_map(CUtensorMap* map, const moe_kv_cache_t& c, bool values, int rows);
+bool encode_query_map(CUtensorMap* map, const AttentionParams& a, bool f16, int group, int tokens);
+int sm_count();
+size_t prefill_attention_workspace_bytes();
 int launch_prefill_attention(const AttentionParams& p, int dtype, cudaStream_t s);  // a moe_status_t
 size_t decode_attention_workspace_bytes();
 int launch_decode_attention(const AttentionParams& p, int dtype, cudaStream_t s);   // a moe_status_t

@@ -124,7 +124,7 @@ int moe_kv_append(const moe_kv_append_args_t* a, moe_stream_t stream) {
   return done(moe::launch_kv_append(p, a->dtype, V, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t moe_paged_attention_workspace_size(void) { return moe::decode_attention_workspace_bytes(); }
+size_t moe_paged_attention_workspace_size(void) { return moe::decode_attention_workspace_bytes() + moe::prefill_attention_workspace_bytes(); }
 
 int moe_paged_attention(const moe_paged_attention_args_t* a, moe_stream_t stream) {
   if (a == nullptr) return MOE_ERR_NULL;
@@ -162,9 +162,10 @@ int moe_paged_attention(const moe_paged_attention_args_t* a, moe_stream_t stream
   p.wait_limit_ns = 1000000ull * static_cast<uint64_t>(a->wait_timeout_ms > 0 ? a->wait_timeout_ms : 2000);
   p.debug_flags = a->debug_flags;
   (void)cudaGetLastError();
-  const cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
-  return p.max_q_len * static_cast<int64_t>(a->Hq / c.kv_heads) <= 64 ? moe::launch_decode_attention(p, a->dtype, st_)
-                                                                     : moe::launch_prefill_attention(p, a->dtype, st_);
+  const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t rows = static_cast<int64_t>(p.max_q_len) * (a->Hq / c.kv_heads);
+  if (rows <= 64 || a->Hq / c.kv_heads > 128) return moe::launch_decode_attention(p, a->dtype, on);
+  return p.debug_flags != 0 ? MOE_ERR_UNSUPPORTED : moe::launch_prefill_attention(p, a->dtype, on);
 }
 
 }  // extern "C"

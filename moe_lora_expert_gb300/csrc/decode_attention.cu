@@ -200,12 +200,13 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   const bool idle = static_cast<int>(blockIdx.x) >= ctas;
   const int x0 = idle ? 0 : begin_of(blockIdx.x), x1 = idle ? 0 : begin_of(blockIdx.x + 1);
 
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_try_wait(smem_u32(bar), parity) || *static_cast<volatile int*>(&s.abort_flag)) return;
-    if (!mbar_wait(bar, parity, a.wait_limit_ns)) {
+  auto wait = [&](uint64_t* bar, uint32_t parity) {          // by a warp, which leaves it together
+    if (!mbar_try_wait(smem_u32(bar), parity) && !*static_cast<volatile int*>(&s.abort_flag) &&
+        !mbar_wait(bar, parity, a.wait_limit_ns)) {
       set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
       *static_cast<volatile int*>(&s.abort_flag) = 1;
     }
+    __syncwarp();
   };
 
   // Each warp streams its own 16 keys of every tile through a ring of its own:
@@ -672,16 +673,16 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+}  // namespace
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
   return n;
 }
-
-int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
-
-}  // namespace
 
 // Keys or values of the cache as {head_dim, page_size, kv_heads, num_pages}
 // bytes; a box is ``rows`` tokens of one page and head, 128 bytes each (zeros
@@ -697,6 +698,20 @@ bool encode_cache_map(CUtensorMap* map, const moe_kv_cache_t& c, bool values, in
   const cuuint32_t box[4] = {128, static_cast<cuuint32_t>(rows), 1, 1}, step[4] = {1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, values ? c.v : c.k, dims, strides, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Queries as {head_dim, Hq, N}; a box is 64 columns (zeros past head_dim) of
+// the ``group`` heads of one key head and ``tokens`` tokens, rows in the order
+// of the attention's rows, with the 128-byte swizzle.
+bool encode_query_map(CUtensorMap* map, const AttentionParams& a, bool f16, int group, int tokens) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.cache.head_dim), static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.N)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.q_head) * 2, static_cast<cuuint64_t>(a.q_token) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tokens)}, step[3] = {1, 1, 1};
+  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides,
+            box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

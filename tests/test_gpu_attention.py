@@ -430,7 +430,7 @@ def test_attention_pages_before_the_window_may_be_gone(new, P):
     assert batch.cache.device_status() == m.MOE_OK
 
 
-@pytest.mark.parametrize("new", [[1, 1], [40, 33]])
+@pytest.mark.parametrize("new", [[1, 1], [8, 5]])
 def test_attention_timeout_is_reported(new):
     """With no key tile arriving the waits run out, the status says so, and
     the next call on the same workspace is right."""
