@@ -31,13 +31,15 @@ namespace moe {
 namespace {
 
 constexpr int kKeys = 128;
+constexpr int kHalf = 64;                  // keys whose weights are handed over at a time
 constexpr int kTileRows = 128;
 constexpr int kCtaRows = 256;
 constexpr int kThreads = 448;
 constexpr int kSlots = 4;                  // converted tiles: K0, V0, K1, V1, ...
 constexpr int kStages = 2;                 // tiles of codes, in the same order
 constexpr int kInfo = 4;                   // key tiles whose scales are held (see the copies)
-constexpr int kMinTiles = 4;               // a CTA takes at least this many key tiles
+constexpr int kUnitCost = 2;               // key tiles' worth of time that a unit takes besides its tiles
+constexpr int kMinTiles = 4;               // least length of a CTA's stretch
 constexpr int kMaxCtas = 160;
 constexpr int kJoin = 8;                   // pieces that are joined at a time
 constexpr int kConvertWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
@@ -50,34 +52,12 @@ struct alignas(16) Group {                 // 8 keys, which lie in one page
   int valid;
 };
 
-struct Control {
-  Group group[kInfo][kKeys / 8];
-  uint64_t code_full[kStages], code_empty[kStages], full[kSlots], empty[kSlots];
-  uint64_t info_full[kInfo], q_raw, q_full, q_empty, s_full[2], p_full[2], o_full[2], drained;
-  int8_t q_exponent[kCtaRows];             // of the power of two taken out of each row
-  int sums[kThreads / 32];
-  uint32_t tmem;
-  int abort_flag, nan_seen, first_entry, first_prefix, last[2];
-};
-
 // Partial sums of a row tile [slot][row tile][column / 4][row] of four columns
-// each, (m, l) [slot][row tile][row], counters [2][slot][row tile].
+// each, (m, l) [slot][row tile][row], counters [level][slot][row tile].
 constexpr int kParts = 2 * kMaxCtas;
 constexpr size_t kPartialBytes = static_cast<size_t>(kParts) * kCtaRows * 128 * 4;
 constexpr size_t kMlBytes = static_cast<size_t>(kParts) * kCtaRows * 8;
-constexpr size_t kCounterBytes = static_cast<size_t>(kParts) * 2 * 2 * 4;
-
-template <int DP>
-struct Layout {
-  static constexpr int kHalves = DP / 64;
-  static constexpr int kHalfBytes = kKeys * 128;                  // 128 keys (or rows) x 64 float16
-  static constexpr int kSlotBytes = kHalves * kHalfBytes;
-  static constexpr int kQBytes = 2 * kHalves * kHalfBytes;
-  static constexpr int kCodeBytes = kKeys * 128;
-  static constexpr int kQ = 0, kRing = kQBytes, kCode = kRing + kSlots * kSlotBytes,
-                       kControl = kCode + kStages * kCodeBytes, kBytes = kControl + static_cast<int>(sizeof(Control));
-};
-static_assert(Layout<128>::kBytes <= 232448, "shared memory of a CTA");
+constexpr size_t kCounterBytes = static_cast<size_t>(kParts) * 2 * 3 * 4;   // three levels of eight: up to 512 pieces
 
 struct Launch {
   AttentionParams a;
@@ -91,23 +71,29 @@ struct Launch {
 __device__ __forceinline__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// V as the B operand with its columns contiguous: 64-column halves kHalfBytes
-// apart (leading offset), groups of 8 keys 1024 bytes apart (stride offset).
-__device__ __forceinline__ uint64_t mn_major_sdesc(uint32_t saddr, uint32_t half_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(half_bytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-__device__ __forceinline__ void mma_ts_f16(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// A shared-memory descriptor's low word: the address, and for V (as the B
+// operand with its columns contiguous) the distance of its 64-column halves.
+// The high word is the same for both: groups of 8 rows 1024 bytes apart,
+// 128-byte swizzle.  The one thread that issues the products adds constants
+// to low words instead of building descriptors.
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t leading) { return (saddr >> 4) | (leading >> 4) << 16; }
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ void mma_ss_f16(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "n"(kDescHigh), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_f16(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "n"(kDescHigh), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // 32 lanes x 32 columns; the registers are valid after tmem_wait.
@@ -136,16 +122,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -213,32 +189,65 @@ struct Entry {
 };
 
 // A CTA's stretch of the line, unit by unit; every warp walks it by itself.
+// On the line a unit is kUnitCost places and then a place a key tile.
 struct Walk {
   Entry en;
-  int e, head, tile, x, x1, n;             // this piece: tiles [tile, tile + n) of the unit
+  int e, head, tile, x, x1, n, u0, span;   // this piece: tiles [tile, tile + n) of the unit that begins at u0
   __device__ __forceinline__ bool next(const Launch& p, int group, bool first, int first_entry, int first_prefix) {
     const int heads = p.a.cache.kv_heads;
+    int v = 0;
     if (first) {
       e = first_entry;
       en.load(p, e, group);
       const int in = x - first_prefix * heads;
-      head = in / en.count;
-      tile = in - head * en.count;
+      head = in / (en.count + kUnitCost);
+      v = in - head * (en.count + kUnitCost);
+      span = 0;
     } else {
-      x += n;
-      tile = 0;
-      if (++head == heads) head = -1;
+      ++head;
     }
-    if (x >= x1) return false;
-    if (head < 0) {
-      head = 0;
-      do en.load(p, ++e, group);
-      while (en.count == 0);
+    while (true) {
+      x += span;
+      if (x >= x1) return false;
+      if (head == heads) {
+        head = 0;
+        do en.load(p, ++e, group);
+        while (en.count == 0);
+      }
+      u0 = x - v;
+      span = min(en.count + kUnitCost - v, x1 - x);
+      tile = max(0, v - kUnitCost);
+      n = max(0, v + span - kUnitCost) - tile;
+      if (n > 0) return true;
+      v = 0;
+      ++head;
     }
-    n = min(en.count - tile, x1 - x);
-    return true;
   }
 };
+
+// ----------------------------------------------------------- shared memory
+struct Control {
+  Group group[kInfo][kKeys / 8];
+  uint64_t code_full[kStages], code_empty[kStages], full[kSlots], empty[kSlots];
+  uint64_t info_full[kInfo], q_raw, q_full, q_empty, s_full[2], p_full[2][2], first_done[2], o_full[2], drained;
+  int8_t q_exponent[kCtaRows];             // of the power of two taken out of each row
+  int sums[kThreads / 32];
+  Walk walk[kThreads / 32];                // each warp's own, here and not in its registers
+  uint32_t tmem;
+  int abort_flag, nan_seen, first_entry, first_prefix, last[2];
+};
+
+template <int DP>
+struct Layout {
+  static constexpr int kHalves = DP / 64;
+  static constexpr int kHalfBytes = kKeys * 128;                  // 128 keys (or rows) x 64 float16
+  static constexpr int kSlotBytes = kHalves * kHalfBytes;
+  static constexpr int kQBytes = 2 * kHalves * kHalfBytes;
+  static constexpr int kCodeBytes = kKeys * 128;
+  static constexpr int kQ = 0, kRing = kQBytes, kCode = kRing + kSlots * kSlotBytes,
+                       kControl = kCode + kStages * kCodeBytes, kBytes = kControl + static_cast<int>(sizeof(Control));
+};
+static_assert(Layout<128>::kBytes <= 232448, "shared memory of a CTA");
 
 // ------------------------------------------------------------------ kernel
 template <typename T, int DP>
@@ -269,7 +278,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     for (int i = 0; i < kInfo; ++i) mbar_init(&s.info_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], kTileRows);
+      for (int h = 0; h < 2; ++h) mbar_init(&s.p_full[i][h], kTileRows);
+      mbar_init(&s.first_done[i], 1);
       mbar_init(&s.o_full[i], 1);
     }
     mbar_init(&s.q_raw, 1);
@@ -289,7 +299,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   for (int e = from; e < to; ++e) {
     Entry en;
     en.load(p, e, group);
-    mine += en.count;
+    if (en.count > 0) mine += en.count + kUnitCost;
   }
   int incl = mine;
 #pragma unroll
@@ -308,20 +318,19 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   const int ctas = min(static_cast<int>(gridDim.x), max(1, total / kMinTiles));
   if (total == 0 || static_cast<int>(blockIdx.x) >= ctas) return;
   auto begin_of = [&](int cta) { return static_cast<int>(static_cast<int64_t>(total) * cta / ctas); };
-  Walk walk;
-  walk.x = begin_of(blockIdx.x);
-  walk.x1 = begin_of(blockIdx.x + 1);
-  if (walk.x < incl * ca.kv_heads && walk.x >= (incl - mine) * ca.kv_heads) {
+  const int x0 = begin_of(blockIdx.x);
+  if (x0 < incl * ca.kv_heads && x0 >= (incl - mine) * ca.kv_heads) {
     int before = incl - mine;
     for (int e = from; e < to; ++e) {
       Entry en;
       en.load(p, e, group);
-      if (walk.x < (before + en.count) * ca.kv_heads) {
+      const int places = en.count > 0 ? en.count + kUnitCost : 0;
+      if (x0 < (before + places) * ca.kv_heads) {
         s.first_entry = e;
         s.first_prefix = before;
         break;
       }
-      before += en.count;
+      before += places;
     }
   }
   if (warp == kMmaWarp) {
@@ -350,8 +359,21 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     const bool ok = wait_one(bar, parity);
     return __all_sync(0xffffffffu, ok) != 0;
   };
-  auto next = [&](bool first) { return walk.next(p, group, first, s.first_entry, s.first_prefix); };
+  Walk& walk = s.walk[warp];
   const Entry& en = walk.en;
+  auto next = [&](bool first) {                              // by the lanes that call it, with the same values
+    if (first) {
+      walk.x = x0;
+      walk.x1 = begin_of(blockIdx.x + 1);
+    }
+    __syncwarp(__activemask());
+    Walk w = walk;
+    const bool more = w.next(p, group, first, s.first_entry, s.first_prefix);
+    __syncwarp(__activemask());
+    walk = w;
+    __syncwarp(__activemask());
+    return more;
+  };
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------ pages, scales, copies
@@ -432,21 +454,22 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     // ------------------------------------------------------------ products
     if (lane == 0) {
       constexpr uint32_t kScores = idesc_f16(kTileRows, kKeys, false), kValues = idesc_f16(kTileRows, DP, true);
-      const uint32_t q_base = smem_u32(smem + L::kQ), ring = smem_u32(smem + L::kRing);
+      constexpr uint32_t kSlot = L::kSlotBytes >> 4;
+      const uint32_t q_low = desc_low(smem_u32(smem + L::kQ), 16), k_low = desc_low(smem_u32(smem + L::kRing), 16),
+                     v_low = desc_low(smem_u32(smem + L::kRing), L::kHalfBytes);
       auto scores = [&](int i, int slot) {
+        const uint32_t q = q_low + i * (L::kHalfBytes >> 4), k = k_low + slot * kSlot;
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t at = (k % 4) * 32;
-          tc_mma_bf16(s_cols(i), make_sdesc_sw128(q_base + (2 * (k / 4) + i) * L::kHalfBytes + at),
-                      make_sdesc_sw128(ring + slot * L::kSlotBytes + (k / 4) * L::kHalfBytes + at), kScores, k > 0);
-        }
+        for (int x = 0; x < DP / 16; ++x)
+          mma_ss_f16(s_cols(i), q + ((2 * (x / 4) * L::kHalfBytes + (x % 4) * 32) >> 4),
+                     k + (((x / 4) * L::kHalfBytes + (x % 4) * 32) >> 4), kScores, x > 0);
         tc_commit(&s.s_full[i]);
       };
-      auto values = [&](int i, int slot, bool more) {
+      // what the weights of half h of a tile's keys add to O
+      auto values = [&](int i, int h, int slot, bool more) {
+        const uint32_t v = v_low + slot * kSlot + h * (kHalf * 128 >> 4), w = s_cols(i) + kHalf * h;
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts_f16(o_cols(i), s_cols(i) + 8 * k, mn_major_sdesc(ring + slot * L::kSlotBytes + 2048 * k, L::kHalfBytes), kValues,
-                     more || k > 0);
+        for (int x = 0; x < kHalf / 16; ++x) mma_ts_f16(o_cols(i), w + 8 * x, v + (2048 * x >> 4), kValues, more || x > 0);
       };
       int t = 0, p_count[2] = {0, 0}, units = 0;
       bool ok = true, issued = false;
@@ -465,10 +488,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           k = 2 * t + 2;
           ok = wait_one(&s.full[v % kSlots], (v / kSlots) & 1);
           for (int i = 0; i < tiles && ok; ++i) {
-            ok = wait_one(&s.p_full[i], p_count[i]++ & 1);
+            for (int h = 0; h < 2 && ok; ++h) {
+              ok = wait_one(&s.p_full[i][h], p_count[i] & 1);
+              if (!ok) break;
+              tc_fence_after_sync();
+              values(i, h, v % kSlots, j > 0 || h > 0);
+              if (h == 0) tc_commit(&s.first_done[i]);
+            }
             if (!ok) break;
-            tc_fence_after_sync();
-            values(i, v % kSlots, j > 0);
             if (i == tiles - 1) tc_commit(&s.empty[v % kSlots]);
             if (j + 1 < walk.n) {
               if (i == 0) {
@@ -485,6 +512,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
               tc_commit(&s.o_full[i]);
             }
           }
+          for (int i = 0; i < tiles; ++i) ++p_count[i];
         }
         ++units;
       }
@@ -519,11 +547,28 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           drop = !__all_sync(0xffffffffu, ok) || !en.whole(tile, 0, en.rows - 1, group, a.window);
         }
         bool nan = false;
-#pragma unroll 4
-        for (int it = w; it < 16 * L::kHalves; it += 4) {
-          const int key = 8 * (it / L::kHalves) + key8, half = it % L::kHalves, x = key & 7;
-          uint4 c = *reinterpret_cast<const uint4*>(src + key * 128 + (((4 * half + sub) ^ x) * 16));
-          if (drop) {
+        // a warp keeps to one half of the columns and every second (fourth) group of 8 keys
+        constexpr int kStep = 8 * (4 / L::kHalves);
+        const int half = L::kHalves == 2 ? w & 1 : 0, key0 = 8 * (L::kHalves == 2 ? w >> 1 : w) + key8, x = key8;
+        src += key0 * 128 + (((4 * half + sub) ^ x) * 16);
+        uint8_t* d0 = dst + half * L::kHalfBytes + key0 * 128 + (((2 * sub) ^ x) * 16);
+        uint8_t* d1 = dst + half * L::kHalfBytes + key0 * 128 + (((2 * sub + 1) ^ x) * 16);
+        auto put = [&](int it, const uint4& c) {
+          uint4 f0, f1;
+          e4m3x4_to_f16x4(c.x, f0.x, f0.y);
+          e4m3x4_to_f16x4(c.y, f0.z, f0.w);
+          e4m3x4_to_f16x4(c.z, f1.x, f1.y);
+          e4m3x4_to_f16x4(c.w, f1.z, f1.w);
+          *reinterpret_cast<uint4*>(d0 + it * kStep * 128) = f0;
+          *reinterpret_cast<uint4*>(d1 + it * kStep * 128) = f1;
+        };
+        if (!drop) {
+#pragma unroll
+          for (int it = 0; it < kKeys / kStep; ++it) put(it, *reinterpret_cast<const uint4*>(src + it * kStep * 128));
+        } else {
+#pragma unroll 1
+          for (int it = 0; it < kKeys / kStep; ++it) {
+            uint4 c = *reinterpret_cast<const uint4*>(src + it * kStep * 128);
             uint32_t seen = 0;
             auto clean = [&](uint32_t& word) {
               const uint32_t bad = __vcmpeq4(word & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
@@ -531,17 +576,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
               word &= ~bad;
             };
             clean(c.x), clean(c.y), clean(c.z), clean(c.w);
-            const int at = tile * kKeys + key;
+            const int key = key0 + it * kStep, at = tile * kKeys + key;
             nan |= seen != 0 && at >= en.lo && at < en.end && info[key >> 3].valid;      // some row sees it
+            put(it, c);
           }
-          uint4 f0, f1;
-          e4m3x4_to_f16x4(c.x, f0.x, f0.y);
-          e4m3x4_to_f16x4(c.y, f0.z, f0.w);
-          e4m3x4_to_f16x4(c.z, f1.x, f1.y);
-          e4m3x4_to_f16x4(c.w, f1.z, f1.w);
-          uint8_t* to = dst + half * L::kHalfBytes + key * 128;
-          *reinterpret_cast<uint4*>(to + (((2 * sub) ^ x) * 16)) = f0;
-          *reinterpret_cast<uint4*>(to + (((2 * sub + 1) ^ x) * 16)) = f1;
         }
         if (nan) *static_cast<volatile int*>(&s.nan_seen) = 1;
         fence_proxy_async_shared();
@@ -618,115 +656,121 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       }
       const bool live = row < en.rows;
       const int pos = live ? en.position(row, group) : -1;
-      const int r0 = kTileRows * i, r1 = min(en.rows, r0 + kTileRows) - 1;
+      // keys below pos_lo are seen by every row of the tile, as far as the window goes
+      const int pos_lo = en.position(kTileRows * i, group);
+      const int pos_hi = en.position(min(en.rows, kTileRows * (i + 1)) - 1, group) - a.window;
       // weights are relative to 2^base; a row's limit is how far above it a
       // weight may be before the sums are rescaled
       float base = 0.f, limit = -INFINITY, l = 0.f;
 
-      for (int j = 0; j < walk.n && good; ++j, ++t) {
-        const int tile = en.tile0 + walk.tile + j, key0 = tile * kKeys;
-        const Group* info = s.group[t % kInfo];
-        good = wait(&s.info_full[t % kInfo], (t / kInfo) & 1) && wait(&s.s_full[i], s_count++ & 1);
+#pragma unroll 1
+      for (int j = 0; j < walk.n && good; ++j, ++t, ++s_count) {
+        const int tile_key = (en.tile0 + walk.tile + j) * kKeys;
+        good = wait(&s.info_full[t % kInfo], (t / kInfo) & 1) && wait(&s.s_full[i], s_count & 1);
         if (!good) break;
-        const bool all = __all_sync(0xffffffffu, lane < 16 ? info[lane].valid : 1) && en.whole(tile, r0, r1, group, a.window);
         tc_fence_after_sync();
 
-        // which of 32 keys from key0 + 32 c on this row sees, a bit each
-        const int low = a.window > 0 ? pos - a.window + 1 - key0 : 0;
-        auto seen = [&](int c) {
-          const int first = low - 32 * c, last = pos - key0 - 32 * c;    // [first, last]
-          uint32_t mask = last < 0 ? 0u : last >= 31 ? 0xffffffffu : (2u << last) - 1u;
-          mask &= first <= 0 ? 0xffffffffu : first > 31 ? 0u : ~((1u << first) - 1u);
+        // 64 keys at a time: their scores to weights, which go over scores
+        // that have been read, and on to the products
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const Group* info = s.group[t % kInfo] + 8 * h;
+          const int key0 = tile_key + kHalf * h;
+          const uint32_t sh = sc + kHalf * h;
+          uint32_t ra[32], rb[32];
+          tmem_ld32(sh, ra);
+          tmem_ld32(sh + 32, rb);
+          tmem_wait(ra);
+          tmem_wait(rb);
+          const bool all = __all_sync(0xffffffffu, info[lane & 7].valid) && key0 + kHalf - 1 <= pos_lo && (a.window == 0 || key0 > pos_hi);
+          float tops[8];
+          auto exponents = [&](uint32_t (&r)[32], int c) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if (!info[4 * c + g].valid) mask &= ~(0xFFu << (8 * g));
-          return mask;
-        };
-        // 32 scores to weights, in the columns of the first 16: what was
-        // there has been read
-        auto weigh = [&](int c, uint32_t (&r)[32]) {
-          float4 gi[4];
-          float top = -INFINITY;
+            for (int g = 0; g < 4; ++g) {
+              const float2 gi = *reinterpret_cast<const float2*>(&info[4 * c + g]);
+              const uint64_t kk = f32x2(gi.x * row_scale, gi.x * row_scale), off = f32x2(gi.y - base, gi.y - base);
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            gi[g] = *reinterpret_cast<const float4*>(&info[4 * c + g]);
-            const uint64_t kk = f32x2(gi[g].x * row_scale, gi[g].x * row_scale), off = f32x2(gi[g].y - base, gi[g].y - base);
-#pragma unroll
-            for (int e = 8 * g; e < 8 * g + 8; e += 2) {
-              float y0, y1;
-              unpack(fma2(f32x2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), kk, off), y0, y1);
-              r[e] = __float_as_uint(y0);
-              r[e + 1] = __float_as_uint(y1);
+              for (int e = 8 * g; e < 8 * g + 8; e += 2) {
+                float y0, y1;
+                unpack(fma2(f32x2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), kk, off), y0, y1);
+                r[e] = __float_as_uint(y0);
+                r[e + 1] = __float_as_uint(y1);
+              }
             }
-          }
-          if (!all) {
-            const uint32_t mask = seen(c);
+            if (!all) {
+              // which of the 32 keys this row sees, a bit each: [first, last]
+              const int first = a.window > 0 ? pos - a.window + 1 - key0 - 32 * c : 0, last = pos - key0 - 32 * c;
+              uint32_t mask = last < 0 ? 0u : last >= 31 ? 0xffffffffu : (2u << last) - 1u;
+              mask &= first <= 0 ? 0xffffffffu : first > 31 ? 0u : ~((1u << first) - 1u);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = (mask >> e) & 1 ? r[e] : 0xFF800000u;
-          }
+              for (int g = 0; g < 4; ++g)
+                if (!info[4 * c + g].valid) mask &= ~(0xFFu << (8 * g));
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) top = max3(top, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+              for (int e = 0; e < 32; ++e) r[e] = (mask >> e) & 1 ? r[e] : 0xFF800000u;
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              auto x = [&](int e) { return __uint_as_float(r[8 * g + e]); };
+              tops[4 * c + g] = max3(max3(x(0), x(1), x(2)), max3(x(3), x(4), x(5)), fmaxf(x(6), x(7)));
+            }
+          };
+          exponents(ra, 0);
+          exponents(rb, 1);
+          const float top = fmaxf(max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), tops[6]), tops[7]);
           if (__any_sync(0xffffffffu, top > limit)) {
-            // a new maximum: what this unit has summed so far, and this
-            // tile's earlier weights, become relative to it
+            // a new maximum: what this unit has summed so far becomes
+            // relative to it
             const float rise = limit == -INFINITY ? (top == -INFINITY ? 0.f : top) : fmaxf(top, 0.f);
             const float keep = limit == -INFINITY ? 0.f : fast_exp2(-rise);
             base += rise;
             if (top > -INFINITY) limit = kSlack;
             l *= keep;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) - rise);
-            if (j > 0) {       // O holds the products up to the tile before: they came before these scores
+            for (int e = 0; e < 32; ++e) {
+              ra[e] = __float_as_uint(__uint_as_float(ra[e]) - rise);
+              rb[e] = __float_as_uint(__uint_as_float(rb[e]) - rise);
+            }
+            // O: the tiles before came before these scores, this tile's first half has its own word
+            if (h > 0) {
+              good = wait(&s.first_done[i], s_count & 1);
+              if (!good) break;
+              tc_fence_after_sync();
+            }
+            if (j > 0 || h > 0) {
 #pragma unroll 1
-              for (int d = 0; d < DP / 32; ++d) {
-                uint32_t o[32];
-                tmem_ld32(oc + 32 * d, o);
-                tmem_wait(o);
+              for (int d = 0; d < DP; d += 16) {
+                float o[16];
+                tmem_ld16(oc + d, o);
+                uint32_t now[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                tmem_st32(oc + 32 * d, o);
+                for (int e = 0; e < 16; ++e) now[e] = __float_as_uint(o[e] * keep);
+                tmem_st16(oc + d, now);
               }
             }
-#pragma unroll 1
-            for (int d = 0; d < c; ++d) {
-              float o[16];
-              tmem_ld16(sc + 16 * d, o);
-              uint32_t wd[16];
+          }
+          auto weights = [&](uint32_t (&r)[32], int c) {
+            uint32_t wd[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const uint32_t bits = __float_as_uint(o[e]);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&bits));
-                wd[e] = f32x2_to_f16x2(f.x * keep, f.y * keep);
+            for (int g = 0; g < 4; ++g) {
+              uint64_t sum = 0;
+#pragma unroll
+              for (int e = 8 * g; e < 8 * g + 8; e += 2) {
+                const float y0 = fast_exp2(__uint_as_float(r[e])), y1 = fast_exp2(__uint_as_float(r[e + 1]));
+                sum = e == 8 * g ? f32x2(y0, y1) : add2(sum, f32x2(y0, y1));
+                wd[e / 2] = f32x2_to_f16x2(y0, y1);
               }
-              tmem_st16(sc + 16 * d, wd);
+              float s0, s1;
+              unpack(sum, s0, s1);
+              l = fmaf(s0 + s1, info[4 * c + g].inv_v, l);
             }
-          }
-          uint32_t wd[16];
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint64_t sum = 0;
-#pragma unroll
-            for (int e = 8 * g; e < 8 * g + 8; e += 2) {
-              const float y0 = fast_exp2(__uint_as_float(r[e])), y1 = fast_exp2(__uint_as_float(r[e + 1]));
-              sum = e == 8 * g ? f32x2(y0, y1) : add2(sum, f32x2(y0, y1));
-              wd[e / 2] = f32x2_to_f16x2(y0, y1);
-            }
-            float s0, s1;
-            unpack(sum, s0, s1);
-            l = fmaf(s0 + s1, gi[g].z, l);
-          }
-          tmem_st16(sc + 16 * c, wd);
-        };
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld32(sc + 32 * c, r);
-          tmem_wait(r);
-          weigh(c, r);
+            tmem_st16(sh + 16 * c, wd);
+          };
+          weights(ra, 0);
+          weights(rb, 1);
+          tmem_wait_st();
+          tc_fence_before_sync();
+          mbar_arrive(&s.p_full[i][h]);
         }
-        tmem_wait_st();
-        tc_fence_before_sync();
-        mbar_arrive(&s.p_full[i]);
       }
 
       // ---------------------------------------------------------- output
@@ -749,14 +793,23 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       const float m = limit == -INFINITY ? -INFINITY : base;
       const int gr = en.row0 + row, tok = en.q_first + gr / group, h = walk.head * group + gr % group;
       T* dst = static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head;
+      const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // whole sectors at a time
       auto put = [&](int d, const float (&v)[32], float inv) {        // columns [d, d + 32)
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
+        for (int e = 0; e < 32; e += 16) {
           if (d + e >= ca.head_dim) continue;
-          float y[8];
+          Pack<T, 16> y;
 #pragma unroll
-          for (int z = 0; z < 8; ++z) y[z] = v[e + z] * inv;
-          store_f32<T, 8>(dst + d + e, y);
+          for (int z = 0; z < 16; ++z) y.v[z] = from_f32<T>(v[e + z] * inv);
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&y);
+          if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + d + e), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                         "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+          } else {
+            *reinterpret_cast<uint4*>(dst + d + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + d + e + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
         }
       };
       auto put_lse = [&](float mm, float ll) {
@@ -784,73 +837,97 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         continue;
       }
 
-      // A part of the unit: pieces of it are in CTAs [cta0, cta1], joined
-      // eight at a time by whoever finishes last among them, then those
-      // results likewise.
+      // A part of the unit: pieces of it are in consecutive CTAs.  Eight at a
+      // time are joined by whoever finishes last among them, then those
+      // results likewise.  Who finds all others done need not write its own.
       float4* parts = reinterpret_cast<float4*>(p.workspace);
       float2* ml = reinterpret_cast<float2*>(p.workspace + kPartialBytes);
       int* counters = reinterpret_cast<int*>(p.workspace + kPartialBytes + kMlBytes);
-      const int u0 = walk.x - walk.tile, u1 = u0 + en.count;
-      auto cta_of = [&](int y) {                                       // the CTA that holds tile y of the line
+      const int first_at = walk.u0 + kUnitCost, last_at = first_at + en.count - 1;
+      auto cta_of = [&](int y) {                                       // the CTA that holds place y of the line
         int cta = static_cast<int>(static_cast<int64_t>(y) * ctas / total);
         while (cta + 1 < ctas && begin_of(cta + 1) <= y) ++cta;
         while (begin_of(cta) > y) --cta;
         return cta;
       };
-      const int cta0 = cta_of(u0), pieces = cta_of(u1 - 1) - cta0 + 1, mine_at = static_cast<int>(blockIdx.x) - cta0;
+      const int cta0 = cta_of(first_at), pieces = cta_of(last_at) - cta0 + 1, mine_at = static_cast<int>(blockIdx.x) - cta0;
       // two slots a CTA: for the unit that began before its stretch, and for one that began in it
       auto slot_of = [&](int piece) { return (2 * (cta0 + piece) + (piece == 0 ? 1 : 0)) * 2 + i; };
       const int r = row & 127;
       auto part = [&](int slot, int d) { return parts + (static_cast<size_t>(slot) * 32 + d / 4) * kTileRows + r; };
-#pragma unroll
-      for (int d = 0; d < DP; d += 32) {
-        float v[32];
-        summed(d, v);
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) __stcg(part(slot_of(mine_at), d + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
-      }
-      __stcg(ml + static_cast<size_t>(slot_of(mine_at)) * kTileRows + r, make_float2(m, l));
-      tc_fence_before_sync();
-      int step = 1, lead = mine_at / kJoin * kJoin, count = min(kJoin, pieces - lead);
+      float m_own = m, l_own = l;
+      int step = 1;
       for (int level = 0;; ++level) {
-        __threadfence();
+        const int lead = mine_at / (kJoin * step) * (kJoin * step), count = min(kJoin, (pieces - lead + step - 1) / step);
+        const int own = (mine_at - lead) / step;                       // this result's place among them
+        int* counter = counters + level * 2 * kParts + slot_of(lead);
+        const bool kept = level == 0;                                  // O is still in TMEM
+        if ((tid & 127) == 0) s.last[i] = kept && ld_acquire_gpu(counter) == count - 1;
         named_barrier_sync(1 + i, kTileRows);
-        if ((tid & 127) == 0) {
-          int* counter = counters + level * 2 * kParts + slot_of(lead);
-          const bool last = atomicAdd(counter, 1) == count - 1;
-          if (last) *counter = 0;                                      // ready for the next call
-          s.last[i] = last;
+        bool last = s.last[i] != 0;
+        const bool unwritten = last;
+        if (!unwritten) {
+          if (kept) {
+#pragma unroll
+            for (int d = 0; d < DP; d += 32) {
+              float v[32];
+              summed(d, v);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) __stcg(part(slot_of(lead + own * step), d + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+            }
+            __stcg(ml + static_cast<size_t>(slot_of(lead + own * step)) * kTileRows + r, make_float2(m_own, l_own));
+          }
+          __threadfence();
+          named_barrier_sync(1 + i, kTileRows);
+          if ((tid & 127) == 0) s.last[i] = atomicAdd(counter, 1) == count - 1;
+          named_barrier_sync(1 + i, kTileRows);
+          last = s.last[i] != 0;
         }
         named_barrier_sync(1 + i, kTileRows);
-        const bool last = s.last[i] != 0;
-        named_barrier_sync(1 + i, kTileRows);
         if (!last) break;
+        if ((tid & 127) == 0) *counter = 0;                            // ready for the next call
         __threadfence();
-        const bool finish = count == pieces || level == 1;
-        auto ml_of = [&](int q) { return __ldcg(ml + static_cast<size_t>(slot_of(lead + q * step)) * kTileRows + r); };
-        float mx = -INFINITY, lx = 0.f;
-        for (int q = 0; q < count; ++q) mx = fmaxf(mx, ml_of(q).x);
+        const bool finish = lead == 0 && count * step >= pieces;
+        float2 z[kJoin];
+#pragma unroll
+        for (int q = 0; q < kJoin; ++q) {
+          z[q] = make_float2(-INFINITY, 0.f);
+          if (q < count && !(unwritten && q == own)) z[q] = __ldcg(ml + static_cast<size_t>(slot_of(lead + q * step)) * kTileRows + r);
+          if (unwritten && q == own) z[q] = make_float2(m_own, l_own);
+        }
+        float mx = -INFINITY, lx = 0.f, f[kJoin];
+#pragma unroll
+        for (int q = 0; q < kJoin; ++q) mx = fmaxf(mx, z[q].x);
         const float ref = mx == -INFINITY ? 0.f : mx;
-        for (int q = 0; q < count; ++q) {
-          const float2 z = ml_of(q);
-          lx = fmaf(z.y, fast_exp2(z.x - ref), lx);
+#pragma unroll
+        for (int q = 0; q < kJoin; ++q) {
+          f[q] = fast_exp2(z[q].x - ref);
+          lx = fmaf(z[q].y, f[q], lx);
         }
         const float inv = lx == 0.f ? 0.f : 1.f / lx;
 #pragma unroll 1
         for (int d = 0; d < DP; d += 32) {
           float v[32] = {};
-          for (int q = 0; q < count; ++q) {
-            const float f = fast_exp2(ml_of(q).x - ref);
-            const int slot = slot_of(lead + q * step);
-            float4 y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __ldcg(part(slot, d + 4 * e));
+          for (int q = 0; q < kJoin; ++q) {
+            if (q >= count) break;
+            if (unwritten && q == own) {
+              float y[32];
+              summed(d, y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              v[4 * e] = fmaf(y[e].x, f, v[4 * e]);
-              v[4 * e + 1] = fmaf(y[e].y, f, v[4 * e + 1]);
-              v[4 * e + 2] = fmaf(y[e].z, f, v[4 * e + 2]);
-              v[4 * e + 3] = fmaf(y[e].w, f, v[4 * e + 3]);
+              for (int e = 0; e < 32; ++e) v[e] = fmaf(y[e], f[q], v[e]);
+            } else {
+              float4 y[8];
+              const float4* from_part = part(slot_of(lead + q * step), d);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = __ldcg(from_part + e * kTileRows);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                v[4 * e] = fmaf(y[e].x, f[q], v[4 * e]);
+                v[4 * e + 1] = fmaf(y[e].y, f[q], v[4 * e + 1]);
+                v[4 * e + 2] = fmaf(y[e].z, f[q], v[4 * e + 2]);
+                v[4 * e + 3] = fmaf(y[e].w, f[q], v[4 * e + 3]);
+              }
             }
           }
           if (finish) {
@@ -865,10 +942,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           break;
         }
         __stcg(ml + static_cast<size_t>(slot_of(lead)) * kTileRows + r, make_float2(mx, lx));
-        step = kJoin;
-        lead = 0;
-        count = (pieces + kJoin - 1) / kJoin;
+        step *= kJoin;
       }
+      tc_fence_before_sync();
     }
   }
   __syncthreads();
@@ -897,7 +973,7 @@ int launch(const AttentionParams& a, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
   const int64_t row_tiles = (static_cast<int64_t>(a.max_q_len) * group + p.unit_rows - 1) / p.unit_rows;
-  const int64_t line = row_tiles * a.B * ((static_cast<int64_t>(a.table_width) * a.cache.page_size) / kKeys + 1) * a.cache.kv_heads;
+  const int64_t line = row_tiles * a.B * ((static_cast<int64_t>(a.table_width) * a.cache.page_size) / kKeys + 1 + kUnitCost) * a.cache.kv_heads;
   if (line > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   p.row_tiles = static_cast<int>(row_tiles);
   int64_t grid = sms < kMaxCtas ? sms : kMaxCtas;
