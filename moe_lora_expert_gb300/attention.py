@@ -77,62 +77,70 @@ _HEAD = struct.Struct("=Ii")
 _APPEND = struct.Struct("=2Q4q2Q4q6Q8i")
 _ATTEND = struct.Struct("=3Q4q6Q8ifI")
 
-_codes = None
+# What the entry points use on every call, bound by the first one (torch is
+# imported lazily, as in the rest of the package).
+_torch = _int32_type = _float32_type = None
+_codes: Dict = {}
+_rope_fn = _append_fn = _attend_fn = _raw_stream = None
+
+
+def _bind():
+    global _torch, _int32_type, _float32_type, _rope_fn, _append_fn, _attend_fn, _raw_stream
+    import torch
+    from . import lib
+    L = lib()
+    _codes.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32})
+    _int32_type, _float32_type = torch.int32, torch.float32
+    _append_fn, _attend_fn, _raw_stream = L.moe_kv_append, L.moe_paged_attention, torch._C._cuda_getCurrentRawStream
+    _rope_fn, _torch = L.moe_rope, torch
+
+
+def _raise(status, what):
+    from . import MoeError
+    raise MoeError(status, what)
 
 
 def _dtype_code(dtype, name):
-    global _codes
-    if _codes is None:
-        import torch
-        _codes = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16,
-                  torch.float32: MOE_DTYPE_F32}
     code = _codes.get(dtype)
     if code is None:
         raise ValueError(f"{name} must be bfloat16, float16 or (moe_rope) float32, got {dtype}")
     return code
 
 
-def _stream(stream, index):
-    import torch
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
-
-
 def _empty(shape, dtype, device, stream):
     """An output of a call on ``stream``: its memory belongs to that stream."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
-def _int32(t, shape, name):
-    import torch
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+def _int32(t, n, name):
+    """Pointer of an int32 [n] tensor."""
+    if t.dtype is not _int32_type or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != (n,):
+        raise ValueError(f"{name} must have shape [{n}], got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _heads(t, N, D, dtype, name):
-    """(pointer, token stride, head stride, heads) of a [N, H, D] tensor."""
-    if t.dim() != 3 or t.shape[0] != N or t.shape[2] != D:
-        raise ValueError(f"{name} must have shape [{N}, heads, {D}], got {tuple(t.shape)}")
-    if t.dtype != dtype or not t.is_cuda:
+def _heads(t, N, H, D, dtype, name):
+    """(pointer, token stride, head stride) of a [N, H, D] tensor."""
+    if t.shape != (N, H, D):
+        raise ValueError(f"{name} must have shape [{N}, {H}, {D}], got {tuple(t.shape)}")
+    if t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{name} must be a {dtype} CUDA tensor")
     st, sh, sd = t.stride()
-    if sd != 1:
+    if sd != 1 and D > 1:
         raise ValueError(f"{name} must be contiguous along the head dimension")
-    return t.data_ptr(), st, sh, t.shape[1]
+    return t.data_ptr(), st, sh
 
 
 def _table(cos_sin):
-    import torch
-    if (cos_sin.dtype != torch.float32 or not cos_sin.is_cuda or cos_sin.dim() != 2
-            or not cos_sin.is_contiguous()):
+    shape = cos_sin.shape
+    if cos_sin.dtype is not _float32_type or not cos_sin.is_cuda or len(shape) != 2 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous float32 CUDA tensor [positions, rotary_dim]")
-    return cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
+    return cos_sin.data_ptr(), shape[0], shape[1]
 
 
 # ----------------------------------------------------------------------------
@@ -204,28 +212,33 @@ def moe_rope(q, positions, cos_sin, k=None, interleaved=False, inverse=False, q_
     columns past the table's rotary_dim are copied.  Returns q_out, or (q_out,
     k_out); pass the inputs as outputs to rotate in place.  ``inverse``: the
     gradient of the forward for an upstream gradient in q's place."""
-    from . import _check, lib
+    if _rope_fn is None:
+        _bind()
     N, Hq, D = q.shape
-    dtype = q.dtype
+    dtype, device = q.dtype, q.device
     code = _dtype_code(dtype, "q")
+    qp, q0, q1 = _heads(q, N, Hq, D, dtype, "q")
     if q_out is None:
-        q_out = _empty((N, Hq, D), dtype, q.device, stream)
-    qp, q0, q1, _ = _heads(q, N, D, dtype, "q")
-    op, o0, o1, ho = _heads(q_out, N, D, dtype, "q_out")
-    kp = kop = k0 = k1 = ko0 = ko1 = Hk = hko = 0
+        q_out = _empty((N, Hq, D), dtype, device, stream)
+        op, o0, o1 = q_out.data_ptr(), Hq * D, D
+    else:
+        op, o0, o1 = _heads(q_out, N, Hq, D, dtype, "q_out")
+    kp = kop = k0 = k1 = ko0 = ko1 = Hk = 0
     if k is not None:
+        Hk = k.shape[1]
+        kp, k0, k1 = _heads(k, N, Hk, D, dtype, "k")
         if k_out is None:
-            k_out = _empty(k.shape, dtype, q.device, stream)
-        kp, k0, k1, Hk = _heads(k, N, D, dtype, "k")
-        kop, ko0, ko1, hko = _heads(k_out, N, D, dtype, "k_out")
-    if ho != Hq or hko != Hk:
-        raise ValueError("an output must have its input's heads")
+            k_out = _empty((N, Hk, D), dtype, device, stream)
+            kop, ko0, ko1 = k_out.data_ptr(), Hk * D, D
+        else:
+            kop, ko0, ko1 = _heads(k_out, N, Hk, D, dtype, "k_out")
     tp, rows, R = _table(cos_sin)
-    args = _ROPE.pack(_ROPE.size, code, qp, op, kp, kop, q0, q1, o0, o1, k0, k1, ko0, ko1,
-                      _int32(positions, (N,), "positions"), tp,
-                      0 if status is None else _int32(status, (4,), "status"),
-                      N, Hq, Hk, D, R, rows, bool(interleaved), bool(inverse))
-    _check(lib().moe_rope(args, _stream(stream, q.device.index)), "moe_rope")
+    args = _ROPE.pack(160, code, qp, op, kp, kop, q0, q1, o0, o1, k0, k1, ko0, ko1,
+                      _int32(positions, N, "positions"), tp, 0 if status is None else _int32(status, 4, "status"),
+                      N, Hq, Hk, D, R, rows, interleaved, inverse)
+    error = _rope_fn(args, _raw_stream(device.index) if stream is None else stream.cuda_stream)
+    if error:
+        _raise(error, "moe_rope")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -240,7 +253,9 @@ class PagedKVCache:
     """
 
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
+        if _rope_fn is None:
+            _bind()
+        torch = _torch
         fp8 = (torch.uint8, torch.float8_e4m3fn)
         for t, name in ((k, "k"), (v, "v")):
             if t.dtype not in fp8 or not t.is_cuda or t.dim() != 4 or t.shape != k.shape or t.stride(3) != 1:
@@ -256,6 +271,7 @@ class PagedKVCache:
         self._status_ptr = self.status.data_ptr()
         self._bytes = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   *k.stride()[:3], *v.stride()[:3], *k.shape)
+        self._index = k.device.index
         self._workspaces = {}
 
     @classmethod
@@ -284,17 +300,15 @@ class PagedKVCache:
         return ws
 
     def _batch(self, N, block_table, seq_lens, cu_q, max_q_len):
-        B = seq_lens.shape[0]
-        if block_table.dim() != 2:
-            raise ValueError("block_table must be [sequences, pages]")
-        width = block_table.shape[1]
-        bt = _int32(block_table, (B, width), "block_table")
-        sl = _int32(seq_lens, (B,), "seq_lens")
+        B, width = block_table.shape
+        if block_table.dtype is not _int32_type or not block_table.is_cuda or not block_table.is_contiguous():
+            raise ValueError("block_table must be a contiguous int32 CUDA tensor [sequences, pages]")
+        sl = _int32(seq_lens, B, "seq_lens")
         if cu_q is None:
             if N != B:
                 raise ValueError("without cu_q there is one new token for each sequence")
-            return B, width, bt, sl, 0, 1
-        return B, width, bt, sl, _int32(cu_q, (B + 1,), "cu_q"), N if max_q_len is None else max_q_len
+            return B, width, block_table.data_ptr(), sl, 0, 1
+        return B, width, block_table.data_ptr(), sl, _int32(cu_q, B + 1, "cu_q"), N if max_q_len is None else max_q_len
 
     def append(self, k, v, block_table, seq_lens, cu_q=None, max_q_len=None, q=None, cos_sin=None,
                interleaved=False, positions=None, q_out=None, stream=None):
@@ -302,29 +316,29 @@ class PagedKVCache:
         head_dim], go into the pages of their sequences: tokens [cu_q[b],
         cu_q[b + 1]) (one each without cu_q) end at seq_lens[b].  ``q`` [N, Hq,
         head_dim] is rotated in the same launch and returned."""
-        from . import _check, lib
-        N, D = k.shape[0], self.head_dim
+        N, D, H = k.shape[0], self.head_dim, self.kv_heads
         dtype = k.dtype
-        kp, k0, k1, hk = _heads(k, N, D, dtype, "k")
-        vp, v0, v1, hv = _heads(v, N, D, dtype, "v")
-        if hk != self.kv_heads or hv != hk:
-            raise ValueError(f"k and v must have the cache's {self.kv_heads} heads")
+        code = _dtype_code(dtype, "k")
+        kp, k0, k1 = _heads(k, N, H, D, dtype, "k")
+        vp, v0, v1 = _heads(v, N, H, D, dtype, "v")
         qp = q0 = q1 = op = o0 = o1 = Hq = 0
         if q is not None:
+            Hq = q.shape[1]
+            qp, q0, q1 = _heads(q, N, Hq, D, dtype, "q")
             if q_out is None:
-                q_out = _empty(q.shape, dtype, q.device, stream)
-            qp, q0, q1, Hq = _heads(q, N, D, dtype, "q")
-            op, o0, o1, ho = _heads(q_out, N, D, dtype, "q_out")
-            if ho != Hq:
-                raise ValueError("q_out must have q's heads")
+                q_out = _empty((N, Hq, D), dtype, self.device, stream)
+                op, o0, o1 = q_out.data_ptr(), Hq * D, D
+            else:
+                op, o0, o1 = _heads(q_out, N, Hq, D, dtype, "q_out")
         B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
         tp, rows, R = (0, 0, 0) if cos_sin is None else _table(cos_sin)
-        args = b"".join((_HEAD.pack(_HEAD.size + _CACHE.size + _APPEND.size, _dtype_code(dtype, "k")), self._bytes,
-                         _APPEND.pack(kp, vp, k0, k1, v0, v1, qp, op, q0, q1, o0, o1, bt, sl, cu,
-                                      0 if positions is None else _int32(positions, (N,), "positions"), tp,
-                                      self._status_ptr, N, B, Hq, width, longest, R, rows,
-                                      bool(interleaved))))
-        _check(lib().moe_kv_append(args, _stream(stream, self.device.index)), "moe_kv_append")
+        args = _HEAD.pack(280, code) + self._bytes + _APPEND.pack(
+            kp, vp, k0, k1, v0, v1, qp, op, q0, q1, o0, o1, bt, sl, cu,
+            0 if positions is None else _int32(positions, N, "positions"), tp, self._status_ptr,
+            N, B, Hq, width, longest, R, rows, interleaved)
+        error = _append_fn(args, _raw_stream(self._index) if stream is None else stream.cuda_stream)
+        if error:
+            _raise(error, "moe_kv_append")
         return q_out
 
     def attend(self, q, block_table, seq_lens, cu_q=None, max_q_len=None, max_seq_len=None, scale=None,
@@ -335,30 +349,30 @@ class PagedKVCache:
         ``max_seq_len``: host-side bounds that size the launch (by default N
         and the block table's width).  Returns out, or (out, lse float32 [N,
         Hq]) with ``return_lse`` or a given ``lse``."""
-        import torch
-        from . import _check, lib
         N, Hq, D = q.shape
         dtype = q.dtype
+        code = _dtype_code(dtype, "q")
+        qp, q0, q1 = _heads(q, N, Hq, self.head_dim, dtype, "q")
         if out is None:
-            out = _empty((N, Hq, D), dtype, q.device, stream)
+            out = _empty((N, Hq, D), dtype, self.device, stream)
+            op, o0, o1 = out.data_ptr(), Hq * D, D
+        else:
+            op, o0, o1 = _heads(out, N, Hq, D, dtype, "out")
         if lse is not None:
-            if lse.dtype != torch.float32 or lse.shape != (N, Hq) or not lse.is_contiguous() or not lse.is_cuda:
+            if lse.dtype is not _float32_type or lse.shape != (N, Hq) or not lse.is_contiguous() or not lse.is_cuda:
                 raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{N}, {Hq}]")
         elif return_lse:
-            lse = _empty((N, Hq), torch.float32, q.device, stream)
-        qp, q0, q1, _ = _heads(q, N, self.head_dim, dtype, "q")
-        op, o0, o1, ho = _heads(out, N, self.head_dim, dtype, "out")
-        if ho != Hq:
-            raise ValueError("out must have q's heads")
+            lse = _empty((N, Hq), _float32_type, self.device, stream)
         B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
-        handle = _stream(stream, self.device.index)
-        ws = self.workspace(handle)
-        args = b"".join((_HEAD.pack(_HEAD.size + _CACHE.size + _ATTEND.size, _dtype_code(dtype, "q")), self._bytes,
-                         _ATTEND.pack(qp, op, 0 if lse is None else lse.data_ptr(), q0, q1, o0, o1, bt, sl, cu,
-                                      self._status_ptr, ws[0], ws[1], N, B, Hq, width, longest,
-                                      width * self.page_size if max_seq_len is None else max_seq_len, window,
-                                      wait_timeout_ms, D ** -0.5 if scale is None else scale, debug_flags)))
-        _check(lib().moe_paged_attention(args, handle), "moe_paged_attention")
+        handle = _raw_stream(self._index) if stream is None else stream.cuda_stream
+        ws = self._workspaces.get(handle) or self.workspace(handle)
+        args = _HEAD.pack(248, code) + self._bytes + _ATTEND.pack(
+            qp, op, 0 if lse is None else lse.data_ptr(), q0, q1, o0, o1, bt, sl, cu, self._status_ptr, ws[0], ws[1],
+            N, B, Hq, width, longest, width * self.page_size if max_seq_len is None else max_seq_len, window,
+            wait_timeout_ms, D ** -0.5 if scale is None else scale, debug_flags)
+        error = _attend_fn(args, handle)
+        if error:
+            _raise(error, "moe_paged_attention")
         return out if lse is None else (out, lse)
 
     def device_status(self) -> int:
