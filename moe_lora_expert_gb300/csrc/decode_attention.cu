@@ -32,7 +32,7 @@ namespace moe {
 namespace {
 
 constexpr int kKeys = 64;                 // keys of a tile
-constexpr int kRows = 16;                 // rows of a row tile
+constexpr int kMaxRows = 16;              // most rows of a row tile: 8 NT
 constexpr int kWarps = 4;                 // 16 keys of a tile each
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRing = 3;                  // tiles in a warp's ring
@@ -59,23 +59,23 @@ struct Shared {
   int prefix[kMaxEntries + 1];            // key tiles before each entry
   int begin[kMaxEntries];                 // first key that some row of each entry sees
   int end[kMaxEntries];                   // end of the keys that some row of it sees
-  float m[kWarps][kRows], l[kWarps][kRows];
+  float m[kWarps][kMaxRows], l[kWarps][kMaxRows];
   int total, abort_flag, last;
 };
 constexpr int kSlotBytes = 2 * 16 * kPitch;
-constexpr int kScratchBytes = 2 * kRows * 128 * 4;            // two warps' sums
-constexpr int kSmemBytes = kWarps * kRing * kSlotBytes + kScratchBytes + static_cast<int>(sizeof(Shared)) + 1024;
+constexpr int kScratch(int rows) { return 2 * rows * 128 * 4; }              // two warps' sums
+constexpr int kSmem(int rows) { return kWarps * kRing * kSlotBytes + kScratch(rows) + static_cast<int>(sizeof(Shared)) + 1024; }
 
 // Partial sums of a row tile: [slot][row][128] and (m, l) [slot][row][2];
 // counters [2][slots].
 constexpr int kSlots = 2 * kMaxCtas;
-constexpr size_t kPartialBytes = static_cast<size_t>(kSlots) * kRows * 128 * 4;
-constexpr size_t kMlBytes = static_cast<size_t>(kSlots) * kRows * 2 * 4;
+constexpr size_t kPartialBytes = static_cast<size_t>(kSlots) * kMaxRows * 128 * 4;
+constexpr size_t kMlBytes = static_cast<size_t>(kSlots) * kMaxRows * 2 * 4;
 constexpr size_t kCounterBytes = static_cast<size_t>(kSlots) * 2 * 4;
 
 struct Launch {
   AttentionParams a;
-  int b0, B, row_tiles;                   // sequences [b0, b0 + B), row tiles of each
+  int b0, B, row_tiles, tile_rows;        // sequences [b0, b0 + B), row tiles of each and their rows
   int box;                                // keys of one TMA box: gcd(page_size, 16)
 };
 
@@ -84,6 +84,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 block of 16-bit values, thread (g, c) with (row g, columns 2c and
+// 2c + 1), to its transpose.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c1, int c2, int c3) {
@@ -98,12 +106,12 @@ struct Entry {
   int b, q_first, q_len, len, row0, rows;
   __device__ __forceinline__ Entry(const Launch& p, int e, int group) {
     b = p.b0 + e / p.row_tiles;
-    row0 = (e % p.row_tiles) * kRows;
+    row0 = (e % p.row_tiles) * p.tile_rows;
     q_first = p.a.cu_q == nullptr ? b : p.a.cu_q[b];
     q_len = p.a.cu_q == nullptr ? 1 : p.a.cu_q[b + 1] - q_first;
     len = p.a.seq_lens[b];
     const int n = min(min(q_len, p.a.max_q_len), p.a.N - q_first);
-    rows = max(0, min(kRows, n * group - row0));
+    rows = max(0, min(p.tile_rows, n * group - row0));
   }
   __device__ __forceinline__ int position(int row, int group) const { return len - q_len + (row0 + row) / group; }
 };
@@ -132,19 +140,19 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w, uint32_t& seen) {
   return w & ~nan;
 }
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+template <typename T, int DP, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3)
 decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const Launch p) {
   extern __shared__ uint8_t raw[];
   uint8_t* const rings = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   float* const scratch = reinterpret_cast<float*>(rings + kWarps * kRing * kSlotBytes);
-  Shared& s = *reinterpret_cast<Shared*>(reinterpret_cast<uint8_t*>(scratch) + kScratchBytes);
+  Shared& s = *reinterpret_cast<Shared*>(reinterpret_cast<uint8_t*>(scratch) + kScratch(8 * NT));
   const AttentionParams& a = p.a;
   const moe_kv_cache_t& ca = a.cache;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.Hq / ca.kv_heads, entries = p.B * p.row_tiles;
   constexpr int kWords = DP / 16;          // 4-code words of a key in one thread: K steps
-  constexpr int kTiles = DP / 8;           // output tiles of 8 columns
+  constexpr int kTiles = DP / 16;          // output tiles of 16 columns
 
   if (tid == 0) {
     tma_prefetch_map(&k_map);
@@ -275,27 +283,20 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       const Entry en(p, at.e, group);
       const int n = min(at.count - at.tile, x1 - x);
       const int first_tile = s.begin[at.e] / kKeys + at.tile;
-      int pos[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = g + 8 * i;
-        pos[i] = r < en.rows ? en.position(r, group) : -1;
-      }
       const int pos_min = en.position(0, group), pos_max = en.position(en.rows - 1, group);
       const int end = s.end[at.e];
 
-      // Q as the A operand: K step i, column pair (0, 1) in a0 / a1 and (2, 3)
-      // in a2 / a3 are columns DP/4 * c + 4 i + (0..3), the order in which a
-      // thread reads the codes of a key.
-      uint32_t qf[kWords][4];
-      float row_scale[2];
+      // Q^T as the B operand: K step w, column pair (0, 1) in b0 and (2, 3) in
+      // b1 are columns DP/4 * c + 4 w + (0..3), the order in which a thread
+      // reads the codes of a key.
+      uint32_t qf[NT][kWords][2];
+      float row_scale[NT][2];
+      int pos[NT][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = g + 8 * i;
-        float q[DP / 4];
-        const int row = en.row0 + r, tok = en.q_first + row / group, h = at.head * group + row % group;
+      for (int t = 0; t < NT; ++t) {
+        const int r = 8 * t + g, row = en.row0 + r, tok = en.q_first + row / group, h = at.head * group + row % group;
         const T* src = static_cast<const T*>(a.q) + tok * a.q_token + h * a.q_head;
-        float amax = 0.f;
+        float q[DP / 4], amax = 0.f, scale = 1.f;
 #pragma unroll
         for (int d = 0; d < DP / 4; d += 8) {
           const int col = DP / 4 * c + d;
@@ -307,14 +308,13 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             amax = fmaxf(amax, fabsf(v[j]));
           }
         }
-        row_scale[i] = 1.f;
-        if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+        if constexpr (!std::is_same<T, __half>::value) {
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
           // a power of two that brings the row's largest value into [1, 2)
           const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
           if (ex > -120 && ex < 120) {
-            row_scale[i] = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+            scale = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
             const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
 #pragma unroll
             for (int d = 0; d < DP / 4; ++d) q[d] *= inv;
@@ -322,16 +322,29 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         }
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
-          qf[w][i] = f32x2_to_f16x2(q[4 * w], q[4 * w + 1]);
-          qf[w][2 + i] = f32x2_to_f16x2(q[4 * w + 2], q[4 * w + 3]);
+          qf[t][w][0] = f32x2_to_f16x2(q[4 * w], q[4 * w + 1]);
+          qf[t][w][1] = f32x2_to_f16x2(q[4 * w + 2], q[4 * w + 3]);
+        }
+        // a thread's scores belong to rows 2 c and 2 c + 1
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          row_scale[t][z] = __shfl_sync(0xffffffffu, scale, 4 * (2 * c + z));
+          const int rz = 8 * t + 2 * c + z;
+          pos[t][z] = rz < en.rows ? en.position(rz, group) : -1;
         }
       }
 
-      float o[kTiles][4];
+      float o[NT][kTiles][4];
+      float m[NT][2], base[NT][2], l[NT][2];   // base: m, or 0 while there is none
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, base[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};   // base: m, or 0 while there is none
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) m[t][z] = -INFINITY, base[t][z] = 0.f, l[t][z] = 0.f;
+      }
 
+#pragma unroll 1
       for (int i = 0; i < n; ++i, ++taken) {
         const int slot = taken % kRing;
         wait(&s.full[warp][slot], (taken / kRing) & 1);
@@ -341,79 +354,25 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         const Group g0 = s.group[warp][slot][0], g1 = s.group[warp][slot][1];
         const bool some = key0 < end && (a.window == 0 || key0 + 15 > pos_min - a.window) && (g0.valid || g1.valid);
         if (some) {
-          // S = Q K^T for 16 keys
-          float sc[2][4] = {};
+          // S^T = K Q^T for 16 keys: sc[t] = (key g, rows 2c and 2c + 1), (key g + 8, the same)
+          float sc[NT][4] = {};
           uint4 kw[2][DP / 64];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint8_t* row = kt + (8 * h + g) * kPitch;
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int u = 0; u < DP / 64; ++u)
-              kw[h][u] = *reinterpret_cast<const uint4*>(row + (((DP / 64) * c + u) ^ g) * 16);
-          }
+              kw[h][u] = *reinterpret_cast<const uint4*>(kt + (8 * h + g) * kPitch + (((DP / 64) * c + u) ^ g) * 16);
 #pragma unroll
           for (int w = 0; w < kWords; ++w) {
+            auto word = [&](const uint4& u) { return (w & 3) == 0 ? u.x : (w & 3) == 1 ? u.y : (w & 3) == 2 ? u.z : u.w; };
+            uint32_t af[4];
+            e4m3x4_to_f16x4(word(kw[0][w / 4]), af[0], af[2]);
+            e4m3x4_to_f16x4(word(kw[1][w / 4]), af[1], af[3]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4& u = kw[h][w / 4];
-              const uint32_t word = (w & 3) == 0 ? u.x : (w & 3) == 1 ? u.y : (w & 3) == 2 ? u.z : u.w;
-              uint32_t b0, b1;
-              e4m3x4_to_f16x4(word, b0, b1);
-              mma_f16(sc[h], qf[w], b0, b1);
-            }
+            for (int t = 0; t < NT; ++t) mma_f16(sc[t], af, qf[t][w][0], qf[t][w][1]);
           }
-          // exponents of the weights
-          float top[2] = {-INFINITY, -INFINITY};
-          const bool whole = key0 + 15 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) && g0.valid && g1.valid;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const Group& gr = h == 0 ? g0 : g1;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float y = fmaf(sc[h][j], gr.k * row_scale[j >> 1], gr.lv);
-              if (!whole) {
-                const int key = key0 + 8 * h + 2 * c + (j & 1), ps = pos[j >> 1];
-                if (!gr.valid || key > ps || (a.window > 0 && key <= ps - a.window)) y = -INFINITY;
-              }
-              sc[h][j] = y;
-              top[j >> 1] = fmaxf(top[j >> 1], y);
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-          }
-          const bool raise = top[0] > m[0] + kSlack || top[1] > m[1] + kSlack;
-          if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float now = fmaxf(m[r], top[r]);
-              const float keep = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - now);
-              m[r] = now;
-              base[r] = now == -INFINITY ? 0.f : now;
-              l[r] *= keep;
-#pragma unroll
-              for (int j = 0; j < kTiles; ++j) {
-                o[j][2 * r] *= keep;
-                o[j][2 * r + 1] *= keep;
-              }
-            }
-          }
-          uint32_t pf[4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const Group& gr = h == 0 ? g0 : g1;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float w0 = fast_exp2(sc[h][2 * r] - base[r]), w1 = fast_exp2(sc[h][2 * r + 1] - base[r]);
-              l[r] = fmaf(w0 + w1, gr.inv_v, l[r]);
-              pf[2 * h + r] = f32x2_to_f16x2(w0, w1);
-            }
-          }
-          // O += P V: a thread reads DP / 8 columns of four keys; column j of
-          // them is output tile j
-          uint32_t vw[4][kTiles / 4];
+          // V while the scores are on their way: DP / 8 columns of four keys
+          uint32_t vw[4][kTiles / 2];
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const int key = 8 * (h >> 1) + 2 * c + (h & 1);
@@ -425,44 +384,95 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
               vw[h][0] = u.x, vw[h][1] = u.y;
             }
           }
+          // exponents of the weights, and whether some maximum has to rise
+          const bool whole = key0 + 15 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) && g0.valid && g1.valid;
+          bool raise = false;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const Group& gr = j < 2 ? g0 : g1;
+              float y = fmaf(sc[t][j], gr.k * row_scale[t][j & 1], gr.lv);
+              if (!whole) {
+                const int key = key0 + (j < 2 ? 0 : 8) + g, ps = pos[t][j & 1];
+                if (!gr.valid || key > ps || (a.window > 0 && key <= ps - a.window)) y = -INFINITY;
+              }
+              sc[t][j] = y;
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) raise |= fmaxf(sc[t][z], sc[t][z + 2]) > m[t][z] + kSlack;
+          }
+          if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                float top = fmaxf(sc[t][z], sc[t][z + 2]);
+#pragma unroll
+                for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                const float now = fmaxf(m[t][z], top);
+                const float keep = m[t][z] == -INFINITY ? 0.f : fast_exp2(m[t][z] - now);
+                m[t][z] = now;
+                base[t][z] = now == -INFINITY ? 0.f : now;
+                l[t][z] *= keep;
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
+                  o[t][j][z] *= keep;
+                  o[t][j][2 + z] *= keep;
+                }
+              }
+          }
+          // P^T as the B operand: the weights' 8 x 8 blocks transposed
+          uint32_t pf[NT][2];
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float w0 = fast_exp2(sc[t][2 * h] - base[t][0]), w1 = fast_exp2(sc[t][2 * h + 1] - base[t][1]);
+              const float inv_v = h == 0 ? g0.inv_v : g1.inv_v;
+              l[t][0] = fmaf(w0, inv_v, l[t][0]);
+              l[t][1] = fmaf(w1, inv_v, l[t][1]);
+              pf[t][h] = transpose_8x8(f32x2_to_f16x2(w0, w1));
+            }
           uint32_t nan = 0;
           if (!whole) {                    // a weight of zero times a NaN code would be NaN
 #pragma unroll
             for (int h = 0; h < 4; ++h)
 #pragma unroll
-              for (int w = 0; w < kTiles / 4; ++w) vw[h][w] = drop_nan(vw[h][w], nan);
+              for (int w = 0; w < kTiles / 2; ++w) vw[h][w] = drop_nan(vw[h][w], nan);
           }
+          // O^T += V^T P^T: columns 2 j and 2 j + 1 of the thread's are rows g and g + 8 of tile j
 #pragma unroll
-          for (int w = 0; w < kTiles / 4; ++w) {
+          for (int w = 0; w < kTiles / 2; ++w) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               const uint32_t sel = half == 0 ? 0x5140 : 0x7362;
-              const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], sel), hi = __byte_perm(vw[2][w], vw[3][w], sel);
-              const int j = 4 * w + 2 * half;
-              uint32_t l0, l1, h0, h1;
-              e4m3x4_to_f16x4(lo, l0, l1);
-              e4m3x4_to_f16x4(hi, h0, h1);
-              mma_f16(o[j], pf, l0, h0);
-              mma_f16(o[j + 1], pf, l1, h1);
+              uint32_t af[4];
+              e4m3x4_to_f16x4(__byte_perm(vw[0][w], vw[1][w], sel), af[0], af[1]);
+              e4m3x4_to_f16x4(__byte_perm(vw[2][w], vw[3][w], sel), af[2], af[3]);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * w + half], af, pf[t][0], pf[t][1]);
             }
           }
           if (!whole && __any_sync(0xffffffffu, nan != 0)) {
             // NaN codes of a partly hidden tile reach the rows that see them
+#pragma unroll 1
             for (int k = 0; k < 16; ++k) {
               const int key = key0 + k;
               const bool ok = (k < 8 ? g0 : g1).valid != 0;
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                if (!ok || key > pos[r] || (a.window > 0 && key <= pos[r] - a.window)) continue;
+              for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j)
+                for (int d = 0; d < 2; ++d) {
+                  const int col = (DP / 8) * g + 2 * j + d;
+                  const uint8_t code = vt[k * kPitch + (((col >> 4) ^ (k & 7)) * 16) + (col & 15)];
+                  const bool bad = ok && (code & 0x7F) == 0x7F;
 #pragma unroll
-                  for (int z = 0; z < 2; ++z) {
-                    const int col = (DP / 8) * (2 * c + z) + j;
-                    const uint8_t code = vt[k * kPitch + (((col >> 4) ^ (k & 7)) * 16) + (col & 15)];
-                    if ((code & 0x7F) == 0x7F) o[j][2 * r + z] = __uint_as_float(0x7FC00000u);
-                  }
-              }
+                  for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+                      if (bad && key <= pos[t][z] && (a.window == 0 || key > pos[t][z] - a.window)) o[t][j][2 * d + z] = __uint_as_float(0x7FC00000u);
+                }
             }
           }
         }
@@ -472,92 +482,97 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 
       // Join the four warps.
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (c == 0) {
-          s.m[warp][g + 8 * r] = m[r];
-          s.l[warp][g + 8 * r] = l[r];
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+#pragma unroll
+          for (int x = 4; x < 32; x *= 2) l[t][z] += __shfl_xor_sync(0xffffffffu, l[t][z], x);
+          if (g == 0) {
+            s.m[warp][8 * t + 2 * c + z] = m[t][z];
+            s.l[warp][8 * t + 2 * c + z] = l[t][z];
+          }
         }
-      }
       __syncthreads();
-      float M[2], L[2];
+      float M[NT][2], Ls[NT][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        M[r] = -INFINITY;
-        L[r] = 0.f;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M[r] = fmaxf(M[r], s.m[w][g + 8 * r]);
-        const float ref = M[r] == -INFINITY ? 0.f : M[r];
+        for (int z = 0; z < 2; ++z) {
+          const int r = 8 * t + 2 * c + z;
+          M[t][z] = -INFINITY;
+          Ls[t][z] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) L[r] += s.l[w][g + 8 * r] * fast_exp2(s.m[w][g + 8 * r] - ref);
-        const float keep = fast_exp2(m[r] - ref);
+          for (int w = 0; w < kWarps; ++w) M[t][z] = fmaxf(M[t][z], s.m[w][r]);
+          const float ref = M[t][z] == -INFINITY ? 0.f : M[t][z];
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-          o[j][2 * r] *= keep;
-          o[j][2 * r + 1] *= keep;
+          for (int w = 0; w < kWarps; ++w) Ls[t][z] += s.l[w][r] * fast_exp2(s.m[w][r] - ref);
+          const float keep = fast_exp2(m[t][z] - ref);
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j) {
+            o[t][j][z] *= keep;
+            o[t][j][2 + z] *= keep;
+          }
         }
-      }
+      constexpr int kSums = NT * kTiles * 4;
       auto put = [&](float* to) {
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-          for (int z = 0; z < 4; ++z) to[(4 * j + z) * 32 + lane] = o[j][z];
+        for (int x = 0; x < kSums; ++x) to[x * 32 + lane] = o[x / (4 * kTiles)][x / 4 % kTiles][x % 4];
       };
       auto add = [&](const float* from) {
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-          for (int z = 0; z < 4; ++z) o[j][z] += from[(4 * j + z) * 32 + lane];
+        for (int x = 0; x < kSums; ++x) o[x / (4 * kTiles)][x / 4 % kTiles][x % 4] += from[x * 32 + lane];
       };
-      if (warp >= 2) put(scratch + (warp - 2) * 2048);
+      if (warp >= 2) put(scratch + (warp - 2) * kSums * 32);
       __syncthreads();
-      if (warp < 2) add(scratch + warp * 2048);
+      if (warp < 2) add(scratch + warp * kSums * 32);
       __syncthreads();
       if (warp == 1) put(scratch);
       __syncthreads();
       if (warp == 0) add(scratch);
+
       const bool begun_before = at.tile > 0, goes_on = at.tile + n < at.count;
       const bool split = begun_before || goes_on;
       float* parts = static_cast<float*>(a.workspace);
       float* ml = parts + kPartialBytes / 4;
       int* counters = reinterpret_cast<int*>(ml + kMlBytes / 4);
 
-      // A thread of warp 0 holds, for rows g and g + 8, columns [DP/4 c, DP/4 c + DP/4).
+      // A thread of warp 0 holds, for rows 2 c and 2 c + 1, columns [DP/8 g, DP/8 g + DP/8).
       if (warp == 0) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = g + 8 * r;
-          if (row >= en.rows) continue;
-          if (!split) {
-            const float inv = L[r] == 0.f ? 0.f : 1.f / L[r];
-            const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
-            T* dst = static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int z = 0; z < 2; ++z)
-#pragma unroll
-              for (int j = 0; j < kTiles; j += 8) {
-                float v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = o[j + k][2 * r + z] * inv;
-                const int col = (DP / 8) * (2 * c + z) + j;
-                if (col < ca.head_dim) store_f32<T, 8>(dst + col, v);
-              }
-            if (c == 0 && a.lse != nullptr)
-              a.lse[static_cast<int64_t>(tok) * a.Hq + h] = L[r] == 0.f ? -INFINITY : (M[r] + log2f(L[r])) * kLn2;
-          } else {
-            const int slot = 2 * blockIdx.x + (begun_before ? 0 : 1);
-            float* dst = parts + (static_cast<size_t>(slot) * kRows + row) * 128;
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
+          for (int z = 0; z < 2; ++z) {
+            const int row = 8 * t + 2 * c + z;
+            if (row >= en.rows) continue;
+            if (!split) {
+              const float inv = Ls[t][z] == 0.f ? 0.f : 1.f / Ls[t][z];
+              const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
+              T* dst = static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head;
 #pragma unroll
               for (int j = 0; j < kTiles; j += 4) {
-                const float v[4] = {o[j][2 * r + z], o[j + 1][2 * r + z], o[j + 2][2 * r + z], o[j + 3][2 * r + z]};
-                store_f32<float, 4>(dst + (DP / 8) * (2 * c + z) + j, v);
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  v[2 * k] = o[t][j + k][z] * inv;
+                  v[2 * k + 1] = o[t][j + k][2 + z] * inv;
+                }
+                const int col = (DP / 8) * g + 2 * j;
+                if (col < ca.head_dim) store_f32<T, 8>(dst + col, v);
               }
-            if (c == 0) *reinterpret_cast<float2*>(ml + (static_cast<size_t>(slot) * kRows + row) * 2) = make_float2(M[r], L[r]);
+              if (g == 0 && a.lse != nullptr)
+                a.lse[static_cast<int64_t>(tok) * a.Hq + h] = Ls[t][z] == 0.f ? -INFINITY : (M[t][z] + log2f(Ls[t][z])) * kLn2;
+            } else {
+              const int slot = 2 * blockIdx.x + (begun_before ? 0 : 1);
+              float* dst = parts + (static_cast<size_t>(slot) * kMaxRows + row) * 128;
+#pragma unroll
+              for (int j = 0; j < kTiles; j += 2) {
+                const float v[4] = {o[t][j][z], o[t][j][2 + z], o[t][j + 1][z], o[t][j + 1][2 + z]};
+                store_f32<float, 4>(dst + (DP / 8) * g + 2 * j, v);
+              }
+              if (g == 0)
+                *reinterpret_cast<float2*>(ml + (static_cast<size_t>(slot) * kMaxRows + row) * 2) = make_float2(M[t][z], Ls[t][z]);
+            }
           }
-        }
       }
 
       if (split) {
@@ -603,7 +618,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                   v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                   continue;
                 }
-                const size_t at_row = static_cast<size_t>(slot_of(from + (i + k) * step)) * kRows + row;
+                const size_t at_row = static_cast<size_t>(slot_of(from + (i + k) * step)) * kMaxRows + row;
                 z[k] = __ldcg(reinterpret_cast<const float2*>(ml + at_row * 2));
                 v[k] = col < DP ? __ldcg(reinterpret_cast<const float4*>(parts + at_row * 128 + col)) : make_float4(0, 0, 0, 0);
               }
@@ -634,7 +649,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
               if (lane == 0 && a.lse != nullptr)
                 a.lse[static_cast<int64_t>(tok) * a.Hq + h] = Lx == 0.f ? -INFINITY : (Mx + log2f(Lx)) * kLn2;
             } else {
-              const size_t at_row = static_cast<size_t>(slot_of(from)) * kRows + row;
+              const size_t at_row = static_cast<size_t>(slot_of(from)) * kMaxRows + row;
               __syncwarp();
               if (col < DP) store_f32<float, 4>(parts + at_row * 128 + col, acc);
               if (lane == 0) *reinterpret_cast<float2*>(ml + at_row * 2) = make_float2(Mx, Lx);
@@ -719,19 +734,21 @@ size_t decode_attention_workspace_bytes() { return kPartialBytes + kMlBytes + kC
 
 namespace {
 
-template <typename T, int DP>
+template <typename T, int DP, int NT>
 int launch(const AttentionParams& a, cudaStream_t stream) {
   CUtensorMap k_map, v_map;
   Launch p = {};
   p.a = a;
   p.box = gcd(a.cache.page_size, 16);
   if (!encode_cache_map(&k_map, a.cache, false, p.box) || !encode_cache_map(&v_map, a.cache, true, p.box)) return MOE_ERR_CUDA;
-  auto kernel = decode_attention_kernel<T, DP>;
-  if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmemBytes) != cudaSuccess) return MOE_ERR_CUDA;
+  auto kernel = decode_attention_kernel<T, DP, NT>;
+  constexpr int bytes = kSmem(8 * NT);
+  p.tile_rows = 8 * NT;
+  if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes) != cudaSuccess) return MOE_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
   const int group = a.Hq / a.cache.kv_heads;
-  const int64_t row_tiles = (static_cast<int64_t>(a.max_q_len) * group + kRows - 1) / kRows;
+  const int64_t row_tiles = (static_cast<int64_t>(a.max_q_len) * group + 8 * NT - 1) / (8 * NT);
   const int64_t line = (static_cast<int64_t>(a.table_width) * a.cache.page_size / kKeys + 1) * kMaxEntries * a.cache.kv_heads;
   if (row_tiles > kMaxEntries || line > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   p.row_tiles = static_cast<int>(row_tiles);
@@ -741,10 +758,10 @@ int launch(const AttentionParams& a, cudaStream_t stream) {
     p.B = a.B - p.b0 < per_launch ? a.B - p.b0 : per_launch;
     // no more CTAs than key tiles there can be
     const int64_t tiles = (longest + kKeys - 1) / kKeys * p.B * p.row_tiles * a.cache.kv_heads;
-    int64_t grid = static_cast<int64_t>(sms) * kCtasPerSm;
+    int64_t grid = static_cast<int64_t>(sms) * (NT == 1 ? kCtasPerSm : 3);
     if (grid > kMaxCtas) grid = kMaxCtas;
     if (grid > tiles) grid = tiles;
-    if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, stream, k_map, v_map, p) != cudaSuccess)
+    if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), bytes, stream, k_map, v_map, p) != cudaSuccess)
       return MOE_ERR_CUDA;
   }
   return MOE_OK;
@@ -752,9 +769,17 @@ int launch(const AttentionParams& a, cudaStream_t stream) {
 
 }  // namespace
 
+namespace {
+template <typename T>
+int launch_rows(const AttentionParams& p, cudaStream_t s) {
+  const bool few = static_cast<int64_t>(p.max_q_len) * (p.Hq / p.cache.kv_heads) <= 8;
+  if (p.cache.head_dim <= 64) return few ? launch<T, 64, 1>(p, s) : launch<T, 64, 2>(p, s);
+  return few ? launch<T, 128, 1>(p, s) : launch<T, 128, 2>(p, s);
+}
+}  // namespace
+
 int launch_decode_attention(const AttentionParams& p, int dtype, cudaStream_t s) {
-  if (dtype == MOE_DTYPE_F16) return p.cache.head_dim <= 64 ? launch<__half, 64>(p, s) : launch<__half, 128>(p, s);
-  return p.cache.head_dim <= 64 ? launch<__nv_bfloat16, 64>(p, s) : launch<__nv_bfloat16, 128>(p, s);
+  return dtype == MOE_DTYPE_F16 ? launch_rows<__half>(p, s) : launch_rows<__nv_bfloat16>(p, s);
 }
 
 }  // namespace moe
