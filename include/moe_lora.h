@@ -481,7 +481,8 @@ int moe_read_device_status(const void* workspace, moe_stream_t stream);
  *   positions [N] int32; one outside [0, num_positions) leaves its token's
  *     heads unturned and reports MOE_ERR_BAD_POSITION.
  *   cos_sin [num_positions, rotary_dim] float32, 16-byte aligned.
- * Limits: 1 <= D <= 1024, rotary_dim even, 2 <= rotary_dim <= D, D even.
+ * Limits: 1 <= D <= 1024, rotary_dim even, 2 <= rotary_dim <= D, D even;
+ * N * (Hq + Hk) * D <= 2^32.
  * ------------------------------------------------------------------------- */
 typedef struct {
   uint32_t struct_size;           /* sizeof(moe_rope_args_t) */

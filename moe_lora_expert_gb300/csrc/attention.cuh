@@ -139,6 +139,76 @@ struct RopeTensor {
   int64_t in_token, in_head, out_token, out_head;
   int heads;
 };
+// Raw stretches, moved as they are so that several can be on their way.
+template <typename T, int V>
+__device__ __forceinline__ void to_f32s(const Pack<T, V>& r, float (&x)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = to_f32(r.v[i]);
+}
+
+// Work item ``item`` of a rotation: one stretch of HEADS consecutive heads of
+// one token (of x's heads, then y's, which may be none).  The constructor puts
+// the loads on their way; finish() takes the token's position, which may be
+// looked up meanwhile, or kUnturned for none, or kSkipped to leave it out.
+constexpr int kUnturned = -1, kSkipped = -2;
+template <int V>
+__host__ __device__ __forceinline__ uint32_t rotation_items(int heads, int per_thread, int D) {
+  return static_cast<uint32_t>((heads + per_thread - 1) / per_thread * (D / (2 * V)));
+}
+template <typename T, int V, int HEADS>
+struct RotationItem {
+  Pack<T, V> ra[HEADS], rb[HEADS];
+  uint32_t t;
+  int h0, c;
+  bool live;
+  __device__ __forceinline__ RotationItem(const RopeTensor& x, const RopeTensor& y, uint32_t item, uint32_t per_token, int N, int D,
+                                          int R, bool interleaved) {
+    const uint32_t per_head = static_cast<uint32_t>(D / (2 * V));
+    t = item / per_token;
+    const uint32_t j = item - t * per_token;
+    h0 = static_cast<int>(j / per_head) * HEADS;
+    c = static_cast<int>(j - j / per_head * per_head);
+    live = t < static_cast<uint32_t>(N);
+    const Stretch<V> s(c, R, interleaved);
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+      const int h = h0 + u;
+      if (!live || h >= x.heads + y.heads) break;
+      const T* in = h < x.heads ? static_cast<const T*>(x.in) + t * x.in_token + h * x.in_head
+                                : static_cast<const T*>(y.in) + t * y.in_token + (h - x.heads) * y.in_head;
+      ra[u] = *reinterpret_cast<const Pack<T, V>*>(in + s.a);
+      rb[u] = *reinterpret_cast<const Pack<T, V>*>(in + s.b);
+    }
+  }
+  __device__ __forceinline__ void finish(const RopeTensor& x, const RopeTensor& y, int pos, int R, bool interleaved, bool inverse,
+                                         const float* cos_sin) const {
+    if (!live || pos == kSkipped) return;
+    const Stretch<V> s(c, R, interleaved);
+    const bool turn = s.turned && pos >= 0;
+    float cs[V], sn[V];
+    if (turn) {
+      load_cos_sin<V>(cos_sin + static_cast<int64_t>(pos) * R, c, R, cs, sn);
+      if (inverse) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) sn[i] = -sn[i];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+      const int h = h0 + u;
+      if (h >= x.heads + y.heads) break;
+      float a[V], b[V];
+      to_f32s<T, V>(ra[u], a);
+      to_f32s<T, V>(rb[u], b);
+      if (turn) rotate<V>(a, b, cs, sn, interleaved);
+      T* out = h < x.heads ? static_cast<T*>(x.out) + t * x.out_token + h * x.out_head
+                           : static_cast<T*>(y.out) + t * y.out_token + (h - x.heads) * y.out_head;
+      store_f32<T, V>(out + s.a, a);
+      store_f32<T, V>(out + s.b, b);
+    }
+  }
+};
+
 struct RopeParams {
   RopeTensor q, k;
   const int32_t* positions;
@@ -158,6 +228,7 @@ struct KvAppendParams {
   int32_t* status;
   int N, B, table_width, R, num_positions, interleaved;
   int slots;                    // pages that one sequence's new tokens can touch
+  uint32_t q_items;             // work items of a token's q
 };
 cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, int V, cudaStream_t s);
 

@@ -65,7 +65,9 @@ int moe_rope(const moe_rope_args_t* a, moe_stream_t stream) {
   if (a->N < 0 || a->Hq < 0 || a->Hk < 0 || a->D <= 0 || a->rotary_dim < 2 || a->rotary_dim > a->D ||
       a->rotary_dim % 2 != 0 || a->D % 2 != 0 || a->num_positions < 0)
     return MOE_ERR_SHAPE;
-  if (a->D > 1024 || a->Hq + static_cast<int64_t>(a->Hk) > 65536) return MOE_ERR_UNSUPPORTED;
+  if (a->D > 1024 || a->Hq + static_cast<int64_t>(a->Hk) > 65536 ||
+      a->N * (a->Hq + static_cast<int64_t>(a->Hk)) * (a->D / 2) > (1ll << 31))
+    return MOE_ERR_UNSUPPORTED;
   if (a->N == 0 || a->Hq + a->Hk == 0) return MOE_OK;
   if ((a->Hq > 0 && (a->q == nullptr || a->q_out == nullptr)) || (a->Hk > 0 && (a->k == nullptr || a->k_out == nullptr)) ||
       a->positions == nullptr || (a->cos_sin == nullptr && a->num_positions > 0))
@@ -114,7 +116,8 @@ int moe_kv_append(const moe_kv_append_args_t* a, moe_stream_t stream) {
   p.interleaved = a->interleaved != 0;
   const int longest = a->cu_q == nullptr ? 1 : a->max_q_len < a->N ? a->max_q_len : a->N;
   p.slots = (longest + c.page_size - 2) / c.page_size + 1;
-  if (2ll * p.B * p.slots * c.kv_heads > (1ll << 30)) return MOE_ERR_UNSUPPORTED;
+  if (2ll * p.B * p.slots * c.kv_heads > (1ll << 30) || static_cast<int64_t>(a->N) * a->Hq * (c.head_dim / 2) > (1ll << 31))
+    return MOE_ERR_UNSUPPORTED;
   const RopeTensor k = {a->k, nullptr, a->k_stride_token, a->k_stride_head, 0, 0, c.kv_heads};
   const RopeTensor v = {a->v, nullptr, a->v_stride_token, a->v_stride_head, 0, 0, c.kv_heads};
   int V = widest(8, 2, c.head_dim, p.R, k, 8);

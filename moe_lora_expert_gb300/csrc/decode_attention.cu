@@ -54,7 +54,7 @@ struct alignas(16) Group {                // 8 keys of a tile, which lie in one 
 };
 
 struct Shared {
-  Group group[kWarps][kRing][2];
+  Group group[kWarps][2][2 * kBatch];     // of two batches of tiles
   uint64_t full[kWarps][kRing];
   int prefix[kMaxEntries + 1];            // key tiles before each entry
   int begin[kMaxEntries];                 // first key that some row of each entry sees
@@ -162,6 +162,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     s.abort_flag = 0;
     fence_mbarrier_init();
   }
+  pdl_launch_dependents();
   pdl_wait();
 
   // The line: each entry's key tiles, one at least so that someone writes its rows.
@@ -220,14 +221,15 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   // Each warp streams its own 16 keys of every tile through a ring of its own:
   // it issues the copies three tiles ahead, and no warp waits for another.
   // Two lanes stand for a tile, one for each group of 8 keys; the 32 lanes
-  // look up the pages and scales of 16 tiles at once, a batch ahead.
+  // look up the pages of 16 tiles at once, two batches ahead, and their scales
+  // one batch ahead.
   struct Ahead {
     int page, off, head;
-    Group g;
+    float ks, vs;
   };
   const int steps = x1 - x0;
   auto find = [&](int batch) {
-    Ahead f = {-1, 0, 0, {0.f, 0.f, 0.f, 0}};
+    Ahead f = {-1, 0, 0, 0.f, 0.f};
     const int k = batch * kBatch + (lane >> 1);
     if (k < steps) {
       const Place at(s, entries, ca.kv_heads, x0 + k);
@@ -241,16 +243,24 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         if (f.page < 0 || f.page >= ca.num_pages) {
           f.page = -1;
           set_status(a.status, MOE_ERR_BAD_PAGE);
-        } else {
-          const int64_t i = static_cast<int64_t>(f.page) * ca.kv_heads + f.head;
-          const float vs = fmaxf(ca.v_scale[i], 5.421010862427522e-20f);   // 2^-64: a zero scale gives zero values
-          f.g = {ca.k_scale[i] * a.scale * kLog2e, log2f(vs), 1.f / vs, 1};
         }
       }
     }
     return f;
   };
-  Ahead now = find(0), next = find(1);
+  auto fetch = [&](Ahead& f) {
+    if (f.page >= 0) {
+      const int64_t i = static_cast<int64_t>(f.page) * ca.kv_heads + f.head;
+      f.ks = ca.k_scale[i];
+      f.vs = ca.v_scale[i];
+    }
+  };
+  // The scales of a batch, where its tiles' weights will look for them.
+  auto put_scales = [&](int batch, const Ahead& f) {
+    const float vs = fmaxf(f.vs, 5.421010862427522e-20f);              // 2^-64: a zero scale gives zero values
+    s.group[warp][batch & 1][lane] = {f.ks * a.scale * kLog2e, log2f(vs), 1.f / vs, f.page >= 0};
+  };
+  Ahead now = find(0), next, later;
   int issued = 0;
   const bool stalled = (a.debug_flags & MOE_DEBUG_STALL_ATTENTION) != 0;   // a failure for the tests: no tile arrives
   auto issue = [&]() {
@@ -258,12 +268,15 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&s.abort_flag))) return;   // a slot that was not filled is not filled again
     const int in = issued % kBatch, slot = issued % kRing;
     if (in == 0 && issued > 0) {
+      // the batch before last has been weighed: kRing tiles at most are between its last and this one's first
       now = next;
-      next = find(issued / kBatch + 1);
+      put_scales(issued / kBatch, now);
+      next = later;
+      fetch(next);
+      later = find(issued / kBatch + 2);
     }
     const bool mine = (lane >> 1) == in, issues = mine && now.page >= 0 && (now.off & (p.box - 1)) == 0;
     const unsigned boxes = __ballot_sync(0xffffffffu, issues);
-    if (mine) s.group[warp][slot][lane & 1] = now.g;
     if (lane == 0) mbar_arrive_expect_tx(&s.full[warp][slot], __popc(boxes) * p.box * kPitch * 2);
     __syncwarp();
     if (issues) {
@@ -274,6 +287,12 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     ++issued;
   };
   for (int i = 0; i < kRing; ++i) issue();
+  next = find(1);
+  fetch(now);
+  later = find(2);
+  put_scales(0, now);
+  fetch(next);
+  __syncwarp();
 
   {
     const int g = lane >> 2, c = lane & 3;
@@ -351,7 +370,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         const int key0 = (first_tile + i) * kKeys + 16 * warp;
         const uint8_t* kt = rings + (warp * kRing + slot) * kSlotBytes;
         const uint8_t* vt = kt + 16 * kPitch;
-        const Group g0 = s.group[warp][slot][0], g1 = s.group[warp][slot][1];
+        const Group* groups = &s.group[warp][taken / kBatch & 1][2 * (taken % kBatch)];
+        const Group g0 = groups[0], g1 = groups[1];
         const bool some = key0 < end && (a.window == 0 || key0 + 15 > pos_min - a.window) && (g0.valid || g1.valid);
         if (some) {
           // S^T = K Q^T for 16 keys: sc[t] = (key g, rows 2c and 2c + 1), (key g + 8, the same)

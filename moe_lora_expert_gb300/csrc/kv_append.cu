@@ -16,7 +16,10 @@
 namespace moe {
 namespace {
 
-constexpr int kHeld = 4;  // stretches a thread keeps in registers between the maximum and the codes
+constexpr int kMaxThreads = 512;
+constexpr int kMinCtas = 2;           // of kMaxThreads an SM: 64 registers a thread
+constexpr int kManyItems = 1 << 17;   // stretches of q from which on a thread takes two heads
+constexpr int kHeld = 2;  // stretches a thread keeps in registers between the maximum and the codes
 
 // Smallest 2^k (k >= -42) with amax <= 448 * 2^k; amax >= 0, not NaN.
 __device__ __forceinline__ float page_scale(float amax) {
@@ -50,9 +53,11 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[V], flo
 
 // CTAs [0, 2 * B * slots * Hkv): one (sequence, page of it, head, K or V) each.
 // The rest rotate q.
-template <typename T, int V>
-__global__ void kv_append_kernel(KvAppendParams p) {
+template <typename T, int V, int HEADS>
+__global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppendParams p) {
   __shared__ float s_max[32];
+  __shared__ int s_pos[kMaxThreads];
+  pdl_launch_dependents();
   pdl_wait();
   const moe_kv_cache_t& ca = p.cache;
   const int per_head = ca.head_dim / (2 * V);
@@ -60,37 +65,28 @@ __global__ void kv_append_kernel(KvAppendParams p) {
   const int tid = threadIdx.x;
 
   if (blockIdx.x >= static_cast<unsigned>(units)) {  // q
-    const int64_t total = static_cast<int64_t>(p.N) * p.q.heads * per_head;
-    const int64_t stride = static_cast<int64_t>(gridDim.x - units) * blockDim.x;
-    for (int64_t j = static_cast<int64_t>(blockIdx.x - units) * blockDim.x + tid; j < total; j += stride) {
-      const int64_t th = j / per_head;
-      const int c = static_cast<int>(j - th * per_head);
-      const int t = static_cast<int>(th / p.q.heads), h = static_cast<int>(th - static_cast<int64_t>(t) * p.q.heads);
-      if (p.cu_q != nullptr && t >= p.cu_q[p.B]) continue;  // a row of no sequence
-      int pos;
-      if (p.positions != nullptr) {
-        pos = p.positions[t];
-      } else {
-        const int b = p.cu_q == nullptr ? t : sequence_of(p.cu_q, p.B, t);
-        pos = p.cu_q == nullptr ? p.seq_lens[b] - 1 : p.seq_lens[b] - p.cu_q[b + 1] + t;
+    const uint32_t item0 = (blockIdx.x - units) * blockDim.x, token0 = item0 / p.q_items;
+    const RotationItem<T, V, HEADS> x(p.q, RopeTensor{}, item0 + tid, p.q_items, p.N, ca.head_dim, p.R, p.interleaved);
+    // the positions of the CTA's tokens, a thread each
+    const uint32_t t = token0 + tid;
+    if (t <= (item0 + blockDim.x - 1) / p.q_items && t < static_cast<uint32_t>(p.N)) {
+      int pos = kSkipped;
+      if (p.cu_q == nullptr || static_cast<int>(t) < p.cu_q[p.B]) {          // else a row of no sequence
+        if (p.positions != nullptr) {
+          pos = p.positions[t];
+        } else {
+          const int b = p.cu_q == nullptr ? t : sequence_of(p.cu_q, p.B, t);
+          pos = p.cu_q == nullptr ? p.seq_lens[b] - 1 : p.seq_lens[b] - p.cu_q[b + 1] + static_cast<int>(t);
+        }
+        if (pos < 0 || pos >= p.num_positions) {
+          if (p.R > 0) set_status(p.status, MOE_ERR_BAD_POSITION);
+          pos = kUnturned;
+        }
       }
-      const bool known = pos >= 0 && pos < p.num_positions;
-      const T* in = static_cast<const T*>(p.q.in) + t * p.q.in_token + h * p.q.in_head;
-      T* out = static_cast<T*>(p.q.out) + t * p.q.out_token + h * p.q.out_head;
-      const Stretch<V> s(c, p.R, p.interleaved);
-      float a[V], b[V];
-      load_f32<T, V>(in + s.a, a);
-      load_f32<T, V>(in + s.b, b);
-      if (s.turned && known) {
-        float cs[V], sn[V];
-        load_cos_sin<V>(p.cos_sin + static_cast<int64_t>(pos) * p.R, c, p.R, cs, sn);
-        rotate<V>(a, b, cs, sn, p.interleaved);
-      } else if (s.turned) {
-        set_status(p.status, MOE_ERR_BAD_POSITION);
-      }
-      store_f32<T, V>(out + s.a, a);
-      store_f32<T, V>(out + s.b, b);
+      s_pos[tid] = pos;
     }
+    __syncthreads();
+    if (x.live) x.finish(p.q, RopeTensor{}, s_pos[x.t - token0], p.R, p.interleaved, false, p.cos_sin);
     return;
   }
 
@@ -125,15 +121,19 @@ __global__ void kv_append_kernel(KvAppendParams p) {
   const float s_old = off > 0 ? *scale : 0.f;         // a page with no earlier token keeps nothing of its last use
   const bool turn = is_k && p.cos_sin != nullptr;
 
-  auto fetch = [&](int j, float (&a)[V], float (&bb)[V]) {
+  auto load = [&](int j, Pack<T, V>& ra, Pack<T, V>& rb) {
     const int r = j / per_head, c = j - r * per_head;
-    const int t = t_first + (p0 - start) + r;
-    const T* row = x + t * x_token;
+    const T* row = x + (t_first + (p0 - start) + r) * x_token;
     const Stretch<V> s(c, turn ? p.R : 0, p.interleaved);
-    load_f32<T, V>(row + s.a, a);
-    load_f32<T, V>(row + s.b, bb);
-    if (s.turned) {
-      const int pos = p.positions != nullptr ? p.positions[t] : p0 + r;
+    ra = *reinterpret_cast<const Pack<T, V>*>(row + s.a);
+    rb = *reinterpret_cast<const Pack<T, V>*>(row + s.b);
+  };
+  auto rotated = [&](int j, const Pack<T, V>& ra, const Pack<T, V>& rb, float (&a)[V], float (&bb)[V]) {
+    const int r = j / per_head, c = j - r * per_head;
+    to_f32s<T, V>(ra, a);
+    to_f32s<T, V>(rb, bb);
+    if (turn && 2 * V * c < p.R) {
+      const int pos = p.positions != nullptr ? p.positions[t_first + (p0 - start) + r] : p0 + r;
       if (pos >= 0 && pos < p.num_positions) {
         float cs[V], sn[V];
         load_cos_sin<V>(p.cos_sin + static_cast<int64_t>(pos) * p.R, c, p.R, cs, sn);
@@ -144,47 +144,53 @@ __global__ void kv_append_kernel(KvAppendParams p) {
     }
   };
 
-  float held_a[kHeld][V], held_b[kHeld][V];
+  // The maximum first, then the codes.  The stretches stay in registers as
+  // they came and are rotated twice: rotated ones would take twice the
+  // registers, and with them half of the threads that keep loads on their way.
+  Pack<T, V> ra[kHeld], rb[kHeld];
   float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int j = tid + i * blockDim.x;
-    if (j < items) {
-      fetch(j, held_a[i], held_b[i]);
-#pragma unroll
-      for (int e = 0; e < V; ++e) amax = fmaxf(amax, fmaxf(fabsf(held_a[i][e]), fabsf(held_b[i][e])));
-    }
-  }
-  for (int j = tid + kHeld * blockDim.x; j < items; j += blockDim.x) {
+  auto reduce = [&](int j, const Pack<T, V>& pa, const Pack<T, V>& pb) {
     float a[V], bb[V];
-    fetch(j, a, bb);
+    rotated(j, pa, pb, a, bb);
 #pragma unroll
     for (int e = 0; e < V; ++e) amax = fmaxf(amax, fmaxf(fabsf(a[e]), fabsf(bb[e])));
+  };
+  const int step = static_cast<int>(blockDim.x);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (tid + i * step < items) load(tid + i * step, ra[i], rb[i]);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (tid + i * step < items) reduce(tid + i * step, ra[i], rb[i]);
+  for (int j = tid + kHeld * step; j < items; j += step) {
+    Pack<T, V> pa, pb;
+    load(j, pa, pb);
+    reduce(j, pa, pb);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((tid & 31) == 0) s_max[tid >> 5] = amax;
   __syncthreads();
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) amax = fmaxf(amax, s_max[w]);
+  for (int w = 0; w < (step >> 5); ++w) amax = fmaxf(amax, s_max[w]);
   const float s_new = fmaxf(s_old, page_scale(amax));
   const float inv = 1.f / s_new;
 
-  auto put = [&](int j, const float (&a)[V], const float (&bb)[V]) {
+  auto put = [&](int j, const Pack<T, V>& pa, const Pack<T, V>& pb) {
     const int r = j / per_head, c = j - r * per_head;
+    float a[V], bb[V];
+    rotated(j, pa, pb, a, bb);
     const Stretch<V> s(c, turn ? p.R : 0, p.interleaved);
     uint8_t* row = codes + (off + r) * row_bytes;
     store_codes<V>(row + s.a, a, inv);
     store_codes<V>(row + s.b, bb, inv);
   };
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int j = tid + i * blockDim.x;
-    if (j < items) put(j, held_a[i], held_b[i]);
-  }
-  for (int j = tid + kHeld * blockDim.x; j < items; j += blockDim.x) {
-    float a[V], bb[V];
-    fetch(j, a, bb);
-    put(j, a, bb);
+  for (int i = 0; i < kHeld; ++i)
+    if (tid + i * step < items) put(tid + i * step, ra[i], rb[i]);
+  for (int j = tid + kHeld * step; j < items; j += step) {
+    Pack<T, V> pa, pb;
+    load(j, pa, pb);
+    put(j, pa, pb);
   }
   if (off > 0 && s_new != s_old) {                     // the codes that the page held before
     const float ratio = s_old * inv;
@@ -204,17 +210,22 @@ __global__ void kv_append_kernel(KvAppendParams p) {
   if (tid == 0 && s_new != *scale) *scale = s_new;     // every thread has its s_old since the barrier
 }
 
-template <typename T, int V>
-cudaError_t launch(const KvAppendParams& p, cudaStream_t s) {
+template <typename T, int V, int HEADS>
+cudaError_t launch_heads(KvAppendParams p, cudaStream_t s) {
   const int per_head = p.cache.head_dim / (2 * V);
   const int rows = p.slots > 1 ? p.cache.page_size : 1;
   int threads = 64;
-  while (threads < 512 && threads * kHeld < rows * per_head) threads *= 2;
+  while (threads < kMaxThreads && threads * kHeld < rows * per_head) threads *= 2;
   const int64_t units = 2ll * p.B * p.slots * p.cache.kv_heads;
-  const int64_t q_items = static_cast<int64_t>(p.N) * p.q.heads * per_head;
-  const int64_t q_ctas = (q_items + threads - 1) / threads;
-  return launch_pdl(kv_append_kernel<T, V>, dim3(static_cast<unsigned>(units + (q_ctas < 65536 ? q_ctas : 65536))),
-                    dim3(threads), 0, s, p);
+  p.q_items = p.q.heads > 0 ? rotation_items<V>(p.q.heads, HEADS, p.cache.head_dim) : 1;
+  const int64_t q_ctas = p.q.heads > 0 ? (static_cast<int64_t>(p.N) * p.q_items + threads - 1) / threads : 0;
+  return launch_pdl(kv_append_kernel<T, V, HEADS>, dim3(static_cast<unsigned>(units + q_ctas)), dim3(threads), 0, s, p);
+}
+
+template <typename T, int V>
+cudaError_t launch(const KvAppendParams& p, cudaStream_t s) {
+  return static_cast<int64_t>(p.N) * rotation_items<V>(p.q.heads, 1, p.cache.head_dim) >= kManyItems ? launch_heads<T, V, 2>(p, s)
+                                                                                                     : launch_heads<T, V, 1>(p, s);
 }
 
 template <typename T>

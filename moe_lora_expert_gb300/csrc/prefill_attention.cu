@@ -290,6 +290,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     s.nan_seen = 0;
     fence_mbarrier_init();
   }
+  pdl_launch_dependents();
   pdl_wait();
 
   // The line's length, and where this CTA's stretch of it begins.

@@ -12,48 +12,28 @@
 namespace moe {
 namespace {
 
-// One CTA a token; a thread takes one stretch of one head at a time.
+constexpr int kThreads = 128;
+
+// A thread a stretch of a head.
 template <typename T, int V>
-__global__ void rope_kernel(RopeParams p) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, uint32_t per_token) {
+  pdl_launch_dependents();
   pdl_wait();
-  const int per_head = p.D / (2 * V);
-  const int items = (p.q.heads + p.k.heads) * per_head;
-  for (int64_t t = blockIdx.x; t < p.N; t += gridDim.x) {
-    const int pos = p.positions[t];
-    const bool known = pos >= 0 && pos < p.num_positions;
-    if (!known && threadIdx.x == 0) set_status(p.status, MOE_ERR_BAD_POSITION);
-    const float* row = p.cos_sin + static_cast<int64_t>(known ? pos : 0) * p.R;
-    for (int j = threadIdx.x; j < items; j += blockDim.x) {
-      const int h = j / per_head, c = j - h * per_head;
-      const bool is_q = h < p.q.heads;
-      const RopeTensor& x = is_q ? p.q : p.k;
-      const int hh = is_q ? h : h - p.q.heads;
-      const T* in = static_cast<const T*>(x.in) + t * x.in_token + hh * x.in_head;
-      T* out = static_cast<T*>(x.out) + t * x.out_token + hh * x.out_head;
-      const Stretch<V> s(c, p.R, p.interleaved);
-      float a[V], b[V];
-      load_f32<T, V>(in + s.a, a);
-      load_f32<T, V>(in + s.b, b);
-      if (s.turned && known) {
-        float cs[V], sn[V];
-        load_cos_sin<V>(row, c, p.R, cs, sn);
-        if (p.inverse) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) sn[i] = -sn[i];
-        }
-        rotate<V>(a, b, cs, sn, p.interleaved);
-      }
-      store_f32<T, V>(out + s.a, a);
-      store_f32<T, V>(out + s.b, b);
-    }
+  const RotationItem<T, V, 1> x(p.q, p.k, blockIdx.x * kThreads + threadIdx.x, per_token, p.N, p.D, p.R, p.interleaved);
+  if (!x.live) return;
+  int pos = p.positions[x.t];
+  if (pos < 0 || pos >= p.num_positions) {
+    set_status(p.status, MOE_ERR_BAD_POSITION);
+    pos = kUnturned;
   }
+  x.finish(p.q, p.k, pos, p.R, p.interleaved, p.inverse, p.cos_sin);
 }
 
 template <typename T, int V>
 cudaError_t launch(const RopeParams& p, cudaStream_t s) {
-  const int items = (p.q.heads + p.k.heads) * (p.D / (2 * V));
-  const int threads = items >= 1024 ? 1024 : (items + 31) / 32 * 32;
-  return launch_pdl(rope_kernel<T, V>, dim3(static_cast<unsigned>(p.N)), dim3(threads), 0, s, p);
+  const uint32_t per_token = rotation_items<V>(p.q.heads + p.k.heads, 1, p.D);
+  const int64_t ctas = (static_cast<int64_t>(p.N) * per_token + kThreads - 1) / kThreads;
+  return launch_pdl(rope_kernel<T, V>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, p, per_token);
 }
 
 template <typename T>
