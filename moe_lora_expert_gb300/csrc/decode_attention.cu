@@ -40,7 +40,8 @@ constexpr int kBatch = 16;                // tiles whose pages are looked up at 
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxCtas = 640;
 constexpr int kMaxEntries = 512;          // (sequence, row tile) pairs of one launch
-constexpr int kJoin = 8;                  // pieces that are joined at a time
+constexpr int kMinTiles = 2;              // a CTA's stretch of the line is at least so long (but for the last tiles)
+constexpr int kJoin = 16;                 // pieces that are joined at a time
 constexpr int kPitch = 128;               // bytes of a key in shared memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -204,7 +205,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     if (lane == 31) s.total = incl * ca.kv_heads;
   }
   __syncthreads();
-  const int total = s.total, ctas = min(static_cast<int>(gridDim.x), total);   // with fewer tiles than CTAs, one each
+  const int total = s.total, ctas = min(static_cast<int>(gridDim.x), (total + kMinTiles - 1) / kMinTiles);
   auto begin_of = [&](int cta) { return static_cast<int>(static_cast<int64_t>(total) * cta / ctas); };
   const bool idle = static_cast<int>(blockIdx.x) >= ctas;
   const int x0 = idle ? 0 : begin_of(blockIdx.x), x1 = idle ? 0 : begin_of(blockIdx.x + 1);
