@@ -46,6 +46,7 @@ constexpr int kConvertWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;
+constexpr int kOColumns = 256;             // TMEM: two row tiles' scores, then their sums, 128 columns each
 
 struct alignas(16) Group {                 // 8 keys, which lie in one page
   float k, lv, inv_v;
@@ -140,11 +141,6 @@ __device__ __forceinline__ uint64_t f32x2(float a, float b) {
   return r;
 }
 __device__ __forceinline__ void unpack(uint64_t p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -225,6 +221,34 @@ struct Walk {
   }
 };
 
+// The kernel's roles share one instruction cache: what is called once a unit,
+// or to wait, is not inlined into each of them.
+__device__ __noinline__ bool walk_next(Walk* at, const Launch& p, int group, int first_entry, int first_prefix) {
+  Walk w = *at;
+  const bool more = w.next(p, group, first_entry >= 0, first_entry, first_prefix);
+  __syncwarp(__activemask());
+  *at = w;
+  __syncwarp(__activemask());
+  return more;
+}
+// The line of ``total`` places in ``ctas`` equal stretches: where one begins, and which holds place y.
+__device__ __noinline__ int stretch_begin(int total, int ctas, int cta) {
+  return static_cast<int>(static_cast<int64_t>(total) * cta / ctas);
+}
+__device__ __noinline__ int stretch_of(int total, int ctas, int y) {
+  int cta = static_cast<int>(static_cast<int64_t>(y) * ctas / total);
+  while (cta + 1 < ctas && stretch_begin(total, ctas, cta + 1) <= y) ++cta;
+  while (stretch_begin(total, ctas, cta) > y) --cta;
+  return cta;
+}
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, uint64_t limit_ns, int* status, int* abort_flag) {
+  if (*static_cast<volatile int*>(abort_flag) != 0) return false;
+  if (mbar_wait(bar, parity, limit_ns)) return true;
+  set_status(status, MOE_ERR_DEVICE_TIMEOUT);
+  *static_cast<volatile int*>(abort_flag) = 1;
+  return false;
+}
+
 // ----------------------------------------------------------- shared memory
 struct Control {
   Group group[kInfo][kKeys / 8];
@@ -234,7 +258,7 @@ struct Control {
   int sums[kThreads / 32];
   Walk walk[kThreads / 32];                // each warp's own, here and not in its registers
   uint32_t tmem;
-  int abort_flag, nan_seen, first_entry, first_prefix, last[2];
+  int abort_flag, nan_seen, first_entry, first_prefix, last[2], issued, issued_units;
 };
 
 template <int DP>
@@ -253,7 +277,7 @@ static_assert(Layout<128>::kBytes <= 232448, "shared memory of a CTA");
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                         const __grid_constant__ CUtensorMap v_map, const Launch p) {
+                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ Launch p) {
   using L = Layout<DP>;
   constexpr bool kBf16 = !std::is_same<T, __half>::value;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -267,17 +291,22 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     tma_prefetch_map(&q_map);
     tma_prefetch_map(&k_map);
     tma_prefetch_map(&v_map);
+#pragma unroll 1
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.code_full[i], 1);
       mbar_init(&s.code_empty[i], 4);
     }
+#pragma unroll 1
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&s.full[i], 4);
       mbar_init(&s.empty[i], 1);
     }
+#pragma unroll 1
     for (int i = 0; i < kInfo; ++i) mbar_init(&s.info_full[i], 1);
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) mbar_init(&s.p_full[i][h], kTileRows);
       mbar_init(&s.first_done[i], 1);
       mbar_init(&s.o_full[i], 1);
@@ -297,6 +326,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   const int entries = a.B * p.row_tiles, per = (entries + kThreads - 1) / kThreads;
   const int from = min(tid * per, entries), to = min(from + per, entries);
   int mine = 0;
+#pragma unroll 1
   for (int e = from; e < to; ++e) {
     Entry en;
     en.load(p, e, group);
@@ -311,6 +341,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   if (lane == 31) s.sums[warp] = incl;
   __syncthreads();
   int all_tiles = 0;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) incl += s.sums[w];
     all_tiles += s.sums[w];
@@ -318,10 +349,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   const int total = all_tiles * ca.kv_heads;
   const int ctas = min(static_cast<int>(gridDim.x), max(1, total / kMinTiles));
   if (total == 0 || static_cast<int>(blockIdx.x) >= ctas) return;
-  auto begin_of = [&](int cta) { return static_cast<int>(static_cast<int64_t>(total) * cta / ctas); };
-  const int x0 = begin_of(blockIdx.x);
+  const int x0 = stretch_begin(total, ctas, blockIdx.x);
   if (x0 < incl * ca.kv_heads && x0 >= (incl - mine) * ca.kv_heads) {
     int before = incl - mine;
+#pragma unroll 1
     for (int e = from; e < to; ++e) {
       Entry en;
       en.load(p, e, group);
@@ -343,18 +374,13 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   tc_fence_after_sync();
   const uint32_t tmem = s.tmem;
   auto s_cols = [&](int i) { return tmem + 128 * i; };
-  auto o_cols = [&](int i) { return tmem + 256 + 128 * i; };
+  auto o_cols = [&](int i) { return tmem + kOColumns + 128 * i; };
 
   // A wait that runs out, here or in another role, ends the CTA's work: no
   // role then issues a copy or a product or touches TMEM any more.
   auto aborted = [&] { return *static_cast<volatile int*>(&s.abort_flag) != 0; };
   auto wait_one = [&](uint64_t* bar, uint32_t parity) {      // by one thread
-    if (!mbar_try_wait(smem_u32(bar), parity) && (aborted() || !mbar_wait(bar, parity, a.wait_limit_ns))) {
-      set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
-      *static_cast<volatile int*>(&s.abort_flag) = 1;
-      return false;
-    }
-    return true;
+    return mbar_try_wait(smem_u32(bar), parity) || wait_long(bar, parity, a.wait_limit_ns, a.status, &s.abort_flag);
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) {          // by a warp, which leaves it together
     const bool ok = wait_one(bar, parity);
@@ -365,15 +391,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   auto next = [&](bool first) {                              // by the lanes that call it, with the same values
     if (first) {
       walk.x = x0;
-      walk.x1 = begin_of(blockIdx.x + 1);
+      walk.x1 = stretch_begin(total, ctas, blockIdx.x + 1);
+      __syncwarp(__activemask());
     }
-    __syncwarp(__activemask());
-    Walk w = walk;
-    const bool more = w.next(p, group, first, s.first_entry, s.first_prefix);
-    __syncwarp(__activemask());
-    walk = w;
-    __syncwarp(__activemask());
-    return more;
+    return walk_next(&walk, p, group, first ? s.first_entry : -1, s.first_prefix);
   };
 
   if (warp == kLoadWarp) {
@@ -405,14 +426,17 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     };
     int issued = 0, units = 0;
     bool stop = false;
+#pragma unroll 1
     for (bool more = next(true); more && !stop; more = next(false)) {
       if (en.position(en.rows - 1, group) >= static_cast<int64_t>(a.table_width) * ca.page_size) set_status(a.status, MOE_ERR_BAD_PAGE);
       Ahead now = find(0);
+#pragma unroll 1
       for (int j = 0; j < walk.n && !stop; ++j) {
         const Ahead later = find(j + 1);
         const int t = issued / 2;
         const bool issues = lane < 16 && now.page >= 0 && (8 * lane) % p.box == 0;
         const unsigned boxes = __ballot_sync(0xffffffffu, issues);
+#pragma unroll 1
         for (int v = 0; v < 2; ++v) {
           const int st = issued % kStages;
           if (issued >= kStages && !wait(&s.code_empty[st], (issued / kStages - 1) & 1)) {
@@ -437,6 +461,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
             }
             if (lane == 0) {
               mbar_arrive_expect_tx(&s.q_raw, L::kHalves * p.unit_rows * 128);
+#pragma unroll 1
               for (int h = 0; h < L::kHalves; ++h)
                 tma_load_3d(smem_u32(smem + L::kQ + 2 * h * L::kHalfBytes), &q_map, &s.q_raw, 64 * h, walk.head * group,
                             en.q_first + en.row0 / group);
@@ -447,9 +472,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         now = later;
       }
     }
-    if (stop) {                                          // nothing of this CTA stays in flight
-      for (int k = max(0, issued - kStages); k < issued; ++k) mbar_wait(&s.code_full[k % kStages], (k / kStages) & 1, a.wait_limit_ns);
-      if (units > 0) mbar_wait(&s.q_raw, (units - 1) & 1, a.wait_limit_ns);
+    if (lane == 0) {
+      s.issued = issued;
+      s.issued_units = units;
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
@@ -531,7 +556,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     const int w = warp - kConvertWarp, sub = lane & 3, key8 = (lane >> 3) ^ (5 * ((lane >> 2) & 1));
     int k = 0, units = 0;
     bool good = true;
+#pragma unroll 1
     for (bool more = next(true); more && good; more = next(false), ++units) {
+#pragma unroll 1
       for (int j = 0; j < 2 * walk.n; ++j, ++k) {
         const int st = k % kStages, slot = k % kSlots;
         const Group* info = s.group[(k / 2) % kInfo];
@@ -623,6 +650,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
             fence_proxy_async_shared();
             __syncwarp();
           } else if (a.scale < 0.f) {
+#pragma unroll 1
             for (int c = 32 * w + lane; c < L::kQBytes / 16; c += 128) {
               uint4* at = reinterpret_cast<uint4*>(smem + L::kQ) + c;
               const uint4 u = *at;
@@ -639,9 +667,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     // ------------------------------------------------------------- softmax
     const int i = warp >> 2, row = kTileRows * i + 32 * (warp & 3) + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t sc = s_cols(i) + lanes, oc = o_cols(i) + lanes;
+    const uint32_t sc = s_cols(i) + lanes;
     int t = 0, s_count = 0, o_count = 0, units = 0;
     bool good = true;
+#pragma unroll 1
     for (bool more = next(true); more; more = next(false), ++units) {
       // after a timeout a unit's rows are left as they are, but its part in the
       // join is still played, so that the counters end at zero
@@ -655,8 +684,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         t += walk.n;
         continue;
       }
-      const bool live = row < en.rows;
-      const int pos = live ? en.position(row, group) : -1;
+      const int pos = row < en.rows ? en.position(row, group) : -1;
       // keys below pos_lo are seen by every row of the tile, as far as the window goes
       const int pos_lo = en.position(kTileRows * i, group);
       const int pos_hi = en.position(min(en.rows, kTileRows * (i + 1)) - 1, group) - a.window;
@@ -684,18 +712,16 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           tmem_wait(ra);
           tmem_wait(rb);
           const bool all = __all_sync(0xffffffffu, info[lane & 7].valid) && key0 + kHalf - 1 <= pos_lo && (a.window == 0 || key0 > pos_hi);
-          float tops[8];
+          float top = -INFINITY;
           auto exponents = [&](uint32_t (&r)[32], int c) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               const float2 gi = *reinterpret_cast<const float2*>(&info[4 * c + g]);
-              const uint64_t kk = f32x2(gi.x * row_scale, gi.x * row_scale), off = f32x2(gi.y - base, gi.y - base);
+              const float kk = gi.x * row_scale, off = gi.y - base;
 #pragma unroll
               for (int e = 8 * g; e < 8 * g + 8; e += 2) {
-                float y0, y1;
-                unpack(fma2(f32x2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), kk, off), y0, y1);
-                r[e] = __float_as_uint(y0);
-                r[e + 1] = __float_as_uint(y1);
+                r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), kk, off));
+                r[e + 1] = __float_as_uint(fmaf(__uint_as_float(r[e + 1]), kk, off));
               }
             }
             if (!all) {
@@ -712,12 +738,11 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               auto x = [&](int e) { return __uint_as_float(r[8 * g + e]); };
-              tops[4 * c + g] = max3(max3(x(0), x(1), x(2)), max3(x(3), x(4), x(5)), fmaxf(x(6), x(7)));
+              top = max3(top, max3(x(0), x(1), x(2)), max3(max3(x(3), x(4), x(5)), x(6), x(7)));
             }
           };
           exponents(ra, 0);
           exponents(rb, 1);
-          const float top = fmaxf(max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), tops[6]), tops[7]);
           if (__any_sync(0xffffffffu, top > limit)) {
             // a new maximum: what this unit has summed so far becomes
             // relative to it
@@ -741,11 +766,11 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
 #pragma unroll 1
               for (int d = 0; d < DP; d += 16) {
                 float o[16];
-                tmem_ld16(oc + d, o);
+                tmem_ld16(sc + kOColumns + d, o);
                 uint32_t now[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) now[e] = __float_as_uint(o[e] * keep);
-                tmem_st16(oc + d, now);
+                tmem_st16(sc + kOColumns + d, now);
               }
             }
           }
@@ -775,19 +800,27 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       }
 
       // ---------------------------------------------------------- output
+      const bool live = row < en.rows;
       good = good && wait(&s.o_full[i], o_count++ & 1);
       tc_fence_after_sync();
       // NaN values of partly hidden tiles, for the rows that see them
       uint32_t nan[4] = {};
+      bool any_nan = false;
       if (live && good && *static_cast<volatile int*>(&s.nan_seen) != 0) {
+#pragma unroll 1
         for (int tile = en.tile0 + walk.tile; tile < en.tile0 + walk.tile + walk.n; ++tile) {
           const int k0 = max(tile * kKeys, a.window > 0 ? pos - a.window + 1 : 0), k1 = min(min(pos, en.end - 1), tile * kKeys + kKeys - 1);
+#pragma unroll 1
           for (int key = k0; key <= k1; ++key) {
             const int page_at = key / ca.page_size, page = a.block_table[static_cast<int64_t>(en.b) * a.table_width + page_at];
             if (page < 0 || page >= ca.num_pages) continue;
             const uint8_t* codes = ca.v + page * ca.v_stride_page + walk.head * ca.v_stride_head + (key - page_at * ca.page_size) * ca.v_stride_token;
+#pragma unroll 1
             for (int d = 0; d < ca.head_dim; ++d)
-              if ((codes[d] & 0x7F) == 0x7F) nan[d >> 5] |= 1u << (d & 31);
+              if ((codes[d] & 0x7F) == 0x7F) {
+                nan[d >> 5] |= 1u << (d & 31);
+                any_nan = true;
+              }
           }
         }
       }
@@ -819,15 +852,21 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       auto summed = [&](int d, float (&v)[32]) {                       // O's columns [d, d + 32)
         uint32_t r[32] = {};
         if (good) {
-          tmem_ld32(oc + d, r);
+          tmem_ld32(sc + kOColumns + d, r);
           tmem_wait(r);
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = (nan[d / 32] >> e) & 1 ? __uint_as_float(0x7FC00000u) : __uint_as_float(r[e]);
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+        if (any_nan) {
+          const uint32_t bits = nan[d / 32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if ((bits >> e) & 1) v[e] = __uint_as_float(0x7FC00000u);
+        }
       };
       if (walk.n == en.count) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
+#pragma unroll 1
         for (int d = 0; d < DP; d += 32) {
           float v[32];
           summed(d, v);
@@ -845,19 +884,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       float2* ml = reinterpret_cast<float2*>(p.workspace + kPartialBytes);
       int* counters = reinterpret_cast<int*>(p.workspace + kPartialBytes + kMlBytes);
       const int first_at = walk.u0 + kUnitCost, last_at = first_at + en.count - 1;
-      auto cta_of = [&](int y) {                                       // the CTA that holds place y of the line
-        int cta = static_cast<int>(static_cast<int64_t>(y) * ctas / total);
-        while (cta + 1 < ctas && begin_of(cta + 1) <= y) ++cta;
-        while (begin_of(cta) > y) --cta;
-        return cta;
-      };
-      const int cta0 = cta_of(first_at), pieces = cta_of(last_at) - cta0 + 1, mine_at = static_cast<int>(blockIdx.x) - cta0;
+      const int cta0 = stretch_of(total, ctas, first_at), pieces = stretch_of(total, ctas, last_at) - cta0 + 1, mine_at = static_cast<int>(blockIdx.x) - cta0;
       // two slots a CTA: for the unit that began before its stretch, and for one that began in it
       auto slot_of = [&](int piece) { return (2 * (cta0 + piece) + (piece == 0 ? 1 : 0)) * 2 + i; };
       const int r = row & 127;
       auto part = [&](int slot, int d) { return parts + (static_cast<size_t>(slot) * 32 + d / 4) * kTileRows + r; };
       float m_own = m, l_own = l;
       int step = 1;
+#pragma unroll 1
       for (int level = 0;; ++level) {
         const int lead = mine_at / (kJoin * step) * (kJoin * step), count = min(kJoin, (pieces - lead + step - 1) / step);
         const int own = (mine_at - lead) / step;                       // this result's place among them
@@ -869,7 +903,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         const bool unwritten = last;
         if (!unwritten) {
           if (kept) {
-#pragma unroll
+#pragma unroll 1
             for (int d = 0; d < DP; d += 32) {
               float v[32];
               summed(d, v);
@@ -889,47 +923,39 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         if ((tid & 127) == 0) *counter = 0;                            // ready for the next call
         __threadfence();
         const bool finish = lead == 0 && count * step >= pieces;
-        float2 z[kJoin];
-#pragma unroll
-        for (int q = 0; q < kJoin; ++q) {
-          z[q] = make_float2(-INFINITY, 0.f);
-          if (q < count && !(unwritten && q == own)) z[q] = __ldcg(ml + static_cast<size_t>(slot_of(lead + q * step)) * kTileRows + r);
-          if (unwritten && q == own) z[q] = make_float2(m_own, l_own);
-        }
-        float mx = -INFINITY, lx = 0.f, f[kJoin];
-#pragma unroll
-        for (int q = 0; q < kJoin; ++q) mx = fmaxf(mx, z[q].x);
+        auto ml_of = [&](int q) {
+          return unwritten && q == own ? make_float2(m_own, l_own)
+                                       : __ldcg(ml + static_cast<size_t>(slot_of(lead + q * step)) * kTileRows + r);
+        };
+        float mx = -INFINITY, lx = 0.f;
+#pragma unroll 1
+        for (int q = 0; q < count; ++q) mx = fmaxf(mx, ml_of(q).x);
         const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-        for (int q = 0; q < kJoin; ++q) {
-          f[q] = fast_exp2(z[q].x - ref);
-          lx = fmaf(z[q].y, f[q], lx);
+#pragma unroll 1
+        for (int q = 0; q < count; ++q) {
+          const float2 z = ml_of(q);
+          lx = fmaf(z.y, fast_exp2(z.x - ref), lx);
         }
         const float inv = lx == 0.f ? 0.f : 1.f / lx;
 #pragma unroll 1
         for (int d = 0; d < DP; d += 32) {
           float v[32] = {};
-#pragma unroll
-          for (int q = 0; q < kJoin; ++q) {
-            if (q >= count) break;
+#pragma unroll 1
+          for (int q = 0; q < count; ++q) {
+            const float f = fast_exp2(ml_of(q).x - ref);
+            float y[32];
             if (unwritten && q == own) {
-              float y[32];
               summed(d, y);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = fmaf(y[e], f[q], v[e]);
             } else {
-              float4 y[8];
               const float4* from_part = part(slot_of(lead + q * step), d);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = __ldcg(from_part + e * kTileRows);
-#pragma unroll
               for (int e = 0; e < 8; ++e) {
-                v[4 * e] = fmaf(y[e].x, f[q], v[4 * e]);
-                v[4 * e + 1] = fmaf(y[e].y, f[q], v[4 * e + 1]);
-                v[4 * e + 2] = fmaf(y[e].z, f[q], v[4 * e + 2]);
-                v[4 * e + 3] = fmaf(y[e].w, f[q], v[4 * e + 3]);
+                const float4 w = __ldcg(from_part + e * kTileRows);
+                y[4 * e] = w.x, y[4 * e + 1] = w.y, y[4 * e + 2] = w.z, y[4 * e + 3] = w.w;
               }
             }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = fmaf(y[e], f, v[e]);
           }
           if (finish) {
             if (live) put(d, v, inv);
@@ -952,6 +978,13 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
+  }
+  // Nothing of this CTA is in flight when it ends: every copy has been waited
+  // for, unless a wait ran out.
+  if (warp == kLoadWarp && aborted()) {
+#pragma unroll 1
+    for (int k = max(0, s.issued - kStages); k < s.issued; ++k) mbar_wait(&s.code_full[k % kStages], (k / kStages) & 1, a.wait_limit_ns);
+    if (s.issued_units > 0) mbar_wait(&s.q_raw, (s.issued_units - 1) & 1, a.wait_limit_ns);
   }
 }
 
