@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "attention.cuh"
+#include "attention_line.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -143,7 +144,7 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w, uint32_t& seen) {
 
 template <typename T, int DP, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3)
-decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const Launch p) {
+decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ Launch p) {
   extern __shared__ uint8_t raw[];
   uint8_t* const rings = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   float* const scratch = reinterpret_cast<float*>(rings + kWarps * kRing * kSlotBytes);
@@ -158,7 +159,9 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   if (tid == 0) {
     tma_prefetch_map(&k_map);
     tma_prefetch_map(&v_map);
+#pragma unroll 1
     for (int w = 0; w < kWarps; ++w)
+#pragma unroll 1
       for (int i = 0; i < kRing; ++i) mbar_init(&s.full[w][i], 1);
     s.abort_flag = 0;
     fence_mbarrier_init();
@@ -168,6 +171,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 
   // The line: each entry's key tiles, one at least so that someone writes its rows.
   const int64_t most = static_cast<int64_t>(a.table_width) * ca.page_size;
+#pragma unroll 1
   for (int e = tid; e < entries; e += kThreads) {
     const Entry en(p, e, group);
     int n = 0, lo = 0, hi = 0;
@@ -189,6 +193,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   if (warp == 0) {
     const int per = (entries + 31) / 32, from = min(lane * per, entries), to = min(from + per, entries);
     int sum = 0;
+#pragma unroll 1
     for (int e = from; e < to; ++e) sum += s.prefix[e + 1];
     int incl = sum;
 #pragma unroll
@@ -197,6 +202,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       if (lane >= o) incl += v;
     }
     int run = incl - sum;
+#pragma unroll 1
     for (int e = from; e < to; ++e) {
       run += s.prefix[e + 1];
       s.prefix[e + 1] = run;
@@ -206,16 +212,11 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   }
   __syncthreads();
   const int total = s.total, ctas = min(static_cast<int>(gridDim.x), (total + kMinTiles - 1) / kMinTiles);
-  auto begin_of = [&](int cta) { return static_cast<int>(static_cast<int64_t>(total) * cta / ctas); };
   const bool idle = static_cast<int>(blockIdx.x) >= ctas;
-  const int x0 = idle ? 0 : begin_of(blockIdx.x), x1 = idle ? 0 : begin_of(blockIdx.x + 1);
+  const int x0 = idle ? 0 : stretch_begin(total, ctas, blockIdx.x), x1 = idle ? 0 : stretch_begin(total, ctas, blockIdx.x + 1);
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {          // by a warp, which leaves it together
-    if (!mbar_try_wait(smem_u32(bar), parity) && !*static_cast<volatile int*>(&s.abort_flag) &&
-        !mbar_wait(bar, parity, a.wait_limit_ns)) {
-      set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
-      *static_cast<volatile int*>(&s.abort_flag) = 1;
-    }
+    if (!mbar_try_wait(smem_u32(bar), parity)) wait_long(bar, parity, a.wait_limit_ns, a.status, &s.abort_flag);
     __syncwarp();
   };
 
@@ -287,17 +288,21 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     }
     ++issued;
   };
+#pragma unroll 1
   for (int i = 0; i < kRing; ++i) issue();
-  next = find(1);
   fetch(now);
-  later = find(2);
+  if (steps > kBatch) {
+    next = find(1);
+    later = find(2);
+  }
   put_scales(0, now);
-  fetch(next);
+  if (steps > kBatch) fetch(next);
   __syncwarp();
 
   {
     const int g = lane >> 2, c = lane & 3;
     int taken = 0;                         // tiles consumed so far
+#pragma unroll 1
     for (int x = x0; x < x1;) {
       const Place at(s, entries, ca.kv_heads, x);
       const Entry en(p, at.e, group);
@@ -600,16 +605,11 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         // Pieces of this row tile: CTAs [cta0, cta1], joined eight at a time
         // by whoever finishes last among them, then those results likewise.
         const int u0 = x - at.tile, u1 = u0 + at.count;      // its stretch of the line
-        auto cta_of = [&](int y) {                            // the CTA that holds tile y
-          int cta = static_cast<int>(static_cast<int64_t>(y) * ctas / total);
-          while (cta + 1 < ctas && begin_of(cta + 1) <= y) ++cta;
-          while (begin_of(cta) > y) --cta;
-          return cta;
-        };
-        const int cta0 = cta_of(u0), cta1 = cta_of(u1 - 1), pieces = cta1 - cta0 + 1;
+        const int cta0 = stretch_of(total, ctas, u0), cta1 = stretch_of(total, ctas, u1 - 1), pieces = cta1 - cta0 + 1;
         auto slot_of = [&](int piece) { return 2 * (cta0 + piece) + (piece == 0 ? 1 : 0); };
         const int mine = static_cast<int>(blockIdx.x) - cta0;
         int step = 1, from = mine / kJoin * kJoin, count = min(kJoin, pieces - from);
+#pragma unroll 1
         for (int level = 0;; ++level) {
           __threadfence();
           __syncthreads();
@@ -627,8 +627,10 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
           const bool finish = count == pieces || level == 1;
           // thread: 4 columns of rows tid / 32, + 4, ...
           const int col = 4 * lane;
+#pragma unroll 1
           for (int row = warp; row < en.rows; row += kWarps) {
             float Mx = -INFINITY, Lx = 0.f, acc[4] = {};
+#pragma unroll 1
             for (int i = 0; i < count; i += 8) {
               float4 v[8];
               float2 z[8];
@@ -689,6 +691,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   // Nothing of this warp is in flight when it ends: it has waited for every
   // tile, unless a wait ran out.
   if (*static_cast<volatile int*>(&s.abort_flag)) {
+#pragma unroll 1
     for (int k = max(0, issued - kRing); k < issued; ++k) mbar_wait(&s.full[warp][k % kRing], (k / kRing) & 1, a.wait_limit_ns);
   }
 }
@@ -775,6 +778,7 @@ int launch(const AttentionParams& a, cudaStream_t stream) {
   p.row_tiles = static_cast<int>(row_tiles);
   const int per_launch = kMaxEntries / p.row_tiles;
   const int64_t longest = a.max_seq_len > 0 ? a.max_seq_len : 1;
+#pragma unroll 1
   for (p.b0 = 0; p.b0 < a.B; p.b0 += per_launch) {
     p.B = a.B - p.b0 < per_launch ? a.B - p.b0 : per_launch;
     // no more CTAs than key tiles there can be

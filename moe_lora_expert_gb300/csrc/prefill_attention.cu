@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "attention.cuh"
+#include "attention_line.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -231,24 +232,6 @@ __device__ __noinline__ bool walk_next(Walk* at, const Launch& p, int group, int
   __syncwarp(__activemask());
   return more;
 }
-// The line of ``total`` places in ``ctas`` equal stretches: where one begins, and which holds place y.
-__device__ __noinline__ int stretch_begin(int total, int ctas, int cta) {
-  return static_cast<int>(static_cast<int64_t>(total) * cta / ctas);
-}
-__device__ __noinline__ int stretch_of(int total, int ctas, int y) {
-  int cta = static_cast<int>(static_cast<int64_t>(y) * ctas / total);
-  while (cta + 1 < ctas && stretch_begin(total, ctas, cta + 1) <= y) ++cta;
-  while (stretch_begin(total, ctas, cta) > y) --cta;
-  return cta;
-}
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, uint64_t limit_ns, int* status, int* abort_flag) {
-  if (*static_cast<volatile int*>(abort_flag) != 0) return false;
-  if (mbar_wait(bar, parity, limit_ns)) return true;
-  set_status(status, MOE_ERR_DEVICE_TIMEOUT);
-  *static_cast<volatile int*>(abort_flag) = 1;
-  return false;
-}
-
 // ----------------------------------------------------------- shared memory
 struct Control {
   Group group[kInfo][kKeys / 8];
