@@ -520,3 +520,19 @@ def test_refusals_of_the_binding():
         m.moe_rope(q, torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros((4, 64), device="cuda").half())
     with pytest.raises(ValueError):
         m.moe_rope(q.double(), torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros((4, 64), device="cuda"))
+
+
+def test_decoder_layer_example():
+    """Prefill and decode steps of the example's layer agree with one prefill.
+    Both see the same tokens; what differs is the rounding of codes on pages
+    whose scale rose later (subnormals), of bf16 intermediates and the order
+    of sums: a few 2^-8 of a layer whose output is mostly its input."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_layer.py")
+    spec = importlib.util.spec_from_file_location("decoder_layer_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    worst, status = example.main()
+    assert status == [m.MOE_OK, m.MOE_OK]
+    assert worst < 2e-2
