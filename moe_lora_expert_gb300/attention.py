@@ -81,17 +81,18 @@ _ATTEND = struct.Struct("=3Q4q6Q8ifI")
 # imported lazily, as in the rest of the package).
 _torch = _int32_type = _float32_type = None
 _codes: Dict = {}
-_rope_fn = _append_fn = _attend_fn = _raw_stream = None
+_rope_fn = _append_fn = _attend_fn = _raw_stream = _empty_like = None
 
 
 def _bind():
-    global _torch, _int32_type, _float32_type, _rope_fn, _append_fn, _attend_fn, _raw_stream
+    global _torch, _int32_type, _float32_type, _rope_fn, _append_fn, _attend_fn, _raw_stream, _empty_like
     import torch
     from . import lib
     L = lib()
     _codes.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32})
     _int32_type, _float32_type = torch.int32, torch.float32
     _append_fn, _attend_fn, _raw_stream = L.moe_kv_append, L.moe_paged_attention, torch._C._cuda_getCurrentRawStream
+    _empty_like = torch.empty_like
     _rope_fn, _torch = L.moe_rope, torch
 
 
@@ -115,6 +116,15 @@ def _empty(shape, dtype, device, stream):
         return _torch.empty(shape, dtype=dtype, device=device)
 
 
+def _out_like(x, token, head, N, H, D, dtype, stream):
+    """A contiguous output of x's shape (token, head: x's strides) and its pointer."""
+    if stream is None and head == D and token == H * D:
+        y = _empty_like(x)
+    else:
+        y = _empty((N, H, D), dtype, x.device, stream)
+    return y, y.data_ptr()
+
+
 def _int32(t, n, name):
     """Pointer of an int32 [n] tensor."""
     if t.dtype is not _int32_type or not t.is_cuda or not t.is_contiguous():
@@ -131,7 +141,7 @@ def _heads(t, N, H, D, dtype, name):
     if t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{name} must be a {dtype} CUDA tensor")
     st, sh, sd = t.stride()
-    if sd != 1 and D > 1:
+    if sd != 1:
         raise ValueError(f"{name} must be contiguous along the head dimension")
     return t.data_ptr(), st, sh
 
@@ -215,12 +225,12 @@ def moe_rope(q, positions, cos_sin, k=None, interleaved=False, inverse=False, q_
     if _rope_fn is None:
         _bind()
     N, Hq, D = q.shape
-    dtype, device = q.dtype, q.device
+    dtype = q.dtype
     code = _dtype_code(dtype, "q")
     qp, q0, q1 = _heads(q, N, Hq, D, dtype, "q")
     if q_out is None:
-        q_out = _empty((N, Hq, D), dtype, device, stream)
-        op, o0, o1 = q_out.data_ptr(), Hq * D, D
+        q_out, op = _out_like(q, q0, q1, N, Hq, D, dtype, stream)
+        o0, o1 = Hq * D, D
     else:
         op, o0, o1 = _heads(q_out, N, Hq, D, dtype, "q_out")
     kp = kop = k0 = k1 = ko0 = ko1 = Hk = 0
@@ -228,15 +238,15 @@ def moe_rope(q, positions, cos_sin, k=None, interleaved=False, inverse=False, q_
         Hk = k.shape[1]
         kp, k0, k1 = _heads(k, N, Hk, D, dtype, "k")
         if k_out is None:
-            k_out = _empty((N, Hk, D), dtype, device, stream)
-            kop, ko0, ko1 = k_out.data_ptr(), Hk * D, D
+            k_out, kop = _out_like(k, k0, k1, N, Hk, D, dtype, stream)
+            ko0, ko1 = Hk * D, D
         else:
             kop, ko0, ko1 = _heads(k_out, N, Hk, D, dtype, "k_out")
     tp, rows, R = _table(cos_sin)
     args = _ROPE.pack(160, code, qp, op, kp, kop, q0, q1, o0, o1, k0, k1, ko0, ko1,
                       _int32(positions, N, "positions"), tp, 0 if status is None else _int32(status, 4, "status"),
                       N, Hq, Hk, D, R, rows, interleaved, inverse)
-    error = _rope_fn(args, _raw_stream(device.index) if stream is None else stream.cuda_stream)
+    error = _rope_fn(args, _raw_stream(q.device.index) if stream is None else stream.cuda_stream)
     if error:
         _raise(error, "moe_rope")
     return q_out if k is None else (q_out, k_out)
@@ -326,8 +336,8 @@ class PagedKVCache:
             Hq = q.shape[1]
             qp, q0, q1 = _heads(q, N, Hq, D, dtype, "q")
             if q_out is None:
-                q_out = _empty((N, Hq, D), dtype, self.device, stream)
-                op, o0, o1 = q_out.data_ptr(), Hq * D, D
+                q_out, op = _out_like(q, q0, q1, N, Hq, D, dtype, stream)
+                o0, o1 = Hq * D, D
             else:
                 op, o0, o1 = _heads(q_out, N, Hq, D, dtype, "q_out")
         B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
@@ -354,8 +364,8 @@ class PagedKVCache:
         code = _dtype_code(dtype, "q")
         qp, q0, q1 = _heads(q, N, Hq, self.head_dim, dtype, "q")
         if out is None:
-            out = _empty((N, Hq, D), dtype, self.device, stream)
-            op, o0, o1 = out.data_ptr(), Hq * D, D
+            out, op = _out_like(q, q0, q1, N, Hq, D, dtype, stream)
+            o0, o1 = Hq * D, D
         else:
             op, o0, o1 = _heads(out, N, Hq, D, dtype, "out")
         if lse is not None:
