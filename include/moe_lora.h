@@ -586,7 +586,8 @@ int moe_kv_append(const moe_kv_append_args_t* args, moe_stream_t stream);
  * Keys that a row does not see do not touch it, whatever their codes are.
  *
  *   q, out [N, Hq, head_dim] of ``dtype`` (bf16 or f16), 16-byte aligned with
- *     strides that are multiples of 8 elements; Hq a multiple of kv_heads.
+ *     strides that are multiples of 8 elements; Hq a multiple of kv_heads, at
+ *     most 256 times it.
  *   lse [N, Hq] float32 or NULL.
  *   block_table, seq_lens, cu_q: as in moe_kv_append.  Rows from cu_q[B] on
  *     are not written.
@@ -618,8 +619,8 @@ typedef struct {
   float scale;
   uint32_t debug_flags;           /* 0 in normal use; see MOE_DEBUG_STALL_ATTENTION */
 } moe_paged_attention_args_t;
-/* Test-only flag, for calls with few rows (max_q_len * Hq / kv_heads <= 64,
- * else MOE_ERR_UNSUPPORTED): no key tile is loaded, so the waits for them run out after
+/* Test-only flag, for calls with max_q_len * Hq / kv_heads <= 32 (larger ones
+ * may return MOE_ERR_UNSUPPORTED): no key tile is loaded, so the waits for them run out after
  * wait_timeout_ms; the call then reports MOE_ERR_DEVICE_TIMEOUT and its output
  * is garbage, but the workspace is ready for the next call. */
 #define MOE_DEBUG_STALL_ATTENTION 4u

@@ -2,8 +2,8 @@
 // tokens a draft proposes.
 //
 // Each key head's rows (new tokens x query heads of its group) are cut into
-// tiles of 16 and the keys into tiles of 64.  All (row tile, key tile) pairs
-// of the call form one line, which the CTAs of the grid share in equal
+// tiles of 8 or 16 and the keys into tiles of 64.  All (row tile, key tile)
+// pairs of the call form one line, which the CTAs of the grid share in equal
 // stretches whatever the sequences' lengths are; a row tile whose keys lie in
 // several stretches is joined by the CTA that finishes it last.
 //
@@ -13,13 +13,26 @@
 // so w_j is what multiplies the codes: it is at most 2^8 in float16 whatever
 // the pages' scales are, and both sums stay in float32.  Codes enter the
 // tensor cores as float16, which holds each exactly; so does q (bf16 rows are
-// first scaled by a power of two), and the scores are exact products.
+// first scaled by a power of two), and the scores are exact products.  Only
+// the weights are rounded, to float16 (2^-12 at most of each): the output has
+// 8 or 11 bits.
 //
-// What bounds it.  One pass over the cache's bytes.  The tensor work of 16
-// rows is far below even mma.sync's rate (a 64-key tile needs 64 m16n8k16 per
-// 16 KB), so fragments go straight from shared memory to registers: a
-// tcgen05 tile would be 128 keys high and need its codes converted and written
-// back to shared memory first.
+// What bounds it: one pass over the cache's bytes.  64 sequences of up to
+// 32768 keys (8 query heads of 128 on each of 4 key heads) take 211 us, 6.4
+// TB/s, 94% of the copy rate; one token on 262140 keys 57 us (40 at the copy
+// rate: the first tiles come after 8 us and the join takes 5).  At smaller
+// sizes it is the chain of latencies from the lengths to the block table, the
+// first tile, and the join: one token on 1022 keys 11 us.
+//
+// Why mma.sync.  The products of 8 rows are far below even its rate, and its
+// fragments go from shared memory to registers: a warp reads each code once,
+// converts it (two codes an instruction) and multiplies.  A tcgen05 tile is
+// 128 keys high and its codes would have to be converted and written back to
+// shared memory first, or q and the weights split into three e4m3 parts each.
+// The keys are the rows of the products and the query rows their columns, so
+// that 8 rows fill an m16n8k16 (as the rows of the products they fill half of
+// one: 291 us instead of 217 on the 64 sequences, with twice the products,
+// weights and sums a key).
 #include <cuda.h>
 
 #include <type_traits>
@@ -36,13 +49,15 @@ constexpr int kKeys = 64;                 // keys of a tile
 constexpr int kMaxRows = 16;              // most rows of a row tile: 8 NT
 constexpr int kWarps = 4;                 // 16 keys of a tile each
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRing = 3;                  // tiles in a warp's ring
+constexpr int kRing = 3;                  // tiles in a warp's ring (2 and 4 are no faster)
 constexpr int kBatch = 16;                // tiles whose pages are looked up at once
-constexpr int kCtasPerSm = 3;
+// 8 rows: 3 CTAs of 168 registers (2: 262 instead of 217 us on 64 sequences of up to 32768 keys); 16 rows: 2 of 250 (3 of 168 spill:
+// 82 instead of 50 us on 8 sequences of 16384 keys).
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 constexpr int kMaxCtas = 640;
 constexpr int kMaxEntries = 512;          // (sequence, row tile) pairs of one launch
-constexpr int kMinTiles = 2;              // a CTA's stretch of the line is at least so long (but for the last tiles)
-constexpr int kJoin = 16;                 // pieces that are joined at a time
+constexpr int kMinTiles = 2;              // a CTA's stretch of the line is at least so long; one token on 1022 keys: 1 13.0, 2 11.3, 4 12.7 us
+constexpr int kJoin = 16;                 // pieces that are joined at a time; 16 sequences of up to 4096 keys: 8 27.6, 16 24.5 us
 constexpr int kPitch = 128;               // bytes of a key in shared memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -143,7 +158,7 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w, uint32_t& seen) {
 }
 
 template <typename T, int DP, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
 decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ Launch p) {
   extern __shared__ uint8_t raw[];
   uint8_t* const rings = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -773,7 +788,8 @@ int launch(const AttentionParams& a, cudaStream_t stream) {
   if (sms <= 0) return MOE_ERR_CUDA;
   const int group = a.Hq / a.cache.kv_heads;
   const int64_t row_tiles = (static_cast<int64_t>(a.max_q_len) * group + 8 * NT - 1) / (8 * NT);
-  const int64_t line = (static_cast<int64_t>(a.table_width) * a.cache.page_size / kKeys + 1) * kMaxEntries * a.cache.kv_heads;
+  const int64_t entries = row_tiles * a.B < kMaxEntries ? row_tiles * a.B : kMaxEntries;
+  const int64_t line = (static_cast<int64_t>(a.table_width) * a.cache.page_size / kKeys + 1) * entries * a.cache.kv_heads;
   if (row_tiles > kMaxEntries || line > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   p.row_tiles = static_cast<int>(row_tiles);
   const int per_launch = kMaxEntries / p.row_tiles;
@@ -783,7 +799,7 @@ int launch(const AttentionParams& a, cudaStream_t stream) {
     p.B = a.B - p.b0 < per_launch ? a.B - p.b0 : per_launch;
     // no more CTAs than key tiles there can be
     const int64_t tiles = (longest + kKeys - 1) / kKeys * p.B * p.row_tiles * a.cache.kv_heads;
-    int64_t grid = static_cast<int64_t>(sms) * (NT == 1 ? kCtasPerSm : 3);
+    int64_t grid = static_cast<int64_t>(sms) * ctas_per_sm(NT);
     if (grid > kMaxCtas) grid = kMaxCtas;
     if (grid > tiles) grid = tiles;
     if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), bytes, stream, k_map, v_map, p) != cudaSuccess)

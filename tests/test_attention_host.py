@@ -155,7 +155,8 @@ def test_append_refusals(lib, cache_over, over, status):
     ({}, {"out": None}, m.MOE_ERR_NULL), ({}, {"q": FAKE + 8}, m.MOE_ERR_ALIGN),
     ({}, {"q_stride_head": 132}, m.MOE_ERR_ALIGN), ({}, {"workspace": None}, m.MOE_ERR_WORKSPACE),
     ({}, {"workspace": FAKE + 64}, m.MOE_ERR_WORKSPACE), ({}, {"workspace_bytes": 16}, m.MOE_ERR_WORKSPACE),
-    ({}, {"debug_flags": 8}, m.MOE_ERR_UNSUPPORTED), ({}, {"N": 0, "B": 0}, m.MOE_OK),
+    ({}, {"debug_flags": 8}, m.MOE_ERR_UNSUPPORTED),
+    ({}, {"Hq": 4 * 257}, m.MOE_ERR_UNSUPPORTED), ({}, {"N": 0, "B": 0}, m.MOE_OK),
 ])
 def test_attention_refusals(lib, cache_over, over, status):
     assert lib.moe_paged_attention(bytes(attend_args(lib, cache_over, **over)), None) == status

@@ -471,6 +471,58 @@ def test_attention_repeats_bit_for_bit_and_on_streams():
     assert all(torch.equal(o, first) for o in outs)
 
 
+@pytest.mark.parametrize("new,lens,Hq,Hkv,P,D,window", [([70], [6001], 2, 1, 16, 64, 0), ([40, 3], [3000, 2500], 8, 2, 64, 128, 0),
+                                                        ([129], [4100], 4, 2, 24, 128, 1500), ([1], [20000], 2, 1, 32, 128, 0),
+                                                        ([3], [9000], 6, 1, 128, 96, 0)])
+def test_attention_long_contexts_are_joined(new, lens, Hq, Hkv, P, D, window):
+    """Rows whose keys lie in the stretches of many CTAs; and the same bits every time."""
+    torch = torch_mod()
+    rng = np.random.default_rng(18)
+    batch = Batch(rng, new, lens, Hkv, P, D, std=0.5)
+    q = rounded(rng, (sum(new), Hq, D), "bfloat16")
+    out, lse = check_attention(batch, q, "bfloat16", window=window, decode=new == [1])
+    for _ in range(3):
+        again = batch.cache.attend(tensor(q, "bfloat16"), **batch.dev, cu_q=None if new == [1] else batch.cu_dev, max_q_len=max(new),
+                                   window=window, return_lse=True)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+def test_attention_and_append_past_32_bits():
+    """Pages more than 2^32 bytes into the cache: the bits are those of a small
+    cache with the same codes."""
+    torch = torch_mod()
+    Hkv, P, D, pages = 8, 128, 128, 33000
+    assert Hkv * P * D * (pages - 5) > 2 ** 32
+    big = [torch.empty((pages, Hkv, P, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones((pages, Hkv), device="cuda") for _ in range(2)]
+    rng = np.random.default_rng(19)
+    for new, lens in (([1, 1], [300, 150]), ([90, 5], [300, 150])):
+        small = Batch(rng, new, lens, Hkv, P, D, std=0.5)
+        cache = m.PagedKVCache(*big, *scales)
+        shift = pages - small.pages
+        for b, c in zip(big, (small.cache.k, small.cache.v)):
+            b[shift:] = c
+        for s, c in zip(scales, (small.cache.k_scale, small.cache.v_scale)):
+            s[shift:] = c
+        table = torch.where(small.dev["block_table"] >= 0, small.dev["block_table"] + shift, small.dev["block_table"])
+        N = sum(new)
+        q, k, v = (tensor(rounded(rng, (N, h, D), "bfloat16"), "bfloat16") for h in (16, Hkv, Hkv))
+        for c, t in ((small.cache, small.dev["block_table"]), (cache, table)):
+            c.append(k, v, t, small.dev["seq_lens"], cu_q=small.cu_dev, max_q_len=max(new))
+        got = cache.attend(q, table, small.dev["seq_lens"], cu_q=small.cu_dev, max_q_len=max(new))
+        want = small.cache.attend(q, small.dev["block_table"], small.dev["seq_lens"], cu_q=small.cu_dev, max_q_len=max(new))
+        assert torch.equal(got, want) and torch.isfinite(got.float()).all()
+        assert torch.equal(big[0][shift:], small.cache.k) and torch.equal(scales[1][shift:], small.cache.v_scale)
+        assert cache.device_status() == m.MOE_OK
+
+
+@pytest.mark.parametrize("Hq,Hkv,new,lens", [(150, 1, [2], [100]), (256, 1, [1, 3], [40, 33]), (200, 1, [30], [64])])
+def test_attention_many_heads_on_one_key_head(Hq, Hkv, new, lens):
+    rng = np.random.default_rng(20)
+    batch = Batch(rng, new, lens, Hkv, 16, 32, std=0.5)
+    check_attention(batch, rounded(rng, (sum(new), Hq, 32), "float16"), "float16")
+
+
 def test_append_and_attention_in_a_graph():
     """A captured decode step replays with new lengths and tokens."""
     torch = torch_mod()
