@@ -619,8 +619,7 @@ typedef struct {
   float scale;
   uint32_t debug_flags;           /* 0 in normal use; see MOE_DEBUG_STALL_ATTENTION */
 } moe_paged_attention_args_t;
-/* Test-only flag, for calls with max_q_len * Hq / kv_heads <= 32 (larger ones
- * may return MOE_ERR_UNSUPPORTED): no key tile is loaded, so the waits for them run out after
+/* Test-only flag: no key tile is loaded, so the waits for them run out after
  * wait_timeout_ms; the call then reports MOE_ERR_DEVICE_TIMEOUT and its output
  * is garbage, but the workspace is ready for the next call. */
 #define MOE_DEBUG_STALL_ATTENTION 4u

@@ -178,7 +178,7 @@ int moe_paged_attention(const moe_paged_attention_args_t* a, moe_stream_t stream
   const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
   const int64_t rows = static_cast<int64_t>(p.max_q_len) * (a->Hq / c.kv_heads);
   if (few_rows(rows, static_cast<int64_t>(a->B) * c.kv_heads)) return moe::launch_decode_attention(p, a->dtype, on);
-  return p.debug_flags != 0 ? MOE_ERR_UNSUPPORTED : moe::launch_prefill_attention(p, a->dtype, on);
+  return moe::launch_prefill_attention(p, a->dtype, on);
 }
 
 }  // extern "C"

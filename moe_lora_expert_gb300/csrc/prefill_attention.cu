@@ -80,6 +80,15 @@ __device__ __forceinline__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_
 // to low words instead of building descriptors.
 __device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t leading) { return (saddr >> 4) | (leading >> 4) << 16; }
 constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+// True in one lane of a converged warp.  The compiler knows that of this
+// instruction but not of a comparison of lane numbers: behind that, each
+// product is issued in a loop over the lanes that might be there (123 instead
+// of 103 us on 2 x 2048 tokens).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t elected;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(elected));
+  return elected != 0;
+}
 __device__ __forceinline__ void mma_ss_f16(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
@@ -290,13 +299,13 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) mbar_init(&s.p_full[i][h], kTileRows);
+      for (int h = 0; h < 2; ++h) mbar_init(&s.p_full[i][h], kTileRows / 32);
       mbar_init(&s.first_done[i], 1);
       mbar_init(&s.o_full[i], 1);
     }
     mbar_init(&s.q_raw, 1);
     mbar_init(&s.q_full, 4);
-    mbar_init(&s.q_empty, 1 + 2 * kTileRows);    // the last scores, and every row's thread has its exponent
+    mbar_init(&s.q_empty, 1 + 2 * kTileRows / 32);   // the last scores, and every row's thread has its exponent
     mbar_init(&s.drained, 1);
     s.abort_flag = 0;
     s.nan_seen = 0;
@@ -408,7 +417,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       return f;
     };
     int issued = 0, units = 0;
-    bool stop = false;
+    bool stop = (a.debug_flags & MOE_DEBUG_STALL_ATTENTION) != 0;      // a failure for the tests: no tile arrives
 #pragma unroll 1
     for (bool more = next(true); more && !stop; more = next(false)) {
       if (en.position(en.rows - 1, group) >= static_cast<int64_t>(a.table_width) * ca.page_size) set_status(a.status, MOE_ERR_BAD_PAGE);
@@ -461,7 +470,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kScores = idesc_f16(kTileRows, kKeys, false), kValues = idesc_f16(kTileRows, DP, true);
       constexpr uint32_t kSlot = L::kSlotBytes >> 4;
       const uint32_t q_low = desc_low(smem_u32(smem + L::kQ), 16), k_low = desc_low(smem_u32(smem + L::kRing), 16),
@@ -660,9 +669,12 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       good = good && wait(&s.q_full, units & 1);
       const float row_scale = kBf16 ? __uint_as_float(static_cast<uint32_t>(127 + s.q_exponent[row]) << 23) : 1.f;
       // Only now may the next unit's queries come: a unit of one tile has its
-      // last scores before its rows' threads have begun it, and two of them
+      // last scores before its rows' warps have begun it, and two of them
       // would carry q_full past the phase that they wait for.
-      mbar_arrive(&s.q_empty);
+      // (After a timeout nothing arrives any more: a phase must not get more
+      // arrivals than it lacks.)
+      __syncwarp();
+      if (good && lane == 0) mbar_arrive(&s.q_empty);
       if (kTileRows * i >= en.rows) {
         t += walk.n;
         continue;
@@ -778,7 +790,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           weights(rb, 1);
           tmem_wait_st();
           tc_fence_before_sync();
-          mbar_arrive(&s.p_full[i][h]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.p_full[i][h]);
         }
       }
 

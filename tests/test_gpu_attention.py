@@ -430,12 +430,12 @@ def test_attention_pages_before_the_window_may_be_gone(new, P):
     assert batch.cache.device_status() == m.MOE_OK
 
 
-@pytest.mark.parametrize("new", [[1, 1], [8, 5]])
+@pytest.mark.parametrize("new", [[1, 1], [8, 5], [300, 233]])
 def test_attention_timeout_is_reported(new):
     """With no key tile arriving the waits run out, the status says so, and
     the next call on the same workspace is right."""
     rng = np.random.default_rng(16)
-    batch = Batch(rng, new, [300, 100], 2, 16, 128, std=0.5)
+    batch = Batch(rng, new, [300, 250], 2, 16, 128, std=0.5)
     q = rounded(rng, (sum(new), 4, 128), "bfloat16")
     decode = max(new) == 1
     batch.cache.attend(tensor(q, "bfloat16"), **batch.dev, cu_q=None if decode else batch.cu_dev, max_q_len=max(new),
