@@ -9,6 +9,15 @@
 // the scale of a page that holds others, their codes are multiplied by
 // s_old / s_new, which moves their exponents and rounds only what becomes
 // subnormal.  With an arbitrary scale every raise would round every code again.
+//
+// A CTA takes the new tokens of one (sequence, page of it, head, K or V), so
+// that a maximum is one CTA's and nothing depends on the order of atomics; the
+// CTAs after those rotate q.  What bounds it: bytes (read k, v and q once,
+// write codes and q) once there are enough; 4096 tokens of 32 and 4 heads of
+// 128 take 18 us, 82 MB at 4.5 TB/s, 66% of the copy rate (64 registers a
+// thread: with 126, which held the rotated stretches, 20.5 us; 4 stretches held
+// instead of 2 the same there, 11.3 instead of 10.3 us on ragged chunks).  64
+// single tokens take 5.8 us: the chain from lengths to table to scale.
 #include "attention.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -18,7 +27,7 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 constexpr int kMinCtas = 2;           // of kMaxThreads an SM: 64 registers a thread
-constexpr int kManyItems = 1 << 17;   // stretches of q from which on a thread takes two heads
+constexpr int kManyItems = 1 << 17;   // stretches of q from which on a thread takes two heads (4096 tokens: one 21.2, two 18.0 us)
 constexpr int kHeld = 2;  // stretches a thread keeps in registers between the maximum and the codes
 
 // Smallest 2^k (k >= -42) with amax <= 448 * 2^k; amax >= 0, not NaN.

@@ -5,6 +5,12 @@
 // cos and sin from a float32 table that was made in float64 (an angle p f_i
 // in float32 is off by p f_i 2^-24, a tenth of a radian at a million).  The
 // gradient is the transposed rotation: the same with -sin.
+//
+// What bounds it: bytes, each read and written once.  A thread takes one
+// stretch of one head (two 16-byte loads): 4096 tokens of 36 heads of 128 take
+// 14.6 us cold, 78 MB at 5.3 TB/s, 78% of the copy rate.  Two, four heads a
+// thread to share its angles 15.1, 20.8 us: they come from the first-level
+// cache anyway, and fewer threads keep fewer loads on their way.
 #include "attention.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
