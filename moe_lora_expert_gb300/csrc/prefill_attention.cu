@@ -18,10 +18,12 @@
 //
 // All units' key tiles form one line that the CTAs cut into equal stretches,
 // so ragged batches and long contexts fill the GPU alike.  A unit whose tiles
-// lie in several stretches is joined by the CTA that finishes it last.
+// lie in several stretches is joined by the CTA that finishes it last.  A cut
+// costs a CTA that writes its part or joins it about four key tiles' time, so
+// where whole units can be dealt out nearly as evenly they are.
 //
-// What bounds it.  2 x 2048 tokens of 32 heads of 128 on 4 key heads take 102
-// us, 671 TFLOP/s of what the causal mask leaves, 36% of the measured bf16
+// What bounds it.  2 x 2048 tokens of 32 heads of 128 on 4 key heads take 90
+// us, 765 TFLOP/s of what the causal mask leaves, 41% of the measured bf16
 // rate (37 us).  The products of a pair of row tiles and a key tile take 2.05
 // thousand cycles, 2.8 with the gaps between groups of them; a softmax takes
 // about 3 (each row tile's four warps share their schedulers with the other's
@@ -51,9 +53,11 @@ constexpr int kThreads = 448;
 constexpr int kSlots = 4;                  // converted tiles: K0, V0, K1, V1, ...
 constexpr int kStages = 2;                 // tiles of codes, in the same order
 constexpr int kInfo = 4;                   // key tiles whose scales are held (see the copies)
-constexpr int kUnitCost = 2;               // key tiles' worth of time that a unit takes besides its tiles; 2 x 2048 tokens: 1 122, 2 103, 3 103, 4 105 us
+constexpr int kUnitCost = 2;               // key tiles' worth of time that a unit takes besides its tiles; 2 x 2048 tokens, cut from the line: 1 122, 2 103, 3 103, 4 105 us
 constexpr int kMinTiles = 4;               // least length of a CTA's stretch (a join costs about as much as four tiles)
 constexpr int kMaxCtas = 160;
+constexpr int kMaxUnits = 16;              // whole units a CTA may be given (see the kernel)
+constexpr int kJoinCost = 8;               // key tiles' worth of time that cutting the line may cost a CTA: part of a unit written, another joined
 constexpr int kJoin = 8;                   // pieces that are joined at a time
 constexpr int kConvertWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -207,12 +211,23 @@ struct Entry {
 };
 
 // A CTA's stretch of the line, unit by unit; every warp walks it by itself.
-// On the line a unit is kUnitCost places and then a place a key tile.
+// On the line a unit is kUnitCost places and then a place a key tile.  Where
+// ``whole`` is given the CTA has those units instead, x to x1.
 struct Walk {
   Entry en;
   int e, head, tile, x, x1, n, u0, span;   // this piece: tiles [tile, tile + n) of the unit that begins at u0
-  __device__ __forceinline__ bool next(const Launch& p, int group, bool first, int first_entry, int first_prefix) {
+  __device__ __forceinline__ bool next(const Launch& p, int group, const int* whole, bool first, int first_entry, int first_prefix) {
     const int heads = p.a.cache.kv_heads;
+    if (whole != nullptr) {
+      if (x == x1) return false;
+      const int unit = whole[x++];
+      e = unit / heads;
+      head = unit - e * heads;
+      en.load(p, e, group);
+      tile = 0;
+      n = en.count;
+      return true;
+    }
     int v = 0;
     if (first) {
       e = first_entry;
@@ -245,9 +260,9 @@ struct Walk {
 
 // The kernel's roles share one instruction cache: what is called once a unit,
 // or to wait, is not inlined into each of them.
-__device__ __noinline__ bool walk_next(Walk* at, const Launch& p, int group, int first_entry, int first_prefix) {
+__device__ __noinline__ bool walk_next(Walk* at, const Launch& p, int group, const int* whole, int first_entry, int first_prefix) {
   Walk w = *at;
-  const bool more = w.next(p, group, first_entry >= 0, first_entry, first_prefix);
+  const bool more = w.next(p, group, whole, first_entry >= 0, first_entry, first_prefix);
   __syncwarp(__activemask());
   *at = w;
   __syncwarp(__activemask());
@@ -260,9 +275,10 @@ struct Control {
   uint64_t info_full[kInfo], q_raw, q_full, q_empty, s_full[2], p_full[2][2], first_done[2], o_full[2], drained;
   int8_t q_exponent[kCtaRows];             // of the power of two taken out of each row
   int sums[kThreads / 32];
+  int units[kMaxUnits];                    // this CTA's, if it has whole ones
   Walk walk[kThreads / 32];                // each warp's own, here and not in its registers
   uint32_t tmem;
-  int abort_flag, nan_seen, first_entry, first_prefix, last[2], issued, issued_units;
+  int abort_flag, nan_seen, first_entry, first_prefix, given, last[2], issued, issued_units;
 };
 
 template <int DP>
@@ -352,9 +368,57 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   }
   const int total = all_tiles * ca.kv_heads;
   const int ctas = min(static_cast<int>(gridDim.x), max(1, total / kMinTiles));
-  if (total == 0 || static_cast<int>(blockIdx.x) >= ctas) return;
+  if (total == 0) return;
+
+  // Whole units, longest first and to the CTAs forwards and backwards in turn,
+  // need no joins.  They are taken where the CTA with the most to do then has
+  // no more than a stretch of the line and its joins.  Every CTA finds the
+  // same: each thread places one entry and adds up one CTA's share.
+  // 512 units of 2 x 2048 tokens: 92 us, cut from the line 104; 220 units of
+  // four ragged chunks: 149 and 120.
+  bool whole = false;
+  if (per == 1) {
+    int* costs = reinterpret_cast<int*>(smem + L::kRing);    // not in use yet
+    int* sorted = costs + kThreads;
+    costs[tid] = mine;
+    const int units = __syncthreads_count(mine > 0) * ca.kv_heads, across = gridDim.x;
+    if (units <= kMaxUnits * across) {
+      int place = 0;
+#pragma unroll 1
+      for (int e = 0; e < entries; e += 4) {
+        const int4 c = *reinterpret_cast<const int4*>(costs + e);
+        place += (c.x > mine || (c.x == mine && e < tid)) + (c.y > mine || (c.y == mine && e + 1 < tid)) +
+                 (c.z > mine || (c.z == mine && e + 2 < tid)) + (c.w > mine || (c.w == mine && e + 3 < tid));
+      }
+      if (mine > 0) sorted[place] = tid;
+      __syncthreads();
+      int share = 0, given = 0;
+      if (tid < across) {
+#pragma unroll 1
+        for (int i = 0; i * across < units; ++i) {
+          const int at = i * across + (i % 2 == 0 ? tid : across - 1 - tid);
+          if (at >= units) break;
+          const int e = sorted[at / ca.kv_heads];
+          share += costs[e];
+          if (tid == static_cast<int>(blockIdx.x)) {
+            s.units[i] = e * ca.kv_heads + at % ca.kv_heads;
+            given = i + 1;
+          }
+        }
+      }
+      const int most = __reduce_max_sync(0xffffffffu, share);
+      if (lane == 0) s.sums[warp] = most;
+      if (tid == static_cast<int>(blockIdx.x)) s.given = given;
+      __syncthreads();
+      int longest = 0;
+#pragma unroll 1
+      for (int w = 0; w < kThreads / 32; ++w) longest = max(longest, s.sums[w]);
+      whole = longest <= (total + ctas - 1) / ctas + kJoinCost;
+    }
+  }
+  if (whole ? s.given == 0 : static_cast<int>(blockIdx.x) >= ctas) return;
   const int x0 = stretch_begin(total, ctas, blockIdx.x);
-  if (x0 < incl * ca.kv_heads && x0 >= (incl - mine) * ca.kv_heads) {
+  if (!whole && x0 < incl * ca.kv_heads && x0 >= (incl - mine) * ca.kv_heads) {
     int before = incl - mine;
 #pragma unroll 1
     for (int e = from; e < to; ++e) {
@@ -394,11 +458,11 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   const Entry& en = walk.en;
   auto next = [&](bool first) {                              // by the lanes that call it, with the same values
     if (first) {
-      walk.x = x0;
-      walk.x1 = stretch_begin(total, ctas, blockIdx.x + 1);
+      walk.x = whole ? 0 : x0;
+      walk.x1 = whole ? s.given : stretch_begin(total, ctas, blockIdx.x + 1);
       __syncwarp(__activemask());
     }
-    return walk_next(&walk, p, group, first ? s.first_entry : -1, s.first_prefix);
+    return walk_next(&walk, p, group, whole ? s.units : nullptr, first ? s.first_entry : -1, s.first_prefix);
   };
 
   if (warp == kLoadWarp) {

@@ -487,6 +487,24 @@ def test_attention_long_contexts_are_joined(new, lens, Hq, Hkv, P, D, window):
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+@pytest.mark.parametrize("new,lens,Hq,Hkv,P,D,window", [
+    ([700, 1, 333, 0, 64], [700, 90, 333, 5, 400], 64, 8, 64, 64, 0),   # more units than CTAs, whole: some CTAs get two, some one
+    ([1500, 40], [1500, 40], 32, 2, 32, 128, 0),                        # twice as many units as CTAs, of 1 to 12 tiles
+    ([300, 300], [300, 3500], 64, 8, 48, 64, 0),                        # long and short units, cut from the line
+    ([100] * 40, [100 + 7 * i for i in range(40)], 8, 2, 16, 128, 96),  # units of one size in a window
+    ([2] * 449 + [40], [9] * 449 + [41], 2, 1, 16, 64, 0),              # more entries than threads
+])
+def test_attention_many_units(new, lens, Hq, Hkv, P, D, window):
+    """More rows than the CTAs take at once, dealt out whole or cut; the same bits every time."""
+    torch = torch_mod()
+    rng = np.random.default_rng(19)
+    batch = Batch(rng, new, lens, Hkv, P, D, std=0.5)
+    q = rounded(rng, (sum(new), Hq, D), "bfloat16")
+    out, lse = check_attention(batch, q, "bfloat16", window=window)
+    again = batch.cache.attend(tensor(q, "bfloat16"), **batch.dev, cu_q=batch.cu_dev, max_q_len=max(new), window=window, return_lse=True)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 def test_attention_and_append_past_32_bits():
     """Pages more than 2^32 bytes into the cache: the bits are those of a small
     cache with the same codes."""
