@@ -29,7 +29,7 @@
 // about 3 (each row tile's four warps share their schedulers with the other's
 // and the converter's: 0.6 thousand instructions a warp, waits on TMEM and
 // on each other), and a row tile's products and softmax follow one another.
-// For heads of 64 the softmax is the same for half the products: 117 us for
+// For heads of 64 the softmax is the same for half the products: 115 us for
 // ragged chunks on up to 8191 keys, 25%.  Scores of 64 keys in two buffers a
 // row tile took the wait out but cost more than it (an M = 128, N = 64
 // product takes the time of N = 128): 148 against 130 us then.
@@ -755,6 +755,13 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         t += walk.n;
         continue;
       }
+      // the CTAs that have parts of the unit, here and not where the result waits
+      int cta0 = 0, pieces = 1;
+      if (walk.n != en.count) {
+        const int first_at = walk.u0 + kUnitCost;
+        cta0 = stretch_of(total, ctas, first_at);
+        pieces = stretch_of(total, ctas, first_at + en.count - 1) - cta0 + 1;
+      }
       const int pos = row < en.rows ? en.position(row, group) : -1;
       // keys below pos_lo are seen by every row of the tile, as far as the window goes
       const int pos_lo = en.position(kTileRows * i, group);
@@ -955,8 +962,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       float4* parts = reinterpret_cast<float4*>(p.workspace);
       float2* ml = reinterpret_cast<float2*>(p.workspace + kPartialBytes);
       int* counters = reinterpret_cast<int*>(p.workspace + kPartialBytes + kMlBytes);
-      const int first_at = walk.u0 + kUnitCost, last_at = first_at + en.count - 1;
-      const int cta0 = stretch_of(total, ctas, first_at), pieces = stretch_of(total, ctas, last_at) - cta0 + 1, mine_at = static_cast<int>(blockIdx.x) - cta0;
+      const int mine_at = static_cast<int>(blockIdx.x) - cta0;
       // two slots a CTA: for the unit that began before its stretch, and for one that began in it
       auto slot_of = [&](int piece) { return (2 * (cta0 + piece) + (piece == 0 ? 1 : 0)) * 2 + i; };
       const int r = row & 127;
@@ -999,14 +1005,18 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           return unwritten && q == own ? make_float2(m_own, l_own)
                                        : __ldcg(ml + static_cast<size_t>(slot_of(lead + q * step)) * kTileRows + r);
         };
+        float2 parts_ml[kJoin];                                        // read together
+#pragma unroll
+        for (int q = 0; q < kJoin; ++q) parts_ml[q] = q < count ? ml_of(q) : make_float2(-INFINITY, 0.f);
         float mx = -INFINITY, lx = 0.f;
-#pragma unroll 1
-        for (int q = 0; q < count; ++q) mx = fmaxf(mx, ml_of(q).x);
+#pragma unroll
+        for (int q = 0; q < kJoin; ++q) mx = fmaxf(mx, parts_ml[q].x);
         const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 1
-        for (int q = 0; q < count; ++q) {
-          const float2 z = ml_of(q);
-          lx = fmaf(z.y, fast_exp2(z.x - ref), lx);
+        float factor[kJoin];
+#pragma unroll
+        for (int q = 0; q < kJoin; ++q) {
+          factor[q] = fast_exp2(parts_ml[q].x - ref);
+          lx = fmaf(parts_ml[q].y, factor[q], lx);
         }
         const float inv = lx == 0.f ? 0.f : 1.f / lx;
 #pragma unroll 1
@@ -1014,7 +1024,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           float v[32] = {};
 #pragma unroll 1
           for (int q = 0; q < count; ++q) {
-            const float f = fast_exp2(ml_of(q).x - ref);
+            const float f = factor[q];
             float y[32];
             if (unwritten && q == own) {
               summed(d, y);
