@@ -14,7 +14,7 @@
 // that a maximum is one CTA's and nothing depends on the order of atomics; the
 // CTAs after those rotate q.  What bounds it: bytes (read k, v and q once,
 // write codes and q) once there are enough; 4096 tokens of 32 and 4 heads of
-// 128 take 18 us, 82 MB at 4.5 TB/s, 66% of the copy rate (64 registers a
+// 128 take 18.7 us, 82 MB at 4.4 TB/s, 65% of the copy rate (64 registers a
 // thread: with 126, which held the rotated stretches, 20.5 us; 4 stretches held
 // instead of 2 the same there, 11.3 instead of 10.3 us on ragged chunks).  64
 // single tokens take 5.8 us: the chain from lengths to table to scale.
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
       if (pos >= 0 && pos < p.num_positions) {
         float cs[V], sn[V];
         load_cos_sin<V>(p.cos_sin + static_cast<int64_t>(pos) * p.R, c, p.R, cs, sn);
-        rotate<V>(a, bb, cs, sn, p.interleaved);
+        rotate<V, true>(a, bb, cs, sn, p.interleaved);
       } else {
         set_status(p.status, MOE_ERR_BAD_POSITION);
       }

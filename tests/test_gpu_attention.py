@@ -260,6 +260,28 @@ def test_append_given_positions_and_token_by_token():
         assert (np.abs(va - vb)[both] <= 2.0 ** -9).all()
 
 
+@pytest.mark.parametrize("D,R,inter", [(128, 128, False), (80, 48, True), (64, 64, True), (48, 8, False)])
+def test_append_codes_of_unfused_products(D, R, inter):
+    """Keys get the codes that float32 with every product rounded gives, ties included."""
+    torch = torch_mod()
+    N, H, P = 4096, 4, 64
+    gen = torch.Generator(device="cuda").manual_seed(20)
+    k, v = (torch.randn((N, H, D), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    table = m.rope_table(N, R, device="cuda")
+    cache = m.PagedKVCache.create(N // P, H, P, D)
+    pages = torch.randperm(N // P, generator=gen, device="cuda").to(torch.int32)
+    cache.append(k, v, pages[None], tensor(np.array([N], np.int32), "int32"), cu_q=tensor(np.array([0, N], np.int32), "int32"),
+                 max_q_len=N, cos_sin=table, interleaved=inter)
+    cos, sin = table[:, None, :].split(R // 2, dim=-1)
+    x = k.float()
+    a, b = (x[..., 0:R:2], x[..., 1:R:2]) if inter else (x[..., :R // 2], x[..., R // 2:R])
+    u, w = a * cos - b * sin, b * cos + a * sin
+    x[..., :R] = torch.stack([u, w], dim=-1).flatten(-2) if inter else torch.cat([u, w], dim=-1)
+    for got, scale, want in ((cache.k, cache.k_scale, x), (cache.v, cache.v_scale, v.float())):
+        want = want.view(N // P, P, H, D).transpose(1, 2) / scale[pages.long()][:, :, None, None]
+        assert torch.equal(got[pages.long()], want.to(torch.float8_e4m3fn).view(torch.uint8))
+
+
 def rounded_like(x):
     torch = torch_mod()
     return torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).to(torch.float64).numpy()
