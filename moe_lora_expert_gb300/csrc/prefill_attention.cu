@@ -260,12 +260,17 @@ struct Walk {
 
 // The kernel's roles share one instruction cache: what is called once a unit,
 // or to wait, is not inlined into each of them.
-__device__ __noinline__ bool walk_next(Walk* at, const Launch& p, int group, const int* whole, int first_entry, int first_prefix) {
+// A walk lies in memory that ``lanes`` share, who all call this: the barriers
+// keep each from writing the next piece while another still reads this one or
+// has yet to take the same step (the loops that come here end in code which a
+// warp's lanes may leave one by one).
+__device__ __noinline__ bool walk_next(Walk* at, const Launch& p, int group, const int* whole, int first_entry, int first_prefix, uint32_t lanes) {
+  __syncwarp(lanes);
   Walk w = *at;
   const bool more = w.next(p, group, whole, first_entry >= 0, first_entry, first_prefix);
-  __syncwarp(__activemask());
+  __syncwarp(lanes);
   *at = w;
-  __syncwarp(__activemask());
+  __syncwarp(lanes);
   return more;
 }
 // ----------------------------------------------------------- shared memory
@@ -456,13 +461,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   };
   Walk& walk = s.walk[warp];
   const Entry& en = walk.en;
-  auto next = [&](bool first) {                              // by the lanes that call it, with the same values
+  // who walks: a whole warp with the same values, or the one lane that issues the products
+  const uint32_t walkers = warp == kMmaWarp ? 1u << lane : 0xffffffffu;
+  auto next = [&](bool first) {
     if (first) {
       walk.x = whole ? 0 : x0;
       walk.x1 = whole ? s.given : stretch_begin(total, ctas, blockIdx.x + 1);
-      __syncwarp(__activemask());
     }
-    return walk_next(&walk, p, group, whole ? s.units : nullptr, first ? s.first_entry : -1, s.first_prefix);
+    return walk_next(&walk, p, group, whole ? s.units : nullptr, first ? s.first_entry : -1, s.first_prefix, walkers);
   };
 
   if (warp == kLoadWarp) {
