@@ -439,6 +439,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     }
   }
   if (warp == kMmaWarp) {
+    __syncwarp();
     tmem_alloc(&s.tmem, 512);
     tmem_relinquish();
   }
@@ -881,6 +882,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.p_full[i][h]);
+          __syncwarp();                    // the next scores, or sums, are read by the warp as one
         }
       }
 
@@ -934,8 +936,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       auto put_lse = [&](float mm, float ll) {
         if (a.lse != nullptr) a.lse[static_cast<int64_t>(tok) * a.Hq + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
       };
-      auto summed = [&](int d, float (&v)[32]) {                       // O's columns [d, d + 32)
+      // O's columns [d, d + 32): read by the warp as one, which it need not be after rows of its own
+      auto summed = [&](int d, float (&v)[32]) {
         uint32_t r[32] = {};
+        __syncwarp();
         if (good) {
           tmem_ld32(sc + kOColumns + d, r);
           tmem_wait(r);

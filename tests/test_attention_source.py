@@ -35,3 +35,13 @@ def test_a_shared_walk_is_stepped_between_barriers():
     it before any writes the next piece."""
     steps = re.findall(r"__syncwarp\(lanes\)|Walk w = \*at|\*at = w", body(code("prefill_attention.cu"), "bool walk_next("))
     assert steps == ["__syncwarp(lanes)", "Walk w = *at", "__syncwarp(lanes)", "*at = w", "__syncwarp(lanes)"]
+
+
+def test_tmem_is_accessed_by_whole_warps():
+    """tcgen05's allocation and loads are one instruction of all lanes; what
+    comes before them (rows that are written, an arrival by one lane) is not."""
+    text = code("prefill_attention.cu")
+    summed = body(text, "auto summed = ")
+    assert 0 <= summed.find("__syncwarp()") < summed.index("tmem_ld32(")
+    assert re.search(r"__syncwarp\(\);\s*tmem_alloc\(", text)
+    assert re.search(r"mbar_arrive\(&s\.p_full\[i\]\[h\]\);\s*__syncwarp\(\);", text)
