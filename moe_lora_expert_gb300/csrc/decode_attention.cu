@@ -8,14 +8,22 @@
 // several stretches is joined by the CTA that finishes it last.
 //
 // Mathematics.  With t_j = log2(e) scale k_scale (q . k_j) the weights are
-//   w_j = 2^(t_j + log2(v_scale) - m),  m the running maximum of that exponent,
+//   w_j = 2^(t_j + log2(v_scale) - m),  m a reference that follows the keys,
 //   out = sum_j w_j code_j / sum_j (w_j / v_scale),
-// so w_j is what multiplies the codes: it is at most 2^8 in float16 whatever
-// the pages' scales are, and both sums stay in float32.  Codes enter the
-// tensor cores as float16, which holds each exactly; so does q (bf16 rows are
-// first scaled by a power of two), and the scores are exact products.  Only
-// the weights are rounded, to float16 (2^-12 at most of each): the output has
-// 8 or 11 bits.
+// so w_j is what multiplies the codes, whatever the pages' scales are, and
+// both sums stay in float32.  Codes enter the tensor cores as float16, which
+// holds each exactly; so it does q, up to the 2^-17 part of a bf16 row's
+// largest value (a power of two is taken out of the row), and the scores are
+// products summed in float32.  The weights are rounded to float16: 2^-12 of
+// each that is normal, which is less than the output's own 8 or 11 bits.
+// Float16 ends at 2^16 and has full precision down to 2^-14 (2^-25 is 0), so m
+// puts the largest weight of each warp's 16 keys of a tile between 2^0 and
+// 2^15: it rises when one would pass that, and falls again when all are below.
+// With m the running maximum alone, one key that takes nearly all of the mass
+// (and whose values may be zero) took the weights of the thousands after it
+// away from the output but not from its denominator.  m falls by 2^24 at most
+// below where it stood highest, and the sums stay inside float32: what is then
+// still lost is under 2^-57 of the largest weight for each key.
 //
 // What bounds it: one pass over the cache's bytes.  64 sequences of up to
 // 32768 keys (8 query heads of 128 on each of 4 key heads) take 211 us, 6.4
@@ -61,7 +69,10 @@ constexpr int kJoin = 16;                 // pieces that are joined at a time; 1
 constexpr int kPitch = 128;               // bytes of a key in shared memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;             // a maximum may rise by 2^8 before the sums are rescaled
+constexpr float kNew = 8.f;               // a new reference makes the largest weight 2^8,
+constexpr float kMost = 15.f;             // which may rise to 2^15 (or fall to 2^0) before the sums are rescaled
+constexpr float kRoom = 24.f;             // how far a reference may fall below its highest
+constexpr float kNone = -3.0e38f;         // the reference before any key: every weight is 0 next to it, and its sums are
 
 struct alignas(16) Group {                // 8 keys of a tile, which lie in one page
   float k;                                // log2(e) * scale * k_scale
@@ -375,13 +386,13 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       }
 
       float o[NT][kTiles][4];
-      float m[NT][2], base[NT][2], l[NT][2];   // base: m, or 0 while there is none
+      float m[NT][2], least[NT][2], l[NT][2];   // least: what m may fall to
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
 #pragma unroll
-        for (int z = 0; z < 2; ++z) m[t][z] = -INFINITY, base[t][z] = 0.f, l[t][z] = 0.f;
+        for (int z = 0; z < 2; ++z) m[t][z] = least[t][z] = kNone, l[t][z] = 0.f;
       }
 
 #pragma unroll 1
@@ -425,9 +436,9 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
               vw[h][0] = u.x, vw[h][1] = u.y;
             }
           }
-          // exponents of the weights, and whether some maximum has to rise
+          // exponents of the weights, and whether some reference has to move
           const bool whole = key0 + 15 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) && g0.valid && g1.valid;
-          bool raise = false;
+          bool near = false;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -441,9 +452,24 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
               sc[t][j] = y;
             }
 #pragma unroll
-            for (int z = 0; z < 2; ++z) raise |= fmaxf(sc[t][z], sc[t][z + 2]) > m[t][z] + kSlack;
+            for (int z = 0; z < 2; ++z) {
+              // a row's 16 keys are with the 8 lanes of the same c: where all are low the first lane's two are
+              const float top = fmaxf(sc[t][z], sc[t][z + 2]);
+              near |= top > m[t][z] + kMost || (g == 0 && top < m[t][z]);
+            }
           }
-          if (__any_sync(0xffffffffu, raise)) {
+          bool move = false;
+          if (__any_sync(0xffffffffu, near)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const float top = fmaxf(sc[t][z], sc[t][z + 2]);
+                const unsigned up = __ballot_sync(0xffffffffu, !(top < m[t][z]));
+                move |= top > m[t][z] + kMost || ((up & 0x11111111u << c) == 0 && m[t][z] > least[t][z]);
+              }
+          }
+          if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -451,10 +477,12 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 float top = fmaxf(sc[t][z], sc[t][z + 2]);
 #pragma unroll
                 for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                const float now = fmaxf(m[t][z], top);
-                const float keep = m[t][z] == -INFINITY ? 0.f : fast_exp2(m[t][z] - now);
+                float now = m[t][z];
+                if (top > m[t][z] + kMost) now = top - kNew;
+                if (top < m[t][z] && top > -INFINITY && m[t][z] > least[t][z]) now = fmaxf(top - kNew, least[t][z]);
+                const float keep = fast_exp2(m[t][z] - now);
                 m[t][z] = now;
-                base[t][z] = now == -INFINITY ? 0.f : now;
+                least[t][z] = fmaxf(least[t][z], now - kRoom);
                 l[t][z] *= keep;
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j) {
@@ -469,7 +497,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float w0 = fast_exp2(sc[t][2 * h] - base[t][0]), w1 = fast_exp2(sc[t][2 * h + 1] - base[t][1]);
+              const float w0 = fast_exp2(sc[t][2 * h] - m[t][0]), w1 = fast_exp2(sc[t][2 * h + 1] - m[t][1]);
               const float inv_v = h == 0 ? g0.inv_v : g1.inv_v;
               l[t][0] = fmaf(w0, inv_v, l[t][0]);
               l[t][1] = fmaf(w1, inv_v, l[t][1]);
@@ -540,14 +568,13 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const int r = 8 * t + 2 * c + z;
-          M[t][z] = -INFINITY;
+          M[t][z] = kNone;
           Ls[t][z] = 0.f;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) M[t][z] = fmaxf(M[t][z], s.m[w][r]);
-          const float ref = M[t][z] == -INFINITY ? 0.f : M[t][z];
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) Ls[t][z] += s.l[w][r] * fast_exp2(s.m[w][r] - ref);
-          const float keep = fast_exp2(m[t][z] - ref);
+          for (int w = 0; w < kWarps; ++w) Ls[t][z] += s.l[w][r] * fast_exp2(s.m[w][r] - M[t][z]);
+          const float keep = fast_exp2(m[t][z] - M[t][z]);
 #pragma unroll
           for (int j = 0; j < kTiles; ++j) {
             o[t][j][z] *= keep;

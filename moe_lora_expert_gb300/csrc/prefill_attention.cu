@@ -3,8 +3,9 @@
 // A unit is up to 256 rows (new tokens x query heads of one key head's group)
 // as two tiles of 128; a CTA walks the keys they see in tiles of 128:
 //   S = Q K^T (TMEM), P = 2^(S k_scale' + log2 v_scale - m) (float16, back into
-//   S's columns), O += P V (TMEM), with the running maximum m of a softmax.
-// The weights carry the pages' value scales, as in decode_attention.cu, so K
+//   S's columns), O += P V (TMEM), with a reference m that follows the keys.
+// The weights carry the pages' value scales, and m keeps the largest of every
+// 64 keys where float16 has all its bits, both as in decode_attention.cu; so K
 // and V enter the tensor cores as the codes themselves.  A code is exact in
 // float16; four warps convert each tile once for both row tiles, from where
 // the TMA put its bytes to the layout that tcgen05.mma reads.  (Feeding e4m3
@@ -62,7 +63,9 @@ constexpr int kJoin = 8;                   // pieces that are joined at a time
 constexpr int kConvertWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;              // a maximum may rise by 2^8 before the sums are rescaled
+constexpr float kNew = 8.f;                // as in decode_attention.cu: a new reference makes the largest weight 2^8,
+constexpr float kMost = 15.f;              // which may rise to 2^15 or fall to 2^0 before the sums are rescaled;
+constexpr float kRoom = 24.f;              // how far a reference may fall below its highest
 constexpr int kOColumns = 256;             // TMEM: two row tiles' scores, then their sums, 128 columns each
 
 struct alignas(16) Group {                 // 8 keys, which lie in one page
@@ -773,9 +776,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       // keys below pos_lo are seen by every row of the tile, as far as the window goes
       const int pos_lo = en.position(kTileRows * i, group);
       const int pos_hi = en.position(min(en.rows, kTileRows * (i + 1)) - 1, group) - a.window;
-      // weights are relative to 2^base; a row's limit is how far above it a
-      // weight may be before the sums are rescaled
-      float base = 0.f, limit = -INFINITY, l = 0.f;
+      // weights are relative to 2^base; a row's room is how far the base may
+      // still fall, negative before the row's first key
+      float base = 0.f, room = -1.f, l = 0.f;
 
 #pragma unroll 1
       for (int j = 0; j < walk.n && good; ++j, ++t, ++s_count) {
@@ -828,13 +831,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           };
           exponents(ra, 0);
           exponents(rb, 1);
-          if (__any_sync(0xffffffffu, top > limit)) {
-            // a new maximum: what this unit has summed so far becomes
-            // relative to it
-            const float rise = limit == -INFINITY ? (top == -INFINITY ? 0.f : top) : fmaxf(top, 0.f);
-            const float keep = limit == -INFINITY ? 0.f : fast_exp2(-rise);
+          const bool above = top > (room < 0.f ? -INFINITY : kMost), below = top < 0.f && top > -INFINITY && room > 0.f;
+          if (__any_sync(0xffffffffu, above | below)) {
+            // new references for the warp's rows: what this unit has summed so
+            // far becomes relative to them
+            const float rise = top > -INFINITY ? fmaxf(top - kNew, room < 0.f ? -INFINITY : -room) : 0.f;
+            const float keep = room < 0.f ? 0.f : fast_exp2(-rise);
             base += rise;
-            if (top > -INFINITY) limit = kSlack;
+            room = room >= 0.f ? fminf(room + rise, kRoom) : top > -INFINITY ? kRoom : room;
             l *= keep;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -916,7 +920,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           }
         }
       }
-      const float m = limit == -INFINITY ? -INFINITY : base;
+      const float m = room < 0.f ? -INFINITY : base;
       const int gr = en.row0 + row, tok = en.q_first + gr / group, h = walk.head * group + gr % group;
       T* dst = static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head;
       const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // whole sectors at a time

@@ -51,3 +51,81 @@ def test_lse_of_many_small_weights_beside_a_large_one(new, B, Hq, keys, rest):
     err = np.abs(f64(lse) - want[:, None])
     assert (err <= 2.0 ** -24 * keys / 64 + 2.0 ** -20 * (1 + want[:, None])).all(), float(err.max())
     assert cache.device_status() == m.MOE_OK
+
+
+# ---------------------------------------------- one key that takes nearly all
+#
+# A weight is a float16 of half step 2^-25 where it is subnormal, and the
+# largest weight among 64 keys that follow one another is kept at 2^0 or more,
+# unless it is under 2^-32 of the row's largest.  A key's code is 448 at most
+# and the largest weight w of its 64 stands for the probability p: dividing by
+# the sum turns 2^-25 * 448 into at most 2^-25 * 448 * p v_scale of that key.
+# So the tests' bound has, in place of a term that knows nothing of how many
+# keys there are,
+#   2^-25 * 448 * sum over runs of 64 keys of 64 max (p v_scale)
+#   + 2^-57 * 448 * keys * max (p v_scale).
+
+def lost_weights(p, vs):
+    """That term for probabilities p [rows, keys] and value scales vs [keys]."""
+    top = np.pad(p * vs, ((0, 0), (0, -p.shape[1] % 64))).reshape(len(p), -1, 64).max(-1)
+    return 2.0 ** -25 * 448 * 64 * top.sum(-1) + 2.0 ** -57 * 448 * p.shape[1] * top.max(-1)
+
+
+@pytest.mark.parametrize("new,B,Hq", [(1, 64, 16), (4, 32, 32), (64, 20, 32)])   # 2, 16 and 256 rows a key head
+@pytest.mark.parametrize("keys,rest,std,at,shift", [
+    (32768, 1e-2, 1.0, 0, 0), (32768, 1e-3, 1.0, 0, 0), (32768, 1e-3, 0.0, 5000, 0), (32768, 1e-5, 0.0, 0, 0),
+    (131072, 1e-3, 0.0, 0, 0), (131072, 1e-4, 1.0, 0, 12), (32768, 1e-3, 1.0, 32000, 0),
+])
+def test_attention_sink(new, B, Hq, keys, rest, std, at, shift):
+    """One key has all but ``rest`` of the mass and values of zero, on a page
+    whose value scale is 2^shift times the others': the output is what the
+    others leave.  The sequences share their pages, so that a CTA has many
+    keys of a row."""
+    torch = torch_mod()
+    rng = np.random.default_rng(keys + at)
+    Hkv, P, D, scale = 8, 64, 64, 0.125
+    shape = (keys // P, Hkv, P, D)
+    k = np.zeros(shape, np.uint8)
+    k[..., 1:] = ao.e4m3_encode(rng.standard_normal(64 * 63) * 32).reshape(64, 63)[rng.integers(0, 64, shape[:3])]
+    v = ao.e4m3_encode((1 + 0.25 * rng.standard_normal(256)) * 128)[rng.integers(0, 256, shape)]
+    ks, vs = np.full(shape[:2], 2.0 ** -5, np.float32), np.full(shape[:2], 2.0 ** -7, np.float32)
+    order = rng.permutation(shape[0])
+    page = order[at // P]
+    k[page, :, at % P] = 0
+    k[page, :, at % P, 0] = ao.e4m3_encode([448.0])[0]
+    v[page] = 0
+    vs[page] *= 2.0 ** shift
+    kv, vv = ao.E4M3_VALUES[k[order]] * 2.0 ** -5, ao.E4M3_VALUES[v[order]] * vs[order][:, :, None, None]
+    kv, vv = (x.transpose(1, 0, 2, 3).reshape(Hkv, keys, D) for x in (kv, vv))
+    q = rounded(rng, (B * new, Hq, D), "bfloat16", std)
+    G = Hq // Hkv
+    rows = [b * new + t for b in (0, B - 1) for t in {0, new // 2, new - 1}]
+    sees = np.array([keys - new + r % new for r in rows])[:, None] >= np.arange(keys)    # [rows, keys]
+    tail = sees & (np.arange(keys) != at)
+    # the same sink for all rows of a head: as large as the first checked row needs it
+    for h in range(Hq):
+        s = scale * (kv[h // G, :, 1:] @ q[rows[0], h, 1:])
+        lse = np.log(np.exp(s[tail[0]] - s.max()).sum()) + s.max()
+        q[:, h, 0] = (lse + np.log((1 - rest) / rest)) / (scale * 448 * 2.0 ** -5)
+    qt = tensor(q, "bfloat16")
+    q = f64(qt)
+    cache = m.PagedKVCache(tensor(k, torch.uint8), tensor(v, torch.uint8), tensor(ks, "float32"), tensor(vs, "float32"))
+    table = tensor(np.broadcast_to(order.astype(np.int32), (B, keys // P)), "int32")
+    out, lse = cache.attend(qt, table, torch.full((B,), keys, dtype=torch.int32, device="cuda"),
+                            cu_q=tensor(np.arange(B + 1, dtype=np.int32) * new, "int32"), max_q_len=new, scale=scale, return_lse=True)
+    out, lse = f64(out), f64(lse)
+    for h in range(Hq):
+        s = np.where(sees, scale * (q[rows, h] @ kv[h // G].T), -np.inf)
+        es = 128 * 2.0 ** -22 * scale * (np.abs(q[rows, h]) @ np.abs(kv[h // G]).T).max(-1)
+        top = s.max(-1, keepdims=True)
+        e = np.exp(s - top)
+        p, ref_lse = e / e.sum(-1, keepdims=True), top[:, 0] + np.log(e.sum(-1))
+        if h == 0:
+            assert 0.5 * rest < 1 - p[0, at] < 2 * rest       # the case is what it is meant to be
+        ref, spread = p @ vv[h // G], p @ np.abs(vv[h // G])
+        bound = ((2.0 ** -11 + 4 * es + 2.0 ** -17)[:, None] * spread + lost_weights(p, np.repeat(vs[order, h // G], P))[:, None]
+                 + 1.01 * HALF_STEP["bfloat16"] * np.abs(ref))
+        err = np.abs(out[rows, h] - ref)
+        assert (err <= bound).all(), (h, float((err / np.abs(ref)).max()), float((bound / np.abs(ref)).max()))
+        assert (np.abs(lse[rows, h] - ref_lse) <= es + 2.0 ** -20 * (1 + np.abs(ref_lse))).all()
+    assert cache.device_status() == m.MOE_OK
