@@ -594,8 +594,10 @@ int moe_kv_append(const moe_kv_append_args_t* args, moe_stream_t stream);
  *   max_q_len, max_seq_len: at least the largest of the call; they size the
  *     launch (rows past max_q_len are not computed).
  *   workspace: moe_paged_attention_workspace_size() bytes, 256-byte aligned,
- *     zero-filled once before its first use; calls leave it ready for the
- *     next.  Calls that overlap on the GPU must not share one.
+ *     zero-filled once before its first use (or made ready by
+ *     moe_paged_attention_workspace_init); calls leave it ready for the next.
+ *     Calls that overlap on the GPU must not share one.  A captured call
+ *     overlaps with whatever runs while its graph does.
  *   wait_timeout_ms: limit of every device-side wait (0 = 2000 ms); a wait
  *     that runs out reports MOE_ERR_DEVICE_TIMEOUT, the output is then garbage.
  * A table entry outside [0, num_pages) reports MOE_ERR_BAD_PAGE and its keys
@@ -624,6 +626,13 @@ typedef struct {
  * is garbage, but the workspace is ready for the next call. */
 #define MOE_DEBUG_STALL_ATTENTION 4u
 size_t moe_paged_attention_workspace_size(void);
+/* Makes a workspace ready for its first call, in the order of ``stream`` (and
+ * as part of the graph, if the stream is being captured): clears the few words
+ * of it that have to be zero.  In place of filling all of it. */
+int moe_paged_attention_workspace_init(void* workspace, size_t workspace_bytes, moe_stream_t stream);
+/* The id of the capture that ``stream`` is in, or 0: a captured call runs
+ * whenever its graph does, so its workspace has to be the graph's own. */
+int moe_stream_capture_id(moe_stream_t stream, uint64_t* id);
 int moe_paged_attention(const moe_paged_attention_args_t* args, moe_stream_t stream);
 
 #ifdef __cplusplus

@@ -47,7 +47,7 @@ EXPORTED_SYMBOLS = [
     "moe_permute", "moe_lora_workspace_plan", "moe_lora_workspace_size", "moe_lora_forward",
     "moe_read_device_status", "moe_permute_noalloc", "moe_per_token_group_quant_fp8",
     "moe_lora_workspace_size_ex", "moe_rope", "moe_kv_append", "moe_paged_attention_workspace_size",
-    "moe_paged_attention",
+    "moe_paged_attention", "moe_paged_attention_workspace_init", "moe_stream_capture_id",
 ]
 
 
@@ -140,6 +140,10 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = [ctypes.c_char_p, vp]     # the argument struct's bytes, stream
         L.moe_paged_attention_workspace_size.restype = sz
         L.moe_paged_attention_workspace_size.argtypes = []
+        L.moe_paged_attention_workspace_init.restype = i32
+        L.moe_paged_attention_workspace_init.argtypes = [vp, sz, vp]
+        L.moe_stream_capture_id.restype = i32
+        L.moe_stream_capture_id.argtypes = [vp, ctypes.POINTER(ctypes.c_uint64)]
         _lib = L
     return _lib
 

@@ -81,18 +81,24 @@ _ATTEND = struct.Struct("=3Q4q6Q8ifI")
 # imported lazily, as in the rest of the package).
 _torch = _int32_type = _float32_type = None
 _codes: Dict = {}
-_rope_fn = _append_fn = _attend_fn = _raw_stream = _empty_like = None
+_rope_fn = _append_fn = _attend_fn = _raw_stream = _empty_like = _capturing = None
+
+# Scratch of attention calls: calls on one stream follow one another and share
+# it, whatever their cache; a captured call runs when its graph does, so each
+# capture has its own.
+_workspaces: Dict = {}       # device index: {stream handle: (pointer, bytes, tensor)}
+_captured: Dict = {}         # (device index, stream handle): (capture id, workspace) of the latest capture
 
 
 def _bind():
-    global _torch, _int32_type, _float32_type, _rope_fn, _append_fn, _attend_fn, _raw_stream, _empty_like
+    global _torch, _int32_type, _float32_type, _rope_fn, _append_fn, _attend_fn, _raw_stream, _empty_like, _capturing
     import torch
     from . import lib
     L = lib()
     _codes.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32})
     _int32_type, _float32_type = torch.int32, torch.float32
     _append_fn, _attend_fn, _raw_stream = L.moe_kv_append, L.moe_paged_attention, torch._C._cuda_getCurrentRawStream
-    _empty_like = torch.empty_like
+    _empty_like, _capturing = torch.empty_like, torch.cuda.is_current_stream_capturing
     _rope_fn, _torch = L.moe_rope, torch
 
 
@@ -123,6 +129,36 @@ def _out_like(x, token, head, N, H, D, dtype, stream):
     else:
         y = _empty((N, H, D), dtype, x.device, stream)
     return y, y.data_ptr()
+
+
+def _new_workspace(index, handle):
+    """Memory of the stream's own, made ready in its order: of the graph's own
+    and as part of it where the stream is being captured."""
+    from . import lib
+    stream = _torch.cuda.ExternalStream(handle, device=index) if handle else _torch.cuda.default_stream(index)
+    with _torch.cuda.stream(stream):
+        n = int(lib().moe_paged_attention_workspace_size())
+        t = _torch.empty(n, dtype=_torch.uint8, device=_torch.device("cuda", index))
+        error = lib().moe_paged_attention_workspace_init(t.data_ptr(), n, handle)
+    if error:
+        _raise(error, "moe_paged_attention_workspace_init")
+    return t.data_ptr(), n, t
+
+
+def _captured_workspace(index, handle):
+    """The workspace of the capture that the stream is in, or None."""
+    from . import lib
+    capture = ctypes.c_uint64(0)
+    error = lib().moe_stream_capture_id(handle, ctypes.byref(capture))
+    if error:
+        _raise(error, "moe_stream_capture_id")
+    if capture.value == 0:
+        return None
+    held = _captured.get((index, handle))
+    if held is None or held[0] != capture.value:
+        # the last capture's goes back to its graph, which keeps the memory
+        held = _captured[index, handle] = (capture.value, _new_workspace(index, handle))
+    return held[1]
 
 
 def _int32(t, n, name):
@@ -282,7 +318,7 @@ class PagedKVCache:
         self._bytes = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   *k.stride()[:3], *v.stride()[:3], *k.shape)
         self._index = k.device.index
-        self._workspaces = {}
+        self._workspaces = _workspaces.setdefault(self._index, {})
 
     @classmethod
     def create(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, tokens_first=False,
@@ -298,15 +334,14 @@ class PagedKVCache:
         return cls(k, v, ks, vs)
 
     def workspace(self, stream_handle: int):
-        """Scratch of one stream's calls (calls on two streams may overlap)."""
+        """(pointer, bytes, tensor): scratch of the calls on a stream, made by
+        the first one.  All caches of a device share it (about 51 MiB a
+        stream); it lives as long as the process, as torch's streams do.
+        Calls inside a graph capture do not use it: each capture has its own,
+        in the graph's memory."""
         ws = self._workspaces.get(stream_handle)
         if ws is None:
-            import torch
-            from . import lib
-            n = int(lib().moe_paged_attention_workspace_size())
-            t = torch.zeros(n, dtype=torch.uint8, device=self.device)
-            torch.cuda.current_stream(self.device).synchronize()   # the zeros come before any stream's use
-            ws = self._workspaces[stream_handle] = (t.data_ptr(), n, t)
+            ws = self._workspaces[stream_handle] = _new_workspace(self._index, stream_handle)
         return ws
 
     def _batch(self, N, block_table, seq_lens, cu_q, max_q_len):
@@ -374,8 +409,14 @@ class PagedKVCache:
         elif return_lse:
             lse = _empty((N, Hq), _float32_type, self.device, stream)
         B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
-        handle = _raw_stream(self._index) if stream is None else stream.cuda_stream
-        ws = self._workspaces.get(handle) or self.workspace(handle)
+        if stream is None:
+            handle = _raw_stream(self._index)
+            ws = _captured_workspace(self._index, handle) if _capturing() else None
+        else:
+            handle = stream.cuda_stream
+            ws = _captured_workspace(self._index, handle)
+        if ws is None:
+            ws = self._workspaces.get(handle) or self.workspace(handle)
         args = _HEAD.pack(248, code) + self._bytes + _ATTEND.pack(
             qp, op, 0 if lse is None else lse.data_ptr(), q0, q1, o0, o1, bt, sl, cu, self._status_ptr, ws[0], ws[1],
             N, B, Hq, width, longest, width * self.page_size if max_seq_len is None else max_seq_len, window,

@@ -263,8 +263,10 @@ bool encode_cache_map(CUtensorMap* map, const moe_kv_cache_t& c, bool values, in
 bool encode_query_map(CUtensorMap* map, const AttentionParams& a, bool f16, int group, int tokens);
 int sm_count();
 size_t prefill_attention_workspace_bytes();
+cudaError_t clear_prefill_counters(void* workspace, cudaStream_t s);
 int launch_prefill_attention(const AttentionParams& p, int dtype, cudaStream_t s);  // a moe_status_t
 size_t decode_attention_workspace_bytes();
+cudaError_t clear_decode_counters(void* workspace, cudaStream_t s);
 int launch_decode_attention(const AttentionParams& p, int dtype, cudaStream_t s);   // a moe_status_t
 
 }  // namespace moe

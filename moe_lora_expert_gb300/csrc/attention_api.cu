@@ -139,6 +139,25 @@ int moe_kv_append(const moe_kv_append_args_t* a, moe_stream_t stream) {
 
 size_t moe_paged_attention_workspace_size(void) { return moe::decode_attention_workspace_bytes() + moe::prefill_attention_workspace_bytes(); }
 
+int moe_paged_attention_workspace_init(void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < moe_paged_attention_workspace_size())
+    return MOE_ERR_WORKSPACE;
+  (void)cudaGetLastError();
+  const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = moe::clear_decode_counters(workspace, on);
+  return done(e != cudaSuccess ? e : moe::clear_prefill_counters(workspace, on));
+}
+
+int moe_stream_capture_id(moe_stream_t stream, uint64_t* id) {
+  if (id == nullptr) return MOE_ERR_NULL;
+  *id = 0;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long capture = 0;
+  if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(stream), &status, &capture) != cudaSuccess) return MOE_ERR_CUDA;
+  if (status == cudaStreamCaptureStatusActive) *id = capture;
+  return MOE_OK;
+}
+
 int moe_paged_attention(const moe_paged_attention_args_t* a, moe_stream_t stream) {
   if (a == nullptr) return MOE_ERR_NULL;
   if (a->struct_size != sizeof(*a)) return MOE_ERR_UNSUPPORTED;

@@ -797,6 +797,9 @@ bool encode_query_map(CUtensorMap* map, const AttentionParams& a, bool f16, int 
 }
 
 size_t decode_attention_workspace_bytes() { return kPartialBytes + kMlBytes + kCounterBytes; }
+cudaError_t clear_decode_counters(void* workspace, cudaStream_t s) {
+  return cudaMemsetAsync(static_cast<uint8_t*>(workspace) + kPartialBytes + kMlBytes, 0, kCounterBytes, s);
+}
 
 namespace {
 

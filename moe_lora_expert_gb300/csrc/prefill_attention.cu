@@ -1122,6 +1122,9 @@ int launch(const AttentionParams& a, cudaStream_t stream) {
 }  // namespace
 
 size_t prefill_attention_workspace_bytes() { return kPartialBytes + kMlBytes + kCounterBytes; }
+cudaError_t clear_prefill_counters(void* workspace, cudaStream_t s) {
+  return cudaMemsetAsync(static_cast<uint8_t*>(workspace) + decode_attention_workspace_bytes() + kPartialBytes + kMlBytes, 0, kCounterBytes, s);
+}
 
 int launch_prefill_attention(const AttentionParams& p, int dtype, cudaStream_t s) {
   if (dtype == MOE_DTYPE_F16) return p.cache.head_dim <= 64 ? launch<__half, 64>(p, s) : launch<__half, 128>(p, s);

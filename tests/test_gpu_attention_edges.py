@@ -129,3 +129,98 @@ def test_attention_sink(new, B, Hq, keys, rest, std, at, shift):
         assert (err <= bound).all(), (h, float((err / np.abs(ref)).max()), float((bound / np.abs(ref)).max()))
         assert (np.abs(lse[rows, h] - ref_lse) <= es + 2.0 ** -20 * (1 + np.abs(ref_lse))).all()
     assert cache.device_status() == m.MOE_OK
+
+
+# ------------------------------------------------------ workspaces and graphs
+
+def decode_batch(seed):
+    """Two sequences whose keys several CTAs share."""
+    rng = np.random.default_rng(seed)
+    batch = Batch(rng, [1, 1], [9000, 5000], 2, 32, 64, std=0.5)
+    return batch, tensor(rounded(rng, (2, 8, 64), "bfloat16"), "bfloat16")
+
+
+def workspace_of(call):
+    """The workspace address that an attention call hands to the library."""
+    from moe_lora_expert_gb300 import attention
+    seen, real = [], attention._attend_fn
+
+    def spy(args, handle):
+        seen.append(m.PagedAttentionArgs.from_buffer_copy(args).workspace)
+        return real(args, handle)
+
+    attention._attend_fn = spy
+    try:
+        result = call()
+    finally:
+        attention._attend_fn = real
+    return result, seen
+
+
+def test_attention_in_a_default_capture():
+    """As graphs are usually captured: a warm-up on the current stream, then
+    torch.cuda.graph with its own stream and nothing prepared for it."""
+    torch = torch_mod()
+    batch, q = decode_batch(30)
+    want = batch.cache.attend(q, **batch.dev)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = batch.cache.attend(q, **batch.dev)
+        twice = batch.cache.attend(q, **batch.dev)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(twice, want)
+    assert torch.equal(batch.cache.attend(q, **batch.dev), want)
+    assert batch.cache.device_status() == m.MOE_OK
+
+
+def test_graphs_replayed_on_two_streams():
+    """Two captures have a workspace each (their calls share it) and may run
+    at once, and beside calls on the streams that they were captured on."""
+    torch = torch_mod()
+    batches = [decode_batch(31), decode_batch(32)]
+    wants = [b.cache.attend(q, **b.dev) for b, q in batches]
+    graphs, outs, used = [], [], []
+    for b, q in batches:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            out, seen = workspace_of(lambda: [b.cache.attend(q, **b.dev) for _ in range(4)])
+        outs.append(out)
+        assert len(set(seen)) == 1
+        used.append(seen[0])
+    current = torch.cuda.current_stream().cuda_stream
+    assert len({*used, batches[0][0].cache.workspace(current)[0]}) == 3
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = [b.cache.attend(q, **b.dev) for b, q in batches]
+        torch.cuda.synchronize()
+        for out, want, e in zip(outs, wants, eager):
+            assert all(torch.equal(o, want) for o in out) and torch.equal(e, want)
+
+
+def test_caches_share_a_streams_workspace():
+    """A cache for each layer costs no workspace of its own, and a workspace
+    belongs to its stream from the first word on: nothing waits for another."""
+    torch = torch_mod()
+    (a, qa), (b, qb) = decode_batch(33), decode_batch(34)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    want_a, want_b = a.cache.attend(qa, **a.dev), b.cache.attend(qb, **b.dev)
+    for stream in (None, side):
+        outs, seen = workspace_of(lambda: [a.cache.attend(qa, **a.dev, stream=stream), b.cache.attend(qb, **b.dev, stream=stream)])
+        torch.cuda.synchronize()
+        assert len(set(seen)) == 1 and torch.equal(outs[0], want_a) and torch.equal(outs[1], want_b)
+
+
+def test_workspace_init_refuses():
+    lib = m.lib()
+    n = lib.moe_paged_attention_workspace_size()
+    for pointer, size in ((None, n), (64, n), (256, n - 1)):
+        assert lib.moe_paged_attention_workspace_init(pointer, size, None) == m.MOE_ERR_WORKSPACE
+    assert lib.moe_stream_capture_id(None, None) == m.MOE_ERR_NULL
