@@ -81,7 +81,7 @@ _ATTEND = struct.Struct("=3Q4q6Q8ifI")
 # imported lazily, as in the rest of the package).
 _torch = _int32_type = _float32_type = None
 _codes: Dict = {}
-_rope_fn = _append_fn = _attend_fn = _raw_stream = _empty_like = _capturing = None
+_rope_fn = _append_fn = _attend_fn = _raw_stream = _empty_like = _capturing = _current_device = None
 
 # Scratch of attention calls: calls on one stream follow one another and share
 # it, whatever their cache; a captured call runs when its graph does, so each
@@ -92,6 +92,7 @@ _captured: Dict = {}         # (device index, stream handle): (capture id, works
 
 def _bind():
     global _torch, _int32_type, _float32_type, _rope_fn, _append_fn, _attend_fn, _raw_stream, _empty_like, _capturing
+    global _current_device
     import torch
     from . import lib
     L = lib()
@@ -99,12 +100,29 @@ def _bind():
     _int32_type, _float32_type = torch.int32, torch.float32
     _append_fn, _attend_fn, _raw_stream = L.moe_kv_append, L.moe_paged_attention, torch._C._cuda_getCurrentRawStream
     _empty_like, _capturing = torch.empty_like, torch.cuda.is_current_stream_capturing
+    _current_device = torch._C._cuda_getDevice
     _rope_fn, _torch = L.moe_rope, torch
 
 
 def _raise(status, what):
     from . import MoeError
     raise MoeError(status, what)
+
+
+def _elsewhere(index, fn, *args):
+    """A call on a device that is not the current one: the library launches on
+    the current device, whose stream 0 is another one."""
+    with _torch.cuda.device(index):
+        return fn(*args)
+
+
+def _handle(stream, index):
+    """The handle of a call's stream on its tensors' device."""
+    if stream is None:
+        return _raw_stream(index)
+    if stream.device_index != index:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, the tensors are on cuda:{index}")
+    return stream.cuda_stream
 
 
 def _dtype_code(dtype, name):
@@ -161,31 +179,31 @@ def _captured_workspace(index, handle):
     return held[1]
 
 
-def _int32(t, n, name):
-    """Pointer of an int32 [n] tensor."""
-    if t.dtype is not _int32_type or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+def _int32(t, n, name, index):
+    """Pointer of an int32 [n] tensor on a call's device."""
+    if t.dtype is not _int32_type or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on cuda:{index}")
     if t.shape != (n,):
         raise ValueError(f"{name} must have shape [{n}], got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _heads(t, N, H, D, dtype, name):
+def _heads(t, N, H, D, dtype, name, index):
     """(pointer, token stride, head stride) of a [N, H, D] tensor."""
     if t.shape != (N, H, D):
         raise ValueError(f"{name} must have shape [{N}, {H}, {D}], got {tuple(t.shape)}")
-    if t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{index}")
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must be contiguous along the head dimension")
     return t.data_ptr(), st, sh
 
 
-def _table(cos_sin):
+def _table(cos_sin, index):
     shape = cos_sin.shape
-    if cos_sin.dtype is not _float32_type or not cos_sin.is_cuda or len(shape) != 2 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be a contiguous float32 CUDA tensor [positions, rotary_dim]")
+    if cos_sin.dtype is not _float32_type or cos_sin.get_device() != index or len(shape) != 2 or not cos_sin.is_contiguous():
+        raise ValueError(f"cos_sin must be a contiguous float32 tensor [positions, rotary_dim] on cuda:{index}")
     return cos_sin.data_ptr(), shape[0], shape[1]
 
 
@@ -263,26 +281,31 @@ def moe_rope(q, positions, cos_sin, k=None, interleaved=False, inverse=False, q_
     N, Hq, D = q.shape
     dtype = q.dtype
     code = _dtype_code(dtype, "q")
-    qp, q0, q1 = _heads(q, N, Hq, D, dtype, "q")
+    index = q.get_device()
+    if index < 0:
+        raise ValueError("q must be a CUDA tensor")
+    handle = _handle(stream, index)
+    qp, q0, q1 = _heads(q, N, Hq, D, dtype, "q", index)
     if q_out is None:
         q_out, op = _out_like(q, q0, q1, N, Hq, D, dtype, stream)
         o0, o1 = Hq * D, D
     else:
-        op, o0, o1 = _heads(q_out, N, Hq, D, dtype, "q_out")
+        op, o0, o1 = _heads(q_out, N, Hq, D, dtype, "q_out", index)
     kp = kop = k0 = k1 = ko0 = ko1 = Hk = 0
     if k is not None:
         Hk = k.shape[1]
-        kp, k0, k1 = _heads(k, N, Hk, D, dtype, "k")
+        kp, k0, k1 = _heads(k, N, Hk, D, dtype, "k", index)
         if k_out is None:
             k_out, kop = _out_like(k, k0, k1, N, Hk, D, dtype, stream)
             ko0, ko1 = Hk * D, D
         else:
-            kop, ko0, ko1 = _heads(k_out, N, Hk, D, dtype, "k_out")
-    tp, rows, R = _table(cos_sin)
+            kop, ko0, ko1 = _heads(k_out, N, Hk, D, dtype, "k_out", index)
+    tp, rows, R = _table(cos_sin, index)
     args = _ROPE.pack(160, code, qp, op, kp, kop, q0, q1, o0, o1, k0, k1, ko0, ko1,
-                      _int32(positions, N, "positions"), tp, 0 if status is None else _int32(status, 4, "status"),
+                      _int32(positions, N, "positions", index), tp,
+                      0 if status is None else _int32(status, 4, "status", index),
                       N, Hq, Hk, D, R, rows, interleaved, inverse)
-    error = _rope_fn(args, _raw_stream(q.device.index) if stream is None else stream.cuda_stream)
+    error = _rope_fn(args, handle) if _current_device() == index else _elsewhere(index, _rope_fn, args, handle)
     if error:
         _raise(error, "moe_rope")
     return q_out if k is None else (q_out, k_out)
@@ -303,6 +326,7 @@ class PagedKVCache:
             _bind()
         torch = _torch
         fp8 = (torch.uint8, torch.float8_e4m3fn)
+        index = k.get_device()
         for t, name in ((k, "k"), (v, "v")):
             if t.dtype not in fp8 or not t.is_cuda or t.dim() != 4 or t.shape != k.shape or t.stride(3) != 1:
                 raise ValueError(f"{name}: uint8 or float8_e4m3fn CUDA [pages, kv_heads, page_size, head_dim], "
@@ -310,6 +334,9 @@ class PagedKVCache:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t.dtype != torch.float32 or not t.is_cuda or t.shape != k.shape[:2] or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 CUDA tensor {tuple(k.shape[:2])}")
+        for t, name in ((v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.get_device() != index:
+                raise ValueError(f"{name} must be on cuda:{index}, as k is")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.device = k.device
@@ -317,7 +344,7 @@ class PagedKVCache:
         self._status_ptr = self.status.data_ptr()
         self._bytes = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   *k.stride()[:3], *v.stride()[:3], *k.shape)
-        self._index = k.device.index
+        self._index = index
         self._workspaces = _workspaces.setdefault(self._index, {})
 
     @classmethod
@@ -346,14 +373,16 @@ class PagedKVCache:
 
     def _batch(self, N, block_table, seq_lens, cu_q, max_q_len):
         B, width = block_table.shape
-        if block_table.dtype is not _int32_type or not block_table.is_cuda or not block_table.is_contiguous():
-            raise ValueError("block_table must be a contiguous int32 CUDA tensor [sequences, pages]")
-        sl = _int32(seq_lens, B, "seq_lens")
+        index = self._index
+        if block_table.dtype is not _int32_type or block_table.get_device() != index or not block_table.is_contiguous():
+            raise ValueError(f"block_table must be a contiguous int32 tensor [sequences, pages] on cuda:{index}")
+        sl = _int32(seq_lens, B, "seq_lens", index)
         if cu_q is None:
             if N != B:
                 raise ValueError("without cu_q there is one new token for each sequence")
             return B, width, block_table.data_ptr(), sl, 0, 1
-        return B, width, block_table.data_ptr(), sl, _int32(cu_q, B + 1, "cu_q"), N if max_q_len is None else max_q_len
+        cu = _int32(cu_q, B + 1, "cu_q", index)
+        return B, width, block_table.data_ptr(), sl, cu, N if max_q_len is None else max_q_len
 
     def append(self, k, v, block_table, seq_lens, cu_q=None, max_q_len=None, q=None, cos_sin=None,
                interleaved=False, positions=None, q_out=None, stream=None):
@@ -361,27 +390,28 @@ class PagedKVCache:
         head_dim], go into the pages of their sequences: tokens [cu_q[b],
         cu_q[b + 1]) (one each without cu_q) end at seq_lens[b].  ``q`` [N, Hq,
         head_dim] is rotated in the same launch and returned."""
-        N, D, H = k.shape[0], self.head_dim, self.kv_heads
+        N, D, H, index = k.shape[0], self.head_dim, self.kv_heads, self._index
         dtype = k.dtype
         code = _dtype_code(dtype, "k")
-        kp, k0, k1 = _heads(k, N, H, D, dtype, "k")
-        vp, v0, v1 = _heads(v, N, H, D, dtype, "v")
+        handle = _handle(stream, index)
+        kp, k0, k1 = _heads(k, N, H, D, dtype, "k", index)
+        vp, v0, v1 = _heads(v, N, H, D, dtype, "v", index)
         qp = q0 = q1 = op = o0 = o1 = Hq = 0
         if q is not None:
             Hq = q.shape[1]
-            qp, q0, q1 = _heads(q, N, Hq, D, dtype, "q")
+            qp, q0, q1 = _heads(q, N, Hq, D, dtype, "q", index)
             if q_out is None:
                 q_out, op = _out_like(q, q0, q1, N, Hq, D, dtype, stream)
                 o0, o1 = Hq * D, D
             else:
-                op, o0, o1 = _heads(q_out, N, Hq, D, dtype, "q_out")
+                op, o0, o1 = _heads(q_out, N, Hq, D, dtype, "q_out", index)
         B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
-        tp, rows, R = (0, 0, 0) if cos_sin is None else _table(cos_sin)
+        tp, rows, R = (0, 0, 0) if cos_sin is None else _table(cos_sin, index)
         args = _HEAD.pack(280, code) + self._bytes + _APPEND.pack(
             kp, vp, k0, k1, v0, v1, qp, op, q0, q1, o0, o1, bt, sl, cu,
-            0 if positions is None else _int32(positions, N, "positions"), tp, self._status_ptr,
+            0 if positions is None else _int32(positions, N, "positions", index), tp, self._status_ptr,
             N, B, Hq, width, longest, R, rows, interleaved)
-        error = _append_fn(args, _raw_stream(self._index) if stream is None else stream.cuda_stream)
+        error = _append_fn(args, handle) if _current_device() == index else _elsewhere(index, _append_fn, args, handle)
         if error:
             _raise(error, "moe_kv_append")
         return q_out
@@ -396,32 +426,31 @@ class PagedKVCache:
         Hq]) with ``return_lse`` or a given ``lse``."""
         N, Hq, D = q.shape
         dtype = q.dtype
-        code = _dtype_code(dtype, "q")
-        qp, q0, q1 = _heads(q, N, Hq, self.head_dim, dtype, "q")
+        code, index = _dtype_code(dtype, "q"), self._index
+        handle = _handle(stream, index)
+        qp, q0, q1 = _heads(q, N, Hq, self.head_dim, dtype, "q", index)
         if out is None:
             out, op = _out_like(q, q0, q1, N, Hq, D, dtype, stream)
             o0, o1 = Hq * D, D
         else:
-            op, o0, o1 = _heads(out, N, Hq, D, dtype, "out")
+            op, o0, o1 = _heads(out, N, Hq, D, dtype, "out", index)
         if lse is not None:
-            if lse.dtype is not _float32_type or lse.shape != (N, Hq) or not lse.is_contiguous() or not lse.is_cuda:
-                raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{N}, {Hq}]")
+            if lse.dtype is not _float32_type or lse.shape != (N, Hq) or not lse.is_contiguous() or lse.get_device() != index:
+                raise ValueError(f"lse must be a contiguous float32 tensor [{N}, {Hq}] on cuda:{index}")
         elif return_lse:
             lse = _empty((N, Hq), _float32_type, self.device, stream)
         B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
-        if stream is None:
-            handle = _raw_stream(self._index)
-            ws = _captured_workspace(self._index, handle) if _capturing() else None
-        else:
-            handle = stream.cuda_stream
-            ws = _captured_workspace(self._index, handle)
+        here = _current_device() == index
+        ws = None
+        if stream is not None or not here or _capturing():
+            ws = _captured_workspace(index, handle)
         if ws is None:
             ws = self._workspaces.get(handle) or self.workspace(handle)
         args = _HEAD.pack(248, code) + self._bytes + _ATTEND.pack(
             qp, op, 0 if lse is None else lse.data_ptr(), q0, q1, o0, o1, bt, sl, cu, self._status_ptr, ws[0], ws[1],
             N, B, Hq, width, longest, width * self.page_size if max_seq_len is None else max_seq_len, window,
             wait_timeout_ms, D ** -0.5 if scale is None else scale, debug_flags)
-        error = _attend_fn(args, handle)
+        error = _attend_fn(args, handle) if here else _elsewhere(index, _attend_fn, args, handle)
         if error:
             _raise(error, "moe_paged_attention")
         return out if lse is None else (out, lse)
