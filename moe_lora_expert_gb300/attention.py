@@ -341,6 +341,7 @@ class PagedKVCache:
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.device = k.device
         self.status = torch.zeros(4, dtype=torch.int32, device=k.device)
+        torch.cuda.current_stream(k.device).synchronize()           # before a call on another stream writes it
         self._status_ptr = self.status.data_ptr()
         self._bytes = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   *k.stride()[:3], *v.stride()[:3], *k.shape)
@@ -457,8 +458,11 @@ class PagedKVCache:
 
     def device_status(self) -> int:
         """The first problem that a call met on the device since the last
-        reading (MOE_OK: none); waits for the device's work and clears it."""
+        reading (MOE_OK: none), and clears it.  Waits for the work of all the
+        device's streams, since a call may be on any."""
+        _torch.cuda.synchronize(self.device)
         code = int(self.status[0].item())
         if code:
             self.status.zero_()
+            _torch.cuda.current_stream(self.device).synchronize()   # before a call on another stream writes it
         return code

@@ -224,3 +224,37 @@ def test_workspace_init_refuses():
     for pointer, size in ((None, n), (64, n), (256, n - 1)):
         assert lib.moe_paged_attention_workspace_init(pointer, size, None) == m.MOE_ERR_WORKSPACE
     assert lib.moe_stream_capture_id(None, None) == m.MOE_ERR_NULL
+
+
+# ----------------------------------------------------------------- the status
+
+def test_status_of_calls_on_other_streams():
+    """A problem of a call that still waits on another stream is reported, once."""
+    torch = torch_mod()
+    batch, q = decode_batch(35)
+    side = torch.cuda.Stream()
+    bad = torch.full_like(batch.dev["block_table"], batch.pages + 1)
+    torch.cuda.synchronize()
+    batch.cache.attend(q, **batch.dev, stream=side)     # what a first call loads and allocates may wait for the device
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)                  # about 50 ms
+    batch.cache.attend(q, bad, batch.dev["seq_lens"], stream=side)
+    assert batch.cache.device_status() == m.MOE_ERR_BAD_PAGE
+    assert batch.cache.device_status() == m.MOE_OK
+
+
+def test_status_of_a_cache_made_on_a_busy_stream():
+    """The status word is cleared before the cache can be used anywhere."""
+    torch = torch_mod()
+    batch, _ = decode_batch(36)
+    k = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    bad = torch.full_like(batch.dev["block_table"], batch.pages + 1)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    batch.cache.append(k, k, **batch.dev, stream=side)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    cache = m.PagedKVCache(batch.cache.k, batch.cache.v, batch.cache.k_scale, batch.cache.v_scale)
+    cache.append(k, k, bad, batch.dev["seq_lens"], stream=side)
+    assert cache.device_status() == m.MOE_ERR_BAD_PAGE
