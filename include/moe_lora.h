@@ -547,6 +547,9 @@ typedef struct {
  *   cos_sin as in moe_rope, or NULL with rotary_dim = 0: no rotation.
  *   max_q_len: at least the most new tokens of one sequence (1 if cu_q is
  *     NULL); more are not appended.
+ * Without cu_q a slot with seq_lens[b] = 0 stands for no sequence (a batch of
+ * fixed size that is not full): nothing of it is appended, and its q is copied
+ * unless ``positions`` has one for it.
  * A page that two sequences of a call append to is not allowed.  A table
  * entry outside [0, num_pages), or a page past table_width, drops its tokens
  * and reports MOE_ERR_BAD_PAGE; a sequence with more new tokens than

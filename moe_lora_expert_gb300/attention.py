@@ -389,7 +389,8 @@ class PagedKVCache:
                interleaved=False, positions=None, q_out=None, stream=None):
         """The new tokens' k (rotated by ``cos_sin``) and v, [N, kv_heads,
         head_dim], go into the pages of their sequences: tokens [cu_q[b],
-        cu_q[b + 1]) (one each without cu_q) end at seq_lens[b].  ``q`` [N, Hq,
+        cu_q[b + 1]) (one each without cu_q) end at seq_lens[b]; a slot whose
+        seq_lens is 0 without cu_q stands for no sequence.  ``q`` [N, Hq,
         head_dim] is rotated in the same launch and returned."""
         N, D, H, index = k.shape[0], self.head_dim, self.kv_heads, self._index
         dtype = k.dtype

@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
           pos = p.cu_q == nullptr ? p.seq_lens[b] - 1 : p.seq_lens[b] - p.cu_q[b + 1] + static_cast<int>(t);
         }
         if (pos < 0 || pos >= p.num_positions) {
-          if (p.R > 0) set_status(p.status, MOE_ERR_BAD_POSITION);
+          const bool padding = p.cu_q == nullptr && p.seq_lens[t] == 0;       // a slot without a sequence
+          if (p.R > 0 && !padding) set_status(p.status, MOE_ERR_BAD_POSITION);
           pos = kUnturned;
         }
       }
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
   int t_end = p.cu_q == nullptr ? b + 1 : p.cu_q[b + 1];
   if (t_end > p.N) t_end = p.N;
   const int len = p.seq_lens[b];
+  if (p.cu_q == nullptr && len == 0) return;          // a slot without a sequence
   const int start = len - (t_end - t_first);          // position of the first new token
   const int P = ca.page_size;
   if (start < 0 && tid == 0) set_status(p.status, MOE_ERR_BAD_POSITION);

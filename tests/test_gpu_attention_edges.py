@@ -258,3 +258,38 @@ def test_status_of_a_cache_made_on_a_busy_stream():
     cache = m.PagedKVCache(batch.cache.k, batch.cache.v, batch.cache.k_scale, batch.cache.v_scale)
     cache.append(k, k, bad, batch.dev["seq_lens"], stream=side)
     assert cache.device_status() == m.MOE_ERR_BAD_PAGE
+
+
+# --------------------------------------------------------------------- append
+
+@pytest.mark.parametrize("given", [False, True])
+def test_append_passes_over_empty_slots(given):
+    """A decode batch of fixed size with slots that hold no sequence: nothing
+    is written for those, their q is copied, and no problem is reported, so
+    that a real one is."""
+    torch = torch_mod()
+    rng = np.random.default_rng(37)
+    lens = [0, 20, 0, 17, 1]
+    batch = Batch(rng, [1] * 5, lens, 2, 16, 64)
+    k, v, q = (rounded(rng, (5, h, 64), "bfloat16") for h in (2, 2, 4))
+    table = m.rope_table(64, 64, device="cuda")
+    pos = np.array([n - 1 for n in lens], np.int32)
+    before = [x.clone() for x in (batch.cache.k, batch.cache.v, batch.cache.k_scale, batch.cache.v_scale)]
+    kw = dict(positions=tensor(pos, "int32")) if given else {}
+    got = batch.cache.append(tensor(k, "bfloat16"), tensor(v, "bfloat16"), **batch.dev, q=tensor(q, "bfloat16"), cos_sin=table, **kw)
+    assert batch.cache.device_status() == m.MOE_OK
+    real = [b for b, n in enumerate(lens) if n]
+    alone = m.PagedKVCache(*before)
+    want = alone.append(tensor(k[real], "bfloat16"), tensor(v[real], "bfloat16"), batch.dev["block_table"][real].contiguous(),
+                        batch.dev["seq_lens"][real].contiguous(), q=tensor(q[real], "bfloat16"), cos_sin=table)
+    assert torch.equal(got[real], want) and (f64(got)[[0, 2]] == q[[0, 2]]).all()
+    for a, b in ((batch.cache.k, alone.k), (batch.cache.v, alone.v), (batch.cache.k_scale, alone.k_scale),
+                 (batch.cache.v_scale, alone.v_scale)):
+        assert torch.equal(a, b)
+    out = batch.cache.attend(got, **batch.dev)
+    assert (f64(out)[[0, 2]] == 0).all() and batch.cache.device_status() == m.MOE_OK
+    # a negative length, and a token without a place in its sequence, still are problems
+    batch.cache.append(tensor(k, "bfloat16"), tensor(v, "bfloat16"), batch.dev["block_table"], batch.dev["seq_lens"] - 1)
+    assert batch.cache.device_status() == m.MOE_ERR_BAD_POSITION
+    batch.cache.append(tensor(k, "bfloat16"), tensor(v, "bfloat16"), **batch.dev, cu_q=batch.cu_dev, max_q_len=1)
+    assert batch.cache.device_status() == m.MOE_ERR_BAD_POSITION
