@@ -60,6 +60,7 @@ constexpr int kMaxCtas = 160;
 constexpr int kMaxUnits = 16;              // whole units a CTA may be given (see the kernel)
 constexpr int kJoinCost = 8;               // key tiles' worth of time that cutting the line may cost a CTA: part of a unit written, another joined
 constexpr int kJoin = 8;                   // pieces that are joined at a time
+constexpr int kNanTiles = 8;               // tiles with NaN that a warp notes for a unit; hidden in part are 6 at most where all pages are there
 constexpr int kConvertWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -276,6 +277,27 @@ __device__ __noinline__ bool walk_next(Walk* at, const Launch& p, int group, con
   __syncwarp(lanes);
   return more;
 }
+// Which columns of keys k0 to k1 (of one tile) of sequence b hold NaN values.
+__device__ __noinline__ uint4 nan_columns(const AttentionParams& a, int b, int head, int k0, int k1) {
+  const moe_kv_cache_t& ca = a.cache;
+  uint32_t nan[4] = {};
+#pragma unroll 1
+  for (int key = k0; key <= k1; ++key) {
+    const int page_at = key / ca.page_size, page = a.block_table[static_cast<int64_t>(b) * a.table_width + page_at];
+    if (page < 0 || page >= ca.num_pages) continue;
+    const uint8_t* codes = ca.v + page * ca.v_stride_page + head * ca.v_stride_head + (key - page_at * ca.page_size) * ca.v_stride_token;
+    uint4 c[8];
+#pragma unroll
+    for (int d = 0; d < 8; ++d) c[d] = 16 * d < ca.head_dim ? *reinterpret_cast<const uint4*>(codes + 16 * d) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      // a bit for each of a word's four codes
+      auto bits = [](uint32_t w) { return ((__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & 0x08040201u) * 0x01010101u) >> 24; };
+      nan[d / 2] |= (bits(c[d].x) | bits(c[d].y) << 4 | bits(c[d].z) << 8 | bits(c[d].w) << 12) << (16 * (d & 1));
+    }
+  }
+  return make_uint4(nan[0], nan[1], nan[2], nan[3]);
+}
 // ----------------------------------------------------------- shared memory
 struct Control {
   Group group[kInfo][kKeys / 8];
@@ -285,8 +307,11 @@ struct Control {
   int sums[kThreads / 32];
   int units[kMaxUnits];                    // this CTA's, if it has whole ones
   Walk walk[kThreads / 32];                // each warp's own, here and not in its registers
+  // Of a unit and the next: the key tiles, hidden from some rows, in which a
+  // converting warp has met and left out NaN values that some row sees.
+  int nan_count[2][4], nan_tiles[2][4][kNanTiles];
   uint32_t tmem;
-  int abort_flag, nan_seen, first_entry, first_prefix, given, last[2], issued, issued_units;
+  int abort_flag, first_entry, first_prefix, given, last[2], issued, issued_units;
 };
 
 template <int DP>
@@ -344,7 +369,6 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     mbar_init(&s.q_empty, 1 + 2 * kTileRows / 32);   // the last scores, and every row's thread has its exponent
     mbar_init(&s.drained, 1);
     s.abort_flag = 0;
-    s.nan_seen = 0;
     fence_mbarrier_init();
   }
   pdl_launch_dependents();
@@ -687,7 +711,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
             put(it, c);
           }
         }
-        if (nan) *static_cast<volatile int*>(&s.nan_seen) = 1;
+        if (drop && __any_sync(0xffffffffu, nan) && lane == 0) {
+          const int n = s.nan_count[units & 1][w]++;
+          if (n < kNanTiles) s.nan_tiles[units & 1][w][n] = tile;
+        }
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
@@ -699,6 +726,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           // rows become float16 in place, a power of two taken out of each.
           good = wait(&s.q_raw, units & 1);
           if (!good) break;
+          // the rows have begun the unit before, so they are done with the one before that
+          if (lane == 0) s.nan_count[units & 1][w] = 0;
           if constexpr (kBf16) {
 #pragma unroll 1
             for (int row = 32 * w + lane; row < kCtaRows; row += 128) {
@@ -899,26 +928,35 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       const bool live = row < en.rows;
       good = good && wait(&s.o_full[i], o_count++ & 1);
       tc_fence_after_sync();
-      // NaN values of partly hidden tiles, for the rows that see them
+      // NaN values that were left out of partly hidden tiles, for the rows that
+      // see them: of the tiles that were noted, one after another, or of all
+      // where a warp met more of them than it could note
       uint32_t nan[4] = {};
       bool any_nan = false;
-      if (live && good && *static_cast<volatile int*>(&s.nan_seen) != 0) {
+      const int(&counts)[4] = s.nan_count[units & 1];
+      if (good && (counts[0] | counts[1] | counts[2] | counts[3]) != 0) {
+        const int first = en.tile0 + walk.tile, end = first + walk.n;
 #pragma unroll 1
-        for (int tile = en.tile0 + walk.tile; tile < en.tile0 + walk.tile + walk.n; ++tile) {
-          const int k0 = max(tile * kKeys, a.window > 0 ? pos - a.window + 1 : 0), k1 = min(min(pos, en.end - 1), tile * kKeys + kKeys - 1);
+        for (int at = first; at < end; ++at) {
+          int tile = end;
 #pragma unroll 1
-          for (int key = k0; key <= k1; ++key) {
-            const int page_at = key / ca.page_size, page = a.block_table[static_cast<int64_t>(en.b) * a.table_width + page_at];
-            if (page < 0 || page >= ca.num_pages) continue;
-            const uint8_t* codes = ca.v + page * ca.v_stride_page + walk.head * ca.v_stride_head + (key - page_at * ca.page_size) * ca.v_stride_token;
+          for (int w = 0; w < 4; ++w) {
+            if (counts[w] > kNanTiles) tile = at;
 #pragma unroll 1
-            for (int d = 0; d < ca.head_dim; ++d)
-              if ((codes[d] & 0x7F) == 0x7F) {
-                nan[d >> 5] |= 1u << (d & 31);
-                any_nan = true;
-              }
+            for (int e = 0; e < min(counts[w], kNanTiles); ++e) {
+              const int noted = s.nan_tiles[units & 1][w][e];
+              if (noted >= at) tile = min(tile, noted);
+            }
+          }
+          if (tile == end) break;
+          at = tile;
+          if (live) {
+            const int k0 = max(tile * kKeys, a.window > 0 ? pos - a.window + 1 : 0), k1 = min(min(pos, en.end - 1), tile * kKeys + kKeys - 1);
+            const uint4 bits = nan_columns(a, en.b, walk.head, k0, k1);
+            nan[0] |= bits.x, nan[1] |= bits.y, nan[2] |= bits.z, nan[3] |= bits.w;
           }
         }
+        any_nan = (nan[0] | nan[1] | nan[2] | nan[3]) != 0;
       }
       const float m = room < 0.f ? -INFINITY : base;
       const int gr = en.row0 + row, tok = en.q_first + gr / group, h = walk.head * group + gr % group;

@@ -293,3 +293,65 @@ def test_append_passes_over_empty_slots(given):
     assert batch.cache.device_status() == m.MOE_ERR_BAD_POSITION
     batch.cache.append(tensor(k, "bfloat16"), tensor(v, "bfloat16"), **batch.dev, cu_q=batch.cu_dev, max_q_len=1)
     assert batch.cache.device_status() == m.MOE_ERR_BAD_POSITION
+
+
+# ------------------------------------------------------------------------ NaN
+
+@pytest.mark.parametrize("D,Hq,Hkv,window", [(64, 16, 16, 0), (128, 16, 4, 9000)])
+def test_attention_one_nan_on_a_long_context(D, Hq, Hkv, window):
+    """A NaN value that some rows of a unit see and others do not costs the
+    unit's CTA a look at that tile, not at every key of its later units: no
+    wait of 10 ms runs out, and only what sees it changes."""
+    torch = torch_mod()
+    gen = torch.Generator(device="cuda").manual_seed(38)
+    new, past, P = 5120, 15360, 64
+    pages = (new + past) // P
+    shape = (pages, Hkv, P, D)
+    k, v = ((torch.randn(shape, generator=gen, device="cuda") * 40).to(torch.float8_e4m3fn).view(torch.uint8) for _ in range(2))
+    cache = m.PagedKVCache(k, v, *[torch.full(shape[:2], 2.0 ** -6, device="cuda") for _ in range(2)])
+    q = torch.randn((new, Hq, D), generator=gen, device="cuda").to(torch.bfloat16)
+    order = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
+    args = dict(block_table=order[None].contiguous(), seq_lens=tensor(np.array([new + past], np.int32), "int32"),
+                cu_q=tensor(np.array([0, new], np.int32), "int32"), window=window, return_lse=True, wait_timeout_ms=10)
+    clean, lse = cache.attend(q, **args)
+    assert cache.device_status() == m.MOE_OK
+    # in the middle of a unit that is late in its sequence, and so among the first to be done, and of an early one
+    where = [past + new - 100, past + 300]
+    for i, j in enumerate(where):
+        v[order[j // P].long(), :, j % P, 33 + 16 * i] = 0x7F if i else 0xFF
+    out, lse_nan = cache.attend(q, **args)
+    assert cache.device_status() == m.MOE_OK
+    assert torch.equal(lse, lse_nan)
+    at = past + torch.arange(new, device="cuda")
+    want = clean.clone()
+    for i, j in enumerate(where):
+        sees = (at >= j) & ((at < j + window) if window else True)
+        want[sees, :, 33 + 16 * i] = float("nan")
+    assert torch.equal(out.isnan(), want.isnan()) and torch.equal(out.nan_to_num(), want.nan_to_num())
+
+
+@pytest.mark.parametrize("bad", [0, 13])
+def test_attention_nan_in_many_partial_tiles(bad):
+    """More tiles with NaN and missing pages than a unit notes: still only the
+    rows that see a NaN have it."""
+    torch = torch_mod()
+    rng = np.random.default_rng(39)
+    batch = Batch(rng, [200], [4000], 1, 16, 64, std=0.5)
+    q = rounded(rng, (200, 2, 64), "float16")
+    table = batch.dev["block_table"]
+    if bad:
+        table[0, 1:240:bad] = -1                        # pages of most of the first 30 tiles
+    clean, lse = batch.cache.attend(tensor(q, "float16"), **batch.dev, cu_q=batch.cu_dev, return_lse=True)
+    for j in range(5, 4000, 128):                       # a NaN in every tile of 128 keys, in columns 0 to 31
+        page = int(table[0, j // 16])
+        if page >= 0:
+            batch.cache.v[page, 0, j % 16, (j // 128) % 64] = 0x7F
+    out, lse_nan = batch.cache.attend(tensor(q, "float16"), **batch.dev, cu_q=batch.cu_dev, return_lse=True)
+    want = f64(clean)
+    host = table[0].cpu().numpy()
+    for j in range(5, 4000, 128):
+        if host[j // 16] >= 0:
+            want[np.arange(200) + 3800 >= j, :, (j // 128) % 64] = np.nan
+    np.testing.assert_array_equal(f64(out), want)
+    assert torch.equal(lse, lse_nan)
+    assert batch.cache.device_status() == (m.MOE_ERR_BAD_PAGE if bad else m.MOE_OK)
