@@ -862,9 +862,11 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           exponents(rb, 1);
           const bool above = top > (room < 0.f ? -INFINITY : kMost), below = top < 0.f && top > -INFINITY && room > 0.f;
           if (__any_sync(0xffffffffu, above | below)) {
-            // new references for the warp's rows: what this unit has summed so
-            // far becomes relative to them
-            const float rise = top > -INFINITY ? fmaxf(top - kNew, room < 0.f ? -INFINITY : -room) : 0.f;
+            // A new reference: what this unit has summed so far becomes
+            // relative to it.  Only for a row that needs one, since the others
+            // (among them rows past the unit's, of any values) must not change
+            // how it is rounded.
+            const float rise = above | below ? fmaxf(top - kNew, room < 0.f ? -INFINITY : -room) : 0.f;
             const float keep = room < 0.f ? 0.f : fast_exp2(-rise);
             base += rise;
             room = room >= 0.f ? fminf(room + rise, kRoom) : top > -INFINITY ? kRoom : room;

@@ -355,3 +355,21 @@ def test_attention_nan_in_many_partial_tiles(bad):
     np.testing.assert_array_equal(f64(out), want)
     assert torch.equal(lse, lse_nan)
     assert batch.cache.device_status() == (m.MOE_ERR_BAD_PAGE if bad else m.MOE_OK)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("new,lens,Hq,Hkv,D", [([120, 33], [270, 183], 6, 2, 80), ([50, 300], [700, 900], 8, 1, 128), ([3, 5], [900, 40], 8, 2, 64)])
+def test_rows_do_not_depend_on_their_neighbours(dtype, new, lens, Hq, Hkv, D):
+    """A sequence's output has the same bits whatever the queries of the next
+    one are, which a tile may hold past its rows."""
+    torch = torch_mod()
+    rng = np.random.default_rng(41)
+    batch = Batch(rng, new, lens, Hkv, 16, D, std=0.5)
+    q = tensor(rounded(rng, (sum(new), Hq, D), dtype), dtype)
+    kw = dict(**batch.dev, cu_q=batch.cu_dev, max_q_len=max(new), return_lse=True)
+    out, lse = batch.cache.attend(q, **kw)
+    for size in (0.0, 30.0, 1000.0):
+        other = q.clone()
+        other[new[0]:] *= size
+        got, got_lse = batch.cache.attend(other, **kw)
+        assert torch.equal(got[:new[0]], out[:new[0]]) and torch.equal(got_lse[:new[0]], lse[:new[0]])
