@@ -589,8 +589,8 @@ int moe_kv_append(const moe_kv_append_args_t* args, moe_stream_t stream);
  * Keys that a row does not see do not touch it, whatever their codes are.
  *
  *   q, out [N, Hq, head_dim] of ``dtype`` (bf16 or f16), 16-byte aligned with
- *     strides that are multiples of 8 elements; Hq a multiple of kv_heads, at
- *     most 256 times it.
+ *     strides that are multiples of 8 elements (q's may be 0 or negative); Hq
+ *     a multiple of kv_heads, at most 256 times it.
  *   lse [N, Hq] float32 or NULL.
  *   block_table, seq_lens, cu_q: as in moe_kv_append.  Rows from cu_q[B] on
  *     are not written.

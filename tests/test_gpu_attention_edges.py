@@ -373,3 +373,40 @@ def test_rows_do_not_depend_on_their_neighbours(dtype, new, lens, Hq, Hkv, D):
         other[new[0]:] *= size
         got, got_lse = batch.cache.attend(other, **kw)
         assert torch.equal(got[:new[0]], out[:new[0]]) and torch.equal(got_lse[:new[0]], lse[:new[0]])
+
+
+# -------------------------------------------------------------------- strides
+
+@pytest.mark.parametrize("dtype,scale", [("bfloat16", 0.2), ("float16", -0.2), ("bfloat16", -0.2), ("float16", 0.2)])
+@pytest.mark.parametrize("new,D", [([1, 1], 64), ([3, 2], 128), ([120, 33], 80), ([300, 2], 64)])
+def test_attention_broadcast_and_reversed_queries(dtype, scale, new, D):
+    """Queries with strides of zero (one for all heads, one for all tokens)
+    and below (tokens and heads backwards) give the bits of a copy of them,
+    whichever kernel the number of rows asks for."""
+    torch = torch_mod()
+    rng = np.random.default_rng(40)
+    Hq, Hkv, N = 6, 2, sum(new)
+    batch = Batch(rng, new, [n + 150 for n in new], Hkv, 16, D, std=0.5)
+    kw = dict(**batch.dev, cu_q=batch.cu_dev, max_q_len=max(new), scale=scale, return_lse=True)
+    one_head = tensor(rounded(rng, (N, 1, D), dtype), dtype).expand(N, Hq, D)
+    one_token = tensor(rounded(rng, (1, Hq, D), dtype), dtype).expand(N, Hq, D)
+    for q in (one_head, one_token):
+        out, lse = batch.cache.attend(q, **kw)
+        want, want_lse = batch.cache.attend(q.contiguous(), **kw)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        ref = ao.attend(f64(q), *batch.codes, *batch.scales, batch.table, batch.lens, batch.cu, scale)[1]
+        assert np.abs(f64(lse) - ref).max() < 1e-2
+    # the library's own interface: from the last token and head backwards
+    q = tensor(rounded(rng, (N, Hq, D), dtype), dtype)
+    want, _ = batch.cache.attend(q.flip(0, 1).contiguous(), **kw)
+    out = torch.empty_like(q)
+    ws = batch.cache.workspace(torch.cuda.current_stream().cuda_stream)
+    c = batch.cache
+    a = m.PagedAttentionArgs(struct_size=248, dtype=m.MOE_DTYPE_BF16 if dtype == "bfloat16" else m.MOE_DTYPE_F16, q=q[-1, -1].data_ptr(),
+                             out=out.data_ptr(), q_stride_token=-Hq * D, q_stride_head=-D, out_stride_token=Hq * D, out_stride_head=D,
+                             block_table=batch.dev["block_table"].data_ptr(), seq_lens=batch.dev["seq_lens"].data_ptr(),
+                             cu_q=batch.cu_dev.data_ptr(), status=c.status.data_ptr(), workspace=ws[0], workspace_bytes=ws[1], N=N, B=len(new),
+                             Hq=Hq, table_width=batch.table.shape[1], max_q_len=max(new), max_seq_len=max(batch.lens), scale=scale)
+    a.cache = m.KvCache(c.k.data_ptr(), c.v.data_ptr(), c.k_scale.data_ptr(), c.v_scale.data_ptr(), *c.k.stride()[:3], *c.v.stride()[:3], *c.k.shape)
+    assert m.lib().moe_paged_attention(bytes(a), torch.cuda.current_stream().cuda_stream) == m.MOE_OK
+    assert torch.equal(out, want) and c.device_status() == m.MOE_OK
