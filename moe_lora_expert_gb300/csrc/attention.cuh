@@ -67,6 +67,14 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// A bf16 row becomes float16 by taking a power of two out of it: its exponent,
+// given that of the row's largest magnitude (-127 to 127; 128: not finite).
+// The largest then lies in [2^14, 2^15), so that all values down to 2^-31 of
+// it stay exact; 112 and -126 hold the ends of bf16's range.
+__device__ __forceinline__ int query_exponent(int largest) {
+  return largest > 127 ? 0 : max(-126, min(112, largest - 14));
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 // Two float32 values to float16, first in the low half.
 __device__ __forceinline__ uint32_t f32x2_to_f16x2(float first, float second) {
   uint32_t r;

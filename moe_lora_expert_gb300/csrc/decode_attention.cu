@@ -12,10 +12,10 @@
 //   out = sum_j w_j code_j / sum_j (w_j / v_scale),
 // so w_j is what multiplies the codes, whatever the pages' scales are, and
 // both sums stay in float32.  Codes enter the tensor cores as float16, which
-// holds each exactly; so it does q, up to the 2^-17 part of a bf16 row's
-// largest value (a power of two is taken out of the row), and the scores are
-// products summed in float32.  The weights are rounded to float16: 2^-12 of
-// each that is normal, which is less than the output's own 8 or 11 bits.
+// holds each exactly; so it does q, down to 2^-31 of a bf16 row's largest
+// value (a power of two is taken out of the row), and the scores are products
+// summed in float32.  The weights are rounded to float16: 2^-12 of each that
+// is normal, which is less than the output's own 8 or 11 bits.
 // Float16 ends at 2^16 and has full precision down to 2^-14 (2^-25 is 0), so m
 // puts the largest weight of each warp's 16 keys of a tile between 2^0 and
 // 2^15: it rises when one would pass that, and falls again when all are below.
@@ -362,14 +362,11 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         if constexpr (!std::is_same<T, __half>::value) {
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          // a power of two that brings the row's largest value into [1, 2)
-          const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-          if (ex > -120 && ex < 120) {
-            scale = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
-            const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+          const int ex = query_exponent(static_cast<int>(__float_as_uint(amax) >> 23) - 127);
+          scale = power_of_two(ex);
+          const float inv = power_of_two(-ex);
 #pragma unroll
-            for (int d = 0; d < DP / 4; ++d) q[d] *= inv;
-          }
+          for (int d = 0; d < DP / 4; ++d) q[d] *= inv;
         }
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {

@@ -766,10 +766,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
                 const uint4 u = *chunk(c);
                 amax = __vmaxu2(amax, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
               }
-              int ex = static_cast<int>(max(amax & 0xFFFF, amax >> 16) >> 7) - 127;
-              if (ex <= -120 || ex >= 120) ex = 0;         // zero, or not finite: nothing to gain
+              const int ex = query_exponent(static_cast<int>(max(amax & 0xFFFF, amax >> 16) >> 7) - 127);
               s.q_exponent[row] = static_cast<int8_t>(ex);
-              float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+              float inv = power_of_two(-ex);
               if (a.scale < 0.f) inv = -inv;               // the sign goes into q, so that a larger score is a larger weight
 #pragma unroll 4
               for (int c = 0; c < DP / 8; ++c) {
@@ -809,7 +808,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       // after a timeout a unit's rows are left as they are, but its part in the
       // join is still played, so that the counters end at zero
       good = good && wait(&s.q_full, units & 1);
-      const float row_scale = kBf16 ? __uint_as_float(static_cast<uint32_t>(127 + s.q_exponent[row]) << 23) : 1.f;
+      const float row_scale = kBf16 ? power_of_two(s.q_exponent[row]) : 1.f;
       // Only now may the next unit's queries come: a unit of one tile has its
       // last scores before its rows' warps have begun it, and two of them
       // would carry q_full past the phase that they wait for.

@@ -410,3 +410,34 @@ def test_attention_broadcast_and_reversed_queries(dtype, scale, new, D):
     a.cache = m.KvCache(c.k.data_ptr(), c.v.data_ptr(), c.k_scale.data_ptr(), c.v_scale.data_ptr(), *c.k.stride()[:3], *c.v.stride()[:3], *c.k.shape)
     assert m.lib().moe_paged_attention(bytes(a), torch.cuda.current_stream().cuda_stream) == m.MOE_OK
     assert torch.equal(out, want) and c.device_status() == m.MOE_OK
+
+
+# ---------------------------------------------------------------- wide queries
+
+@pytest.mark.parametrize("new,lens", [([1, 1], [300, 40]), ([90, 5], [300, 40])])
+@pytest.mark.parametrize("ratio", [20, 28])
+def test_attention_queries_of_a_wide_range(new, lens, ratio):
+    """A bf16 row with one value 2^ratio times the others, in a column where
+    all keys are zero: what the others say is not lost."""
+    rng = np.random.default_rng(42)
+    batch = Batch(rng, new, lens, 2, 16, 64, std=0.5)
+    batch.codes[0][..., 7] = 0
+    batch.cache.k.copy_(tensor(batch.codes[0], torch_mod().uint8))
+    q = rounded(rng, (sum(new), 4, 64), "bfloat16")
+    q[..., 7] = 2.0 ** ratio
+    check_attention(batch, q, "bfloat16", scale=0.3, decode=max(new) == 1)
+
+
+@pytest.mark.parametrize("new,lens", [([1, 1], [300, 40]), ([90, 5], [300, 40])])
+@pytest.mark.parametrize("power", [122, 100, -100, -125])
+def test_attention_queries_at_the_ends_of_their_type(new, lens, power):
+    """bf16 rows near the largest and smallest finite values, with key scales
+    that make ordinary scores of them."""
+    rng = np.random.default_rng(43)
+    batch = Batch(rng, new, lens, 2, 16, 64, std=0.5)
+    back = np.float32(2.0 ** (-power // 2))
+    batch.scales[0] *= back
+    batch.cache.k_scale.copy_(tensor(batch.scales[0], "float32"))
+    q = rounded(rng, (sum(new), 4, 64), "bfloat16") * 2.0 ** power
+    scale = 0.3 * 2.0 ** (-power - (-power // 2))
+    check_attention(batch, f64(tensor(q, "bfloat16")), "bfloat16", scale=float(np.float32(scale)), decode=max(new) == 1)
