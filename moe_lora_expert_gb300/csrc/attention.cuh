@@ -243,7 +243,7 @@ struct KvAppendParams {
   const int32_t *block_table, *seq_lens, *cu_q, *positions;
   const float* cos_sin;
   int32_t* status;
-  int N, B, table_width, R, num_positions, interleaved;
+  int N, B, table_width, max_q_len, R, num_positions, interleaved;
   int slots;                    // pages that one sequence's new tokens can touch
   uint32_t q_items;             // work items of a token's q
 };

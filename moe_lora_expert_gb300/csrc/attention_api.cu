@@ -125,6 +125,7 @@ int moe_kv_append(const moe_kv_append_args_t* a, moe_stream_t stream) {
   p.N = a->N, p.B = a->B, p.table_width = a->table_width, p.R = a->rotary_dim, p.num_positions = a->num_positions;
   p.interleaved = a->interleaved != 0;
   const int longest = a->cu_q == nullptr ? 1 : a->max_q_len < a->N ? a->max_q_len : a->N;
+  p.max_q_len = longest;
   p.slots = (longest + c.page_size - 2) / c.page_size + 1;
   if (2ll * p.B * p.slots * c.kv_heads > (1ll << 30) || static_cast<int64_t>(a->N) * a->Hq * (c.head_dim / 2) > (1ll << 31))
     return MOE_ERR_UNSUPPORTED;

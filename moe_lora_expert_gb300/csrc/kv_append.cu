@@ -107,15 +107,15 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
   u /= ca.kv_heads;
   const int slot = u % p.slots, b = u / p.slots;
   const int t_first = p.cu_q == nullptr ? b : p.cu_q[b];
-  int t_end = p.cu_q == nullptr ? b + 1 : p.cu_q[b + 1];
-  if (t_end > p.N) t_end = p.N;
+  const int t_end = p.cu_q == nullptr ? b + 1 : p.cu_q[b + 1];
   const int len = p.seq_lens[b];
   if (p.cu_q == nullptr && len == 0) return;          // a slot without a sequence
   const int start = len - (t_end - t_first);          // position of the first new token
   const int P = ca.page_size;
   if (start < 0 && tid == 0) set_status(p.status, MOE_ERR_BAD_POSITION);
   const int page_at = (start < 0 ? 0 : start) / P + slot;
-  const int p0 = max(start < 0 ? 0 : start, page_at * P), p1 = min(len, (page_at + 1) * P);
+  const int end = min(len, start + min(p.max_q_len, p.N - t_first));          // after the last token that is appended
+  const int p0 = max(start < 0 ? 0 : start, page_at * P), p1 = min(end, (page_at + 1) * P);
   if (p0 >= p1) return;
   const int page = page_at < p.table_width ? p.block_table[static_cast<int64_t>(b) * p.table_width + page_at] : -1;
   if (page < 0 || page >= ca.num_pages) {

@@ -441,3 +441,33 @@ def test_attention_queries_at_the_ends_of_their_type(new, lens, power):
     q = rounded(rng, (sum(new), 4, 64), "bfloat16") * 2.0 ** power
     scale = 0.3 * 2.0 ** (-power - (-power // 2))
     check_attention(batch, f64(tensor(q, "bfloat16")), "bfloat16", scale=float(np.float32(scale)), decode=max(new) == 1)
+
+
+# ------------------------------------------------------- append, once more
+
+@pytest.mark.parametrize("P,limit", [(16, 5), (16, 1), (8, 20), (64, 33)])
+def test_append_ends_at_max_q_len(P, limit):
+    """A sequence with more new tokens than max_q_len: its first max_q_len
+    are appended, at their places, and nothing else is written."""
+    torch = torch_mod()
+    rng = np.random.default_rng(44)
+    new, lens = [limit + 9, 3, limit], [limit + 40, 30, limit + 1]
+    batch = Batch(rng, new, lens, 2, P, 32)
+    k, v = (tensor(rounded(rng, (sum(new), 2, 32), "bfloat16"), "bfloat16") for _ in range(2))
+    parts = [x.clone() for x in (batch.cache.k, batch.cache.v, batch.cache.k_scale, batch.cache.v_scale)]
+    batch.cache.append(k, v, **batch.dev, cu_q=batch.cu_dev, max_q_len=limit)
+    keep = np.concatenate([np.arange(a, a + min(n, limit)) for a, n in zip(batch.cu, new)])
+    kept = [min(n, limit) for n in new]
+    want = m.PagedKVCache(*[x.clone() for x in parts])
+    want.append(k[keep], v[keep], batch.dev["block_table"], tensor(np.array([e - n + t for n, e, t in zip(new, lens, kept)], np.int32), "int32"),
+                cu_q=tensor(np.cumsum([0] + kept).astype(np.int32), "int32"), max_q_len=limit)
+    for a, b in ((batch.cache.k, want.k), (batch.cache.v, want.v), (batch.cache.k_scale, want.k_scale), (batch.cache.v_scale, want.v_scale)):
+        assert torch.equal(a, b)
+    # tokens that the arrays do not hold are left out, those before them keep their places
+    less = sum(new) - 2
+    again = m.PagedKVCache(*[x.clone() for x in parts])
+    again.append(k[:less], v[:less], **batch.dev, cu_q=batch.cu_dev, max_q_len=max(new))
+    full = m.PagedKVCache(*[x.clone() for x in parts])
+    full.append(k[:less], v[:less], batch.dev["block_table"], tensor(np.array([*lens[:2], lens[2] - 2], np.int32), "int32"),
+                cu_q=tensor(np.array([*batch.cu[:3], less], np.int32), "int32"), max_q_len=max(new))
+    assert torch.equal(again.k, full.k) and torch.equal(again.v_scale, full.v_scale)
