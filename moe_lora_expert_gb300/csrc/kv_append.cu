@@ -18,6 +18,8 @@
 // thread: with 126, which held the rotated stretches, 20.5 us; 4 stretches held
 // instead of 2 the same there, 11.3 instead of 10.3 us on ragged chunks).  64
 // single tokens take 5.8 us: the chain from lengths to table to scale.
+#include <type_traits>
+
 #include "attention.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -48,14 +50,16 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu_q, int B, int t) {
   return lo;
 }
 
-template <int V>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[V], float inv) {
+// Codes of x / by, or of x * by.
+template <bool DIVIDE, int V>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[V], float by) {
+  auto scaled = [&](int i) { return DIVIDE ? x[i] / by : x[i] * by; };
   if constexpr (V == 1) {
-    *p = static_cast<uint8_t>(f32x2_to_e4m3x2(x[0] * inv, 0.f));
+    *p = static_cast<uint8_t>(f32x2_to_e4m3x2(scaled(0), 0.f));
   } else {
     Pack<uint16_t, V / 2> r;
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) r.v[i] = f32x2_to_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+    for (int i = 0; i < V / 2; ++i) r.v[i] = f32x2_to_e4m3x2(scaled(2 * i), scaled(2 * i + 1));
     *reinterpret_cast<Pack<uint16_t, V / 2>*>(p) = r;
   }
 }
@@ -186,22 +190,32 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
   const float s_new = fmaxf(s_old, page_scale(amax));
   const float inv = 1.f / s_new;
 
-  auto put = [&](int j, const Pack<T, V>& pa, const Pack<T, V>& pb) {
+  auto put = [&](int j, const Pack<T, V>& pa, const Pack<T, V>& pb, auto divide) {
     const int r = j / per_head, c = j - r * per_head;
     float a[V], bb[V];
     rotated(j, pa, pb, a, bb);
     const Stretch<V> s(c, turn ? p.R : 0, p.interleaved);
     uint8_t* row = codes + (off + r) * row_bytes;
-    store_codes<V>(row + s.a, a, inv);
-    store_codes<V>(row + s.b, bb, inv);
+    constexpr bool kDivide = decltype(divide)::value;
+    store_codes<kDivide, V>(row + s.a, a, kDivide ? s_new : inv);
+    store_codes<kDivide, V>(row + s.b, bb, kDivide ? s_new : inv);
   };
+  if ((__float_as_uint(s_new) & 0x7FFFFFu) == 0) {
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (tid + i * step < items) put(tid + i * step, ra[i], rb[i]);
-  for (int j = tid + kHeld * step; j < items; j += step) {
-    Pack<T, V> pa, pb;
-    load(j, pa, pb);
-    put(j, pa, pb);
+    for (int i = 0; i < kHeld; ++i)
+      if (tid + i * step < items) put(tid + i * step, ra[i], rb[i], std::false_type());
+    for (int j = tid + kHeld * step; j < items; j += step) {
+      Pack<T, V> pa, pb;
+      load(j, pa, pb);
+      put(j, pa, pb, std::false_type());
+    }
+  } else {   // a scale of the caller's own, which the page has kept: dividing is not multiplying by its inverse
+#pragma unroll 1
+    for (int j = tid; j < items; j += step) {
+      Pack<T, V> pa, pb;
+      load(j, pa, pb);
+      put(j, pa, pb, std::true_type());
+    }
   }
   if (off > 0 && s_new != s_old) {                     // the codes that the page held before
     const float ratio = s_old * inv;

@@ -471,3 +471,30 @@ def test_append_ends_at_max_q_len(P, limit):
     full.append(k[:less], v[:less], batch.dev["block_table"], tensor(np.array([*lens[:2], lens[2] - 2], np.int32), "int32"),
                 cu_q=tensor(np.array([*batch.cu[:3], less], np.int32), "int32"), max_q_len=max(new))
     assert torch.equal(again.k, full.k) and torch.equal(again.v_scale, full.v_scale)
+
+
+@pytest.mark.parametrize("D", [16, 80])
+def test_append_divides_by_a_scale_of_the_callers(D):
+    """Pages that hold tokens under any scale keep it if it is large enough,
+    and the new codes are those of x / scale: here each close to the middle of
+    two codes, where x times the scale's inverse gives the other one."""
+    torch = torch_mod()
+    mids = (ao.E4M3_VALUES[8:0x70] + ao.E4M3_VALUES[9:0x71]) / 2
+    cases = []
+    for x in 1 + np.arange(128) / np.float32(128):
+        for c in mids:
+            s = np.float32(x) / np.float32(c)
+            codes = ao.e4m3_encode([np.float32(x) / s, np.float32(x) * (np.float32(1) / s)])
+            if codes[0] != codes[1]:
+                cases.append((x, s, codes[0]))
+    assert len(cases) > 100
+    x, s, want = (np.array(t) for t in zip(*cases))
+    B = len(cases)
+    cache = m.PagedKVCache(*[torch.zeros((B, 1, 8, D), dtype=torch.uint8, device="cuda") for _ in range(2)],
+                           *[tensor(s.astype(np.float32)[:, None], "float32") for _ in range(2)])
+    k = tensor(np.broadcast_to(x.astype(np.float32)[:, None, None], (B, 1, D)), "bfloat16")
+    cache.append(k, -k, torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous(),
+                 torch.full((B,), 2, dtype=torch.int32, device="cuda"))
+    assert torch.equal(cache.k_scale[:, 0].cpu(), torch.from_numpy(s.astype(np.float32)))
+    assert (cache.k[:, 0, 1].cpu().numpy() == want[:, None]).all()
+    assert (cache.v[:, 0, 1].cpu().numpy() == (want | 0x80)[:, None]).all()
