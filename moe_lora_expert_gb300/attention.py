@@ -125,6 +125,14 @@ def _handle(stream, index):
     return stream.cuda_stream
 
 
+def _record(stream, *tensors):
+    """A call on a stream of the caller's choice uses these: their memory is
+    not given to others before it is done."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _dtype_code(dtype, name):
     code = _codes.get(dtype)
     if code is None:
@@ -305,6 +313,8 @@ def moe_rope(q, positions, cos_sin, k=None, interleaved=False, inverse=False, q_
                       _int32(positions, N, "positions", index), tp,
                       0 if status is None else _int32(status, 4, "status", index),
                       N, Hq, Hk, D, R, rows, interleaved, inverse)
+    if stream is not None:
+        _record(stream, q, k, positions, cos_sin, q_out, k_out, status)
     error = _rope_fn(args, handle) if _current_device() == index else _elsewhere(index, _rope_fn, args, handle)
     if error:
         _raise(error, "moe_rope")
@@ -343,6 +353,7 @@ class PagedKVCache:
         self.status = torch.zeros(4, dtype=torch.int32, device=k.device)
         torch.cuda.current_stream(k.device).synchronize()           # before a call on another stream writes it
         self._status_ptr = self.status.data_ptr()
+        self._tensors = (k, v, k_scale, v_scale, self.status)
         self._bytes = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   *k.stride()[:3], *v.stride()[:3], *k.shape)
         self._index = index
@@ -413,6 +424,8 @@ class PagedKVCache:
             kp, vp, k0, k1, v0, v1, qp, op, q0, q1, o0, o1, bt, sl, cu,
             0 if positions is None else _int32(positions, N, "positions", index), tp, self._status_ptr,
             N, B, Hq, width, longest, R, rows, interleaved)
+        if stream is not None:
+            _record(stream, k, v, q, q_out, block_table, seq_lens, cu_q, cos_sin, positions, *self._tensors)
         error = _append_fn(args, handle) if _current_device() == index else _elsewhere(index, _append_fn, args, handle)
         if error:
             _raise(error, "moe_kv_append")
@@ -452,6 +465,8 @@ class PagedKVCache:
             qp, op, 0 if lse is None else lse.data_ptr(), q0, q1, o0, o1, bt, sl, cu, self._status_ptr, ws[0], ws[1],
             N, B, Hq, width, longest, width * self.page_size if max_seq_len is None else max_seq_len, window,
             wait_timeout_ms, D ** -0.5 if scale is None else scale, debug_flags)
+        if stream is not None:
+            _record(stream, q, out, lse, block_table, seq_lens, cu_q, *self._tensors)
         error = _attend_fn(args, handle) if here else _elsewhere(index, _attend_fn, args, handle)
         if error:
             _raise(error, "moe_paged_attention")

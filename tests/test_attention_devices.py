@@ -32,6 +32,9 @@ class Stand:
     def data_ptr(self):
         return 4096
 
+    def record_stream(self, stream):
+        self.used_on = stream
+
     def moved(self, index):
         return Stand(self.shape, self.dtype, index)
 
@@ -150,3 +153,15 @@ def test_a_cache_is_on_one_device(fake, part):
     parts = cache_parts()
     with pytest.raises(ValueError, match=part):
         m.PagedKVCache(**{**parts, part: parts[part].moved(0)})
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_operands_of_a_call_on_another_stream_are_kept(fake, name):
+    """Their memory may not be handed out while that stream still uses it."""
+    call, args = CALLS[name]
+    args = {k: t.moved(1) for k, t in args.items()}
+    call(**args)
+    assert not any(hasattr(t, "used_on") for t in args.values())
+    stream = Stream(7, 1)
+    call(**args, stream=stream)
+    assert all(t.used_on is stream for t in args.values())

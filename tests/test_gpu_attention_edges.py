@@ -498,3 +498,22 @@ def test_append_divides_by_a_scale_of_the_callers(D):
     assert torch.equal(cache.k_scale[:, 0].cpu(), torch.from_numpy(s.astype(np.float32)))
     assert (cache.k[:, 0, 1].cpu().numpy() == want[:, None]).all()
     assert (cache.v[:, 0, 1].cpu().numpy() == (want | 0x80)[:, None]).all()
+
+
+def test_memory_of_a_call_on_another_stream_is_not_handed_out():
+    """Operands that are dropped while the call still waits on its stream."""
+    torch = torch_mod()
+    batch, _ = decode_batch(45)
+    side = torch.cuda.Stream()
+    q = torch.randn((2, 8, 64), device="cuda").to(torch.bfloat16)
+    want = batch.cache.attend(q, **batch.dev, stream=side)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    mine, size = q.data_ptr(), q.shape
+    out = batch.cache.attend(q, **batch.dev, stream=side)
+    del q
+    taken = [torch.empty(size, dtype=torch.bfloat16, device="cuda") for _ in range(64)]
+    assert all(t.data_ptr() != mine for t in taken)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
