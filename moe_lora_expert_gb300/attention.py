@@ -236,10 +236,12 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[D
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and at least 2")
     R, sc = rotary_dim, dict(scaling or {"kind": "none"})
-    kind = sc.pop("kind")
+    kind = sc.pop("kind", None)
     factor = float(sc.pop("factor", 1.0))
-    if not factor > 0:
-        raise ValueError("factor must be positive")
+    if not 0 < factor < math.inf or not 0 < base < math.inf:
+        raise ValueError("factor and base must be positive and finite")
+    if kind in ("yarn", "llama3") and not float(sc.get("original", 0)) > 0:
+        raise ValueError(f"scaling kind {kind!r} needs the trained length, original > 0")
     mscale = 1.0
     if kind == "ntk" and R > 2:
         base = base * factor ** (R / (R - 2.0))
@@ -249,6 +251,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[D
     elif kind == "yarn":
         original = float(sc.pop("original"))
         fast, slow = float(sc.pop("beta_fast", 32.0)), float(sc.pop("beta_slow", 1.0))
+        if not fast > 0 or not slow > 0 or not base > 1:
+            raise ValueError("yarn needs beta_fast > 0, beta_slow > 0 and base > 1")
         pair = lambda turns: R * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
         lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), R - 1)
         ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(R // 2)]
@@ -258,6 +262,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[D
     elif kind == "llama3":
         original = float(sc.pop("original"))
         low, high = float(sc.pop("low", 1.0)), float(sc.pop("high", 4.0))
+        if not low < high:
+            raise ValueError("llama3 needs low < high")
         blend = [min(max((original * x / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for x in f]
         f = [x / factor * (1 - b) + x * b for x, b in zip(f, blend)]
     elif kind not in ("none", "ntk"):
