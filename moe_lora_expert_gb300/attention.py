@@ -2,7 +2,7 @@
 
 The attention half of a decoder layer, for serving next to ``MoeLoraLayer``:
 
-    cos_sin = rope_table(131072, 128, scaling={"kind": "yarn", "factor": 4.0, "original": 32768})
+    cos_sin = rope_table(131072, 128, scaling={"kind": "yarn", "factor": 4.0, "original": 32768}, device="cuda")
     cache = PagedKVCache.create(num_pages=4096, kv_heads=4, page_size=64, head_dim=128)
     q = cache.append(k, v, block_table, seq_lens, q=q, cos_sin=cos_sin)    # k and q rotated on the way
     out = cache.attend(q, block_table, seq_lens)                           # one new token a sequence

@@ -17,3 +17,10 @@ import moe_lora_expert_gb300 as m
 def test_scaling_that_has_no_angles_is_refused(bad):
     with pytest.raises(ValueError):
         m.rope_frequencies(64, **bad)
+
+
+def test_the_modules_example_runs_where_its_calls_do():
+    """The table of the module's own example is made where the cache is."""
+    import moe_lora_expert_gb300.attention as attention
+    lines = [ln for ln in attention.__doc__.splitlines() if "rope_table(" in ln]
+    assert len(lines) == 1 and 'device="cuda"' in lines[0]
