@@ -605,6 +605,9 @@ int moe_kv_append(const moe_kv_append_args_t* args, moe_stream_t stream);
  *     that runs out reports MOE_ERR_DEVICE_TIMEOUT, the output is then garbage.
  * A table entry outside [0, num_pages) reports MOE_ERR_BAD_PAGE and its keys
  * are left out.
+ * Any positive scales; a value scale below 2^-64, 0 included, counts as 2^-64
+ * (moe_kv_append makes none below 2^-42).  Softmax weights are rounded to
+ * float16, everything else is float32 or exact.
  * ------------------------------------------------------------------------- */
 typedef struct {
   uint32_t struct_size;           /* sizeof(moe_paged_attention_args_t) */

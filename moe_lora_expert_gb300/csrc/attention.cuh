@@ -1,6 +1,6 @@
 // What the kernels of the attention half share: element types, the rotation of
 // one stretch of a head, float8 e4m3 conversions, and the launch interfaces of
-// rope.cu, kv_append.cu and paged_attention.cu.
+// rope.cu, kv_append.cu, decode_attention.cu and prefill_attention.cu.
 #pragma once
 
 #include <cuda.h>

@@ -18,11 +18,17 @@ inline int element_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 // Which attention kernel: rows a key head has (new tokens x query heads of its
 // group) and how many (sequence, key head) pairs there are.  The kernel for
 // few rows reads the cache once for every 16 rows; the other one does 256 rows
-// at the price of 128 and needs some pairs to fill its CTAs.  Both measured,
-// 8 query heads of 128 on each of 4 key heads, few / many in us:
-//   16 sequences of 2048 keys: 16 rows 25 / 40, 32 rows 32 / 40, 64 rows 46 / 40;
-//   8 of 16384: 16 rows 50 / 92, 32 rows 75 / 92, 48 rows 105 / 92;
-//   1 of 32768: 64 rows 46 / 65, 96 rows 61 / 65, 128 rows 77 / 65;  1 of 2048: 96 rows 22 / 34.
+// at the price of 128 and needs some pairs to fill its CTAs.  Both measured on
+// 4 key heads (4 or 8 query heads each: the same times), few / many in us:
+//   heads of 128: 16 sequences of 2048 keys: 16 rows 26 / 37, 32 rows 33 / 37, 48 rows 41 / 37;
+//     8 of 16384: 16 rows 52 / 78, 32 rows 79 / 78;  1 of 32768: 64 rows 49 / 53, 96 rows 64 / 53;
+//     1 of 2048: 96 rows 23 / 30, 192 rows 23 / 33;
+//   heads of 64: 16 of 2048: 32 rows 29 / 30, 48 rows 36 / 30;  8 of 16384: 16 rows 43 / 64, 32 rows 67 / 64;
+//     1 of 32768: 32 rows 31 / 38, 64 rows 43 / 38, 96 rows 56 / 38;  1 of 2048: 96 rows 20 / 24.
+// So 32 rows are where the sides cross for many pairs.  For few pairs it is
+// between 32 and over 192, later the shorter the contexts, whose lengths the
+// host does not have: 96 saves 15 to 25% on a short one and costs up to 46% on
+// one long context (on 8 key heads 77%: 109 / 62).
 bool few_rows(int64_t rows, int64_t pairs) { return rows <= 32 || (rows <= 96 && pairs <= 16); }
 
 // Elements a thread may move at once, of 8, 4 and 1: V elements of a type

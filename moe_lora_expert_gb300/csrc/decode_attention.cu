@@ -15,7 +15,9 @@
 // holds each exactly; so it does q, down to 2^-31 of a bf16 row's largest
 // value (a power of two is taken out of the row), and the scores are products
 // summed in float32.  The weights are rounded to float16: 2^-12 of each that
-// is normal, which is less than the output's own 8 or 11 bits.
+// is normal, an eighth of what a bf16 output is rounded by and as much as a
+// float16 one is (whose error grows from 2.1e-4 to 2.9e-4 by it; two parts to
+// each weight would take it out at twice the products).
 // Float16 ends at 2^16 and has full precision down to 2^-14 (2^-25 is 0), so m
 // puts the largest weight of each warp's 16 keys of a tile between 2^0 and
 // 2^15: it rises when one would pass that, and falls again when all are below.
@@ -26,8 +28,8 @@
 // still lost is under 2^-57 of the largest weight for each key.
 //
 // What bounds it: one pass over the cache's bytes.  64 sequences of up to
-// 32768 keys (8 query heads of 128 on each of 4 key heads) take 211 us, 6.4
-// TB/s, 94% of the copy rate; one token on 262140 keys 57 us (40 at the copy
+// 32768 keys (8 query heads of 128 on each of 4 key heads) take 216 us, 6.2
+// TB/s, 92% of the copy rate; one token on 262140 keys 57 us (40 at the copy
 // rate: the first tiles come after 8 us and the join takes 5).  At smaller
 // sizes it is the chain of latencies from the lengths to the block table, the
 // first tile, and the join: one token on 1022 keys 11 us.
@@ -641,7 +643,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       }
 
       if (split) {
-        // Pieces of this row tile: CTAs [cta0, cta1], joined eight at a time
+        // Pieces of this row tile: CTAs [cta0, cta1], joined kJoin at a time
         // by whoever finishes last among them, then those results likewise.
         const int u0 = x - at.tile, u1 = u0 + at.count;      // its stretch of the line
         const int cta0 = stretch_of(total, ctas, u0), cta1 = stretch_of(total, ctas, u1 - 1), pieces = cta1 - cta0 + 1;

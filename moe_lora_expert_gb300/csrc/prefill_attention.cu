@@ -23,17 +23,18 @@
 // costs a CTA that writes its part or joins it about four key tiles' time, so
 // where whole units can be dealt out nearly as evenly they are.
 //
-// What bounds it.  2 x 2048 tokens of 32 heads of 128 on 4 key heads take 90
-// us, 765 TFLOP/s of what the causal mask leaves, 41% of the measured bf16
+// What bounds it.  2 x 2048 tokens of 32 heads of 128 on 4 key heads take 91.5
+// us, 751 TFLOP/s of what the causal mask leaves, 40% of the measured bf16
 // rate (37 us).  The products of a pair of row tiles and a key tile take 2.05
 // thousand cycles, 2.8 with the gaps between groups of them; a softmax takes
 // about 3 (each row tile's four warps share their schedulers with the other's
 // and the converter's: 0.6 thousand instructions a warp, waits on TMEM and
 // on each other), and a row tile's products and softmax follow one another.
-// For heads of 64 the softmax is the same for half the products: 115 us for
+// For heads of 64 the softmax is the same for half the products: 116 us for
 // ragged chunks on up to 8191 keys, 25%.  Scores of 64 keys in two buffers a
 // row tile took the wait out but cost more than it (an M = 128, N = 64
-// product takes the time of N = 128): 148 against 130 us then.
+// product takes the time of N = 128): 148 against 130 us then.  Looking
+// whether a reference has to fall costs 1 us of the 91.5.
 #include <cuda.h>
 
 #include <type_traits>
