@@ -19,16 +19,24 @@
 // float16 one is (whose error grows from 2.1e-4 to 2.9e-4 by it; two parts to
 // each weight would take it out at twice the products).
 // Float16 ends at 2^16 and has full precision down to 2^-14 (2^-25 is 0), so m
-// puts the largest weight of each warp's 16 keys of a tile between 2^0 and
-// 2^15: it rises when one would pass that, and falls again when all are below.
+// puts the largest weight of each warp's 16 keys of a tile between 2^-8 and
+// 2^15.9: it rises when one would pass that, and falls again when all are below.
 // With m the running maximum alone, one key that takes nearly all of the mass
 // (and whose values may be zero) took the weights of the thousands after it
 // away from the output but not from its denominator.  m falls by 2^24 at most
 // below where it stood highest, and the sums stay inside float32: what is then
-// still lost is under 2^-57 of the largest weight for each key.
+// still lost is under 2^-56 of the largest weight for each key.
+// A fall costs a pass over the sums, and where scores are far apart low tiles
+// lie between others, so that m would have to rise again.  It therefore falls
+// no further than it has to, at every eighth tile, and not for tiles at the
+// end of what a row sees, which have few keys.  The tiles in between lose under
+// 2^-32 of the weight that made m rise, for each key: 2^-23 of the values'
+// range in all.  (64 sequences of 16384 keys with scores of standard deviation
+// 1, 6 and 12: 176, 176 and 179 us, 175 each without the fall; falling in any
+// tile under 2^0, to 2^8: 177, 204 and 206.)
 //
 // What bounds it: one pass over the cache's bytes.  64 sequences of up to
-// 32768 keys (8 query heads of 128 on each of 4 key heads) take 216 us, 6.2
+// 32768 keys (8 query heads of 128 on each of 4 key heads) take 214 us, 6.3
 // TB/s, 92% of the copy rate; one token on 262140 keys 57 us (40 at the copy
 // rate: the first tiles come after 8 us and the join takes 5).  At smaller
 // sizes it is the chain of latencies from the lengths to the block table, the
@@ -71,9 +79,10 @@ constexpr int kJoin = 16;                 // pieces that are joined at a time; 1
 constexpr int kPitch = 128;               // bytes of a key in shared memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNew = 8.f;               // a new reference makes the largest weight 2^8,
-constexpr float kMost = 15.f;             // which may rise to 2^15 (or fall to 2^0) before the sums are rescaled
-constexpr float kRoom = 24.f;             // how far a reference may fall below its highest
+constexpr float kMost = 15.9f, kNew = 7.f;// a weight past 2^15.9 makes the reference rise, so that it becomes 2^7;
+constexpr float kLow = -8.f, kBack = -5.f;// all of a tile's under 2^-8 make it fall, so that the largest becomes 2^-5,
+constexpr float kRoom = 24.f;             // by 2^24 at most below its highest,
+constexpr int kLook = 8;                  // looked for at every eighth tile
 constexpr float kNone = -3.0e38f;         // the reference before any key: every weight is 0 next to it, and its sums are
 
 struct alignas(16) Group {                // 8 keys of a tile, which lie in one page
@@ -437,7 +446,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
           }
           // exponents of the weights, and whether some reference has to move
           const bool whole = key0 + 15 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) && g0.valid && g1.valid;
-          bool near = false;
+          bool move = false;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -451,21 +460,16 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
               sc[t][j] = y;
             }
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              // a row's 16 keys are with the 8 lanes of the same c: where all are low the first lane's two are
-              const float top = fmaxf(sc[t][z], sc[t][z + 2]);
-              near |= top > m[t][z] + kMost || (g == 0 && top < m[t][z]);
-            }
+            for (int z = 0; z < 2; ++z) move |= fmaxf(sc[t][z], sc[t][z + 2]) > m[t][z] + kMost;
           }
-          bool move = false;
-          if (__any_sync(0xffffffffu, near)) {
+          const bool look = whole && i % kLook == 0;
+          if (look) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const float top = fmaxf(sc[t][z], sc[t][z + 2]);
-                const unsigned up = __ballot_sync(0xffffffffu, !(top < m[t][z]));
-                move |= top > m[t][z] + kMost || ((up & 0x11111111u << c) == 0 && m[t][z] > least[t][z]);
+              for (int z = 0; z < 2; ++z) {  // a row's 16 keys are with the 8 lanes of the same c
+                const unsigned up = __ballot_sync(0xffffffffu, !(fmaxf(sc[t][z], sc[t][z + 2]) < m[t][z] + kLow));
+                move |= (up & 0x11111111u << c) == 0 && m[t][z] > least[t][z];
               }
           }
           if (__any_sync(0xffffffffu, move)) {
@@ -477,8 +481,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 #pragma unroll
                 for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
                 float now = m[t][z];
-                if (top > m[t][z] + kMost) now = top - kNew;
-                if (top < m[t][z] && top > -INFINITY && m[t][z] > least[t][z]) now = fmaxf(top - kNew, least[t][z]);
+                if (top > m[t][z] + kNew) now = top - kNew;
+                if (look && top < m[t][z] + kLow && m[t][z] > least[t][z]) now = fmaxf(top - kBack, least[t][z]);
                 const float keep = fast_exp2(m[t][z] - now);
                 m[t][z] = now;
                 least[t][z] = fmaxf(least[t][z], now - kRoom);

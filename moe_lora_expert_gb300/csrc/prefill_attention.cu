@@ -23,8 +23,8 @@
 // costs a CTA that writes its part or joins it about four key tiles' time, so
 // where whole units can be dealt out nearly as evenly they are.
 //
-// What bounds it.  2 x 2048 tokens of 32 heads of 128 on 4 key heads take 91.5
-// us, 751 TFLOP/s of what the causal mask leaves, 40% of the measured bf16
+// What bounds it.  2 x 2048 tokens of 32 heads of 128 on 4 key heads take 90.6
+// us, 759 TFLOP/s of what the causal mask leaves, 40% of the measured bf16
 // rate (37 us).  The products of a pair of row tiles and a key tile take 2.05
 // thousand cycles, 2.8 with the gaps between groups of them; a softmax takes
 // about 3 (each row tile's four warps share their schedulers with the other's
@@ -33,8 +33,10 @@
 // For heads of 64 the softmax is the same for half the products: 116 us for
 // ragged chunks on up to 8191 keys, 25%.  Scores of 64 keys in two buffers a
 // row tile took the wait out but cost more than it (an M = 128, N = 64
-// product takes the time of N = 128): 148 against 130 us then.  Looking
-// whether a reference has to fall costs 1 us of the 91.5.
+// product takes the time of N = 128): 148 against 130 us then.  A reference
+// that falls as well costs nothing on scores of standard deviation 1 and 3
+// (91 and 99 us), 1% on 6 and 2% on 12 there; 1, 1, 5 and 12% on chunks of 1000
+// with heads of 64.
 #include <cuda.h>
 
 #include <type_traits>
@@ -65,9 +67,10 @@ constexpr int kNanTiles = 8;               // tiles with NaN that a warp notes f
 constexpr int kConvertWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNew = 8.f;                // as in decode_attention.cu: a new reference makes the largest weight 2^8,
-constexpr float kMost = 15.f;              // which may rise to 2^15 or fall to 2^0 before the sums are rescaled;
-constexpr float kRoom = 24.f;              // how far a reference may fall below its highest
+constexpr float kMost = 15.9f, kNew = 7.f; // as in decode_attention.cu: a weight past 2^15.9 makes the reference rise, so that it becomes 2^7;
+constexpr float kLow = -8.f, kBack = -5.f; // all of 64 keys' under 2^-8 make it fall, so that the largest becomes 2^-5,
+constexpr float kRoom = 24.f;              // by 2^24 at most below its highest,
+constexpr int kLook = 4;                   // looked for at every fourth tile
 constexpr int kOColumns = 256;             // TMEM: two row tiles' scores, then their sums, 128 columns each
 
 struct alignas(16) Group {                 // 8 keys, which lie in one page
@@ -833,8 +836,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       const int pos_lo = en.position(kTileRows * i, group);
       const int pos_hi = en.position(min(en.rows, kTileRows * (i + 1)) - 1, group) - a.window;
       // weights are relative to 2^base; a row's room is how far the base may
-      // still fall, negative before the row's first key
-      float base = 0.f, room = -1.f, l = 0.f;
+      // still fall, negative before the row's first key.  Rows past the unit's
+      // have weights of zero, whatever their queries are.
+      float base = row < en.rows ? 0.f : INFINITY, room = -1.f, l = 0.f;
 
 #pragma unroll 1
       for (int j = 0; j < walk.n && good; ++j, ++t, ++s_count) {
@@ -887,13 +891,13 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           };
           exponents(ra, 0);
           exponents(rb, 1);
-          const bool above = top > (room < 0.f ? -INFINITY : kMost), below = top < 0.f && top > -INFINITY && room > 0.f;
+          const bool above = top > (room < 0.f ? -INFINITY : kMost), below = all && j % kLook == 0 && top < kLow && room > 0.f;
           if (__any_sync(0xffffffffu, above | below)) {
-            // A new reference: what this unit has summed so far becomes
-            // relative to it.  Only for a row that needs one, since the others
-            // (among them rows past the unit's, of any values) must not change
-            // how it is rounded.
-            const float rise = above | below ? fmaxf(top - kNew, room < 0.f ? -INFINITY : -room) : 0.f;
+            // New references: what this unit has summed so far becomes relative
+            // to them.  A row that would rise by less gets one too, since it
+            // costs nothing more (without: 107 instead of 99 us on 2 x 2048
+            // tokens with scores of standard deviation 3).
+            const float rise = room < 0.f ? (top > -INFINITY ? top - kNew : 0.f) : top > kNew ? top - kNew : below ? fmaxf(top - kBack, -room) : 0.f;
             const float keep = room < 0.f ? 0.f : fast_exp2(-rise);
             base += rise;
             room = room >= 0.f ? fminf(room + rise, kRoom) : top > -INFINITY ? kRoom : room;

@@ -55,20 +55,36 @@ def test_lse_of_many_small_weights_beside_a_large_one(new, B, Hq, keys, rest):
 
 # ---------------------------------------------- one key that takes nearly all
 #
-# A weight is a float16 of half step 2^-25 where it is subnormal, and the
-# largest weight among 64 keys that follow one another is kept at 2^0 or more,
-# unless it is under 2^-32 of the row's largest.  A key's code is 448 at most
-# and the largest weight w of its 64 stands for the probability p: dividing by
-# the sum turns 2^-25 * 448 into at most 2^-25 * 448 * p v_scale of that key.
-# So the tests' bound has, in place of a term that knows nothing of how many
-# keys there are,
-#   2^-25 * 448 * sum over runs of 64 keys of 64 max (p v_scale)
-#   + 2^-57 * 448 * keys * max (p v_scale).
+# A weight 2^(y - b) is a float16, off by 2^-25 where it is subnormal; a key's
+# exponent y stands for p v_scale = 2^y / Z.  So a key loses at most 2^-25
+# |code| 2^b / Z of the output, and no more than its own part p |v|.  The
+# reference b is 7 below some earlier key's exponent when it rises, so 2^b / Z
+# <= 2^-7 max (p v_scale) at all times.  It falls when 64 keys that follow one
+# another, and that all rows of a tile see, are more than 8 below it, which is
+# looked for at one of 8 such runs at least.  So among 9 runs of 64 keys one
+# made it rise, or is not that low, or made it fall: at the last of them 2^b / Z
+# <= 2^8 max (p v_scale) over the 9, unless b stands 31 below the row's largest
+# already.
+# Keys that not all rows of a tile see are among the last 192 that a row sees:
+# there b is what the runs before left, or 7 below one of their own.  The
+# tests' bound has, in place of a term that knows nothing of how many keys
+# there are, the sum of that over the keys.
 
-def lost_weights(p, vs):
-    """That term for probabilities p [rows, keys] and value scales vs [keys]."""
-    top = np.pad(p * vs, ((0, 0), (0, -p.shape[1] % 64))).reshape(len(p), -1, 64).max(-1)
-    return 2.0 ** -25 * 448 * 64 * top.sum(-1) + 2.0 ** -57 * 448 * p.shape[1] * top.max(-1)
+def lost_weights(p, vs, codes):
+    """That term for probabilities p [rows, keys], value scales vs [keys] and
+    value codes [keys, columns]: [rows, columns]."""
+    pad, D = -p.shape[1] % 64, codes.shape[1]
+    runs = lambda x: np.pad(x, ((0, 0), (0, pad))).reshape(len(x), -1, 64)   # noqa: E731
+    top, size = runs(p * vs).max(-1), np.pad(np.abs(codes), ((0, pad), (0, 0))).reshape(-1, 64, D)
+    before = np.pad(top, ((0, 0), (8, 0)))
+    nine = np.max([before[:, i:i + top.shape[1]] for i in range(9)], axis=0)
+    most = top.max(-1, keepdims=True)
+    at = np.minimum(2.0 ** 8 * nine, 2.0 ** -7 * most)
+    for r, row in enumerate(p):
+        first = max(1, (np.flatnonzero(row)[-1] - 191) // 64)         # of the runs with keys that not all rows see
+        at[r, first:] = min(max(2.0 ** 8 * nine[r, first - 1], 2.0 ** -7 * top[r, first:].max()), 2.0 ** -7 * most[r, 0])
+    own = np.einsum("rck,ckd->rcd", runs(p * vs), size, optimize=True)
+    return np.minimum(2.0 ** -25 * (at + 2.0 ** -31 * most)[..., None] * size.sum(1), own).sum(1)
 
 
 @pytest.mark.parametrize("new,B,Hq", [(1, 64, 16), (4, 32, 32), (64, 20, 32)])   # 2, 16 and 256 rows a key head
@@ -96,7 +112,7 @@ def test_attention_sink(new, B, Hq, keys, rest, std, at, shift):
     v[page] = 0
     vs[page] *= 2.0 ** shift
     kv, vv = ao.E4M3_VALUES[k[order]] * 2.0 ** -5, ao.E4M3_VALUES[v[order]] * vs[order][:, :, None, None]
-    kv, vv = (x.transpose(1, 0, 2, 3).reshape(Hkv, keys, D) for x in (kv, vv))
+    kv, vv, code = (x.transpose(1, 0, 2, 3).reshape(Hkv, keys, D) for x in (kv, vv, ao.E4M3_VALUES[v[order]]))
     q = rounded(rng, (B * new, Hq, D), "bfloat16", std)
     G = Hq // Hkv
     rows = [b * new + t for b in (0, B - 1) for t in {0, new // 2, new - 1}]
@@ -123,7 +139,7 @@ def test_attention_sink(new, B, Hq, keys, rest, std, at, shift):
         if h == 0:
             assert 0.5 * rest < 1 - p[0, at] < 2 * rest       # the case is what it is meant to be
         ref, spread = p @ vv[h // G], p @ np.abs(vv[h // G])
-        bound = ((2.0 ** -11 + 4 * es + 2.0 ** -17)[:, None] * spread + lost_weights(p, np.repeat(vs[order, h // G], P))[:, None]
+        bound = ((2.0 ** -11 + 4 * es + 2.0 ** -17)[:, None] * spread + lost_weights(p, np.repeat(vs[order, h // G], P), code[h // G])
                  + 1.01 * HALF_STEP["bfloat16"] * np.abs(ref))
         err = np.abs(out[rows, h] - ref)
         assert (err <= bound).all(), (h, float((err / np.abs(ref)).max()), float((bound / np.abs(ref)).max()))
