@@ -501,6 +501,30 @@ typedef struct {
 int moe_rope(const moe_rope_args_t* args, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * moe_rope_axes -- moe_rope for tokens that have a position on each of
+ * several axes: time, height and width of images and video.
+ *
+ * Pair i turns by the position on its axis, p = positions[axis_of_pair[i]][t],
+ * with its own column of the table as in moe_rope:
+ *   u' = u C[p,i] - w S[p,i],   w' = w C[p,i] + u S[p,i].
+ *   args: as in moe_rope, but positions are [num_axes][N], axis a's beginning
+ *     at a * positions_stride elements.  A token with a position outside
+ *     [0, num_positions) on any axis stays unturned and reports
+ *     MOE_ERR_BAD_POSITION.
+ *   axes->axis_of_pair: rotary_dim / 2 axes below num_axes; they travel with
+ *     the launch, so a captured graph keeps them.  The rest is not read.
+ * Limits: 1 <= num_axes <= 4, positions_stride >= 0 (0: all axes alike).
+ * ------------------------------------------------------------------------- */
+#define MOE_MAX_ROPE_AXES 4
+typedef struct {
+  uint32_t struct_size;           /* sizeof(moe_rope_axes_t) */
+  int num_axes;
+  int64_t positions_stride;
+  uint8_t axis_of_pair[512];
+} moe_rope_axes_t;
+int moe_rope_axes(const moe_rope_args_t* args, const moe_rope_axes_t* axes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * A paged cache of float8 e4m3 codes (max 448, 0x7F / 0xFF are NaN).
  *
  * Page g holds page_size tokens of kv_heads heads of head_dim codes; the code
@@ -575,6 +599,11 @@ typedef struct {
   int N, B, Hq, table_width, max_q_len, rotary_dim, num_positions, interleaved;
 } moe_kv_append_args_t;
 int moe_kv_append(const moe_kv_append_args_t* args, moe_stream_t stream);
+
+/* moe_kv_append with keys and queries turned as in moe_rope_axes: positions,
+ * which may not be NULL, are [num_axes][N].  They are the angles' alone; a
+ * token's place in the cache is still its place in its sequence. */
+int moe_kv_append_axes(const moe_kv_append_args_t* args, const moe_rope_axes_t* axes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * moe_paged_attention -- causal attention of new tokens over the cache, their

@@ -17,7 +17,7 @@ from __future__ import annotations
 import ctypes
 import math
 import struct
-from typing import Dict, Optional
+from typing import Dict, Optional, Sequence
 
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F16 = 1
@@ -57,6 +57,11 @@ class KvAppendArgs(ctypes.Structure):
                                               "num_positions", "interleaved")]]
 
 
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("num_axes", ctypes.c_int), ("positions_stride", ctypes.c_int64),
+                ("axis_of_pair", ctypes.c_uint8 * 512)]
+
+
 class PagedAttentionArgs(ctypes.Structure):
     _fields_ = [("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_int), ("cache", KvCache),
                 *[(n, ctypes.c_void_p) for n in ("q", "out", "lse")],
@@ -76,12 +81,13 @@ _CACHE = struct.Struct("=4Q6q4i")
 _HEAD = struct.Struct("=Ii")
 _APPEND = struct.Struct("=2Q4q2Q4q6Q8i")
 _ATTEND = struct.Struct("=3Q4q6Q8ifI")
+_AXES = struct.Struct("=Iiq512s")
 
 # What the entry points use on every call, bound by the first one (torch is
 # imported lazily, as in the rest of the package).
 _torch = _int32_type = _float32_type = None
 _codes: Dict = {}
-_rope_fn = _append_fn = _attend_fn = _raw_stream = _empty_like = _capturing = _current_device = None
+_rope_fn = _append_fn = _attend_fn = _rope_axes_fn = _append_axes_fn = _raw_stream = _empty_like = _capturing = _current_device = None
 
 # Scratch of attention calls: calls on one stream follow one another and share
 # it, whatever their cache; a captured call runs when its graph does, so each
@@ -92,7 +98,7 @@ _captured: Dict = {}         # (device index, stream handle): (capture id, works
 
 def _bind():
     global _torch, _int32_type, _float32_type, _rope_fn, _append_fn, _attend_fn, _raw_stream, _empty_like, _capturing
-    global _current_device
+    global _current_device, _rope_axes_fn, _append_axes_fn
     import torch
     from . import lib
     L = lib()
@@ -101,6 +107,7 @@ def _bind():
     _append_fn, _attend_fn, _raw_stream = L.moe_kv_append, L.moe_paged_attention, torch._C._cuda_getCurrentRawStream
     _empty_like, _capturing = torch.empty_like, torch.cuda.is_current_stream_capturing
     _current_device = torch._C._cuda_getDevice
+    _rope_axes_fn, _append_axes_fn = L.moe_rope_axes, L.moe_kv_append_axes
     _rope_fn, _torch = L.moe_rope, torch
 
 
@@ -215,6 +222,20 @@ def _table(cos_sin, index):
     return cos_sin.data_ptr(), shape[0], shape[1]
 
 
+def _axis_args(axes, positions, N, R, index):
+    """(pointer of the positions [axes, N], the axes' struct as bytes)."""
+    if type(axes) is not bytes:
+        axes = bytes(axes)
+    if positions is None or positions.dtype is not _int32_type or positions.get_device() != index or positions.dim() != 2:
+        raise ValueError(f"positions must be an int32 tensor [axes, {N}] on cuda:{index}")
+    A = positions.shape[0]
+    if positions.shape[1] != N or (N > 1 and positions.stride(1) != 1):
+        raise ValueError(f"positions must have shape [axes, {N}] and be contiguous along the tokens, got {tuple(positions.shape)}")
+    if R == 0 or 2 * len(axes) != R or not 1 <= A <= 4 or max(axes) >= A:
+        raise ValueError(f"axes must name one of {A} axes (4 at most) for each of rotary_dim / 2 = {R // 2} pairs")
+    return positions.data_ptr(), _AXES.pack(528, A, positions.stride(0), axes)
+
+
 # ----------------------------------------------------------------------------
 # Angles
 # ----------------------------------------------------------------------------
@@ -273,23 +294,49 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[D
     return f, mscale
 
 
+def rope_axes(sections: Sequence[int], turns: bool = False) -> bytes:
+    """The axis of each pair of columns, for ``axes`` of moe_rope and append:
+    sections[a] pairs turn by the position on axis a (time, height, width, ...).
+    A run of pairs for each axis, or, with ``turns``, the axes one after another
+    for as long as each has pairs left (of [3, 1, 2]: 0 1 2 0 2 0)."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0 or sum(left) < 1:
+        raise ValueError("sections: how many pairs each of one to four axes has")
+    if not turns:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    return bytes(a for i in range(max(left)) for a, n in enumerate(left) if i < n)
+
+
 def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0,
-               scaling: Optional[Dict] = None, device=None):
+               scaling: Optional[Dict] = None, device=None, axes: Optional[bytes] = None):
     """float32 [max_positions, rotary_dim]: cosines, then sines, of each
-    position's angles, computed in float64.  Made once, at load time."""
+    position's angles, computed in float64.  Made once, at load time.  Without
+    ``axes`` the frequencies fall over all pairs, whatever axes these are given
+    in a call; with it (see ``rope_axes``) each axis's pairs have frequencies of
+    their own that begin at the fastest, as for an image's height and width."""
     import torch
-    f, mscale = rope_frequencies(rotary_dim, base, scaling)
+    if axes is None:
+        f, mscale = rope_frequencies(rotary_dim, base, scaling)
+    else:
+        if 2 * len(axes) != rotary_dim:
+            raise ValueError("axes must name an axis for each of rotary_dim / 2 pairs")
+        own = {a: rope_frequencies(2 * list(axes).count(a), base, scaling) for a in set(axes)}
+        mscale = next(iter(own.values()))[1]
+        rest = {a: iter(fs) for a, (fs, _) in own.items()}
+        f = [next(rest[a]) for a in axes]
     at = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None]
     at = at * torch.tensor(f, dtype=torch.float64, device=device)
     return torch.cat([at.cos() * mscale, at.sin() * mscale], dim=1).float()
 
 
 def moe_rope(q, positions, cos_sin, k=None, interleaved=False, inverse=False, q_out=None, k_out=None,
-             status=None, stream=None):
+             status=None, stream=None, axes=None):
     """q [N, Hq, D] (and k [N, Hk, D]) rotated by ``positions`` int32 [N]; the
     columns past the table's rotary_dim are copied.  Returns q_out, or (q_out,
     k_out); pass the inputs as outputs to rotate in place.  ``inverse``: the
-    gradient of the forward for an upstream gradient in q's place."""
+    gradient of the forward for an upstream gradient in q's place.  ``axes``
+    (see ``rope_axes``): positions are [axes, N], and each pair turns by the
+    one on its axis."""
     if _rope_fn is None:
         _bind()
     N, Hq, D = q.shape
@@ -315,15 +362,21 @@ def moe_rope(q, positions, cos_sin, k=None, interleaved=False, inverse=False, q_
         else:
             kop, ko0, ko1 = _heads(k_out, N, Hk, D, dtype, "k_out", index)
     tp, rows, R = _table(cos_sin, index)
-    args = _ROPE.pack(160, code, qp, op, kp, kop, q0, q1, o0, o1, k0, k1, ko0, ko1,
-                      _int32(positions, N, "positions", index), tp,
+    if axes is None:
+        pp = _int32(positions, N, "positions", index)
+    else:
+        pp, turn = _axis_args(axes, positions, N, R, index)
+    args = _ROPE.pack(160, code, qp, op, kp, kop, q0, q1, o0, o1, k0, k1, ko0, ko1, pp, tp,
                       0 if status is None else _int32(status, 4, "status", index),
                       N, Hq, Hk, D, R, rows, interleaved, inverse)
     if stream is not None:
         _record(stream, q, k, positions, cos_sin, q_out, k_out, status)
-    error = _rope_fn(args, handle) if _current_device() == index else _elsewhere(index, _rope_fn, args, handle)
+    if axes is None:
+        error = _rope_fn(args, handle) if _current_device() == index else _elsewhere(index, _rope_fn, args, handle)
+    else:
+        error = _rope_axes_fn(args, turn, handle) if _current_device() == index else _elsewhere(index, _rope_axes_fn, args, turn, handle)
     if error:
-        _raise(error, "moe_rope")
+        _raise(error, "moe_rope" if axes is None else "moe_rope_axes")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -403,12 +456,13 @@ class PagedKVCache:
         return B, width, block_table.data_ptr(), sl, cu, N if max_q_len is None else max_q_len
 
     def append(self, k, v, block_table, seq_lens, cu_q=None, max_q_len=None, q=None, cos_sin=None,
-               interleaved=False, positions=None, q_out=None, stream=None):
+               interleaved=False, positions=None, q_out=None, stream=None, axes=None):
         """The new tokens' k (rotated by ``cos_sin``) and v, [N, kv_heads,
         head_dim], go into the pages of their sequences: tokens [cu_q[b],
         cu_q[b + 1]) (one each without cu_q) end at seq_lens[b]; a slot whose
         seq_lens is 0 without cu_q stands for no sequence.  ``q`` [N, Hq,
-        head_dim] is rotated in the same launch and returned."""
+        head_dim] is rotated in the same launch and returned.  ``axes``:
+        positions [axes, N] and an axis for each pair, as in moe_rope."""
         N, D, H, index = k.shape[0], self.head_dim, self.kv_heads, self._index
         dtype = k.dtype
         code = _dtype_code(dtype, "k")
@@ -426,15 +480,21 @@ class PagedKVCache:
                 op, o0, o1 = _heads(q_out, N, Hq, D, dtype, "q_out", index)
         B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
         tp, rows, R = (0, 0, 0) if cos_sin is None else _table(cos_sin, index)
+        if axes is None:
+            pp = 0 if positions is None else _int32(positions, N, "positions", index)
+        else:
+            pp, turn = _axis_args(axes, positions, N, R, index)
         args = _HEAD.pack(280, code) + self._bytes + _APPEND.pack(
-            kp, vp, k0, k1, v0, v1, qp, op, q0, q1, o0, o1, bt, sl, cu,
-            0 if positions is None else _int32(positions, N, "positions", index), tp, self._status_ptr,
+            kp, vp, k0, k1, v0, v1, qp, op, q0, q1, o0, o1, bt, sl, cu, pp, tp, self._status_ptr,
             N, B, Hq, width, longest, R, rows, interleaved)
         if stream is not None:
             _record(stream, k, v, q, q_out, block_table, seq_lens, cu_q, cos_sin, positions, *self._tensors)
-        error = _append_fn(args, handle) if _current_device() == index else _elsewhere(index, _append_fn, args, handle)
+        if axes is None:
+            error = _append_fn(args, handle) if _current_device() == index else _elsewhere(index, _append_fn, args, handle)
+        else:
+            error = _append_axes_fn(args, turn, handle) if _current_device() == index else _elsewhere(index, _append_axes_fn, args, turn, handle)
         if error:
-            _raise(error, "moe_kv_append")
+            _raise(error, "moe_kv_append" if axes is None else "moe_kv_append_axes")
         return q_out
 
     def attend(self, q, block_table, seq_lens, cu_q=None, max_q_len=None, max_seq_len=None, scale=None,

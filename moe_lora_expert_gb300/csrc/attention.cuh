@@ -114,6 +114,57 @@ __device__ __forceinline__ void load_cos_sin(const float* row, int c, int R, flo
   load_f32<float, V>(row + R / 2 + V * c, sn);
 }
 
+// Positions of several axes (time, height, width): each pair has an axis, two
+// bits each in of_pair, and a token a position on each axis, [count][N] with
+// ``stride`` between axes.  By value with a launch, so that a captured call
+// keeps it.
+constexpr int kMaxAxes = 4, kMaxPairs = 512;
+struct RopeAxes {
+  int64_t stride;
+  int count;
+  uint32_t of_pair[kMaxPairs / 16];
+};
+struct OneAxis {};
+// A token's position on each axis.  Whether all are in the table.
+struct AxisPositions {
+  int on[kMaxAxes];
+  __device__ __forceinline__ bool load(const RopeAxes& axes, const int32_t* positions, int64_t t, int num_positions) {
+    bool good = true;
+#pragma unroll
+    for (int a = 0; a < kMaxAxes; ++a) {
+      on[a] = a < axes.count ? positions[a * axes.stride + t] : 0;
+      good &= a >= axes.count || (on[a] >= 0 && on[a] < num_positions);
+    }
+    return good;
+  }
+};
+// cos and sin of frequencies [Vc, Vc + V), each at its own axis's position: a
+// table row's run where they have one axis, else a run of each axis's row and
+// from it what is that axis's.
+template <int V>
+__device__ __forceinline__ void load_cos_sin(const float* cos_sin, const AxisPositions& pos, const RopeAxes& axes, int c, int R,
+                                             float (&cs)[V], float (&sn)[V]) {
+  constexpr uint32_t kEach = 0x55555555u >> (32 - 2 * V);
+  const uint32_t bits = axes.of_pair[V * c / 16] >> (2 * (V * c % 16)) & (3 * kEach);
+#pragma unroll
+  for (int a = 0; a < kMaxAxes; ++a) {
+    const uint32_t other = bits ^ (a * kEach), mine = ~(other | other >> 1) & kEach;   // a bit for each pair on axis a
+    if (mine == 0) continue;
+    const float* row = cos_sin + static_cast<int64_t>(pos.on[a]) * R;
+    if (mine == kEach) {
+      load_cos_sin<V>(row, c, R, cs, sn);
+    } else {
+      float x[V], y[V];
+      load_cos_sin<V>(row, c, R, x, y);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        cs[i] = mine >> (2 * i) & 1 ? x[i] : cs[i];
+        sn[i] = mine >> (2 * i) & 1 ? y[i] : sn[i];
+      }
+    }
+  }
+}
+
 // (u, w) -> (u cos - w sin, w cos + u sin), in float32.  ROUNDED: each product
 // is rounded, for keys that become codes.  Next to the table's rounding that
 // changes little, but a key close to the middle of two codes then gets the
@@ -203,12 +254,24 @@ struct RotationItem {
     const Stretch<V> s(c, R, interleaved);
     const bool turn = s.turned && pos >= 0;
     float cs[V], sn[V];
-    if (turn) {
-      load_cos_sin<V>(cos_sin + static_cast<int64_t>(pos) * R, c, R, cs, sn);
-      if (inverse) {
+    if (turn) load_cos_sin<V>(cos_sin + static_cast<int64_t>(pos) * R, c, R, cs, sn);
+    write(x, y, s, turn, interleaved, inverse, cs, sn);
+  }
+  // With an axis for each pair; ``good``: all of the token's positions are in the table.
+  __device__ __forceinline__ void finish(const RopeTensor& x, const RopeTensor& y, const AxisPositions& pos, bool good, const RopeAxes& axes,
+                                         int R, bool interleaved, bool inverse, const float* cos_sin) const {
+    if (!live) return;
+    const Stretch<V> s(c, R, interleaved);
+    const bool turn = s.turned && good;
+    float cs[V], sn[V];
+    if (turn) load_cos_sin<V>(cos_sin, pos, axes, c, R, cs, sn);
+    write(x, y, s, turn, interleaved, inverse, cs, sn);
+  }
+  __device__ __forceinline__ void write(const RopeTensor& x, const RopeTensor& y, const Stretch<V>& s, bool turn, bool interleaved, bool inverse,
+                                        const float (&cs)[V], float (&sn)[V]) const {
+    if (turn && inverse) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) sn[i] = -sn[i];
-      }
+      for (int i = 0; i < V; ++i) sn[i] = -sn[i];
     }
 #pragma unroll
     for (int u = 0; u < HEADS; ++u) {
@@ -233,7 +296,7 @@ struct RopeParams {
   int32_t* status;
   int N, D, R, num_positions, interleaved, inverse;
 };
-cudaError_t launch_rope(const RopeParams& p, int dtype, int V, cudaStream_t s);
+cudaError_t launch_rope(const RopeParams& p, const RopeAxes* axes, int dtype, int V, cudaStream_t s);   // axes: NULL = one
 
 struct KvAppendParams {
   moe_kv_cache_t cache;
@@ -247,7 +310,7 @@ struct KvAppendParams {
   int slots;                    // pages that one sequence's new tokens can touch
   uint32_t q_items;             // work items of a token's q
 };
-cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, int V, cudaStream_t s);
+cudaError_t launch_kv_append(const KvAppendParams& p, const RopeAxes* axes, int dtype, int V, cudaStream_t s);
 
 // Attention.  A "row" is one (new token, query head) of a key head's group:
 // row r of sequence b and key head h is token r / group, query head h * group

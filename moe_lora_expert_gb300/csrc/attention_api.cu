@@ -8,6 +8,7 @@ namespace {
 
 using moe::AttentionParams;
 using moe::KvAppendParams;
+using moe::RopeAxes;
 using moe::RopeParams;
 using moe::RopeTensor;
 
@@ -70,17 +71,34 @@ int check_batch(int N, int B, int table_width, int max_q_len, const int32_t* tab
   return MOE_OK;
 }
 
-}  // namespace
+// The axes of a rotation's pairs, two bits each.
+int pack_axes(const moe_rope_axes_t* x, int rotary_dim, RopeAxes* to) {
+  if (x == nullptr) return MOE_ERR_NULL;
+  if (x->struct_size != sizeof(*x)) return MOE_ERR_UNSUPPORTED;
+  if (x->num_axes < 1 || x->positions_stride < 0 || rotary_dim < 2) return MOE_ERR_SHAPE;
+  if (x->num_axes > moe::kMaxAxes || rotary_dim > 2 * moe::kMaxPairs) return MOE_ERR_UNSUPPORTED;
+  *to = RopeAxes{};
+  to->stride = x->positions_stride;
+  to->count = x->num_axes;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    if (x->axis_of_pair[i] >= x->num_axes) return MOE_ERR_SHAPE;
+    to->of_pair[i / 16] |= static_cast<uint32_t>(x->axis_of_pair[i]) << (2 * (i % 16));
+  }
+  return MOE_OK;
+}
 
-extern "C" {
-
-int moe_rope(const moe_rope_args_t* a, moe_stream_t stream) {
+int rope(const moe_rope_args_t* a, bool with_axes, const moe_rope_axes_t* x, moe_stream_t stream) {
   if (a == nullptr) return MOE_ERR_NULL;
   if (a->struct_size != sizeof(*a)) return MOE_ERR_UNSUPPORTED;
   if (a->dtype < MOE_DTYPE_BF16 || a->dtype > MOE_DTYPE_F32) return MOE_ERR_UNSUPPORTED;
   if (a->N < 0 || a->Hq < 0 || a->Hk < 0 || a->D <= 0 || a->rotary_dim < 2 || a->rotary_dim > a->D ||
       a->rotary_dim % 2 != 0 || a->D % 2 != 0 || a->num_positions < 0)
     return MOE_ERR_SHAPE;
+  RopeAxes axes;
+  if (with_axes) {
+    const int st = pack_axes(x, a->rotary_dim, &axes);
+    if (st != MOE_OK) return st;
+  }
   if (a->D > 1024 || a->Hq + static_cast<int64_t>(a->Hk) > 65536 ||
       a->N * (a->Hq + static_cast<int64_t>(a->Hk)) * (a->D / 2) > (1ll << 31))
     return MOE_ERR_UNSUPPORTED;
@@ -101,10 +119,10 @@ int moe_rope(const moe_rope_args_t* a, moe_stream_t stream) {
   int V = widest(most, e, p.D, p.R, p.q, most);
   V = widest(most, e, p.D, p.R, p.k, V);
   (void)cudaGetLastError();
-  return done(moe::launch_rope(p, a->dtype, V, reinterpret_cast<cudaStream_t>(stream)));
+  return done(moe::launch_rope(p, with_axes ? &axes : nullptr, a->dtype, V, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int moe_kv_append(const moe_kv_append_args_t* a, moe_stream_t stream) {
+int kv_append(const moe_kv_append_args_t* a, bool with_axes, const moe_rope_axes_t* x, moe_stream_t stream) {
   if (a == nullptr) return MOE_ERR_NULL;
   if (a->struct_size != sizeof(*a)) return MOE_ERR_UNSUPPORTED;
   if (a->dtype != MOE_DTYPE_BF16 && a->dtype != MOE_DTYPE_F16) return MOE_ERR_UNSUPPORTED;
@@ -116,9 +134,15 @@ int moe_kv_append(const moe_kv_append_args_t* a, moe_stream_t stream) {
   if (a->Hq < 0 || a->rotary_dim < 0 || a->rotary_dim > c.head_dim || a->rotary_dim % 2 != 0 || a->num_positions < 0)
     return MOE_ERR_SHAPE;
   if ((a->cos_sin == nullptr) != (a->rotary_dim == 0)) return MOE_ERR_NULL;
+  RopeAxes axes;
+  if (with_axes) {
+    st = pack_axes(x, a->rotary_dim, &axes);
+    if (st != MOE_OK) return st;
+  }
   if (!aligned(a->cos_sin, 16)) return MOE_ERR_ALIGN;
   if (a->Hq > 65536) return MOE_ERR_UNSUPPORTED;
   if (a->N == 0 || a->B == 0 || a->max_q_len == 0) return MOE_OK;
+  if (with_axes && a->positions == nullptr) return MOE_ERR_NULL;
   if (a->k == nullptr || a->v == nullptr || (a->Hq > 0 && (a->q == nullptr || a->q_out == nullptr))) return MOE_ERR_NULL;
   KvAppendParams p = {};
   p.cache = c;
@@ -141,8 +165,17 @@ int moe_kv_append(const moe_kv_append_args_t* a, moe_stream_t stream) {
   V = widest(8, 2, c.head_dim, 0, v, V);
   V = widest(8, 2, c.head_dim, p.R, p.q, V);
   (void)cudaGetLastError();
-  return done(moe::launch_kv_append(p, a->dtype, V, reinterpret_cast<cudaStream_t>(stream)));
+  return done(moe::launch_kv_append(p, with_axes ? &axes : nullptr, a->dtype, V, reinterpret_cast<cudaStream_t>(stream)));
 }
+
+}  // namespace
+
+extern "C" {
+
+int moe_rope(const moe_rope_args_t* a, moe_stream_t stream) { return rope(a, false, nullptr, stream); }
+int moe_rope_axes(const moe_rope_args_t* a, const moe_rope_axes_t* axes, moe_stream_t stream) { return rope(a, true, axes, stream); }
+int moe_kv_append(const moe_kv_append_args_t* a, moe_stream_t stream) { return kv_append(a, false, nullptr, stream); }
+int moe_kv_append_axes(const moe_kv_append_args_t* a, const moe_rope_axes_t* axes, moe_stream_t stream) { return kv_append(a, true, axes, stream); }
 
 size_t moe_paged_attention_workspace_size(void) { return moe::decode_attention_workspace_bytes() + moe::prefill_attention_workspace_bytes(); }
 

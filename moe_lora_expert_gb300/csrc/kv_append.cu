@@ -65,9 +65,10 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[V], flo
 }
 
 // CTAs [0, 2 * B * slots * Hkv): one (sequence, page of it, head, K or V) each.
-// The rest rotate q.
-template <typename T, int V, int HEADS>
-__global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppendParams p) {
+// The rest rotate q.  Axes: RopeAxes, where each pair has an axis, or OneAxis.
+template <typename T, int V, int HEADS, typename Axes>
+__global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppendParams p, const __grid_constant__ Axes axes) {
+  constexpr bool kAxes = !std::is_same<Axes, OneAxis>::value;
   __shared__ float s_max[32];
   __shared__ int s_pos[kMaxThreads];
   pdl_launch_dependents();
@@ -85,7 +86,10 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
     if (t <= (item0 + blockDim.x - 1) / p.q_items && t < static_cast<uint32_t>(p.N)) {
       int pos = kSkipped;
       if (p.cu_q == nullptr || static_cast<int>(t) < p.cu_q[p.B]) {          // else a row of no sequence
-        if (p.positions != nullptr) {
+        if constexpr (kAxes) {
+          AxisPositions at;                                                   // the threads that turn the token read them again
+          pos = at.load(axes, p.positions, t, p.num_positions) ? 0 : kUnturned;
+        } else if (p.positions != nullptr) {
           pos = p.positions[t];
         } else {
           const int b = p.cu_q == nullptr ? t : sequence_of(p.cu_q, p.B, t);
@@ -100,7 +104,15 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
       s_pos[tid] = pos;
     }
     __syncthreads();
-    if (x.live) x.finish(p.q, RopeTensor{}, s_pos[x.t - token0], p.R, p.interleaved, false, p.cos_sin);
+    if constexpr (kAxes) {
+      const int state = x.live ? s_pos[x.t - token0] : kSkipped;
+      if (state == kSkipped) return;
+      AxisPositions at;
+      at.load(axes, p.positions, x.t, p.num_positions);
+      x.finish(p.q, RopeTensor{}, at, state != kUnturned, axes, p.R, p.interleaved, false, p.cos_sin);
+    } else {
+      if (x.live) x.finish(p.q, RopeTensor{}, s_pos[x.t - token0], p.R, p.interleaved, false, p.cos_sin);
+    }
     return;
   }
 
@@ -147,7 +159,18 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
     const int r = j / per_head, c = j - r * per_head;
     to_f32s<T, V>(ra, a);
     to_f32s<T, V>(rb, bb);
-    if (turn && 2 * V * c < p.R) {
+    if constexpr (kAxes) {
+      if (turn && 2 * V * c < p.R) {
+        AxisPositions at;
+        if (at.load(axes, p.positions, t_first + (p0 - start) + r, p.num_positions)) {
+          float cs[V], sn[V];
+          load_cos_sin<V>(p.cos_sin, at, axes, c, p.R, cs, sn);
+          rotate<V, true>(a, bb, cs, sn, p.interleaved);
+        } else {
+          set_status(p.status, MOE_ERR_BAD_POSITION);
+        }
+      }
+    } else if (turn && 2 * V * c < p.R) {
       const int pos = p.positions != nullptr ? p.positions[t_first + (p0 - start) + r] : p0 + r;
       if (pos >= 0 && pos < p.num_positions) {
         float cs[V], sn[V];
@@ -235,8 +258,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
   if (tid == 0 && s_new != *scale) *scale = s_new;     // every thread has its s_old since the barrier
 }
 
-template <typename T, int V, int HEADS>
-cudaError_t launch_heads(KvAppendParams p, cudaStream_t s) {
+template <typename T, int V, int HEADS, typename Axes>
+cudaError_t launch_heads(KvAppendParams p, const Axes& axes, cudaStream_t s) {
   const int per_head = p.cache.head_dim / (2 * V);
   const int rows = p.slots > 1 ? p.cache.page_size : 1;
   int threads = 64;
@@ -244,26 +267,31 @@ cudaError_t launch_heads(KvAppendParams p, cudaStream_t s) {
   const int64_t units = 2ll * p.B * p.slots * p.cache.kv_heads;
   p.q_items = p.q.heads > 0 ? rotation_items<V>(p.q.heads, HEADS, p.cache.head_dim) : 1;
   const int64_t q_ctas = p.q.heads > 0 ? (static_cast<int64_t>(p.N) * p.q_items + threads - 1) / threads : 0;
-  return launch_pdl(kv_append_kernel<T, V, HEADS>, dim3(static_cast<unsigned>(units + q_ctas)), dim3(threads), 0, s, p);
+  return launch_pdl(kv_append_kernel<T, V, HEADS, Axes>, dim3(static_cast<unsigned>(units + q_ctas)), dim3(threads), 0, s, p, axes);
 }
 
-template <typename T, int V>
-cudaError_t launch(const KvAppendParams& p, cudaStream_t s) {
-  return static_cast<int64_t>(p.N) * rotation_items<V>(p.q.heads, 1, p.cache.head_dim) >= kManyItems ? launch_heads<T, V, 2>(p, s)
-                                                                                                     : launch_heads<T, V, 1>(p, s);
+template <typename T, int V, typename Axes>
+cudaError_t launch(const KvAppendParams& p, const Axes& axes, cudaStream_t s) {
+  return static_cast<int64_t>(p.N) * rotation_items<V>(p.q.heads, 1, p.cache.head_dim) >= kManyItems ? launch_heads<T, V, 2>(p, axes, s)
+                                                                                                     : launch_heads<T, V, 1>(p, axes, s);
 }
 
-template <typename T>
-cudaError_t launch_v(const KvAppendParams& p, int V, cudaStream_t s) {
-  if (V >= 8) return launch<T, 8>(p, s);
-  if (V == 4) return launch<T, 4>(p, s);
-  return launch<T, 1>(p, s);
+template <typename T, typename Axes>
+cudaError_t launch_v(const KvAppendParams& p, const Axes& axes, int V, cudaStream_t s) {
+  if (V >= 8) return launch<T, 8>(p, axes, s);
+  if (V == 4) return launch<T, 4>(p, axes, s);
+  return launch<T, 1>(p, axes, s);
+}
+
+template <typename Axes>
+cudaError_t launch_type(const KvAppendParams& p, const Axes& axes, int dtype, int V, cudaStream_t s) {
+  return dtype == MOE_DTYPE_F16 ? launch_v<__half>(p, axes, V, s) : launch_v<__nv_bfloat16>(p, axes, V, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, int V, cudaStream_t s) {
-  return dtype == MOE_DTYPE_F16 ? launch_v<__half>(p, V, s) : launch_v<__nv_bfloat16>(p, V, s);
+cudaError_t launch_kv_append(const KvAppendParams& p, const RopeAxes* axes, int dtype, int V, cudaStream_t s) {
+  return axes != nullptr ? launch_type(p, *axes, dtype, V, s) : launch_type(p, OneAxis{}, dtype, V, s);
 }
 
 }  // namespace moe

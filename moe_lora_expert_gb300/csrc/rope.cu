@@ -35,26 +35,40 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, uint32_t p
   x.finish(p.q, p.k, pos, p.R, p.interleaved, p.inverse, p.cos_sin);
 }
 
+// The same with an axis for each pair: a token has a position on each axis.
 template <typename T, int V>
-cudaError_t launch(const RopeParams& p, cudaStream_t s) {
+__global__ void __launch_bounds__(kThreads) rope_axes_kernel(RopeParams p, const __grid_constant__ RopeAxes axes, uint32_t per_token) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const RotationItem<T, V, 1> x(p.q, p.k, blockIdx.x * kThreads + threadIdx.x, per_token, p.N, p.D, p.R, p.interleaved);
+  if (!x.live) return;
+  AxisPositions pos;
+  const bool good = pos.load(axes, p.positions, x.t, p.num_positions);
+  if (!good) set_status(p.status, MOE_ERR_BAD_POSITION);
+  x.finish(p.q, p.k, pos, good, axes, p.R, p.interleaved, p.inverse, p.cos_sin);
+}
+
+template <typename T, int V>
+cudaError_t launch(const RopeParams& p, const RopeAxes* axes, cudaStream_t s) {
   const uint32_t per_token = rotation_items<V>(p.q.heads + p.k.heads, 1, p.D);
-  const int64_t ctas = (static_cast<int64_t>(p.N) * per_token + kThreads - 1) / kThreads;
-  return launch_pdl(rope_kernel<T, V>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, p, per_token);
+  const dim3 ctas(static_cast<unsigned>((static_cast<int64_t>(p.N) * per_token + kThreads - 1) / kThreads));
+  if (axes != nullptr) return launch_pdl(rope_axes_kernel<T, V>, ctas, dim3(kThreads), 0, s, p, *axes, per_token);
+  return launch_pdl(rope_kernel<T, V>, ctas, dim3(kThreads), 0, s, p, per_token);
 }
 
 template <typename T>
-cudaError_t launch_v(const RopeParams& p, int V, cudaStream_t s) {
-  if (V >= 8) return launch<T, 8>(p, s);
-  if (V == 4) return launch<T, 4>(p, s);
-  return launch<T, 1>(p, s);
+cudaError_t launch_v(const RopeParams& p, const RopeAxes* axes, int V, cudaStream_t s) {
+  if (V >= 8) return launch<T, 8>(p, axes, s);
+  if (V == 4) return launch<T, 4>(p, axes, s);
+  return launch<T, 1>(p, axes, s);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeParams& p, int dtype, int V, cudaStream_t s) {
-  if (dtype == MOE_DTYPE_F32) return V >= 4 ? launch<float, 4>(p, s) : launch<float, 1>(p, s);
-  if (dtype == MOE_DTYPE_F16) return launch_v<__half>(p, V, s);
-  return launch_v<__nv_bfloat16>(p, V, s);
+cudaError_t launch_rope(const RopeParams& p, const RopeAxes* axes, int dtype, int V, cudaStream_t s) {
+  if (dtype == MOE_DTYPE_F32) return V >= 4 ? launch<float, 4>(p, axes, s) : launch<float, 1>(p, axes, s);
+  if (dtype == MOE_DTYPE_F16) return launch_v<__half>(p, axes, V, s);
+  return launch_v<__nv_bfloat16>(p, axes, V, s);
 }
 
 }  // namespace moe

@@ -44,6 +44,17 @@ def rotate(x, pos, freqs, mscale=1.0, interleaved=False, inverse=False):
     return y
 
 
+def rotate_axes(x, pos, axis_of_pair, freqs, mscale=1.0, interleaved=False, inverse=False):
+    """x [H, D] of one token with a position pos[a] on each axis."""
+    y = np.array(x, dtype=np.float64)
+    for a, p in enumerate(pos):
+        turned = rotate(x, int(p), freqs, mscale, interleaved, inverse)
+        for i in [i for i, axis in enumerate(axis_of_pair) if axis == a]:
+            for col in ((2 * i, 2 * i + 1) if interleaved else (i, i + len(freqs))):
+                y[:, col] = turned[:, col]
+    return y
+
+
 def page_scale(amax):
     """The smallest power of two, at least 2^-42, with amax <= 448 times it."""
     s = 2.0 ** -42
