@@ -670,6 +670,50 @@ int moe_paged_attention_workspace_init(void* workspace, size_t workspace_bytes, 
 int moe_stream_capture_id(moe_stream_t stream, uint64_t* id);
 int moe_paged_attention(const moe_paged_attention_args_t* args, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * moe_paged_attention_sinks -- moe_paged_attention with a window and first
+ * tokens that stay visible: row at position i sees the keys j <= i with
+ * j > i - window or j < sinks.  With window = 0 all keys are seen anyway.
+ * Pages whose keys no row sees, those between the sinks and the window, are
+ * not looked up: their table entries may hold anything.
+ * ------------------------------------------------------------------------- */
+int moe_paged_attention_sinks(const moe_paged_attention_args_t* args, int sinks, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_paged_attention_shared -- moe_paged_attention of a batch in which groups
+ * of sequences begin with the same tokens, whose keys and values are read once
+ * for all new tokens of a group and not by every sequence.
+ *
+ * Sequences [seqs[g], seqs[g + 1]) have the same first lens[g] tokens, which
+ * count in their seq_lens and have their places in every block table row.  The
+ * output is that of moe_paged_attention up to rounding (the sums over the two
+ * parts are joined in float32).  The shared keys are read through the table
+ * row of the group's first sequence, whatever its seq_lens says (a slot without
+ * a sequence may come first if its row has the prefix's pages); a prefix may end
+ * inside a page.  A sequence whose new tokens begin before lens[g], or that is
+ * in no group, or whose tokens are not all among the first max_tokens of its
+ * group's, reads all of its keys itself.
+ *   args: as in moe_paged_attention, with window = 0 (MOE_ERR_UNSUPPORTED).
+ *   seqs [groups + 1] int32, device, not decreasing, or NULL with groups = 1:
+ *     all sequences.  lens [groups] int32, device; 0 or less: nothing shared.
+ *   max_tokens: at least the most new tokens of one group; it sizes the launch.
+ *   partial: device scratch of the call, moe_shared_prefix_partial_size bytes,
+ *     16-byte aligned, of any contents.
+ * Sequences of many rows (new tokens times query heads of a key head, by
+ * max_q_len) fill the tiles of a product by themselves: for more than 128 the
+ * call does as moe_paged_attention does.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;           /* sizeof(moe_shared_prefix_t) */
+  int groups, max_tokens;
+  const int32_t* seqs;
+  const int32_t* lens;
+  void* partial;
+  size_t partial_bytes;
+} moe_shared_prefix_t;
+size_t moe_shared_prefix_partial_size(int N, int Hq, int head_dim);
+int moe_paged_attention_shared(const moe_paged_attention_args_t* args, const moe_shared_prefix_t* shared, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

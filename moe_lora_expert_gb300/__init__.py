@@ -48,7 +48,8 @@ EXPORTED_SYMBOLS = [
     "moe_read_device_status", "moe_permute_noalloc", "moe_per_token_group_quant_fp8",
     "moe_lora_workspace_size_ex", "moe_rope", "moe_kv_append", "moe_paged_attention_workspace_size",
     "moe_paged_attention", "moe_paged_attention_workspace_init", "moe_stream_capture_id",
-    "moe_rope_axes", "moe_kv_append_axes",
+    "moe_rope_axes", "moe_kv_append_axes", "moe_paged_attention_sinks", "moe_paged_attention_shared",
+    "moe_shared_prefix_partial_size",
 ]
 
 
@@ -139,9 +140,13 @@ def lib() -> ctypes.CDLL:
         for fn in (L.moe_rope, L.moe_kv_append, L.moe_paged_attention):
             fn.restype = i32
             fn.argtypes = [ctypes.c_char_p, vp]     # the argument struct's bytes, stream
-        for fn in (L.moe_rope_axes, L.moe_kv_append_axes):
+        for fn in (L.moe_rope_axes, L.moe_kv_append_axes, L.moe_paged_attention_shared):
             fn.restype = i32
             fn.argtypes = [ctypes.c_char_p, ctypes.c_char_p, vp]    # two structs' bytes, stream
+        L.moe_paged_attention_sinks.restype = i32
+        L.moe_paged_attention_sinks.argtypes = [ctypes.c_char_p, i32, vp]
+        L.moe_shared_prefix_partial_size.restype = sz
+        L.moe_shared_prefix_partial_size.argtypes = [i32, i32, i32]
         L.moe_paged_attention_workspace_size.restype = sz
         L.moe_paged_attention_workspace_size.argtypes = []
         L.moe_paged_attention_workspace_init.restype = i32
@@ -444,5 +449,5 @@ class MoeLoraLayer:
 
 
 from .attention import (MOE_DEBUG_STALL_ATTENTION, MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32,  # noqa: E402
-                        KvAppendArgs, KvCache, PagedAttentionArgs, PagedKVCache, RopeArgs, RopeAxes, moe_rope, rope_axes, rope_frequencies,
+                        KvAppendArgs, KvCache, PagedAttentionArgs, PagedKVCache, RopeArgs, RopeAxes, SharedPrefix, moe_rope, rope_axes, rope_frequencies,
                         rope_table)

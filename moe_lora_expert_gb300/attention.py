@@ -74,6 +74,12 @@ class PagedAttentionArgs(ctypes.Structure):
                 ("scale", ctypes.c_float), ("debug_flags", ctypes.c_uint32)]
 
 
+class SharedPrefix(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("groups", ctypes.c_int), ("max_tokens", ctypes.c_int),
+                ("seqs", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("partial", ctypes.c_void_p),
+                ("partial_bytes", ctypes.c_size_t)]
+
+
 # The same layouts as bytes (64-bit pointers; the structs have no padding but
 # where every 8-byte field is aligned already).
 _ROPE = struct.Struct("=Ii4Q8q3Q8i")
@@ -82,12 +88,13 @@ _HEAD = struct.Struct("=Ii")
 _APPEND = struct.Struct("=2Q4q2Q4q6Q8i")
 _ATTEND = struct.Struct("=3Q4q6Q8ifI")
 _AXES = struct.Struct("=Iiq512s")
+_SHARED = struct.Struct("=Iii4x4Q")
 
 # What the entry points use on every call, bound by the first one (torch is
 # imported lazily, as in the rest of the package).
 _torch = _int32_type = _float32_type = None
 _codes: Dict = {}
-_rope_fn = _append_fn = _attend_fn = _rope_axes_fn = _append_axes_fn = _raw_stream = _empty_like = _capturing = _current_device = None
+_rope_fn = _append_fn = _attend_fn = _rope_axes_fn = _append_axes_fn = _sinks_fn = _shared_fn = _raw_stream = _empty_like = _capturing = _current_device = None
 
 # Scratch of attention calls: calls on one stream follow one another and share
 # it, whatever their cache; a captured call runs when its graph does, so each
@@ -98,7 +105,7 @@ _captured: Dict = {}         # (device index, stream handle): (capture id, works
 
 def _bind():
     global _torch, _int32_type, _float32_type, _rope_fn, _append_fn, _attend_fn, _raw_stream, _empty_like, _capturing
-    global _current_device, _rope_axes_fn, _append_axes_fn
+    global _current_device, _rope_axes_fn, _append_axes_fn, _sinks_fn, _shared_fn
     import torch
     from . import lib
     L = lib()
@@ -108,6 +115,7 @@ def _bind():
     _empty_like, _capturing = torch.empty_like, torch.cuda.is_current_stream_capturing
     _current_device = torch._C._cuda_getDevice
     _rope_axes_fn, _append_axes_fn = L.moe_rope_axes, L.moe_kv_append_axes
+    _sinks_fn, _shared_fn = L.moe_paged_attention_sinks, L.moe_paged_attention_shared
     _rope_fn, _torch = L.moe_rope, torch
 
 
@@ -498,13 +506,23 @@ class PagedKVCache:
         return q_out
 
     def attend(self, q, block_table, seq_lens, cu_q=None, max_q_len=None, max_seq_len=None, scale=None,
-               window=0, out=None, return_lse=False, lse=None, wait_timeout_ms=0, debug_flags=0, stream=None):
+               window=0, out=None, return_lse=False, lse=None, wait_timeout_ms=0, debug_flags=0, stream=None, sinks=0,
+               shared_lens=None, shared_seqs=None, max_shared_q=None):
         """Causal attention of q [N, Hq, head_dim] over the cache: rows as in
         ``append``, whose keys have to be in the cache already.  ``window``:
-        how many keys a row sees, its own included (0: all).  ``max_q_len``,
-        ``max_seq_len``: host-side bounds that size the launch (by default N
-        and the block table's width).  Returns out, or (out, lse float32 [N,
-        Hq]) with ``return_lse`` or a given ``lse``."""
+        how many keys a row sees, its own included (0: all).  ``sinks``: how
+        many first keys of a sequence every row sees besides its window.
+        ``max_q_len``, ``max_seq_len``: host-side bounds that size the launch
+        (by default N and the block table's width).  Returns out, or (out, lse
+        float32 [N, Hq]) with ``return_lse`` or a given ``lse``.
+
+        ``shared_lens`` int32 [G], ``shared_seqs`` int32 [G + 1]: sequences
+        [shared_seqs[g], shared_seqs[g + 1]) begin with the same shared_lens[g]
+        tokens (without shared_seqs all do, G = 1), whose keys are then read
+        once for the group, from the pages of its first sequence's table row.
+        The result is the same up to rounding; not with a window.
+        ``max_shared_q``: at least the most new tokens of one group (by default
+        N); sequences past it read their keys themselves."""
         N, Hq, D = q.shape
         dtype = q.dtype
         code, index = _dtype_code(dtype, "q"), self._index
@@ -521,6 +539,22 @@ class PagedKVCache:
         elif return_lse:
             lse = _empty((N, Hq), _float32_type, self.device, stream)
         B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
+        fn, more, partial = _attend_fn, (), None
+        if sinks:
+            fn, more = _sinks_fn, (min(sinks, 1 << 30),)        # ctypes drops what an int does not hold
+        if shared_lens is not None:
+            if window or sinks:
+                raise ValueError("shared prefixes go with no window")
+            G = shared_lens.shape[0]
+            if shared_seqs is None and G != 1:
+                raise ValueError("without shared_seqs there is one group, of all sequences")
+            lens = _int32(shared_lens, G, "shared_lens", index)
+            seqs = 0 if shared_seqs is None else _int32(shared_seqs, G + 1, "shared_seqs", index)
+            partial = _empty((N * Hq * (4 * D + 8),), _torch.uint8, self.device, stream)
+            fn, more = _shared_fn, (_SHARED.pack(48, G, N if max_shared_q is None else max_shared_q, seqs, lens, partial.data_ptr(),
+                                                 partial.shape[0]),)
+        elif shared_seqs is not None:
+            raise ValueError("shared_seqs goes with shared_lens")
         here = _current_device() == index
         ws = None
         if stream is not None or not here or _capturing():
@@ -532,10 +566,10 @@ class PagedKVCache:
             N, B, Hq, width, longest, width * self.page_size if max_seq_len is None else max_seq_len, window,
             wait_timeout_ms, D ** -0.5 if scale is None else scale, debug_flags)
         if stream is not None:
-            _record(stream, q, out, lse, block_table, seq_lens, cu_q, *self._tensors)
-        error = _attend_fn(args, handle) if here else _elsewhere(index, _attend_fn, args, handle)
+            _record(stream, q, out, lse, block_table, seq_lens, cu_q, shared_lens, shared_seqs, *self._tensors)
+        error = fn(args, *more, handle) if here else _elsewhere(index, fn, args, *more, handle)
         if error:
-            _raise(error, "moe_paged_attention")
+            _raise(error, "moe_paged_attention" + ("_sinks" if sinks else "_shared" if partial is not None else ""))
         return out if lse is None else (out, lse)
 
     def device_status(self) -> int:

@@ -125,43 +125,40 @@ struct RopeAxes {
   uint32_t of_pair[kMaxPairs / 16];
 };
 struct OneAxis {};
-// A token's position on each axis.  Whether all are in the table.
-struct AxisPositions {
-  int on[kMaxAxes];
-  __device__ __forceinline__ bool load(const RopeAxes& axes, const int32_t* positions, int64_t t, int num_positions) {
-    bool good = true;
+// The axis of pair i.
+__device__ __forceinline__ uint32_t axis_of(const RopeAxes& axes, int i) { return axes.of_pair[i / 16] >> (2 * (i % 16)) & 3; }
+// A token's position on the axis of pair i, and whether its positions on all
+// axes are in the table.
+__device__ __forceinline__ int axis_position(const RopeAxes& axes, const int32_t* positions, int64_t t, int num_positions, int i, bool& good) {
+  const uint32_t mine = axis_of(axes, i);
+  int pos = 0;
+  good = true;
 #pragma unroll
-    for (int a = 0; a < kMaxAxes; ++a) {
-      on[a] = a < axes.count ? positions[a * axes.stride + t] : 0;
-      good &= a >= axes.count || (on[a] >= 0 && on[a] < num_positions);
-    }
-    return good;
+  for (uint32_t a = 0; a < kMaxAxes; ++a) {
+    if (a >= static_cast<uint32_t>(axes.count)) break;
+    const int p = positions[a * axes.stride + t];
+    good &= p >= 0 && p < num_positions;
+    pos = a == mine ? p : pos;
   }
-};
-// cos and sin of frequencies [Vc, Vc + V), each at its own axis's position: a
-// table row's run where they have one axis, else a run of each axis's row and
-// from it what is that axis's.
-template <int V>
-__device__ __forceinline__ void load_cos_sin(const float* cos_sin, const AxisPositions& pos, const RopeAxes& axes, int c, int R,
-                                             float (&cs)[V], float (&sn)[V]) {
-  constexpr uint32_t kEach = 0x55555555u >> (32 - 2 * V);
-  const uint32_t bits = axes.of_pair[V * c / 16] >> (2 * (V * c % 16)) & (3 * kEach);
-#pragma unroll
-  for (int a = 0; a < kMaxAxes; ++a) {
-    const uint32_t other = bits ^ (a * kEach), mine = ~(other | other >> 1) & kEach;   // a bit for each pair on axis a
-    if (mine == 0) continue;
-    const float* row = cos_sin + static_cast<int64_t>(pos.on[a]) * R;
-    if (mine == kEach) {
-      load_cos_sin<V>(row, c, R, cs, sn);
-    } else {
-      float x[V], y[V];
-      load_cos_sin<V>(row, c, R, x, y);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        cs[i] = mine >> (2 * i) & 1 ? x[i] : cs[i];
-        sn[i] = mine >> (2 * i) & 1 ? y[i] : sn[i];
-      }
-    }
+  return pos;
+}
+// The most tokens that ``threads`` consecutive items lie in.
+__host__ __device__ __forceinline__ uint32_t axes_tokens(uint32_t threads, uint32_t per_token) { return (threads - 2) / per_token + 2; }
+// The angles of tokens [t0, t0 + tokens) as rows of cosines and sines, each
+// pair's from its own axis's row of the table, by all threads of a CTA; good[j]:
+// whether token t0 + j has all its positions in the table.  Each angle is looked
+// up once and not by every head, and a row then serves as one of the table
+// does: 4096 tokens of 36 heads of 128 in this way XX us, each thread by itself
+// 24 (a run of pairs for each axis) and 33 (axes in turns).
+__device__ __forceinline__ void gather_angles(float* rows, int* good, const RopeAxes& axes, const int32_t* positions, const float* cos_sin,
+                                              int64_t t0, int tokens, int R, int num_positions) {
+  const int threads = blockDim.x * blockDim.y * blockDim.z;
+  for (int j = threadIdx.x + blockDim.x * (threadIdx.y + blockDim.y * threadIdx.z); j < tokens * R; j += threads) {
+    const int token = j / R, col = j - token * R;
+    bool all;
+    const int pos = axis_position(axes, positions, t0 + token, num_positions, col < R / 2 ? col : col - R / 2, all);
+    rows[j] = all ? cos_sin[static_cast<int64_t>(pos) * R + col] : 0.f;
+    if (col == 0 && good != nullptr) good[token] = all;
   }
 }
 
@@ -251,27 +248,19 @@ struct RotationItem {
   __device__ __forceinline__ void finish(const RopeTensor& x, const RopeTensor& y, int pos, int R, bool interleaved, bool inverse,
                                          const float* cos_sin) const {
     if (!live || pos == kSkipped) return;
-    const Stretch<V> s(c, R, interleaved);
-    const bool turn = s.turned && pos >= 0;
-    float cs[V], sn[V];
-    if (turn) load_cos_sin<V>(cos_sin + static_cast<int64_t>(pos) * R, c, R, cs, sn);
-    write(x, y, s, turn, interleaved, inverse, cs, sn);
+    turn_by(x, y, pos >= 0 ? cos_sin + static_cast<int64_t>(pos) * R : nullptr, R, interleaved, inverse);
   }
-  // With an axis for each pair; ``good``: all of the token's positions are in the table.
-  __device__ __forceinline__ void finish(const RopeTensor& x, const RopeTensor& y, const AxisPositions& pos, bool good, const RopeAxes& axes,
-                                         int R, bool interleaved, bool inverse, const float* cos_sin) const {
-    if (!live) return;
+  // ``row``: the token's cosines and sines, or nullptr for none.
+  __device__ __forceinline__ void turn_by(const RopeTensor& x, const RopeTensor& y, const float* row, int R, bool interleaved, bool inverse) const {
     const Stretch<V> s(c, R, interleaved);
-    const bool turn = s.turned && good;
+    const bool turn = s.turned && row != nullptr;
     float cs[V], sn[V];
-    if (turn) load_cos_sin<V>(cos_sin, pos, axes, c, R, cs, sn);
-    write(x, y, s, turn, interleaved, inverse, cs, sn);
-  }
-  __device__ __forceinline__ void write(const RopeTensor& x, const RopeTensor& y, const Stretch<V>& s, bool turn, bool interleaved, bool inverse,
-                                        const float (&cs)[V], float (&sn)[V]) const {
-    if (turn && inverse) {
+    if (turn) {
+      load_cos_sin<V>(row, c, R, cs, sn);
+      if (inverse) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) sn[i] = -sn[i];
+        for (int i = 0; i < V; ++i) sn[i] = -sn[i];
+      }
     }
 #pragma unroll
     for (int u = 0; u < HEADS; ++u) {
@@ -330,14 +319,61 @@ struct AttentionParams {
   uint64_t wait_limit_ns;
   uint32_t debug_flags;
 };
+// What an attention call may ask for besides, in kernels of their own.
+//
+// Sinks: the first ``sinks`` keys stay visible to every row of a window.
+//
+// Shared prefixes: sequences [seqs[g], seqs[g + 1]) of a group (seqs NULL: all)
+// begin with the same lens[g] tokens.  The prefix pass takes a group as one
+// sequence whose rows are all of its new tokens' and all see the prefix's keys,
+// through the block table's row of the group's first sequence, and leaves
+// unnormalised sums with their references; the own pass takes each sequence's
+// other keys and joins the two.  A sequence that begins inside the prefix, or
+// whose tokens are not all among the group's first max_tokens, takes no part
+// and reads its keys itself.
+enum AttentionPass { kWholePass, kPrefixPass, kOwnPass };
+struct AttentionForms {
+  int sinks;
+  int pass;                     // AttentionPass
+  int groups, sequences, max_tokens;
+  const int32_t *seqs, *lens;
+  float* sums;                  // [N][Hq][head_dim]
+  float2* refs;                 // [N][Hq]: reference and denominator
+  int late;                     // the own pass waits for the prefix pass where it joins, not where it begins
+
+  // Group g's sequences and their tokens; nothing, where the list is out of order.
+  __device__ __forceinline__ void group(const int32_t* cu_q, int g, int& s0, int& q0, int& q1) const {
+    s0 = seqs == nullptr ? 0 : max(0, min(sequences, seqs[g]));
+    const int s1 = seqs == nullptr ? sequences : max(s0, min(sequences, seqs[g + 1]));
+    q0 = cu_q == nullptr ? s0 : cu_q[s0];
+    q1 = cu_q == nullptr ? s1 : cu_q[s1];
+  }
+  // How many keys of sequence b, whose rows are tokens [q_first, q_first +
+  // q_len) and begin at position ``start``, the prefix pass has taken.
+  __device__ __forceinline__ int taken(const int32_t* cu_q, int b, int q_first, int q_len, int start) const {
+    int g = 0;
+    if (seqs != nullptr) {
+      int hi = groups;                                   // the last group that begins at b or before
+      while (hi - g > 1) {
+        const int mid = (g + hi) / 2;
+        if (seqs[mid] <= b) g = mid; else hi = mid;
+      }
+      if (b < seqs[g] || b >= seqs[g + 1]) return 0;
+    }
+    int s0, q0, q1;
+    group(cu_q, g, s0, q0, q1);
+    const int n = lens[g];
+    return n > 0 && start >= n && q_first >= q0 && q_first + q_len <= min(q1, q0 + max_tokens) ? n : 0;
+  }
+};
 bool encode_cache_map(CUtensorMap* map, const moe_kv_cache_t& c, bool values, int rows);
 bool encode_query_map(CUtensorMap* map, const AttentionParams& a, bool f16, int group, int tokens);
 int sm_count();
 size_t prefill_attention_workspace_bytes();
 cudaError_t clear_prefill_counters(void* workspace, cudaStream_t s);
-int launch_prefill_attention(const AttentionParams& p, int dtype, cudaStream_t s);  // a moe_status_t
+int launch_prefill_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s);  // a moe_status_t; forms NULL: none
 size_t decode_attention_workspace_bytes();
 cudaError_t clear_decode_counters(void* workspace, cudaStream_t s);
-int launch_decode_attention(const AttentionParams& p, int dtype, cudaStream_t s);   // a moe_status_t
+int launch_decode_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s);   // a moe_status_t
 
 }  // namespace moe

@@ -6,6 +6,7 @@
 
 namespace {
 
+using moe::AttentionForms;
 using moe::AttentionParams;
 using moe::KvAppendParams;
 using moe::RopeAxes;
@@ -31,6 +32,10 @@ inline int element_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 // host does not have: 96 saves 15 to 25% on a short one and costs up to 46% on
 // one long context (on 8 key heads 77%: 109 / 62).
 bool few_rows(int64_t rows, int64_t pairs) { return rows <= 32 || (rows <= 96 && pairs <= 16); }
+
+// Up to how many rows of a sequence and key head the prefix of a group is read
+// once for all of them.
+constexpr int64_t kSharedRows = 128;
 
 // Elements a thread may move at once, of 8, 4 and 1: V elements of a type
 // with e bytes need addresses and strides in multiples of V * e bytes (16 at
@@ -168,6 +173,52 @@ int kv_append(const moe_kv_append_args_t* a, bool with_axes, const moe_rope_axes
   return done(moe::launch_kv_append(p, with_axes ? &axes : nullptr, a->dtype, V, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// The arguments of a call, checked; MOE_OK with p.N = 0 where there is nothing to do.
+int check_attention(const moe_paged_attention_args_t* a, AttentionParams& p) {
+  if (a == nullptr) return MOE_ERR_NULL;
+  if (a->struct_size != sizeof(*a)) return MOE_ERR_UNSUPPORTED;
+  if (a->dtype != MOE_DTYPE_BF16 && a->dtype != MOE_DTYPE_F16) return MOE_ERR_UNSUPPORTED;
+  int st = check_cache(a->cache);
+  if (st != MOE_OK) return st;
+  st = check_batch(a->N, a->B, a->table_width, a->max_q_len, a->block_table, a->seq_lens, a->cu_q);
+  if (st != MOE_OK) return st;
+  const moe_kv_cache_t& c = a->cache;
+  if (a->Hq <= 0 || a->Hq % c.kv_heads != 0 || a->max_seq_len < 0 || a->window < 0 || a->wait_timeout_ms < 0)
+    return MOE_ERR_SHAPE;
+  if (a->Hq / c.kv_heads > 256 || (a->debug_flags & ~MOE_DEBUG_STALL_ATTENTION) != 0) return MOE_ERR_UNSUPPORTED;
+  p.N = 0;
+  if (a->N == 0 || a->B == 0 || a->max_q_len == 0) return MOE_OK;
+  if (a->q == nullptr || a->out == nullptr) return MOE_ERR_NULL;
+  const int64_t strides[4] = {a->q_stride_token, a->q_stride_head, a->out_stride_token, a->out_stride_head};
+  for (int64_t s : strides)
+    if (s % 8 != 0) return MOE_ERR_ALIGN;
+  if (!aligned(a->q, 16) || !aligned(a->out, 16)) return MOE_ERR_ALIGN;
+  if (a->workspace == nullptr || !aligned(a->workspace, 256) || a->workspace_bytes < moe_paged_attention_workspace_size())
+    return MOE_ERR_WORKSPACE;
+  p = AttentionParams{};
+  p.cache = c;
+  p.q = a->q, p.out = a->out, p.lse = a->lse;
+  p.q_token = a->q_stride_token, p.q_head = a->q_stride_head;
+  p.out_token = a->out_stride_token, p.out_head = a->out_stride_head;
+  p.block_table = a->block_table, p.seq_lens = a->seq_lens, p.cu_q = a->cu_q;
+  p.status = a->status;
+  p.N = a->N, p.B = a->B, p.Hq = a->Hq, p.table_width = a->table_width;
+  p.max_q_len = a->cu_q == nullptr ? 1 : a->max_q_len < a->N ? a->max_q_len : a->N;
+  p.window = a->window;
+  p.max_seq_len = a->max_seq_len;
+  p.scale = a->scale;
+  p.workspace = a->workspace;
+  p.wait_limit_ns = 1000000ull * static_cast<uint64_t>(a->wait_timeout_ms > 0 ? a->wait_timeout_ms : 2000);
+  p.debug_flags = a->debug_flags;
+  return MOE_OK;
+}
+
+int64_t rows_of(const AttentionParams& p) { return static_cast<int64_t>(p.max_q_len) * (p.Hq / p.cache.kv_heads); }
+int attend(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t on) {
+  if (few_rows(rows_of(p), static_cast<int64_t>(p.B) * p.cache.kv_heads)) return moe::launch_decode_attention(p, forms, dtype, on);
+  return moe::launch_prefill_attention(p, forms, dtype, on);
+}
+
 }  // namespace
 
 extern "C" {
@@ -199,45 +250,61 @@ int moe_stream_capture_id(moe_stream_t stream, uint64_t* id) {
 }
 
 int moe_paged_attention(const moe_paged_attention_args_t* a, moe_stream_t stream) {
-  if (a == nullptr) return MOE_ERR_NULL;
-  if (a->struct_size != sizeof(*a)) return MOE_ERR_UNSUPPORTED;
-  if (a->dtype != MOE_DTYPE_BF16 && a->dtype != MOE_DTYPE_F16) return MOE_ERR_UNSUPPORTED;
-  int st = check_cache(a->cache);
+  AttentionParams p;
+  const int st = check_attention(a, p);
+  if (st != MOE_OK || p.N == 0) return st;
+  (void)cudaGetLastError();
+  return attend(p, nullptr, a->dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_paged_attention_sinks(const moe_paged_attention_args_t* a, int sinks, moe_stream_t stream) {
+  AttentionParams p;
+  const int st = check_attention(a, p);
   if (st != MOE_OK) return st;
-  st = check_batch(a->N, a->B, a->table_width, a->max_q_len, a->block_table, a->seq_lens, a->cu_q);
+  if (sinks < 0) return MOE_ERR_SHAPE;
+  if (p.N == 0) return MOE_OK;
+  (void)cudaGetLastError();
+  AttentionForms f = {};
+  f.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
+  return attend(p, sinks == 0 || p.window == 0 ? nullptr : &f, a->dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moe_shared_prefix_partial_size(int N, int Hq, int head_dim) {
+  return N <= 0 || Hq <= 0 || head_dim <= 0 ? 0 : static_cast<size_t>(N) * Hq * (static_cast<size_t>(head_dim) * 4 + 8);
+}
+
+int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_shared_prefix_t* x, moe_stream_t stream) {
+  AttentionParams p;
+  const int st = check_attention(a, p);
   if (st != MOE_OK) return st;
-  const moe_kv_cache_t& c = a->cache;
-  if (a->Hq <= 0 || a->Hq % c.kv_heads != 0 || a->max_seq_len < 0 || a->window < 0 || a->wait_timeout_ms < 0)
-    return MOE_ERR_SHAPE;
-  if (a->Hq / c.kv_heads > 256 || (a->debug_flags & ~MOE_DEBUG_STALL_ATTENTION) != 0) return MOE_ERR_UNSUPPORTED;
-  if (a->N == 0 || a->B == 0 || a->max_q_len == 0) return MOE_OK;
-  if (a->q == nullptr || a->out == nullptr) return MOE_ERR_NULL;
-  const int64_t strides[4] = {a->q_stride_token, a->q_stride_head, a->out_stride_token, a->out_stride_head};
-  for (int64_t s : strides)
-    if (s % 8 != 0) return MOE_ERR_ALIGN;
-  if (!aligned(a->q, 16) || !aligned(a->out, 16)) return MOE_ERR_ALIGN;
-  if (a->workspace == nullptr || !aligned(a->workspace, 256) || a->workspace_bytes < moe_paged_attention_workspace_size())
-    return MOE_ERR_WORKSPACE;
-  AttentionParams p = {};
-  p.cache = c;
-  p.q = a->q, p.out = a->out, p.lse = a->lse;
-  p.q_token = a->q_stride_token, p.q_head = a->q_stride_head;
-  p.out_token = a->out_stride_token, p.out_head = a->out_stride_head;
-  p.block_table = a->block_table, p.seq_lens = a->seq_lens, p.cu_q = a->cu_q;
-  p.status = a->status;
-  p.N = a->N, p.B = a->B, p.Hq = a->Hq, p.table_width = a->table_width;
-  p.max_q_len = a->cu_q == nullptr ? 1 : a->max_q_len < a->N ? a->max_q_len : a->N;
-  p.window = a->window;
-  p.max_seq_len = a->max_seq_len;
-  p.scale = a->scale;
-  p.workspace = a->workspace;
-  p.wait_limit_ns = 1000000ull * static_cast<uint64_t>(a->wait_timeout_ms > 0 ? a->wait_timeout_ms : 2000);
-  p.debug_flags = a->debug_flags;
+  if (x == nullptr) return MOE_ERR_NULL;
+  if (x->struct_size != sizeof(*x)) return MOE_ERR_UNSUPPORTED;
+  if (x->groups < 0 || x->max_tokens < 0) return MOE_ERR_SHAPE;
+  if (a->window != 0) return MOE_ERR_UNSUPPORTED;       // its rows would see different parts of a prefix
+  if (p.N == 0) return MOE_OK;
   (void)cudaGetLastError();
   const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t rows = static_cast<int64_t>(p.max_q_len) * (a->Hq / c.kv_heads);
-  if (few_rows(rows, static_cast<int64_t>(a->B) * c.kv_heads)) return moe::launch_decode_attention(p, a->dtype, on);
-  return moe::launch_prefill_attention(p, a->dtype, on);
+  if (x->groups == 0 || x->max_tokens == 0) return attend(p, nullptr, a->dtype, on);
+  if (x->lens == nullptr || (x->seqs == nullptr && x->groups != 1)) return MOE_ERR_NULL;
+  const size_t need = moe_shared_prefix_partial_size(p.N, p.Hq, p.cache.head_dim);
+  if (x->partial == nullptr || !aligned(x->partial, 16) || x->partial_bytes < need) return MOE_ERR_WORKSPACE;
+  if (rows_of(p) > kSharedRows) return attend(p, nullptr, a->dtype, on);
+  AttentionForms f = {};
+  f.groups = x->groups, f.sequences = p.B;
+  f.max_tokens = x->max_tokens < p.N ? x->max_tokens : p.N;
+  f.seqs = x->seqs, f.lens = x->lens;
+  f.sums = static_cast<float*>(x->partial);
+  f.refs = reinterpret_cast<float2*>(f.sums + static_cast<size_t>(p.N) * p.Hq * p.cache.head_dim);
+  f.pass = moe::kPrefixPass;
+  AttentionParams prefix = p;
+  prefix.B = x->groups;
+  prefix.max_q_len = f.max_tokens;
+  const bool few = few_rows(rows_of(prefix), static_cast<int64_t>(prefix.B) * p.cache.kv_heads);
+  const int error = few ? moe::launch_decode_attention(prefix, &f, a->dtype, on) : moe::launch_prefill_attention(prefix, &f, a->dtype, on);
+  if (error != MOE_OK) return error;
+  f.pass = moe::kOwnPass;
+  f.late = !few;                                        // the two kernels have workspaces of their own
+  return moe::launch_decode_attention(p, &f, a->dtype, on);
 }
 
 }  // extern "C"

@@ -117,6 +117,13 @@ struct Launch {
   int b0, B, row_tiles, tile_rows;        // sequences [b0, b0 + B), row tiles of each and their rows
   int box;                                // keys of one TMA box: gcd(page_size, 16)
 };
+// With sinks or shared prefixes; all their tests are behind FORMS, so that the
+// kernels without have none of them.
+struct FormsLaunch : Launch {
+  AttentionForms f;
+};
+template <bool FORMS> struct LaunchOf { using type = Launch; };
+template <> struct LaunchOf<true> { using type = FormsLaunch; };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -140,19 +147,37 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// The rows of entry e (a sequence and a row tile of it).
-struct Entry {
+// The rows of entry e (a sequence, or in the prefix pass a group of them, and a
+// row tile of it); b is its row of the block table.
+template <bool FORMS>
+struct EntryOf {
   int b, q_first, q_len, len, row0, rows;
-  __device__ __forceinline__ Entry(const Launch& p, int e, int group) {
+  bool flat;                              // every row sees all ``len`` keys
+  __device__ __forceinline__ EntryOf(const typename LaunchOf<FORMS>::type& p, int e, int group) {
     b = p.b0 + e / p.row_tiles;
     row0 = (e % p.row_tiles) * p.tile_rows;
-    q_first = p.a.cu_q == nullptr ? b : p.a.cu_q[b];
-    q_len = p.a.cu_q == nullptr ? 1 : p.a.cu_q[b + 1] - q_first;
-    len = p.a.seq_lens[b];
+    flat = false;
+    if constexpr (FORMS) {
+      if (p.f.pass == kPrefixPass) {
+        int s0, q_end;
+        p.f.group(p.a.cu_q, b, s0, q_first, q_end);
+        len = p.f.lens[b];
+        q_len = len > 0 ? q_end - q_first : 0;
+        b = s0;
+        flat = true;
+      }
+    }
+    if (!FORMS || !flat) {
+      q_first = p.a.cu_q == nullptr ? b : p.a.cu_q[b];
+      q_len = p.a.cu_q == nullptr ? 1 : p.a.cu_q[b + 1] - q_first;
+      len = p.a.seq_lens[b];
+    }
     const int n = min(min(q_len, p.a.max_q_len), p.a.N - q_first);
     rows = max(0, min(p.tile_rows, n * group - row0));
   }
-  __device__ __forceinline__ int position(int row, int group) const { return len - q_len + (row0 + row) / group; }
+  __device__ __forceinline__ int position(int row, int group) const {
+    return FORMS && flat ? len - 1 : len - q_len + (row0 + row) / group;
+  }
 };
 
 // Where tile x of the line lies.
@@ -179,9 +204,11 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w, uint32_t& seen) {
   return w & ~nan;
 }
 
-template <typename T, int DP, int NT>
+template <typename T, int DP, int NT, bool FORMS>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
-decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ Launch p) {
+decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                        const __grid_constant__ typename LaunchOf<FORMS>::type p) {
+  using Entry = EntryOf<FORMS>;
   extern __shared__ uint8_t raw[];
   uint8_t* const rings = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   float* const scratch = reinterpret_cast<float*>(rings + kWarps * kRing * kSlotBytes);
@@ -203,9 +230,25 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     s.abort_flag = 0;
     fence_mbarrier_init();
   }
+  bool late = false;
+  int sinks = 0;
+  if constexpr (FORMS) {
+    // The own pass may run beside the prefix pass, which lets it start when all
+    // that came before is done, and only waits for its sums.
+    late = p.f.late != 0;
+    sinks = p.f.sinks;
+    if (p.f.pass == kPrefixPass) pdl_wait();
+  }
   pdl_launch_dependents();
-  pdl_wait();
+  if (!late) pdl_wait();
 
+  // The tiles before those of the window that hold keys which stay visible, and
+  // the first key of tile i of an entry that begins at ``lo``.
+  auto sink_tiles = [&](int lo) { return FORMS ? min((sinks + kKeys - 1) / kKeys, lo / kKeys) : 0; };
+  auto key_of = [&](int lo, int i) {
+    const int before = sink_tiles(lo);
+    return (FORMS && i < before ? i : lo / kKeys + i - before) * kKeys;
+  };
   // The line: each entry's key tiles, one at least so that someone writes its rows.
   const int64_t most = static_cast<int64_t>(a.table_width) * ca.page_size;
 #pragma unroll 1
@@ -215,12 +258,15 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     if (en.rows > 0) {
       const int pos0 = en.position(0, group), pos1 = en.position(en.rows - 1, group);
       lo = a.window > 0 && pos0 >= a.window ? pos0 + 1 - a.window : 0;
+      if constexpr (FORMS) {
+        if (p.f.pass == kOwnPass) lo = p.f.taken(a.cu_q, en.b, en.q_first, en.q_len, en.len - en.q_len);
+      }
       hi = max(0, pos1 + 1);
       if (hi > most) {
         hi = static_cast<int>(most);
         set_status(a.status, MOE_ERR_BAD_PAGE);
       }
-      n = max(1, (hi + kKeys - 1) / kKeys - lo / kKeys);
+      n = max(1, (hi + kKeys - 1) / kKeys - lo / kKeys + sink_tiles(lo));
     }
     s.prefix[e + 1] = n;
     s.begin[e] = lo;
@@ -272,13 +318,17 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     const int k = batch * kBatch + (lane >> 1);
     if (k < steps) {
       const Place at(s, entries, ca.kv_heads, x0 + k);
-      const int key = (s.begin[at.e] / kKeys + at.tile) * kKeys + 16 * warp + 8 * (lane & 1);
+      const int key = key_of(s.begin[at.e], at.tile) + 16 * warp + 8 * (lane & 1);
       // boxes that no row sees are not looked up: their pages may be gone
-      if (key < s.end[at.e] && (key & ~(p.box - 1)) + p.box > s.begin[at.e]) {
+      if (key < s.end[at.e] && ((key & ~(p.box - 1)) + p.box > s.begin[at.e] || (FORMS && (key & ~(p.box - 1)) < sinks))) {
         const int page_at = key / ca.page_size;
         f.off = key - page_at * ca.page_size;
         f.head = at.head;
-        f.page = a.block_table[static_cast<int64_t>(p.b0 + at.e / p.row_tiles) * a.table_width + page_at];
+        int row = p.b0 + at.e / p.row_tiles;
+        if constexpr (FORMS) {
+          if (p.f.pass == kPrefixPass) row = p.f.seqs == nullptr ? 0 : max(0, p.f.seqs[row]);
+        }
+        f.page = a.block_table[static_cast<int64_t>(row) * a.table_width + page_at];
         if (f.page < 0 || f.page >= ca.num_pages) {
           f.page = -1;
           set_status(a.status, MOE_ERR_BAD_PAGE);
@@ -338,13 +388,15 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 
   {
     const int g = lane >> 2, c = lane & 3;
-    int taken = 0;                         // tiles consumed so far
+    int done = 0;                          // tiles consumed so far
 #pragma unroll 1
     for (int x = x0; x < x1;) {
       const Place at(s, entries, ca.kv_heads, x);
       const Entry en(p, at.e, group);
       const int n = min(at.count - at.tile, x1 - x);
-      const int first_tile = s.begin[at.e] / kKeys + at.tile;
+      const int begin = s.begin[at.e];
+      int taken = 0;                       // keys that the prefix pass has taken
+      if constexpr (FORMS) taken = p.f.pass == kOwnPass ? begin : 0;
       const int pos_min = en.position(0, group), pos_max = en.position(en.rows - 1, group);
       const int end = s.end[at.e];
 
@@ -404,15 +456,19 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       }
 
 #pragma unroll 1
-      for (int i = 0; i < n; ++i, ++taken) {
-        const int slot = taken % kRing;
-        wait(&s.full[warp][slot], (taken / kRing) & 1);
-        const int key0 = (first_tile + i) * kKeys + 16 * warp;
+      for (int i = 0; i < n; ++i, ++done) {
+        const int slot = done % kRing;
+        wait(&s.full[warp][slot], (done / kRing) & 1);
+        const int key0 = key_of(begin, at.tile + i) + 16 * warp;
         const uint8_t* kt = rings + (warp * kRing + slot) * kSlotBytes;
         const uint8_t* vt = kt + 16 * kPitch;
-        const Group* groups = &s.group[warp][taken / kBatch & 1][2 * (taken % kBatch)];
+        const Group* groups = &s.group[warp][done / kBatch & 1][2 * (done % kBatch)];
         const Group g0 = groups[0], g1 = groups[1];
-        const bool some = key0 < end && (a.window == 0 || key0 + 15 > pos_min - a.window) && (g0.valid || g1.valid);
+        // what a row at position ps sees
+        auto sees = [&](int key, int ps) {
+          return key <= ps && (a.window == 0 || key > ps - a.window || (FORMS && key < sinks)) && (!FORMS || key >= taken);
+        };
+        const bool some = key0 < end && (a.window == 0 || key0 + 15 > pos_min - a.window || (FORMS && key0 < sinks)) && (g0.valid || g1.valid);
         if (some) {
           // S^T = K Q^T for 16 keys: sc[t] = (key g, rows 2c and 2c + 1), (key g + 8, the same)
           float sc[NT][4] = {};
@@ -445,7 +501,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             }
           }
           // exponents of the weights, and whether some reference has to move
-          const bool whole = key0 + 15 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) && g0.valid && g1.valid;
+          const bool whole = key0 + 15 <= pos_min && (a.window == 0 || key0 > pos_max - a.window || (FORMS && key0 + 15 < sinks)) &&
+                             (!FORMS || key0 >= taken) && g0.valid && g1.valid;
           bool move = false;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
@@ -455,7 +512,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
               float y = fmaf(sc[t][j], gr.k * row_scale[t][j & 1], gr.lv);
               if (!whole) {
                 const int key = key0 + (j < 2 ? 0 : 8) + g, ps = pos[t][j & 1];
-                if (!gr.valid || key > ps || (a.window > 0 && key <= ps - a.window)) y = -INFINITY;
+                if (!gr.valid || !sees(key, ps)) y = -INFINITY;
               }
               sc[t][j] = y;
             }
@@ -543,7 +600,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                   for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int z = 0; z < 2; ++z)
-                      if (bad && key <= pos[t][z] && (a.window == 0 || key > pos[t][z] - a.window)) o[t][j][2 * d + z] = __uint_as_float(0x7FC00000u);
+                      if (bad && sees(key, pos[t][z])) o[t][j][2 * d + z] = __uint_as_float(0x7FC00000u);
                 }
             }
           }
@@ -616,8 +673,38 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             const int row = 8 * t + 2 * c + z;
             if (row >= en.rows) continue;
             if (!split) {
-              const float inv = Ls[t][z] == 0.f ? 0.f : 1.f / Ls[t][z];
               const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
+              if constexpr (FORMS) {
+                float* sums = p.f.sums + (static_cast<int64_t>(tok) * a.Hq + h) * ca.head_dim;
+                float2* ref = p.f.refs + static_cast<int64_t>(tok) * a.Hq + h;
+                if (p.f.pass == kPrefixPass) {
+#pragma unroll
+                  for (int j = 0; j < kTiles; j += 2) {
+                    const float v[4] = {o[t][j][z], o[t][j][2 + z], o[t][j + 1][z], o[t][j + 1][2 + z]};
+                    const int col = (DP / 8) * g + 2 * j;
+                    if (col < ca.head_dim) store_f32<float, 4>(sums + col, v);
+                  }
+                  if (g == 0) *ref = make_float2(M[t][z], Ls[t][z]);
+                  continue;
+                }
+                if (taken > 0) {
+                  if (late) pdl_wait();
+                  const float2 other = __ldcg(ref);
+                  const float top = fmaxf(M[t][z], other.x), mine = fast_exp2(M[t][z] - top), theirs = fast_exp2(other.x - top);
+                  M[t][z] = top;
+                  Ls[t][z] = fmaf(Ls[t][z], mine, other.y * theirs);
+#pragma unroll
+                  for (int j = 0; j < kTiles; j += 2) {
+                    const int col = (DP / 8) * g + 2 * j;
+                    const float4 v = col < ca.head_dim ? __ldcg(reinterpret_cast<const float4*>(sums + col)) : make_float4(0, 0, 0, 0);
+                    o[t][j][z] = fmaf(o[t][j][z], mine, v.x * theirs);
+                    o[t][j][2 + z] = fmaf(o[t][j][2 + z], mine, v.y * theirs);
+                    o[t][j + 1][z] = fmaf(o[t][j + 1][z], mine, v.z * theirs);
+                    o[t][j + 1][2 + z] = fmaf(o[t][j + 1][2 + z], mine, v.w * theirs);
+                  }
+                }
+              }
+              const float inv = Ls[t][z] == 0.f ? 0.f : 1.f / Ls[t][z];
               T* dst = static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head;
 #pragma unroll
               for (int j = 0; j < kTiles; j += 4) {
@@ -709,8 +796,29 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
               Mx = now;
             }
             if (finish) {
-              const float inv = Lx == 0.f ? 0.f : 1.f / Lx;
               const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
+              if constexpr (FORMS) {
+                float* sums = p.f.sums + (static_cast<int64_t>(tok) * a.Hq + h) * ca.head_dim + col;
+                float2* ref = p.f.refs + static_cast<int64_t>(tok) * a.Hq + h;
+                if (p.f.pass == kPrefixPass) {
+                  if (col < ca.head_dim) store_f32<float, 4>(sums, acc);
+                  if (lane == 0) *ref = make_float2(Mx, Lx);
+                  continue;
+                }
+                if (taken > 0) {
+                  if (late) pdl_wait();
+                  const float2 other = __ldcg(ref);
+                  const float4 v = col < ca.head_dim ? __ldcg(reinterpret_cast<const float4*>(sums)) : make_float4(0, 0, 0, 0);
+                  const float top = fmaxf(Mx, other.x), mine = fast_exp2(Mx - top), theirs = fast_exp2(other.x - top);
+                  Mx = top;
+                  Lx = fmaf(Lx, mine, other.y * theirs);
+                  acc[0] = fmaf(acc[0], mine, v.x * theirs);
+                  acc[1] = fmaf(acc[1], mine, v.y * theirs);
+                  acc[2] = fmaf(acc[2], mine, v.z * theirs);
+                  acc[3] = fmaf(acc[3], mine, v.w * theirs);
+                }
+              }
+              const float inv = Lx == 0.f ? 0.f : 1.f / Lx;
 #pragma unroll
               for (int q = 0; q < 4; ++q) acc[q] *= inv;
               if (col < ca.head_dim) store_f32<T, 4>(static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head + col, acc);
@@ -733,6 +841,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     }
   }
 
+  if (late) pdl_wait();                    // who waits for this kernel waits for the one before it
   // Nothing of this warp is in flight when it ends: it has waited for every
   // tile, unless a wait ran out.
   if (*static_cast<volatile int*>(&s.abort_flag)) {
@@ -806,14 +915,15 @@ cudaError_t clear_decode_counters(void* workspace, cudaStream_t s) {
 
 namespace {
 
-template <typename T, int DP, int NT>
-int launch(const AttentionParams& a, cudaStream_t stream) {
+template <typename T, int DP, int NT, bool FORMS>
+int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t stream) {
   CUtensorMap k_map, v_map;
-  Launch p = {};
+  typename LaunchOf<FORMS>::type p = {};
   p.a = a;
+  if constexpr (FORMS) p.f = *forms;
   p.box = gcd(a.cache.page_size, 16);
   if (!encode_cache_map(&k_map, a.cache, false, p.box) || !encode_cache_map(&v_map, a.cache, true, p.box)) return MOE_ERR_CUDA;
-  auto kernel = decode_attention_kernel<T, DP, NT>;
+  auto kernel = decode_attention_kernel<T, DP, NT, FORMS>;
   constexpr int bytes = kSmem(8 * NT);
   p.tile_rows = 8 * NT;
   if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes) != cudaSuccess) return MOE_ERR_CUDA;
@@ -837,23 +947,26 @@ int launch(const AttentionParams& a, cudaStream_t stream) {
     if (grid > tiles) grid = tiles;
     if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), bytes, stream, k_map, v_map, p) != cudaSuccess)
       return MOE_ERR_CUDA;
+    if constexpr (FORMS) p.f.late = 0;     // the next launch uses the same workspace as this one
   }
   return MOE_OK;
 }
 
-}  // namespace
-
-namespace {
-template <typename T>
-int launch_rows(const AttentionParams& p, cudaStream_t s) {
+template <typename T, bool FORMS>
+int launch_rows(const AttentionParams& p, const AttentionForms* forms, cudaStream_t s) {
   const bool few = static_cast<int64_t>(p.max_q_len) * (p.Hq / p.cache.kv_heads) <= 8;
-  if (p.cache.head_dim <= 64) return few ? launch<T, 64, 1>(p, s) : launch<T, 64, 2>(p, s);
-  return few ? launch<T, 128, 1>(p, s) : launch<T, 128, 2>(p, s);
+  if (p.cache.head_dim <= 64) return few ? launch<T, 64, 1, FORMS>(p, forms, s) : launch<T, 64, 2, FORMS>(p, forms, s);
+  return few ? launch<T, 128, 1, FORMS>(p, forms, s) : launch<T, 128, 2, FORMS>(p, forms, s);
+}
+
+template <bool FORMS>
+int launch_type(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s) {
+  return dtype == MOE_DTYPE_F16 ? launch_rows<__half, FORMS>(p, forms, s) : launch_rows<__nv_bfloat16, FORMS>(p, forms, s);
 }
 }  // namespace
 
-int launch_decode_attention(const AttentionParams& p, int dtype, cudaStream_t s) {
-  return dtype == MOE_DTYPE_F16 ? launch_rows<__half>(p, s) : launch_rows<__nv_bfloat16>(p, s);
+int launch_decode_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s) {
+  return forms != nullptr ? launch_type<true>(p, forms, dtype, s) : launch_type<false>(p, forms, dtype, s);
 }
 
 }  // namespace moe

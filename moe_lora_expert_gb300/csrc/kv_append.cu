@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
   constexpr bool kAxes = !std::is_same<Axes, OneAxis>::value;
   __shared__ float s_max[32];
   __shared__ int s_pos[kMaxThreads];
+  extern __shared__ __align__(16) float angles[];     // with axes: a row of R for each token of the CTA
   pdl_launch_dependents();
   pdl_wait();
   const moe_kv_cache_t& ca = p.cache;
@@ -87,8 +88,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
       int pos = kSkipped;
       if (p.cu_q == nullptr || static_cast<int>(t) < p.cu_q[p.B]) {          // else a row of no sequence
         if constexpr (kAxes) {
-          AxisPositions at;                                                   // the threads that turn the token read them again
-          pos = at.load(axes, p.positions, t, p.num_positions) ? 0 : kUnturned;
+          bool good;
+          axis_position(axes, p.positions, t, p.num_positions, 0, good);
+          pos = good ? 0 : kUnturned;
         } else if (p.positions != nullptr) {
           pos = p.positions[t];
         } else {
@@ -103,13 +105,15 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
       }
       s_pos[tid] = pos;
     }
+    if constexpr (kAxes) {
+      const uint32_t end = min((item0 + blockDim.x - 1) / p.q_items + 1, static_cast<uint32_t>(p.N));
+      gather_angles(angles, nullptr, axes, p.positions, p.cos_sin, token0, end - token0, p.R, p.num_positions);
+    }
     __syncthreads();
     if constexpr (kAxes) {
-      const int state = x.live ? s_pos[x.t - token0] : kSkipped;
+      const int j = x.live ? static_cast<int>(x.t - token0) : 0, state = x.live ? s_pos[j] : kSkipped;
       if (state == kSkipped) return;
-      AxisPositions at;
-      at.load(axes, p.positions, x.t, p.num_positions);
-      x.finish(p.q, RopeTensor{}, at, state != kUnturned, axes, p.R, p.interleaved, false, p.cos_sin);
+      x.turn_by(p.q, RopeTensor{}, state == kUnturned ? nullptr : angles + j * p.R, p.R, p.interleaved, false);
     } else {
       if (x.live) x.finish(p.q, RopeTensor{}, s_pos[x.t - token0], p.R, p.interleaved, false, p.cos_sin);
     }
@@ -155,16 +159,17 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
     ra = *reinterpret_cast<const Pack<T, V>*>(row + s.a);
     rb = *reinterpret_cast<const Pack<T, V>*>(row + s.b);
   };
+  [[maybe_unused]] int* good = nullptr;
+  if constexpr (kAxes) good = reinterpret_cast<int*>(angles + rows * p.R);
   auto rotated = [&](int j, const Pack<T, V>& ra, const Pack<T, V>& rb, float (&a)[V], float (&bb)[V]) {
     const int r = j / per_head, c = j - r * per_head;
     to_f32s<T, V>(ra, a);
     to_f32s<T, V>(rb, bb);
     if constexpr (kAxes) {
       if (turn && 2 * V * c < p.R) {
-        AxisPositions at;
-        if (at.load(axes, p.positions, t_first + (p0 - start) + r, p.num_positions)) {
+        if (good[r] != 0) {
           float cs[V], sn[V];
-          load_cos_sin<V>(p.cos_sin, at, axes, c, p.R, cs, sn);
+          load_cos_sin<V>(angles + r * p.R, c, p.R, cs, sn);
           rotate<V, true>(a, bb, cs, sn, p.interleaved);
         } else {
           set_status(p.status, MOE_ERR_BAD_POSITION);
@@ -197,6 +202,12 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
     if (tid + i * step < items) load(tid + i * step, ra[i], rb[i]);
+  if constexpr (kAxes) {
+    if (turn) {
+      gather_angles(angles, good, axes, p.positions, p.cos_sin, t_first + (p0 - start), rows, p.R, p.num_positions);
+      __syncthreads();
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
     if (tid + i * step < items) reduce(tid + i * step, ra[i], rb[i]);
@@ -267,7 +278,15 @@ cudaError_t launch_heads(KvAppendParams p, const Axes& axes, cudaStream_t s) {
   const int64_t units = 2ll * p.B * p.slots * p.cache.kv_heads;
   p.q_items = p.q.heads > 0 ? rotation_items<V>(p.q.heads, HEADS, p.cache.head_dim) : 1;
   const int64_t q_ctas = p.q.heads > 0 ? (static_cast<int64_t>(p.N) * p.q_items + threads - 1) / threads : 0;
-  return launch_pdl(kv_append_kernel<T, V, HEADS, Axes>, dim3(static_cast<unsigned>(units + q_ctas)), dim3(threads), 0, s, p, axes);
+  size_t bytes = 0;
+  const auto kernel = kv_append_kernel<T, V, HEADS, Axes>;
+  if constexpr (!std::is_same<Axes, OneAxis>::value) {
+    // a row of angles and a word for each token of a page, or of a CTA's stretches of q: up to 129 KB (a page of 256, whose CTA has an SM to itself)
+    const uint32_t tokens = q_ctas > 0 ? axes_tokens(static_cast<uint32_t>(threads), p.q_items) : 1;
+    bytes = (tokens > static_cast<uint32_t>(rows) ? tokens : rows) * static_cast<size_t>(p.R + 1) * 4;
+    if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), static_cast<int>(bytes)) != cudaSuccess) return cudaErrorInvalidValue;
+  }
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(units + q_ctas)), dim3(threads), bytes, s, p, axes);
 }
 
 template <typename T, int V, typename Axes>

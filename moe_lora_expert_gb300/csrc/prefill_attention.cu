@@ -92,6 +92,13 @@ struct Launch {
   uint8_t* workspace;
   int box;                                 // keys of one TMA box: gcd(page_size, 128)
 };
+// With sinks or as a prefix pass, in kernels of their own: all of it is behind
+// FORMS, since the other ones have no instructions to spare.
+struct FormsLaunch : Launch {
+  AttentionForms f;
+};
+template <bool FORMS> struct LaunchOf { using type = Launch; };
+template <> struct LaunchOf<true> { using type = FormsLaunch; };
 
 // ------------------------------------------------------------------ tcgen05
 __device__ __forceinline__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
@@ -190,41 +197,75 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 }
 
 // ------------------------------------------------------------------- units
-// The rows of one (sequence, row tile) and the keys they see.
-struct Entry {
+// The rows of one (sequence, row tile) and the keys they see; in the prefix
+// pass of a group of sequences, and b is its first one.
+template <bool FORMS>
+struct EntryForms {
+  int before;                              // tiles of sinks before those of the window
+  bool flat;                               // every row sees all keys
+};
+template <>
+struct EntryForms<false> {
+  static constexpr int before = 0;
+  static constexpr bool flat = false;
+};
+template <bool FORMS>
+struct Entry : EntryForms<FORMS> {
+  using EntryForms<FORMS>::before;
+  using EntryForms<FORMS>::flat;
   int b, q_first, row0, rows, start, lo, end, tile0, count;
-  __device__ __forceinline__ void load(const Launch& p, int e, int group) {
+  __device__ __forceinline__ void load(const typename LaunchOf<FORMS>::type& p, int e, int group) {
     const AttentionParams& a = p.a;
     b = e / p.row_tiles;
     row0 = (e - b * p.row_tiles) * p.unit_rows;
-    q_first = a.cu_q == nullptr ? b : a.cu_q[b];
-    const int q_len = a.cu_q == nullptr ? 1 : a.cu_q[b + 1] - q_first;
-    start = a.seq_lens[b] - q_len;
+    int q_len, len = 0;
+    if constexpr (FORMS) {
+      flat = p.f.pass == kPrefixPass;
+      if (flat) {
+        int s0, q_end;
+        p.f.group(a.cu_q, b, s0, q_first, q_end);
+        len = p.f.lens[b];
+        q_len = len > 0 ? q_end - q_first : 0;
+        b = s0;
+      }
+    }
+    if (!flat) {
+      q_first = a.cu_q == nullptr ? b : a.cu_q[b];
+      q_len = a.cu_q == nullptr ? 1 : a.cu_q[b + 1] - q_first;
+      len = a.seq_lens[b];
+    }
+    start = flat ? len - 1 : len - q_len;
     rows = max(0, min(p.unit_rows, min(min(q_len, a.max_q_len), a.N - q_first) * group - row0));
     lo = end = tile0 = count = 0;
+    if constexpr (FORMS) before = 0;
     if (rows > 0) {
       lo = a.window > 0 ? max(0, position(0, group) + 1 - a.window) : 0;
       const int64_t most = static_cast<int64_t>(a.table_width) * a.cache.page_size;
       end = static_cast<int>(min(static_cast<int64_t>(max(0, position(rows - 1, group) + 1)), most));
       tile0 = lo / kKeys;
-      count = max(1, (end + kKeys - 1) / kKeys - tile0);      // one at least, so that someone writes the rows
+      if constexpr (FORMS) before = min((p.f.sinks + kKeys - 1) / kKeys, tile0);
+      count = max(1, (end + kKeys - 1) / kKeys - tile0 + before);   // one at least, so that someone writes the rows
     }
   }
-  __device__ __forceinline__ int position(int row, int group) const { return start + (row0 + row) / group; }
+  __device__ __forceinline__ int position(int row, int group) const { return flat ? start : start + (row0 + row) / group; }
+  // Which of the sequence's key tiles is the entry's tile i.
+  __device__ __forceinline__ int tile_at(int i) const { return i < before ? i : tile0 + i - before; }
   // Whether rows r0 to r1 all see every key of a tile (if its pages are there).
-  __device__ __forceinline__ bool whole(int tile, int r0, int r1, int group, int window) const {
+  __device__ __forceinline__ bool whole(int tile, int r0, int r1, int group, int window, int sinks) const {
     const int key0 = tile * kKeys;
-    return key0 + kKeys - 1 <= position(r0, group) && (window == 0 || key0 > position(r1, group) - window);
+    return key0 + kKeys - 1 <= position(r0, group) &&
+           (window == 0 || key0 > position(r1, group) - window || (FORMS && key0 + kKeys <= sinks));
   }
 };
 
 // A CTA's stretch of the line, unit by unit; every warp walks it by itself.
 // On the line a unit is kUnitCost places and then a place a key tile.  Where
 // ``whole`` is given the CTA has those units instead, x to x1.
-struct Walk {
-  Entry en;
+template <bool FORMS>
+struct WalkOf {
+  Entry<FORMS> en;
   int e, head, tile, x, x1, n, u0, span;   // this piece: tiles [tile, tile + n) of the unit that begins at u0
-  __device__ __forceinline__ bool next(const Launch& p, int group, const int* whole, bool first, int first_entry, int first_prefix) {
+  __device__ __forceinline__ bool next(const typename LaunchOf<FORMS>::type& p, int group, const int* whole, bool first, int first_entry, int first_prefix) {
     const int heads = p.a.cache.kv_heads;
     if (whole != nullptr) {
       if (x == x1) return false;
@@ -272,7 +313,9 @@ struct Walk {
 // keep each from writing the next piece while another still reads this one or
 // has yet to take the same step (the loops that come here end in code which a
 // warp's lanes may leave one by one).
-__device__ __noinline__ bool walk_next(Walk* at, const Launch& p, int group, const int* whole, int first_entry, int first_prefix, uint32_t lanes) {
+template <bool FORMS>
+__device__ __noinline__ bool walk_next(WalkOf<FORMS>* at, const typename LaunchOf<FORMS>::type& p, int group, const int* whole, int first_entry, int first_prefix, uint32_t lanes) {
+  using Walk = WalkOf<FORMS>;
   __syncwarp(lanes);
   Walk w = *at;
   const bool more = w.next(p, group, whole, first_entry >= 0, first_entry, first_prefix);
@@ -303,6 +346,7 @@ __device__ __noinline__ uint4 nan_columns(const AttentionParams& a, int b, int h
   return make_uint4(nan[0], nan[1], nan[2], nan[3]);
 }
 // ----------------------------------------------------------- shared memory
+template <bool FORMS>
 struct Control {
   Group group[kInfo][kKeys / 8];
   uint64_t code_full[kStages], code_empty[kStages], full[kSlots], empty[kSlots];
@@ -310,7 +354,7 @@ struct Control {
   int8_t q_exponent[kCtaRows];             // of the power of two taken out of each row
   int sums[kThreads / 32];
   int units[kMaxUnits];                    // this CTA's, if it has whole ones
-  Walk walk[kThreads / 32];                // each warp's own, here and not in its registers
+  WalkOf<FORMS> walk[kThreads / 32];                // each warp's own, here and not in its registers
   // Of a unit and the next: the key tiles, hidden from some rows, in which a
   // converting warp has met and left out NaN values that some row sees.
   int nan_count[2][4], nan_tiles[2][4][kNanTiles];
@@ -326,14 +370,15 @@ struct Layout {
   static constexpr int kQBytes = 2 * kHalves * kHalfBytes;
   static constexpr int kCodeBytes = kKeys * 128;
   static constexpr int kQ = 0, kRing = kQBytes, kCode = kRing + kSlots * kSlotBytes,
-                       kControl = kCode + kStages * kCodeBytes, kBytes = kControl + static_cast<int>(sizeof(Control));
+                       kControl = kCode + kStages * kCodeBytes;
+  template <bool FORMS> static constexpr int kBytes = kControl + static_cast<int>(sizeof(Control<FORMS>));
 };
-static_assert(Layout<128>::kBytes <= 232448, "shared memory of a CTA");
+static_assert(Layout<128>::kBytes<true> <= 232448, "shared memory of a CTA");
 
 // The queries of a unit by plain loads, to where and how the TMA would put
 // them (f16 rows with the sign of the scale): rows first, first + 128, ...
-template <typename T, int DP>
-__device__ __noinline__ void load_queries(const AttentionParams& a, const Entry& en, int head, int group, uint8_t* to, int first) {
+template <typename T, int DP, bool FORMS>
+__device__ __noinline__ void load_queries(const AttentionParams& a, const Entry<FORMS>& en, int head, int group, uint8_t* to, int first) {
 #pragma unroll 1
   for (int row = first; row < kCtaRows; row += kTileRows) {
     const int gr = en.row0 + row;
@@ -351,14 +396,20 @@ __device__ __noinline__ void load_queries(const AttentionParams& a, const Entry&
 // MAPPED: queries come by TMA.  A tensor map holds no strides of zero or below;
 // with those they come by plain loads, in a kernel of its own, as the other one
 // has no instructions to spare (117.5 instead of 116.5 us on ragged chunks).
-template <typename T, int DP, bool MAPPED>
+template <typename T, int DP, bool MAPPED, bool FORMS>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ Launch p) {
+                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ typename LaunchOf<FORMS>::type p) {
   using L = Layout<DP>;
+  int sinks = 0;
+  bool prefix = false;
+  if constexpr (FORMS) {
+    sinks = p.f.sinks;
+    prefix = p.f.pass == kPrefixPass;
+  }
   constexpr bool kBf16 = !std::is_same<T, __half>::value;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Control& s = *reinterpret_cast<Control*>(smem + L::kControl);
+  Control<FORMS>& s = *reinterpret_cast<Control<FORMS>*>(smem + L::kControl);
   const AttentionParams& a = p.a;
   const moe_kv_cache_t& ca = a.cache;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -395,6 +446,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     s.abort_flag = 0;
     fence_mbarrier_init();
   }
+  if (FORMS) pdl_wait();                   // the own pass may begin beside this one, when all that came before is done
   pdl_launch_dependents();
   pdl_wait();
 
@@ -404,7 +456,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   int mine = 0;
 #pragma unroll 1
   for (int e = from; e < to; ++e) {
-    Entry en;
+    Entry<FORMS> en;
     en.load(p, e, group);
     if (en.count > 0) mine += en.count + kUnitCost;
   }
@@ -478,7 +530,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     int before = incl - mine;
 #pragma unroll 1
     for (int e = from; e < to; ++e) {
-      Entry en;
+      Entry<FORMS> en;
       en.load(p, e, group);
       const int places = en.count > 0 ? en.count + kUnitCost : 0;
       if (x0 < (before + places) * ca.kv_heads) {
@@ -511,8 +563,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     const bool ok = wait_one(bar, parity);
     return __all_sync(0xffffffffu, ok) != 0;
   };
-  Walk& walk = s.walk[warp];
-  const Entry& en = walk.en;
+  WalkOf<FORMS>& walk = s.walk[warp];
+  const Entry<FORMS>& en = walk.en;
   // who walks: a whole warp with the same values, or the one lane that issues the products
   const uint32_t walkers = warp == kMmaWarp ? 1u << lane : 0xffffffffu;
   auto next = [&](bool first) {
@@ -520,7 +572,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       walk.x = whole ? 0 : x0;
       walk.x1 = whole ? s.given : stretch_begin(total, ctas, blockIdx.x + 1);
     }
-    return walk_next(&walk, p, group, whole ? s.units : nullptr, first ? s.first_entry : -1, s.first_prefix, walkers);
+    return walk_next<FORMS>(&walk, p, group, whole ? s.units : nullptr, first ? s.first_entry : -1, s.first_prefix, walkers);
   };
 
   if (warp == kLoadWarp) {
@@ -534,8 +586,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     };
     auto find = [&](int j) {
       Ahead f = {-1, 0, {0.f, 0.f, 0.f, 0}};
-      const int key = (en.tile0 + walk.tile + j) * kKeys + 8 * (lane & 15);
-      if (j < walk.n && key < en.end && (key & ~(p.box - 1)) + p.box > en.lo) {
+      const int key = en.tile_at(walk.tile + j) * kKeys + 8 * (lane & 15);
+      if (j < walk.n && key < en.end && ((key & ~(p.box - 1)) + p.box > en.lo || (FORMS && (key & ~(p.box - 1)) < sinks))) {
         const int page_at = key / ca.page_size;
         f.off = key - page_at * ca.page_size;
         f.page = a.block_table[static_cast<int64_t>(en.b) * a.table_width + page_at];
@@ -696,11 +748,11 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         uint8_t* dst = smem + L::kRing + slot * L::kSlotBytes;
         // a weight of zero times a NaN code would be NaN: where some row does
         // not see some key, NaN values are left out here and added at the end
-        const int tile = en.tile0 + walk.tile + j / 2;
+        const int tile = en.tile_at(walk.tile + j / 2);
         bool drop = false;
         if ((j & 1) != 0) {
           const int ok = lane < 16 ? info[lane].valid : 1;
-          drop = !__all_sync(0xffffffffu, ok) || !en.whole(tile, 0, en.rows - 1, group, a.window);
+          drop = !__all_sync(0xffffffffu, ok) || !en.whole(tile, 0, en.rows - 1, group, a.window, sinks);
         }
         bool nan = false;
         // a warp keeps to one half of the columns and every second (fourth) group of 8 keys
@@ -733,7 +785,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
             };
             clean(c.x), clean(c.y), clean(c.z), clean(c.w);
             const int key = key0 + it * kStep, at = tile * kKeys + key;
-            nan |= seen != 0 && at >= en.lo && at < en.end && info[key >> 3].valid;      // some row sees it
+            nan |= seen != 0 && (at >= en.lo || (FORMS && at < sinks)) && at < en.end && info[key >> 3].valid;      // some row sees it
             put(it, c);
           }
         }
@@ -755,7 +807,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           // the rows have begun the unit before, so they are done with the one before that
           if (lane == 0) s.nan_count[units & 1][w] = 0;
           if constexpr (!MAPPED) {
-            load_queries<T, DP>(a, en, walk.head, group, smem + L::kQ, 32 * w + lane);
+            load_queries<T, DP, FORMS>(a, en, walk.head, group, smem + L::kQ, 32 * w + lane);
             fence_proxy_async_shared();
             __syncwarp();
           }
@@ -842,7 +894,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
 
 #pragma unroll 1
       for (int j = 0; j < walk.n && good; ++j, ++t, ++s_count) {
-        const int tile_key = (en.tile0 + walk.tile + j) * kKeys;
+        const int tile_key = en.tile_at(walk.tile + j) * kKeys;
         good = wait(&s.info_full[t % kInfo], (t / kInfo) & 1) && wait(&s.s_full[i], s_count & 1);
         if (!good) break;
         tc_fence_after_sync();
@@ -859,7 +911,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           tmem_ld32(sh + 32, rb);
           tmem_wait(ra);
           tmem_wait(rb);
-          const bool all = __all_sync(0xffffffffu, info[lane & 7].valid) && key0 + kHalf - 1 <= pos_lo && (a.window == 0 || key0 > pos_hi);
+          const bool all = __all_sync(0xffffffffu, info[lane & 7].valid) && key0 + kHalf - 1 <= pos_lo &&
+                           (a.window == 0 || key0 > pos_hi || (FORMS && key0 + kHalf <= sinks));
           float top = -INFINITY;
           auto exponents = [&](uint32_t (&r)[32], int c) {
 #pragma unroll
@@ -875,8 +928,12 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
             if (!all) {
               // which of the 32 keys this row sees, a bit each: [first, last]
               const int first = a.window > 0 ? pos - a.window + 1 - key0 - 32 * c : 0, last = pos - key0 - 32 * c;
-              uint32_t mask = last < 0 ? 0u : last >= 31 ? 0xffffffffu : (2u << last) - 1u;
-              mask &= first <= 0 ? 0xffffffffu : first > 31 ? 0u : ~((1u << first) - 1u);
+              uint32_t mask = first <= 0 ? 0xffffffffu : first > 31 ? 0u : ~((1u << first) - 1u);
+              if constexpr (FORMS) {
+                const int stay = sinks - key0 - 32 * c;
+                mask |= stay <= 0 ? 0u : stay > 31 ? 0xffffffffu : (1u << stay) - 1u;
+              }
+              mask &= last < 0 ? 0u : last >= 31 ? 0xffffffffu : (2u << last) - 1u;
 #pragma unroll
               for (int g = 0; g < 4; ++g)
                 if (!info[4 * c + g].valid) mask &= ~(0xFFu << (8 * g));
@@ -968,7 +1025,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       bool any_nan = false;
       const int(&counts)[4] = s.nan_count[units & 1];
       if (good && (counts[0] | counts[1] | counts[2] | counts[3]) != 0) {
-        const int first = en.tile0 + walk.tile, end = first + walk.n;
+        const int first = en.tile_at(walk.tile), end = en.tile_at(walk.tile + walk.n - 1) + 1;
 #pragma unroll 1
         for (int at = first; at < end; ++at) {
           int tile = end;
@@ -985,8 +1042,12 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           at = tile;
           if (live) {
             const int k0 = max(tile * kKeys, a.window > 0 ? pos - a.window + 1 : 0), k1 = min(min(pos, en.end - 1), tile * kKeys + kKeys - 1);
-            const uint4 bits = nan_columns(a, en.b, walk.head, k0, k1);
+            uint4 bits = nan_columns(a, en.b, walk.head, k0, k1);
             nan[0] |= bits.x, nan[1] |= bits.y, nan[2] |= bits.z, nan[3] |= bits.w;
+            if constexpr (FORMS) {
+              bits = nan_columns(a, en.b, walk.head, tile * kKeys, min(sinks - 1, k1));
+              nan[0] |= bits.x, nan[1] |= bits.y, nan[2] |= bits.z, nan[3] |= bits.w;
+            }
           }
         }
         any_nan = (nan[0] | nan[1] | nan[2] | nan[3]) != 0;
@@ -996,6 +1057,15 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       T* dst = static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head;
       const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // whole sectors at a time
       auto put = [&](int d, const float (&v)[32], float inv) {        // columns [d, d + 32)
+        if constexpr (FORMS) {
+          if (prefix) {
+            float* sums = p.f.sums + (static_cast<int64_t>(tok) * a.Hq + h) * ca.head_dim + d;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if (d + e < ca.head_dim) __stcg(reinterpret_cast<float4*>(sums + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+            return;
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 32; e += 16) {
           if (d + e >= ca.head_dim) continue;
@@ -1014,6 +1084,12 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         }
       };
       auto put_lse = [&](float mm, float ll) {
+        if constexpr (FORMS) {
+          if (prefix) {
+            p.f.refs[static_cast<int64_t>(tok) * a.Hq + h] = make_float2(mm, ll);
+            return;
+          }
+        }
         if (a.lse != nullptr) a.lse[static_cast<int64_t>(tok) * a.Hq + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
       };
       // O's columns [d, d + 32): read by the warp as one, which it need not be after rows of its own
@@ -1160,11 +1236,12 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   }
 }
 
-template <typename T, int DP, bool MAPPED>
-int launch(const AttentionParams& a, cudaStream_t stream) {
+template <typename T, int DP, bool MAPPED, bool FORMS>
+int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t stream) {
   CUtensorMap q_map = {}, k_map, v_map;
-  Launch p = {};
+  typename LaunchOf<FORMS>::type p = {};
   p.a = a;
+  if constexpr (FORMS) p.f = *forms;
   p.workspace = static_cast<uint8_t*>(a.workspace) + decode_attention_workspace_bytes();
   p.box = 8;
   while (p.box < kKeys && a.cache.page_size % (2 * p.box) == 0) p.box *= 2;
@@ -1173,8 +1250,8 @@ int launch(const AttentionParams& a, cudaStream_t stream) {
   if (!encode_cache_map(&k_map, a.cache, false, p.box) || !encode_cache_map(&v_map, a.cache, true, p.box) ||
       (MAPPED && !encode_query_map(&q_map, a, std::is_same<T, __half>::value, group, kCtaRows / group)))
     return MOE_ERR_CUDA;
-  auto kernel = prefill_attention_kernel<T, DP, MAPPED>;
-  constexpr int bytes = Layout<DP>::kBytes;
+  auto kernel = prefill_attention_kernel<T, DP, MAPPED, FORMS>;
+  constexpr int bytes = Layout<DP>::template kBytes<FORMS>;
   if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes) != cudaSuccess) return MOE_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
@@ -1198,16 +1275,20 @@ cudaError_t clear_prefill_counters(void* workspace, cudaStream_t s) {
 }
 
 namespace {
-template <typename T>
-int launch_type(const AttentionParams& p, cudaStream_t s) {
+template <typename T, bool FORMS>
+int launch_type(const AttentionParams& p, const AttentionForms* forms, cudaStream_t s) {
   const bool mapped = p.q_token > 0 && p.q_head > 0;
-  if (p.cache.head_dim <= 64) return mapped ? launch<T, 64, true>(p, s) : launch<T, 64, false>(p, s);
-  return mapped ? launch<T, 128, true>(p, s) : launch<T, 128, false>(p, s);
+  if (p.cache.head_dim <= 64) return mapped ? launch<T, 64, true, FORMS>(p, forms, s) : launch<T, 64, false, FORMS>(p, forms, s);
+  return mapped ? launch<T, 128, true, FORMS>(p, forms, s) : launch<T, 128, false, FORMS>(p, forms, s);
+}
+template <bool FORMS>
+int launch_forms(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s) {
+  return dtype == MOE_DTYPE_F16 ? launch_type<__half, FORMS>(p, forms, s) : launch_type<__nv_bfloat16, FORMS>(p, forms, s);
 }
 }  // namespace
 
-int launch_prefill_attention(const AttentionParams& p, int dtype, cudaStream_t s) {
-  return dtype == MOE_DTYPE_F16 ? launch_type<__half>(p, s) : launch_type<__nv_bfloat16>(p, s);
+int launch_prefill_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s) {
+  return forms != nullptr ? launch_forms<true>(p, forms, dtype, s) : launch_forms<false>(p, forms, dtype, s);
 }
 
 }  // namespace moe

@@ -63,7 +63,7 @@ def page_scale(amax):
     return s
 
 
-def attend(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, cu_q, scale, window=0):
+def attend(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, cu_q, scale, window=0, sinks=0):
     """q [N, Hq, D]; codes [pages, Hkv, P, D] uint8.  Returns out, lse, and for
     error bounds sum_j p_j |v_j| [N, Hq, D] and the largest sum_d |q_d k_jd| *
     scale of a row [N, Hq]."""
@@ -76,8 +76,8 @@ def attend(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, cu_q, s
         n = cu_q[b + 1] - cu_q[b]
         for t in range(n):
             i = seq_lens[b] - n + t
-            js = [j for j in range(max(0, i - window + 1) if window else 0, i + 1)
-                  if 0 <= block_table[b][j // P] < k_codes.shape[0]]
+            js = [j for j in range(0, i + 1) if (not window or j > i - window or j < sinks)
+                  and 0 <= block_table[b][j // P] < k_codes.shape[0]]
             if not js:
                 continue
             pg = np.array([block_table[b][j // P] for j in js])
