@@ -698,7 +698,7 @@ int moe_paged_attention_sinks(const moe_paged_attention_args_t* args, int sinks,
  *     all sequences.  lens [groups] int32, device; 0 or less: nothing shared.
  *   max_tokens: at least the most new tokens of one group; it sizes the launch.
  *   partial: device scratch of the call, moe_shared_prefix_partial_size bytes,
- *     16-byte aligned, of any contents.
+ *     32-byte aligned, of any contents.
  * Sequences of many rows (new tokens times query heads of a key head, by
  * max_q_len) fill the tiles of a product by themselves: for more than 128 the
  * call does as moe_paged_attention does.
@@ -711,7 +711,7 @@ typedef struct {
   void* partial;
   size_t partial_bytes;
 } moe_shared_prefix_t;
-size_t moe_shared_prefix_partial_size(int N, int Hq, int head_dim);
+size_t moe_shared_prefix_partial_size(int N, int Hq, int head_dim, int groups);
 int moe_paged_attention_shared(const moe_paged_attention_args_t* args, const moe_shared_prefix_t* shared, moe_stream_t stream);
 
 #ifdef __cplusplus

@@ -146,7 +146,7 @@ def lib() -> ctypes.CDLL:
         L.moe_paged_attention_sinks.restype = i32
         L.moe_paged_attention_sinks.argtypes = [ctypes.c_char_p, i32, vp]
         L.moe_shared_prefix_partial_size.restype = sz
-        L.moe_shared_prefix_partial_size.argtypes = [i32, i32, i32]
+        L.moe_shared_prefix_partial_size.argtypes = [i32, i32, i32, i32]
         L.moe_paged_attention_workspace_size.restype = sz
         L.moe_paged_attention_workspace_size.argtypes = []
         L.moe_paged_attention_workspace_init.restype = i32

@@ -94,7 +94,7 @@ _SHARED = struct.Struct("=Iii4x4Q")
 # imported lazily, as in the rest of the package).
 _torch = _int32_type = _float32_type = None
 _codes: Dict = {}
-_rope_fn = _append_fn = _attend_fn = _rope_axes_fn = _append_axes_fn = _sinks_fn = _shared_fn = _raw_stream = _empty_like = _capturing = _current_device = None
+_rope_fn = _append_fn = _attend_fn = _rope_axes_fn = _append_axes_fn = _sinks_fn = _shared_fn = _partial_size = _raw_stream = _empty_like = _capturing = _current_device = None
 
 # Scratch of attention calls: calls on one stream follow one another and share
 # it, whatever their cache; a captured call runs when its graph does, so each
@@ -105,7 +105,7 @@ _captured: Dict = {}         # (device index, stream handle): (capture id, works
 
 def _bind():
     global _torch, _int32_type, _float32_type, _rope_fn, _append_fn, _attend_fn, _raw_stream, _empty_like, _capturing
-    global _current_device, _rope_axes_fn, _append_axes_fn, _sinks_fn, _shared_fn
+    global _current_device, _rope_axes_fn, _append_axes_fn, _sinks_fn, _shared_fn, _partial_size
     import torch
     from . import lib
     L = lib()
@@ -115,7 +115,7 @@ def _bind():
     _empty_like, _capturing = torch.empty_like, torch.cuda.is_current_stream_capturing
     _current_device = torch._C._cuda_getDevice
     _rope_axes_fn, _append_axes_fn = L.moe_rope_axes, L.moe_kv_append_axes
-    _sinks_fn, _shared_fn = L.moe_paged_attention_sinks, L.moe_paged_attention_shared
+    _sinks_fn, _shared_fn, _partial_size = L.moe_paged_attention_sinks, L.moe_paged_attention_shared, L.moe_shared_prefix_partial_size
     _rope_fn, _torch = L.moe_rope, torch
 
 
@@ -550,7 +550,7 @@ class PagedKVCache:
                 raise ValueError("without shared_seqs there is one group, of all sequences")
             lens = _int32(shared_lens, G, "shared_lens", index)
             seqs = 0 if shared_seqs is None else _int32(shared_seqs, G + 1, "shared_seqs", index)
-            partial = _empty((N * Hq * (4 * D + 8),), _torch.uint8, self.device, stream)
+            partial = _empty((_partial_size(N, Hq, D, G),), _torch.uint8, self.device, stream)
             fn, more = _shared_fn, (_SHARED.pack(48, G, N if max_shared_q is None else max_shared_q, seqs, lens, partial.data_ptr(),
                                                  partial.shape[0]),)
         elif shared_seqs is not None:

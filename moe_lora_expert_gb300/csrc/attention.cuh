@@ -324,22 +324,26 @@ struct AttentionParams {
 // Sinks: the first ``sinks`` keys stay visible to every row of a window.
 //
 // Shared prefixes: sequences [seqs[g], seqs[g + 1]) of a group (seqs NULL: all)
-// begin with the same lens[g] tokens.  The prefix pass takes a group as one
-// sequence whose rows are all of its new tokens' and all see the prefix's keys,
-// through the block table's row of the group's first sequence, and leaves
-// unnormalised sums with their references; the own pass takes each sequence's
-// other keys and joins the two.  A sequence that begins inside the prefix, or
-// whose tokens are not all among the group's first max_tokens, takes no part
-// and reads its keys itself.
+// begin with the same lens[g] tokens.  The prefix pass (the kernel for many
+// rows) takes a group as one sequence whose rows are all of its new tokens' and
+// all see the prefix's keys, through the block table's row of the group's first
+// sequence.  It cuts the keys in pieces and leaves each piece's unnormalised
+// sums with their references.  The own pass (the kernel for few rows) takes
+// each sequence's other keys and joins all of them: it has more CTAs, with few
+// rows each, and so joins faster than the prefix pass could.  A sequence that
+// begins inside the prefix, or whose tokens are not all among the group's first
+// max_tokens, takes no part and reads its keys itself.
 enum AttentionPass { kWholePass, kPrefixPass, kOwnPass };
 struct AttentionForms {
   int sinks;
   int pass;                     // AttentionPass
   int groups, sequences, max_tokens;
   const int32_t *seqs, *lens;
-  float* sums;                  // [N][Hq][head_dim]
-  float2* refs;                 // [N][Hq]: reference and denominator
-  int late;                     // the own pass waits for the prefix pass where it joins, not where it begins
+  int most_pieces;
+  int64_t rows;                 // N * Hq
+  float* sums;                  // [most_pieces][rows][head_dim]
+  float2* refs;                 // [most_pieces][rows]: reference and denominator
+  int32_t* pieces;              // [groups]
 
   // Group g's sequences and their tokens; nothing, where the list is out of order.
   __device__ __forceinline__ void group(const int32_t* cu_q, int g, int& s0, int& q0, int& q1) const {
@@ -349,9 +353,10 @@ struct AttentionForms {
     q1 = cu_q == nullptr ? s1 : cu_q[s1];
   }
   // How many keys of sequence b, whose rows are tokens [q_first, q_first +
-  // q_len) and begin at position ``start``, the prefix pass has taken.
-  __device__ __forceinline__ int taken(const int32_t* cu_q, int b, int q_first, int q_len, int start) const {
-    int g = 0;
+  // q_len) and begin at position ``start``, the prefix pass has taken, and in
+  // which group.
+  __device__ __forceinline__ int taken(const int32_t* cu_q, int b, int q_first, int q_len, int start, int& g) const {
+    g = 0;
     if (seqs != nullptr) {
       int hi = groups;                                   // the last group that begins at b or before
       while (hi - g > 1) {
@@ -360,9 +365,9 @@ struct AttentionForms {
       }
       if (b < seqs[g] || b >= seqs[g + 1]) return 0;
     }
+    const int n = lens[g];
     int s0, q0, q1;
     group(cu_q, g, s0, q0, q1);
-    const int n = lens[g];
     return n > 0 && start >= n && q_first >= q0 && q_first + q_len <= min(q1, q0 + max_tokens) ? n : 0;
   }
 };

@@ -33,9 +33,15 @@ inline int element_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 // one long context (on 8 key heads 77%: 109 / 62).
 bool few_rows(int64_t rows, int64_t pairs) { return rows <= 32 || (rows <= 96 && pairs <= 16); }
 
-// Up to how many rows of a sequence and key head the prefix of a group is read
-// once for all of them.
-constexpr int64_t kSharedRows = 128;
+// The prefix of a group is read once for all its sequences where these have at
+// most so many rows each, and all of a group together at least so many.
+constexpr int64_t kSharedRows = 128, kPrefixRows = 17;
+// How many pieces the prefix pass may leave for a row: with one group whose
+// rows fill 256-row units, twice as many as give each SM one of them.
+int most_pieces(int N, int Hq) {
+  const int64_t rows = static_cast<int64_t>(N) * Hq, n = 2ll * 160 * 256 / rows;
+  return n < 2 ? 2 : n > 32 ? 32 : static_cast<int>(n);
+}
 
 // Elements a thread may move at once, of 8, 4 and 1: V elements of a type
 // with e bytes need addresses and strides in multiples of V * e bytes (16 at
@@ -269,8 +275,9 @@ int moe_paged_attention_sinks(const moe_paged_attention_args_t* a, int sinks, mo
   return attend(p, sinks == 0 || p.window == 0 ? nullptr : &f, a->dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t moe_shared_prefix_partial_size(int N, int Hq, int head_dim) {
-  return N <= 0 || Hq <= 0 || head_dim <= 0 ? 0 : static_cast<size_t>(N) * Hq * (static_cast<size_t>(head_dim) * 4 + 8);
+size_t moe_shared_prefix_partial_size(int N, int Hq, int head_dim, int groups) {
+  if (N <= 0 || Hq <= 0 || head_dim <= 0 || groups <= 0) return 0;
+  return most_pieces(N, Hq) * static_cast<size_t>(N) * Hq * (static_cast<size_t>(head_dim) * 4 + 8) + static_cast<size_t>(groups) * 4;
 }
 
 int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_shared_prefix_t* x, moe_stream_t stream) {
@@ -286,24 +293,25 @@ int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_sh
   const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
   if (x->groups == 0 || x->max_tokens == 0) return attend(p, nullptr, a->dtype, on);
   if (x->lens == nullptr || (x->seqs == nullptr && x->groups != 1)) return MOE_ERR_NULL;
-  const size_t need = moe_shared_prefix_partial_size(p.N, p.Hq, p.cache.head_dim);
-  if (x->partial == nullptr || !aligned(x->partial, 16) || x->partial_bytes < need) return MOE_ERR_WORKSPACE;
-  if (rows_of(p) > kSharedRows) return attend(p, nullptr, a->dtype, on);
+  const size_t need = moe_shared_prefix_partial_size(p.N, p.Hq, p.cache.head_dim, x->groups);
+  if (x->partial == nullptr || !aligned(x->partial, 32) || x->partial_bytes < need) return MOE_ERR_WORKSPACE;
   AttentionForms f = {};
   f.groups = x->groups, f.sequences = p.B;
   f.max_tokens = x->max_tokens < p.N ? x->max_tokens : p.N;
   f.seqs = x->seqs, f.lens = x->lens;
+  f.most_pieces = most_pieces(p.N, p.Hq);
+  f.rows = static_cast<int64_t>(p.N) * p.Hq;
   f.sums = static_cast<float*>(x->partial);
-  f.refs = reinterpret_cast<float2*>(f.sums + static_cast<size_t>(p.N) * p.Hq * p.cache.head_dim);
+  f.refs = reinterpret_cast<float2*>(f.sums + f.most_pieces * f.rows * p.cache.head_dim);
+  f.pieces = reinterpret_cast<int32_t*>(f.refs + f.most_pieces * f.rows);
   f.pass = moe::kPrefixPass;
   AttentionParams prefix = p;
   prefix.B = x->groups;
   prefix.max_q_len = f.max_tokens;
-  const bool few = few_rows(rows_of(prefix), static_cast<int64_t>(prefix.B) * p.cache.kv_heads);
-  const int error = few ? moe::launch_decode_attention(prefix, &f, a->dtype, on) : moe::launch_prefill_attention(prefix, &f, a->dtype, on);
+  if (rows_of(p) > kSharedRows || rows_of(prefix) < kPrefixRows) return attend(p, nullptr, a->dtype, on);
+  const int error = moe::launch_prefill_attention(prefix, &f, a->dtype, on);
   if (error != MOE_OK) return error;
   f.pass = moe::kOwnPass;
-  f.late = !few;                                        // the two kernels have workspaces of their own
   return moe::launch_decode_attention(p, &f, a->dtype, on);
 }
 

@@ -77,6 +77,7 @@ constexpr int kMaxEntries = 512;          // (sequence, row tile) pairs of one l
 constexpr int kMinTiles = 2;              // a CTA's stretch of the line is at least so long; one token on 1022 keys: 1 13.0, 2 11.3, 4 12.7 us
 constexpr int kJoin = 16;                 // pieces that are joined at a time; 16 sequences of up to 4096 keys: 8 27.6, 16 24.5 us
 constexpr int kPitch = 128;               // bytes of a key in shared memory
+constexpr int kCutCost = 16;              // tiles' worth of time that a row tile which is cut takes
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMost = 15.9f, kNew = 7.f;// a weight past 2^15.9 makes the reference rise, so that it becomes 2^7;
@@ -99,11 +100,18 @@ struct Shared {
   int begin[kMaxEntries];                 // first key that some row of each entry sees
   int end[kMaxEntries];                   // end of the keys that some row of it sees
   float m[kWarps][kMaxRows], l[kWarps][kMaxRows];
-  int total, abort_flag, last;
+  int total, longest, abort_flag, last;
 };
+// With the group of each entry.
+struct FormsShared : Shared {
+  int of[kMaxEntries];
+};
+template <bool FORMS> struct SharedOf { using type = Shared; };
+template <> struct SharedOf<true> { using type = FormsShared; };
 constexpr int kSlotBytes = 2 * 16 * kPitch;
 constexpr int kScratch(int rows) { return 2 * rows * 128 * 4; }              // two warps' sums
-constexpr int kSmem(int rows) { return kWarps * kRing * kSlotBytes + kScratch(rows) + static_cast<int>(sizeof(Shared)) + 1024; }
+template <bool FORMS>
+constexpr int kSmem(int rows) { return kWarps * kRing * kSlotBytes + kScratch(rows) + static_cast<int>(sizeof(typename SharedOf<FORMS>::type)) + 1024; }
 
 // Partial sums of a row tile: [slot][row][128] and (m, l) [slot][row][2];
 // counters [2][slots].
@@ -117,8 +125,8 @@ struct Launch {
   int b0, B, row_tiles, tile_rows;        // sequences [b0, b0 + B), row tiles of each and their rows
   int box;                                // keys of one TMA box: gcd(page_size, 16)
 };
-// With sinks or shared prefixes; all their tests are behind FORMS, so that the
-// kernels without have none of them.
+// With sinks, or as the own pass of shared prefixes; all their tests are behind
+// FORMS, so that the kernels without have none of them.
 struct FormsLaunch : Launch {
   AttentionForms f;
 };
@@ -147,37 +155,19 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// The rows of entry e (a sequence, or in the prefix pass a group of them, and a
-// row tile of it); b is its row of the block table.
-template <bool FORMS>
-struct EntryOf {
+// The rows of entry e (a sequence and a row tile of it).
+struct Entry {
   int b, q_first, q_len, len, row0, rows;
-  bool flat;                              // every row sees all ``len`` keys
-  __device__ __forceinline__ EntryOf(const typename LaunchOf<FORMS>::type& p, int e, int group) {
+  __device__ __forceinline__ Entry(const Launch& p, int e, int group) {
     b = p.b0 + e / p.row_tiles;
     row0 = (e % p.row_tiles) * p.tile_rows;
-    flat = false;
-    if constexpr (FORMS) {
-      if (p.f.pass == kPrefixPass) {
-        int s0, q_end;
-        p.f.group(p.a.cu_q, b, s0, q_first, q_end);
-        len = p.f.lens[b];
-        q_len = len > 0 ? q_end - q_first : 0;
-        b = s0;
-        flat = true;
-      }
-    }
-    if (!FORMS || !flat) {
-      q_first = p.a.cu_q == nullptr ? b : p.a.cu_q[b];
-      q_len = p.a.cu_q == nullptr ? 1 : p.a.cu_q[b + 1] - q_first;
-      len = p.a.seq_lens[b];
-    }
+    q_first = p.a.cu_q == nullptr ? b : p.a.cu_q[b];
+    q_len = p.a.cu_q == nullptr ? 1 : p.a.cu_q[b + 1] - q_first;
+    len = p.a.seq_lens[b];
     const int n = min(min(q_len, p.a.max_q_len), p.a.N - q_first);
     rows = max(0, min(p.tile_rows, n * group - row0));
   }
-  __device__ __forceinline__ int position(int row, int group) const {
-    return FORMS && flat ? len - 1 : len - q_len + (row0 + row) / group;
-  }
+  __device__ __forceinline__ int position(int row, int group) const { return len - q_len + (row0 + row) / group; }
 };
 
 // Where tile x of the line lies.
@@ -208,11 +198,11 @@ template <typename T, int DP, int NT, bool FORMS>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
 decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                         const __grid_constant__ typename LaunchOf<FORMS>::type p) {
-  using Entry = EntryOf<FORMS>;
   extern __shared__ uint8_t raw[];
   uint8_t* const rings = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   float* const scratch = reinterpret_cast<float*>(rings + kWarps * kRing * kSlotBytes);
-  Shared& s = *reinterpret_cast<Shared*>(reinterpret_cast<uint8_t*>(scratch) + kScratch(8 * NT));
+  using S = typename SharedOf<FORMS>::type;
+  S& s = *reinterpret_cast<S*>(reinterpret_cast<uint8_t*>(scratch) + kScratch(8 * NT));
   const AttentionParams& a = p.a;
   const moe_kv_cache_t& ca = a.cache;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -230,17 +220,16 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     s.abort_flag = 0;
     fence_mbarrier_init();
   }
-  bool late = false;
+  // The own pass may run beside the prefix pass, which lets it start when all
+  // that came before is done; it waits where it needs the other's sums.
+  bool own = false;
   int sinks = 0;
   if constexpr (FORMS) {
-    // The own pass may run beside the prefix pass, which lets it start when all
-    // that came before is done, and only waits for its sums.
-    late = p.f.late != 0;
+    own = p.f.pass == kOwnPass;
     sinks = p.f.sinks;
-    if (p.f.pass == kPrefixPass) pdl_wait();
   }
   pdl_launch_dependents();
-  if (!late) pdl_wait();
+  if (!FORMS || !own || p.b0 > 0) pdl_wait();          // a further launch for one call uses the first one's workspace
 
   // The tiles before those of the window that hold keys which stay visible, and
   // the first key of tile i of an entry that begins at ``lo``.
@@ -259,7 +248,9 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       const int pos0 = en.position(0, group), pos1 = en.position(en.rows - 1, group);
       lo = a.window > 0 && pos0 >= a.window ? pos0 + 1 - a.window : 0;
       if constexpr (FORMS) {
-        if (p.f.pass == kOwnPass) lo = p.f.taken(a.cu_q, en.b, en.q_first, en.q_len, en.len - en.q_len);
+        int g = 0;
+        if (own) lo = p.f.taken(a.cu_q, en.b, en.q_first, en.q_len, en.len - en.q_len, g);
+        s.of[e] = g;
       }
       hi = max(0, pos1 + 1);
       if (hi > most) {
@@ -292,11 +283,27 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     }
     if (lane == 0) s.prefix[0] = 0;
     if (lane == 31) s.total = incl * ca.kv_heads;
+    if constexpr (FORMS) {
+      int longest = 0;
+#pragma unroll 1
+      for (int e = from; e < to; ++e) longest = max(longest, s.prefix[e + 1] - (e > from ? s.prefix[e] : incl - sum));
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      if (lane == 0) s.longest = longest;
+    }
   }
   __syncthreads();
   const int total = s.total, ctas = min(static_cast<int>(gridDim.x), (total + kMinTiles - 1) / kMinTiles);
   const bool idle = static_cast<int>(blockIdx.x) >= ctas;
-  const int x0 = idle ? 0 : stretch_begin(total, ctas, blockIdx.x), x1 = idle ? 0 : stretch_begin(total, ctas, blockIdx.x + 1);
+  int x0 = idle ? 0 : stretch_begin(total, ctas, blockIdx.x), x1 = idle ? 0 : stretch_begin(total, ctas, blockIdx.x + 1);
+  if constexpr (FORMS) {
+    // A row tile each, where that takes no CTA much longer than its stretch of
+    // the line would with the joins that come with it.
+    if (own && entries * ca.kv_heads <= static_cast<int>(gridDim.x) && s.longest <= (total + ctas - 1) / ctas + kCutCost) {
+      const int e = min(static_cast<int>(blockIdx.x) / ca.kv_heads, entries - 1), count = s.prefix[e + 1] - s.prefix[e];
+      x0 = s.prefix[e] * ca.kv_heads + (static_cast<int>(blockIdx.x) - e * ca.kv_heads) * count;
+      x1 = static_cast<int>(blockIdx.x) < entries * ca.kv_heads ? x0 + count : x0;
+    }
+  }
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {          // by a warp, which leaves it together
     if (!mbar_try_wait(smem_u32(bar), parity)) wait_long(bar, parity, a.wait_limit_ns, a.status, &s.abort_flag);
@@ -324,11 +331,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         const int page_at = key / ca.page_size;
         f.off = key - page_at * ca.page_size;
         f.head = at.head;
-        int row = p.b0 + at.e / p.row_tiles;
-        if constexpr (FORMS) {
-          if (p.f.pass == kPrefixPass) row = p.f.seqs == nullptr ? 0 : max(0, p.f.seqs[row]);
-        }
-        f.page = a.block_table[static_cast<int64_t>(row) * a.table_width + page_at];
+        f.page = a.block_table[static_cast<int64_t>(p.b0 + at.e / p.row_tiles) * a.table_width + page_at];
         if (f.page < 0 || f.page >= ca.num_pages) {
           f.page = -1;
           set_status(a.status, MOE_ERR_BAD_PAGE);
@@ -396,7 +399,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       const int n = min(at.count - at.tile, x1 - x);
       const int begin = s.begin[at.e];
       int taken = 0;                       // keys that the prefix pass has taken
-      if constexpr (FORMS) taken = p.f.pass == kOwnPass ? begin : 0;
+      if constexpr (FORMS) taken = own ? begin : 0;
       const int pos_min = en.position(0, group), pos_max = en.position(en.rows - 1, group);
       const int end = s.end[at.e];
 
@@ -664,8 +667,84 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       float* ml = parts + kPartialBytes / 4;
       int* counters = reinterpret_cast<int*>(ml + kMlBytes / 4);
 
+      // What the prefix pass has left of a row, joined to four columns of it, by a warp.
+      auto join_prefix = [&](int64_t at_row, int g, float& Mx, float& Lx, float (&acc)[4]) {
+        if constexpr (FORMS) {
+          pdl_wait();
+          const int col = 4 * lane, count = min(__ldcg(p.f.pieces + g), p.f.most_pieces);
+#pragma unroll 1
+          for (int i = 0; i < count; i += 8) {
+            float4 v[8];
+            float2 z[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int64_t from = (i + k) * p.f.rows + at_row;
+              z[k] = i + k < count ? __ldcg(p.f.refs + from) : make_float2(-INFINITY, 0.f);
+              v[k] = i + k < count && col < ca.head_dim ? __ldcg(reinterpret_cast<const float4*>(p.f.sums + from * ca.head_dim + col))
+                                                        : make_float4(0, 0, 0, 0);
+            }
+            float now = Mx;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) now = fmaxf(now, z[k].x);
+            const float base = now == -INFINITY ? 0.f : now, keep = fast_exp2(Mx - base);
+            Lx *= keep;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[q] *= keep;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float e = fast_exp2(z[k].x - base);
+              Lx = fmaf(z[k].y, e, Lx);
+              acc[0] = fmaf(v[k].x, e, acc[0]);
+              acc[1] = fmaf(v[k].y, e, acc[1]);
+              acc[2] = fmaf(v[k].z, e, acc[2]);
+              acc[3] = fmaf(v[k].w, e, acc[3]);
+            }
+            Mx = now;
+          }
+        }
+      };
+      if constexpr (FORMS) {
+        if (!split && taken > 0) {
+          // the row tile is whole here: all warps join and write its rows
+          if (warp == 0) {
+            __syncwarp();                  // every lane has added what the scratch held
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int row = 8 * t + 2 * c + z;
+#pragma unroll
+                for (int j = 0; j < kTiles; j += 2) {
+                  const float v[4] = {o[t][j][z], o[t][j][2 + z], o[t][j + 1][z], o[t][j + 1][2 + z]};
+                  store_f32<float, 4>(scratch + row * 128 + (DP / 8) * g + 2 * j, v);
+                }
+                if (g == 0) {
+                  s.m[0][row] = M[t][z];
+                  s.l[0][row] = Ls[t][z];
+                }
+              }
+          }
+          __syncthreads();
+          const int col = 4 * lane;
+#pragma unroll 1
+          for (int row = warp; row < en.rows; row += kWarps) {
+            float Mx = s.m[0][row], Lx = s.l[0][row], acc[4] = {};
+            if (col < DP) load_f32<float, 4>(scratch + row * 128 + col, acc);
+            const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
+            join_prefix(static_cast<int64_t>(tok) * a.Hq + h, s.of[at.e], Mx, Lx, acc);
+            const float inv = Lx == 0.f ? 0.f : 1.f / Lx;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[q] *= inv;
+            if (col < ca.head_dim) store_f32<T, 4>(static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head + col, acc);
+            if (lane == 0 && a.lse != nullptr)
+              a.lse[static_cast<int64_t>(tok) * a.Hq + h] = Lx == 0.f ? -INFINITY : (Mx + log2f(Lx)) * kLn2;
+          }
+          __syncthreads();                 // before the next row tile's sums
+        }
+      }
+
       // A thread of warp 0 holds, for rows 2 c and 2 c + 1, columns [DP/8 g, DP/8 g + DP/8).
-      if (warp == 0) {
+      if (warp == 0 && (!FORMS || split || taken == 0)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -674,36 +753,6 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             if (row >= en.rows) continue;
             if (!split) {
               const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
-              if constexpr (FORMS) {
-                float* sums = p.f.sums + (static_cast<int64_t>(tok) * a.Hq + h) * ca.head_dim;
-                float2* ref = p.f.refs + static_cast<int64_t>(tok) * a.Hq + h;
-                if (p.f.pass == kPrefixPass) {
-#pragma unroll
-                  for (int j = 0; j < kTiles; j += 2) {
-                    const float v[4] = {o[t][j][z], o[t][j][2 + z], o[t][j + 1][z], o[t][j + 1][2 + z]};
-                    const int col = (DP / 8) * g + 2 * j;
-                    if (col < ca.head_dim) store_f32<float, 4>(sums + col, v);
-                  }
-                  if (g == 0) *ref = make_float2(M[t][z], Ls[t][z]);
-                  continue;
-                }
-                if (taken > 0) {
-                  if (late) pdl_wait();
-                  const float2 other = __ldcg(ref);
-                  const float top = fmaxf(M[t][z], other.x), mine = fast_exp2(M[t][z] - top), theirs = fast_exp2(other.x - top);
-                  M[t][z] = top;
-                  Ls[t][z] = fmaf(Ls[t][z], mine, other.y * theirs);
-#pragma unroll
-                  for (int j = 0; j < kTiles; j += 2) {
-                    const int col = (DP / 8) * g + 2 * j;
-                    const float4 v = col < ca.head_dim ? __ldcg(reinterpret_cast<const float4*>(sums + col)) : make_float4(0, 0, 0, 0);
-                    o[t][j][z] = fmaf(o[t][j][z], mine, v.x * theirs);
-                    o[t][j][2 + z] = fmaf(o[t][j][2 + z], mine, v.y * theirs);
-                    o[t][j + 1][z] = fmaf(o[t][j + 1][z], mine, v.z * theirs);
-                    o[t][j + 1][2 + z] = fmaf(o[t][j + 1][2 + z], mine, v.w * theirs);
-                  }
-                }
-              }
               const float inv = Ls[t][z] == 0.f ? 0.f : 1.f / Ls[t][z];
               T* dst = static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head;
 #pragma unroll
@@ -798,25 +847,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             if (finish) {
               const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
               if constexpr (FORMS) {
-                float* sums = p.f.sums + (static_cast<int64_t>(tok) * a.Hq + h) * ca.head_dim + col;
-                float2* ref = p.f.refs + static_cast<int64_t>(tok) * a.Hq + h;
-                if (p.f.pass == kPrefixPass) {
-                  if (col < ca.head_dim) store_f32<float, 4>(sums, acc);
-                  if (lane == 0) *ref = make_float2(Mx, Lx);
-                  continue;
-                }
-                if (taken > 0) {
-                  if (late) pdl_wait();
-                  const float2 other = __ldcg(ref);
-                  const float4 v = col < ca.head_dim ? __ldcg(reinterpret_cast<const float4*>(sums)) : make_float4(0, 0, 0, 0);
-                  const float top = fmaxf(Mx, other.x), mine = fast_exp2(Mx - top), theirs = fast_exp2(other.x - top);
-                  Mx = top;
-                  Lx = fmaf(Lx, mine, other.y * theirs);
-                  acc[0] = fmaf(acc[0], mine, v.x * theirs);
-                  acc[1] = fmaf(acc[1], mine, v.y * theirs);
-                  acc[2] = fmaf(acc[2], mine, v.z * theirs);
-                  acc[3] = fmaf(acc[3], mine, v.w * theirs);
-                }
+                if (taken > 0) join_prefix(static_cast<int64_t>(tok) * a.Hq + h, s.of[at.e], Mx, Lx, acc);
               }
               const float inv = Lx == 0.f ? 0.f : 1.f / Lx;
 #pragma unroll
@@ -841,7 +872,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     }
   }
 
-  if (late) pdl_wait();                    // who waits for this kernel waits for the one before it
+  if (FORMS) pdl_wait();                   // who waits for this kernel waits for the one before it
   // Nothing of this warp is in flight when it ends: it has waited for every
   // tile, unless a wait ran out.
   if (*static_cast<volatile int*>(&s.abort_flag)) {
@@ -924,7 +955,7 @@ int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t s
   p.box = gcd(a.cache.page_size, 16);
   if (!encode_cache_map(&k_map, a.cache, false, p.box) || !encode_cache_map(&v_map, a.cache, true, p.box)) return MOE_ERR_CUDA;
   auto kernel = decode_attention_kernel<T, DP, NT, FORMS>;
-  constexpr int bytes = kSmem(8 * NT);
+  constexpr int bytes = kSmem<FORMS>(8 * NT);
   p.tile_rows = 8 * NT;
   if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes) != cudaSuccess) return MOE_ERR_CUDA;
   const int sms = sm_count();
@@ -947,7 +978,6 @@ int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t s
     if (grid > tiles) grid = tiles;
     if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), bytes, stream, k_map, v_map, p) != cudaSuccess)
       return MOE_ERR_CUDA;
-    if constexpr (FORMS) p.f.late = 0;     // the next launch uses the same workspace as this one
   }
   return MOE_OK;
 }

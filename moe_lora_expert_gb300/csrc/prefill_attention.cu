@@ -59,6 +59,7 @@ constexpr int kStages = 2;                 // tiles of codes, in the same order
 constexpr int kInfo = 4;                   // key tiles whose scales are held (see the copies)
 constexpr int kUnitCost = 2;               // key tiles' worth of time that a unit takes besides its tiles; 2 x 2048 tokens, cut from the line: 1 122, 2 103, 3 103, 4 105 us
 constexpr int kMinTiles = 4;               // least length of a CTA's stretch (a join costs about as much as four tiles)
+constexpr int kMinPiece = 2;               // key tiles of a piece in the prefix pass, at least
 constexpr int kMaxCtas = 160;
 constexpr int kMaxUnits = 16;              // whole units a CTA may be given (see the kernel)
 constexpr int kJoinCost = 8;               // key tiles' worth of time that cutting the line may cost a CTA: part of a unit written, another joined
@@ -199,6 +200,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 // ------------------------------------------------------------------- units
 // The rows of one (sequence, row tile) and the keys they see; in the prefix
 // pass of a group of sequences, and b is its first one.
+// In the prefix pass a unit is cut in pieces of about ``chunk`` tiles.
+__device__ __forceinline__ int pieces_of(int tiles, int chunk) { return (tiles + chunk - 1) / chunk; }
 template <bool FORMS>
 struct EntryForms {
   int before;                              // tiles of sinks before those of the window
@@ -265,6 +268,32 @@ template <bool FORMS>
 struct WalkOf {
   Entry<FORMS> en;
   int e, head, tile, x, x1, n, u0, span;   // this piece: tiles [tile, tile + n) of the unit that begins at u0
+  // The prefix pass: x counts pieces, which are shared evenly.  Instead of u0
+  // and span it has the place among the unit's pieces and how long they are.
+  __device__ __forceinline__ int& piece() { return u0; }
+  __device__ __forceinline__ int& chunk() { return span; }
+  __device__ __forceinline__ bool next_piece(const typename LaunchOf<FORMS>::type& p, int group, bool first, int first_entry, int first_prefix) {
+    if (x == x1) return false;
+    if (first) {
+      e = first_entry;
+      en.load(p, e, group);
+      const int in = x - first_prefix * p.a.cache.kv_heads, each = pieces_of(en.count, chunk());
+      head = in / each;
+      piece() = in - head * each;
+    } else if (++piece() == pieces_of(en.count, chunk())) {
+      piece() = 0;
+      if (++head == p.a.cache.kv_heads) {
+        head = 0;
+        do en.load(p, ++e, group);
+        while (en.count == 0);
+      }
+    }
+    ++x;
+    const int each = pieces_of(en.count, chunk());
+    tile = en.count * piece() / each;
+    n = en.count * (piece() + 1) / each - tile;
+    return true;
+  }
   __device__ __forceinline__ bool next(const typename LaunchOf<FORMS>::type& p, int group, const int* whole, bool first, int first_entry, int first_prefix) {
     const int heads = p.a.cache.kv_heads;
     if (whole != nullptr) {
@@ -318,7 +347,13 @@ __device__ __noinline__ bool walk_next(WalkOf<FORMS>* at, const typename LaunchO
   using Walk = WalkOf<FORMS>;
   __syncwarp(lanes);
   Walk w = *at;
-  const bool more = w.next(p, group, whole, first_entry >= 0, first_entry, first_prefix);
+  bool more;
+  if constexpr (FORMS) {
+    more = p.f.pass == kPrefixPass ? w.next_piece(p, group, first_entry >= 0, first_entry, first_prefix)
+                       : w.next(p, group, whole, first_entry >= 0, first_entry, first_prefix);
+  } else {
+    more = w.next(p, group, whole, first_entry >= 0, first_entry, first_prefix);
+  }
   __syncwarp(lanes);
   *at = w;
   __syncwarp(lanes);
@@ -446,19 +481,41 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     s.abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (FORMS) pdl_wait();                   // the own pass may begin beside this one, when all that came before is done
+  if (FORMS && prefix) pdl_wait();         // the own pass may begin beside this one, when all that came before is done
   pdl_launch_dependents();
   pdl_wait();
 
   // The line's length, and where this CTA's stretch of it begins.
   const int entries = a.B * p.row_tiles, per = (entries + kThreads - 1) / kThreads;
   const int from = min(tid * per, entries), to = min(from + per, entries);
-  int mine = 0;
+  int mine = 0, chunk = 0;                 // chunk > 0: the prefix pass
+  if constexpr (FORMS) {
+    if (prefix) {
+      // Pieces of a length for which there is about one for each CTA: n units of
+      // t tiles give at most t / chunk + n.
+      if (tid == 0) s.sums[0] = s.sums[1] = s.sums[2] = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (int e = from; e < to; ++e) {
+        Entry<FORMS> en;
+        en.load(p, e, group);
+        if (en.count == 0) continue;
+        atomicAdd(&s.sums[0], en.count * ca.kv_heads);
+        atomicAdd(&s.sums[1], ca.kv_heads);
+        atomicMax(&s.sums[2], en.count);
+      }
+      __syncthreads();
+      const int tiles = s.sums[0], spare = static_cast<int>(gridDim.x) - s.sums[1], longest = s.sums[2];
+      chunk = spare > 0 ? max(kMinPiece, (tiles + spare - 1) / spare) : longest;
+      chunk = max(max(chunk, 1), (longest + p.f.most_pieces - 1) / p.f.most_pieces);
+      __syncthreads();
+    }
+  }
 #pragma unroll 1
   for (int e = from; e < to; ++e) {
     Entry<FORMS> en;
     en.load(p, e, group);
-    if (en.count > 0) mine += en.count + kUnitCost;
+    if (en.count > 0) mine += FORMS && chunk > 0 ? pieces_of(en.count, chunk) : en.count + kUnitCost;
   }
   int incl = mine;
 #pragma unroll
@@ -475,7 +532,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     all_tiles += s.sums[w];
   }
   const int total = all_tiles * ca.kv_heads;
-  const int ctas = min(static_cast<int>(gridDim.x), max(1, total / kMinTiles));
+  const int ctas = min(static_cast<int>(gridDim.x), max(1, FORMS && chunk > 0 ? total : total / kMinTiles));
   if (total == 0) return;
 
   // Whole units, longest first and to the CTAs forwards and backwards in turn,
@@ -485,7 +542,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   // 512 units of 2 x 2048 tokens: 92 us, cut from the line 104; 220 units of
   // four ragged chunks: 149 and 120.
   bool whole = false;
-  if (per == 1) {
+  if (per == 1 && (!FORMS || chunk == 0)) {
     int* costs = reinterpret_cast<int*>(smem + L::kRing);    // not in use yet
     int* sorted = costs + kThreads;
     costs[tid] = mine;
@@ -532,7 +589,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     for (int e = from; e < to; ++e) {
       Entry<FORMS> en;
       en.load(p, e, group);
-      const int places = en.count > 0 ? en.count + kUnitCost : 0;
+      const int places = en.count == 0 ? 0 : FORMS && chunk > 0 ? pieces_of(en.count, chunk) : en.count + kUnitCost;
       if (x0 < (before + places) * ca.kv_heads) {
         s.first_entry = e;
         s.first_prefix = before;
@@ -569,6 +626,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   const uint32_t walkers = warp == kMmaWarp ? 1u << lane : 0xffffffffu;
   auto next = [&](bool first) {
     if (first) {
+      if (FORMS && prefix) walk.chunk() = chunk;
       walk.x = whole ? 0 : x0;
       walk.x1 = whole ? s.given : stretch_begin(total, ctas, blockIdx.x + 1);
     }
@@ -878,7 +936,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       }
       // the CTAs that have parts of the unit, here and not where the result waits
       int cta0 = 0, pieces = 1;
-      if (walk.n != en.count) {
+      if (walk.n != en.count && !prefix) {
         const int first_at = walk.u0 + kUnitCost;
         cta0 = stretch_of(total, ctas, first_at);
         pieces = stretch_of(total, ctas, first_at + en.count - 1) - cta0 + 1;
@@ -1059,10 +1117,13 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       auto put = [&](int d, const float (&v)[32], float inv) {        // columns [d, d + 32)
         if constexpr (FORMS) {
           if (prefix) {
-            float* sums = p.f.sums + (static_cast<int64_t>(tok) * a.Hq + h) * ca.head_dim + d;
+            float* sums = p.f.sums + (walk.piece() * p.f.rows + static_cast<int64_t>(tok) * a.Hq + h) * ca.head_dim + d;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              if (d + e < ca.head_dim) __stcg(reinterpret_cast<float4*>(sums + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+            for (int e = 0; e < 32; e += 8)
+              if (d + e < ca.head_dim)
+                asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(sums + e), "f"(v[e]), "f"(v[e + 1]), "f"(v[e + 2]),
+                             "f"(v[e + 3]), "f"(v[e + 4]), "f"(v[e + 5]), "f"(v[e + 6]), "f"(v[e + 7])
+                             : "memory");
             return;
           }
         }
@@ -1086,7 +1147,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       auto put_lse = [&](float mm, float ll) {
         if constexpr (FORMS) {
           if (prefix) {
-            p.f.refs[static_cast<int64_t>(tok) * a.Hq + h] = make_float2(mm, ll);
+            p.f.refs[walk.piece() * p.f.rows + static_cast<int64_t>(tok) * a.Hq + h] = make_float2(mm, ll);
+            if (gr == 0 && walk.head == 0 && walk.piece() == 0) p.f.pieces[walk.e / p.row_tiles] = pieces_of(en.count, walk.chunk());
             return;
           }
         }
@@ -1109,7 +1171,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
             if ((bits >> e) & 1) v[e] = __uint_as_float(0x7FC00000u);
         }
       };
-      if (walk.n == en.count) {
+      if (walk.n == en.count || prefix) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int d = 0; d < DP; d += 32) {

@@ -217,11 +217,12 @@ def test_shared(dtype, new, held, seqs, shared, strays, Hkv, Hq, P, D, bound):
     N = sum(new)
     q = rounded(rng, (N, Hq, D), dtype)
     decode = all(n == 1 for n in new)
-    many = max(new) * (Hq // Hkv) > 128
-    most = max(sum(new[a:b]) for a, b in zip(seqs, seqs[1:]))
+    most = max(sum(new[a:b]) for a, b in zip(seqs, seqs[1:])) if bound else N
+    # sequences of many rows, and groups of few, are not worth the sharing: then each table row is looked at
+    alone = max(new) * (Hq // Hkv) > 128 or most * (Hq // Hkv) < 17
     del_me = torch.full((N * Hq * (4 * D + 8) // 4,), float("nan"), device="cuda")       # what the partial sums' memory may hold
     del del_me
-    out, lse = batch.cache.attend(tensor(q, dtype, (1, 8) if bound else None), tensor(batch.table, "int32") if many else batch.dev["block_table"],
+    out, lse = batch.cache.attend(tensor(q, dtype, (1, 8) if bound else None), tensor(batch.table, "int32") if alone else batch.dev["block_table"],
                                   batch.dev["seq_lens"], cu_q=None if decode else batch.cu_dev, max_q_len=max(new), return_lse=True,
                                   max_shared_q=most if bound else None, **batch.groups)
     compare(out, lse, batch, q, dtype)
