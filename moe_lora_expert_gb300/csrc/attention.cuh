@@ -339,16 +339,16 @@ struct AttentionForms {
   int pass;                     // AttentionPass
   int groups, sequences, max_tokens;
   const int32_t *seqs, *lens;
-  int most_pieces;
+  int most_pieces, own_row_tiles; // row tiles of a sequence in the own pass
   int64_t rows;                 // N * Hq
   float* sums;                  // [most_pieces][rows][head_dim]
   float2* refs;                 // [most_pieces][rows]: reference and denominator
   int32_t* pieces;              // [groups]
 
   // Group g's sequences and their tokens; nothing, where the list is out of order.
-  __device__ __forceinline__ void group(const int32_t* cu_q, int g, int& s0, int& q0, int& q1) const {
+  __device__ __forceinline__ void group(const int32_t* cu_q, int g, int& s0, int& s1, int& q0, int& q1) const {
     s0 = seqs == nullptr ? 0 : max(0, min(sequences, seqs[g]));
-    const int s1 = seqs == nullptr ? sequences : max(s0, min(sequences, seqs[g + 1]));
+    s1 = seqs == nullptr ? sequences : max(s0, min(sequences, seqs[g + 1]));
     q0 = cu_q == nullptr ? s0 : cu_q[s0];
     q1 = cu_q == nullptr ? s1 : cu_q[s1];
   }
@@ -366,8 +366,8 @@ struct AttentionForms {
       if (b < seqs[g] || b >= seqs[g + 1]) return 0;
     }
     const int n = lens[g];
-    int s0, q0, q1;
-    group(cu_q, g, s0, q0, q1);
+    int s0, s1, q0, q1;
+    group(cu_q, g, s0, s1, q0, q1);
     return n > 0 && start >= n && q_first >= q0 && q_first + q_len <= min(q1, q0 + max_tokens) ? n : 0;
   }
 };

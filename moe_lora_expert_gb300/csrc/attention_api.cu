@@ -305,6 +305,7 @@ int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_sh
   f.refs = reinterpret_cast<float2*>(f.sums + f.most_pieces * f.rows * p.cache.head_dim);
   f.pieces = reinterpret_cast<int32_t*>(f.refs + f.most_pieces * f.rows);
   f.pass = moe::kPrefixPass;
+  f.own_row_tiles = static_cast<int>((rows_of(p) + 15) / 16);
   AttentionParams prefix = p;
   prefix.B = x->groups;
   prefix.max_q_len = f.max_tokens;

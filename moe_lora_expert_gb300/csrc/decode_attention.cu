@@ -667,37 +667,46 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       float* ml = parts + kPartialBytes / 4;
       int* counters = reinterpret_cast<int*>(ml + kMlBytes / 4);
 
-      // What the prefix pass has left of a row, joined to four columns of it, by a warp.
+      // What the prefix pass has left of a row, joined to four columns of it, by a
+      // warp: 16 pieces at a time, whose loads are on their way together.
+      int pieces_left = -1;
       auto join_prefix = [&](int64_t at_row, int g, float& Mx, float& Lx, float (&acc)[4]) {
         if constexpr (FORMS) {
-          pdl_wait();
-          const int col = 4 * lane, count = min(__ldcg(p.f.pieces + g), p.f.most_pieces);
+          if (pieces_left < 0) {
+            pdl_wait();
+            pieces_left = min(__ldcg(p.f.pieces + g), p.f.most_pieces);
+          }
+          const int col = 4 * lane;
+          const float2* refs = p.f.refs + at_row;
+          const float* sums = p.f.sums + at_row * ca.head_dim + col;
+          const int64_t step = p.f.rows * ca.head_dim;
 #pragma unroll 1
-          for (int i = 0; i < count; i += 8) {
-            float4 v[8];
-            float2 z[8];
+          for (int i = 0; i < pieces_left; i += 16) {
+            float4 v[16];
+            // a lane holds one piece's reference and denominator
+            float2 z = make_float2(-INFINITY, 0.f);
+            if (lane < 16 && i + lane < pieces_left) z = __ldcg(refs + (i + lane) * p.f.rows);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int64_t from = (i + k) * p.f.rows + at_row;
-              z[k] = i + k < count ? __ldcg(p.f.refs + from) : make_float2(-INFINITY, 0.f);
-              v[k] = i + k < count && col < ca.head_dim ? __ldcg(reinterpret_cast<const float4*>(p.f.sums + from * ca.head_dim + col))
-                                                        : make_float4(0, 0, 0, 0);
-            }
-            float now = Mx;
+            for (int k = 0; k < 16; ++k)
+              v[k] = i + k < pieces_left && col < ca.head_dim ? __ldcg(reinterpret_cast<const float4*>(sums + (i + k) * step)) : make_float4(0, 0, 0, 0);
+            float now = z.x;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) now = fmaxf(now, z[k].x);
-            const float base = now == -INFINITY ? 0.f : now, keep = fast_exp2(Mx - base);
-            Lx *= keep;
+            for (int x = 1; x < 16; x *= 2) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
+            now = fmaxf(Mx, __shfl_sync(0xffffffffu, now, 0));
+            const float base = now == -INFINITY ? 0.f : now, keep = fast_exp2(Mx - base), e = fast_exp2(z.x - base);
+            float l = z.y * e;
+#pragma unroll
+            for (int x = 1; x < 16; x *= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
+            Lx = fmaf(Lx, keep, __shfl_sync(0xffffffffu, l, 0));
 #pragma unroll
             for (int q = 0; q < 4; ++q) acc[q] *= keep;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float e = fast_exp2(z[k].x - base);
-              Lx = fmaf(z[k].y, e, Lx);
-              acc[0] = fmaf(v[k].x, e, acc[0]);
-              acc[1] = fmaf(v[k].y, e, acc[1]);
-              acc[2] = fmaf(v[k].z, e, acc[2]);
-              acc[3] = fmaf(v[k].w, e, acc[3]);
+            for (int k = 0; k < 16; ++k) {
+              const float f = __shfl_sync(0xffffffffu, e, k);
+              acc[0] = fmaf(v[k].x, f, acc[0]);
+              acc[1] = fmaf(v[k].y, f, acc[1]);
+              acc[2] = fmaf(v[k].z, f, acc[2]);
+              acc[3] = fmaf(v[k].w, f, acc[3]);
             }
             Mx = now;
           }

@@ -59,6 +59,11 @@ constexpr int kStages = 2;                 // tiles of codes, in the same order
 constexpr int kInfo = 4;                   // key tiles whose scales are held (see the copies)
 constexpr int kUnitCost = 2;               // key tiles' worth of time that a unit takes besides its tiles; 2 x 2048 tokens, cut from the line: 1 122, 2 103, 3 103, 4 105 us
 constexpr int kMinTiles = 4;               // least length of a CTA's stretch (a join costs about as much as four tiles)
+// The prefix pass, in units of 0.1 us: what a piece takes besides its tiles, a
+// tile of one and of two row tiles; and the own pass before and after its tiles,
+// of which each of three CTAs on an SM reads one in 1 us.
+constexpr float kPrefixTime = 140.f, kOwnTime = 90.f;
+constexpr int kTileTime = 12, kPairTime = 21, kOwnKeys = 64;
 constexpr int kMinPiece = 2;               // key tiles of a piece in the prefix pass, at least
 constexpr int kMaxCtas = 160;
 constexpr int kMaxUnits = 16;              // whole units a CTA may be given (see the kernel)
@@ -93,13 +98,14 @@ struct Launch {
   uint8_t* workspace;
   int box;                                 // keys of one TMA box: gcd(page_size, 128)
 };
-// With sinks or as a prefix pass, in kernels of their own: all of it is behind
-// FORMS, since the other ones have no instructions to spare.
+// With sinks, and as the prefix pass, in kernels of their own: the plain ones
+// have no instructions to spare.
+enum Form { kPlain, kSinks, kPrefix };
 struct FormsLaunch : Launch {
   AttentionForms f;
 };
-template <bool FORMS> struct LaunchOf { using type = Launch; };
-template <> struct LaunchOf<true> { using type = FormsLaunch; };
+template <int FORM> struct LaunchOf { using type = FormsLaunch; };
+template <> struct LaunchOf<kPlain> { using type = Launch; };
 
 // ------------------------------------------------------------------ tcgen05
 __device__ __forceinline__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
@@ -202,37 +208,35 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 // pass of a group of sequences, and b is its first one.
 // In the prefix pass a unit is cut in pieces of about ``chunk`` tiles.
 __device__ __forceinline__ int pieces_of(int tiles, int chunk) { return (tiles + chunk - 1) / chunk; }
-template <bool FORMS>
+template <int FORM>
 struct EntryForms {
-  int before;                              // tiles of sinks before those of the window
-  bool flat;                               // every row sees all keys
+  static constexpr int before = 0;
 };
 template <>
-struct EntryForms<false> {
-  static constexpr int before = 0;
-  static constexpr bool flat = false;
+struct EntryForms<kSinks> {
+  int before;                              // tiles of sinks before those of the window
 };
-template <bool FORMS>
-struct Entry : EntryForms<FORMS> {
-  using EntryForms<FORMS>::before;
-  using EntryForms<FORMS>::flat;
+template <>
+struct EntryForms<kPrefix> : EntryForms<kPlain> {
+  int sequences;                           // of the group
+};
+template <int FORM>
+struct Entry : EntryForms<FORM> {
+  using EntryForms<FORM>::before;
+  static constexpr bool flat = FORM == kPrefix;           // every row sees all keys
   int b, q_first, row0, rows, start, lo, end, tile0, count;
-  __device__ __forceinline__ void load(const typename LaunchOf<FORMS>::type& p, int e, int group) {
+  __device__ __forceinline__ void load(const typename LaunchOf<FORM>::type& p, int e, int group) {
     const AttentionParams& a = p.a;
     b = e / p.row_tiles;
     row0 = (e - b * p.row_tiles) * p.unit_rows;
-    int q_len, len = 0;
-    if constexpr (FORMS) {
-      flat = p.f.pass == kPrefixPass;
-      if (flat) {
-        int s0, q_end;
-        p.f.group(a.cu_q, b, s0, q_first, q_end);
-        len = p.f.lens[b];
-        q_len = len > 0 ? q_end - q_first : 0;
-        b = s0;
-      }
-    }
-    if (!flat) {
+    int q_len, len;
+    if constexpr (FORM == kPrefix) {
+      int s1, q_end;
+      len = p.f.lens[b];
+      p.f.group(a.cu_q, b, b, s1, q_first, q_end);
+      q_len = len > 0 ? q_end - q_first : 0;
+      this->sequences = s1 - b;
+    } else {
       q_first = a.cu_q == nullptr ? b : a.cu_q[b];
       q_len = a.cu_q == nullptr ? 1 : a.cu_q[b + 1] - q_first;
       len = a.seq_lens[b];
@@ -240,13 +244,13 @@ struct Entry : EntryForms<FORMS> {
     start = flat ? len - 1 : len - q_len;
     rows = max(0, min(p.unit_rows, min(min(q_len, a.max_q_len), a.N - q_first) * group - row0));
     lo = end = tile0 = count = 0;
-    if constexpr (FORMS) before = 0;
+    if constexpr (FORM == kSinks) before = 0;
     if (rows > 0) {
       lo = a.window > 0 ? max(0, position(0, group) + 1 - a.window) : 0;
       const int64_t most = static_cast<int64_t>(a.table_width) * a.cache.page_size;
       end = static_cast<int>(min(static_cast<int64_t>(max(0, position(rows - 1, group) + 1)), most));
       tile0 = lo / kKeys;
-      if constexpr (FORMS) before = min((p.f.sinks + kKeys - 1) / kKeys, tile0);
+      if constexpr (FORM == kSinks) before = min((p.f.sinks + kKeys - 1) / kKeys, tile0);
       count = max(1, (end + kKeys - 1) / kKeys - tile0 + before);   // one at least, so that someone writes the rows
     }
   }
@@ -257,30 +261,35 @@ struct Entry : EntryForms<FORMS> {
   __device__ __forceinline__ bool whole(int tile, int r0, int r1, int group, int window, int sinks) const {
     const int key0 = tile * kKeys;
     return key0 + kKeys - 1 <= position(r0, group) &&
-           (window == 0 || key0 > position(r1, group) - window || (FORMS && key0 + kKeys <= sinks));
+           (window == 0 || key0 > position(r1, group) - window || (FORM == kSinks && key0 + kKeys <= sinks));
   }
 };
 
 // A CTA's stretch of the line, unit by unit; every warp walks it by itself.
 // On the line a unit is kUnitCost places and then a place a key tile.  Where
 // ``whole`` is given the CTA has those units instead, x to x1.
-template <bool FORMS>
+template <int FORM>
 struct WalkOf {
-  Entry<FORMS> en;
+  Entry<FORM> en;
   int e, head, tile, x, x1, n, u0, span;   // this piece: tiles [tile, tile + n) of the unit that begins at u0
   // The prefix pass: x counts pieces, which are shared evenly.  Instead of u0
   // and span it has the place among the unit's pieces and how long they are.
   __device__ __forceinline__ int& piece() { return u0; }
   __device__ __forceinline__ int& chunk() { return span; }
-  __device__ __forceinline__ bool next_piece(const typename LaunchOf<FORMS>::type& p, int group, bool first, int first_entry, int first_prefix) {
+  __device__ __forceinline__ void take_piece(int each) {
+    ++x;
+    tile = en.count * piece() / each;
+    n = en.count * (piece() + 1) / each - tile;
+  }
+  __device__ __forceinline__ void first_piece(int heads, int first_prefix) {
+    const int in = x - first_prefix * heads, each = pieces_of(en.count, chunk());
+    head = in / each;
+    piece() = in - head * each;
+    take_piece(each);
+  }
+  __device__ __forceinline__ bool next_piece(const typename LaunchOf<FORM>::type& p, int group) {
     if (x == x1) return false;
-    if (first) {
-      e = first_entry;
-      en.load(p, e, group);
-      const int in = x - first_prefix * p.a.cache.kv_heads, each = pieces_of(en.count, chunk());
-      head = in / each;
-      piece() = in - head * each;
-    } else if (++piece() == pieces_of(en.count, chunk())) {
+    if (++piece() == pieces_of(en.count, chunk())) {
       piece() = 0;
       if (++head == p.a.cache.kv_heads) {
         head = 0;
@@ -288,13 +297,10 @@ struct WalkOf {
         while (en.count == 0);
       }
     }
-    ++x;
-    const int each = pieces_of(en.count, chunk());
-    tile = en.count * piece() / each;
-    n = en.count * (piece() + 1) / each - tile;
+    take_piece(pieces_of(en.count, chunk()));
     return true;
   }
-  __device__ __forceinline__ bool next(const typename LaunchOf<FORMS>::type& p, int group, const int* whole, bool first, int first_entry, int first_prefix) {
+  __device__ __forceinline__ bool next(const typename LaunchOf<FORM>::type& p, int group, const int* whole, bool first, int first_entry, int first_prefix) {
     const int heads = p.a.cache.kv_heads;
     if (whole != nullptr) {
       if (x == x1) return false;
@@ -342,15 +348,14 @@ struct WalkOf {
 // keep each from writing the next piece while another still reads this one or
 // has yet to take the same step (the loops that come here end in code which a
 // warp's lanes may leave one by one).
-template <bool FORMS>
-__device__ __noinline__ bool walk_next(WalkOf<FORMS>* at, const typename LaunchOf<FORMS>::type& p, int group, const int* whole, int first_entry, int first_prefix, uint32_t lanes) {
-  using Walk = WalkOf<FORMS>;
+template <int FORM>
+__device__ __noinline__ bool walk_next(WalkOf<FORM>* at, const typename LaunchOf<FORM>::type& p, int group, const int* whole, int first_entry, int first_prefix, uint32_t lanes) {
+  using Walk = WalkOf<FORM>;
   __syncwarp(lanes);
   Walk w = *at;
   bool more;
-  if constexpr (FORMS) {
-    more = p.f.pass == kPrefixPass ? w.next_piece(p, group, first_entry >= 0, first_entry, first_prefix)
-                       : w.next(p, group, whole, first_entry >= 0, first_entry, first_prefix);
+  if constexpr (FORM == kPrefix) {
+    more = w.next_piece(p, group);
   } else {
     more = w.next(p, group, whole, first_entry >= 0, first_entry, first_prefix);
   }
@@ -381,7 +386,7 @@ __device__ __noinline__ uint4 nan_columns(const AttentionParams& a, int b, int h
   return make_uint4(nan[0], nan[1], nan[2], nan[3]);
 }
 // ----------------------------------------------------------- shared memory
-template <bool FORMS>
+template <int FORM>
 struct Control {
   Group group[kInfo][kKeys / 8];
   uint64_t code_full[kStages], code_empty[kStages], full[kSlots], empty[kSlots];
@@ -389,7 +394,7 @@ struct Control {
   int8_t q_exponent[kCtaRows];             // of the power of two taken out of each row
   int sums[kThreads / 32];
   int units[kMaxUnits];                    // this CTA's, if it has whole ones
-  WalkOf<FORMS> walk[kThreads / 32];                // each warp's own, here and not in its registers
+  WalkOf<FORM> walk[kThreads / 32];                // each warp's own, here and not in its registers
   // Of a unit and the next: the key tiles, hidden from some rows, in which a
   // converting warp has met and left out NaN values that some row sees.
   int nan_count[2][4], nan_tiles[2][4][kNanTiles];
@@ -406,16 +411,16 @@ struct Layout {
   static constexpr int kCodeBytes = kKeys * 128;
   static constexpr int kQ = 0, kRing = kQBytes, kCode = kRing + kSlots * kSlotBytes,
                        kControl = kCode + kStages * kCodeBytes;
-  template <bool FORMS> static constexpr int kBytes = kControl + static_cast<int>(sizeof(Control<FORMS>));
+  template <int FORM> static constexpr int kBytes = kControl + static_cast<int>(sizeof(Control<FORM>));
 };
-static_assert(Layout<128>::kBytes<true> <= 232448, "shared memory of a CTA");
+static_assert(Layout<128>::kBytes<kPrefix> <= 232448 && Layout<128>::kBytes<kSinks> <= 232448, "shared memory of a CTA");
 
 // The queries of a unit by plain loads, to where and how the TMA would put
-// them (f16 rows with the sign of the scale): rows first, first + 128, ...
-template <typename T, int DP, bool FORMS>
-__device__ __noinline__ void load_queries(const AttentionParams& a, const Entry<FORMS>& en, int head, int group, uint8_t* to, int first) {
+// them (f16 rows with the sign of the scale): rows first, first + step, ...
+template <typename T, int DP, int FORM>
+__device__ __noinline__ void load_queries(const AttentionParams& a, const Entry<FORM>& en, int head, int group, uint8_t* to, int first, int step) {
 #pragma unroll 1
-  for (int row = first; row < kCtaRows; row += kTileRows) {
+  for (int row = first; row < kCtaRows; row += step) {
     const int gr = en.row0 + row;
     const T* src = static_cast<const T*>(a.q) + (en.q_first + gr / group) * a.q_token + (head * group + gr % group) * a.q_head;
 #pragma unroll 4
@@ -427,24 +432,49 @@ __device__ __noinline__ void load_queries(const AttentionParams& a, const Entry<
   }
 }
 
+// A bf16 row of queries to float16 in place, a power of two taken out of it,
+// whose exponent is returned.  The sign of the scale goes into it, so that a
+// larger score is a larger weight.
+template <int DP>
+__device__ __forceinline__ int queries_to_f16(uint8_t* q, int row, float scale) {
+  uint8_t* at = q + row * 128;             // half h of row r: (2 h + r / 128) * 128 rows + r % 128
+  auto chunk = [&](int c) { return reinterpret_cast<uint4*>(at + 2 * (c / 8) * Layout<DP>::kHalfBytes + (((c & 7) ^ (row & 7)) * 16)); };
+  uint32_t amax = 0;                       // of the magnitudes' bits, which order as they do
+#pragma unroll 4
+  for (int c = 0; c < DP / 8; ++c) {
+    const uint4 u = *chunk(c);
+    amax = __vmaxu2(amax, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
+  }
+  const int ex = query_exponent(static_cast<int>(max(amax & 0xFFFF, amax >> 16) >> 7) - 127);
+  float inv = power_of_two(-ex);
+  if (scale < 0.f) inv = -inv;
+#pragma unroll 4
+  for (int c = 0; c < DP / 8; ++c) {
+    uint4 u = *chunk(c);
+    auto turn = [&](uint32_t v) {
+      return f32x2_to_f16x2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xFFFF0000u) * inv);
+    };
+    u = make_uint4(turn(u.x), turn(u.y), turn(u.z), turn(u.w));
+    *chunk(c) = u;
+  }
+  return ex;
+}
+
 // ------------------------------------------------------------------ kernel
 // MAPPED: queries come by TMA.  A tensor map holds no strides of zero or below;
 // with those they come by plain loads, in a kernel of its own, as the other one
 // has no instructions to spare (117.5 instead of 116.5 us on ragged chunks).
-template <typename T, int DP, bool MAPPED, bool FORMS>
+template <typename T, int DP, bool MAPPED, int FORM>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ typename LaunchOf<FORMS>::type p) {
+                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ typename LaunchOf<FORM>::type p) {
   using L = Layout<DP>;
+  constexpr bool kIsPrefix = FORM == kPrefix;
   int sinks = 0;
-  bool prefix = false;
-  if constexpr (FORMS) {
-    sinks = p.f.sinks;
-    prefix = p.f.pass == kPrefixPass;
-  }
+  if constexpr (FORM == kSinks) sinks = p.f.sinks;
   constexpr bool kBf16 = !std::is_same<T, __half>::value;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Control<FORMS>& s = *reinterpret_cast<Control<FORMS>*>(smem + L::kControl);
+  Control<FORM>& s = *reinterpret_cast<Control<FORM>*>(smem + L::kControl);
   const AttentionParams& a = p.a;
   const moe_kv_cache_t& ca = a.cache;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -475,47 +505,68 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       mbar_init(&s.o_full[i], 1);
     }
     mbar_init(&s.q_raw, 1);
-    mbar_init(&s.q_full, 4);
+    mbar_init(&s.q_full, kIsPrefix ? 8 : 4);
     mbar_init(&s.q_empty, 1 + 2 * kTileRows / 32);   // the last scores, and every row's thread has its exponent
     mbar_init(&s.drained, 1);
     s.abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (FORMS && prefix) pdl_wait();         // the own pass may begin beside this one, when all that came before is done
+  if (kIsPrefix) pdl_wait();         // the own pass may begin beside this one, when all that came before is done
   pdl_launch_dependents();
   pdl_wait();
 
   // The line's length, and where this CTA's stretch of it begins.
   const int entries = a.B * p.row_tiles, per = (entries + kThreads - 1) / kThreads;
   const int from = min(tid * per, entries), to = min(from + per, entries);
-  int mine = 0, chunk = 0;                 // chunk > 0: the prefix pass
-  if constexpr (FORMS) {
-    if (prefix) {
-      // Pieces of a length for which there is about one for each CTA: n units of
-      // t tiles give at most t / chunk + n.
-      if (tid == 0) s.sums[0] = s.sums[1] = s.sums[2] = 0;
-      __syncthreads();
+  int mine = 0;
+  [[maybe_unused]] int chunk = 0, most_ctas = gridDim.x;
+  if constexpr (kIsPrefix) {
+    if (tid < 4) s.sums[tid] = 0;
+    __syncthreads();
+    int own = 0;                           // key tiles of the own pass, a head's
+    Entry<FORM> en;
 #pragma unroll 1
-      for (int e = from; e < to; ++e) {
-        Entry<FORMS> en;
-        en.load(p, e, group);
-        if (en.count == 0) continue;
-        atomicAdd(&s.sums[0], en.count * ca.kv_heads);
-        atomicAdd(&s.sums[1], ca.kv_heads);
-        atomicMax(&s.sums[2], en.count);
-      }
-      __syncthreads();
-      const int tiles = s.sums[0], spare = static_cast<int>(gridDim.x) - s.sums[1], longest = s.sums[2];
-      chunk = spare > 0 ? max(kMinPiece, (tiles + spare - 1) / spare) : longest;
-      chunk = max(max(chunk, 1), (longest + p.f.most_pieces - 1) / p.f.most_pieces);
-      __syncthreads();
+    for (int e = from; e < to; ++e) {
+      en.load(p, e, group);
+      if (en.count == 0) continue;
+      atomicAdd(&s.sums[0], en.count * ca.kv_heads);
+      atomicAdd(&s.sums[1], ca.kv_heads);
+      atomicMax(&s.sums[2], en.count);
+      if (en.row0 == 0) own -= en.sequences * (en.end / kOwnKeys);
     }
+#pragma unroll 1
+    for (int b = tid; b < p.f.sequences; b += kThreads) own += (a.seq_lens[b] + kOwnKeys - 1) / kOwnKeys;
+    own = __reduce_add_sync(0xffffffffu, own);
+    if (lane == 0) atomicAdd(&s.sums[3], own);
+    __syncthreads();
+    const int tiles = s.sums[0], units = s.sums[1], longest = s.sums[2];
+    // How many CTAs: the other SMs are the own pass's meanwhile.  Each thread
+    // works out what a number of them would take, in units of 0.1 us.
+    int* best = s.units;                   // not in use here
+    if (tid == 0) *best = 0x7fffffff;
+    __syncthreads();
+    if (tid < static_cast<int>(gridDim.x)) {
+      const int sms = gridDim.x, n = tid + 1, each = static_cast<int64_t>(a.max_q_len) * group > kTileRows ? kPairTime : kTileTime;
+      const float here = kPrefixTime + static_cast<float>(each * ((tiles + n - 1) / n));
+      const float work = static_cast<float>(max(0, s.sums[3])) * ca.kv_heads * p.f.own_row_tiles * (10.f / 3.f);
+      const float rest = work - fmaxf(0.f, here - kOwnTime) * static_cast<float>(sms - n);
+      const float time = rest <= 0.f ? here : here + kOwnTime + rest / static_cast<float>(sms);
+      atomicMin(best, static_cast<int>(fminf(time, 8.0e6f)) << 8 | n);
+    }
+    __syncthreads();
+    most_ctas = *best & 255;
+    // Pieces of a length for which there is about one for each CTA: n units of
+    // t tiles give at most t / chunk + n.
+    const int spare = most_ctas - units;
+    chunk = spare > 0 ? max(kMinPiece, (tiles + spare - 1) / spare) : longest;
+    chunk = max(max(chunk, 1), (longest + p.f.most_pieces - 1) / p.f.most_pieces);
+    __syncthreads();
   }
 #pragma unroll 1
   for (int e = from; e < to; ++e) {
-    Entry<FORMS> en;
+    Entry<FORM> en;
     en.load(p, e, group);
-    if (en.count > 0) mine += FORMS && chunk > 0 ? pieces_of(en.count, chunk) : en.count + kUnitCost;
+    if (en.count > 0) mine += kIsPrefix ? pieces_of(en.count, chunk) : en.count + kUnitCost;
   }
   int incl = mine;
 #pragma unroll
@@ -532,7 +583,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     all_tiles += s.sums[w];
   }
   const int total = all_tiles * ca.kv_heads;
-  const int ctas = min(static_cast<int>(gridDim.x), max(1, FORMS && chunk > 0 ? total : total / kMinTiles));
+  const int ctas = min(most_ctas, max(1, kIsPrefix ? total : total / kMinTiles));
   if (total == 0) return;
 
   // Whole units, longest first and to the CTAs forwards and backwards in turn,
@@ -542,7 +593,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   // 512 units of 2 x 2048 tokens: 92 us, cut from the line 104; 220 units of
   // four ragged chunks: 149 and 120.
   bool whole = false;
-  if (per == 1 && (!FORMS || chunk == 0)) {
+  if (!kIsPrefix && per == 1) {
     int* costs = reinterpret_cast<int*>(smem + L::kRing);    // not in use yet
     int* sorted = costs + kThreads;
     costs[tid] = mine;
@@ -582,17 +633,23 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     }
   }
   if (whole ? s.given == 0 : static_cast<int>(blockIdx.x) >= ctas) return;
-  const int x0 = stretch_begin(total, ctas, blockIdx.x);
+  const bool one_each = kIsPrefix && total <= ctas;
+  [[maybe_unused]] auto first_one = [&] {
+    static_assert(sizeof(Entry<FORM>) <= sizeof(s.units), "an entry in the place of the units");
+    return reinterpret_cast<Entry<FORM>*>(s.units);
+  };
+  const int x0 = one_each ? blockIdx.x : stretch_begin(total, ctas, blockIdx.x);
   if (!whole && x0 < incl * ca.kv_heads && x0 >= (incl - mine) * ca.kv_heads) {
     int before = incl - mine;
 #pragma unroll 1
     for (int e = from; e < to; ++e) {
-      Entry<FORMS> en;
+      Entry<FORM> en;
       en.load(p, e, group);
-      const int places = en.count == 0 ? 0 : FORMS && chunk > 0 ? pieces_of(en.count, chunk) : en.count + kUnitCost;
+      const int places = en.count == 0 ? 0 : kIsPrefix ? pieces_of(en.count, chunk) : en.count + kUnitCost;
       if (x0 < (before + places) * ca.kv_heads) {
         s.first_entry = e;
         s.first_prefix = before;
+        if constexpr (kIsPrefix) *first_one() = en;         // for all warps
         break;
       }
       before += places;
@@ -620,17 +677,28 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     const bool ok = wait_one(bar, parity);
     return __all_sync(0xffffffffu, ok) != 0;
   };
-  WalkOf<FORMS>& walk = s.walk[warp];
-  const Entry<FORMS>& en = walk.en;
+  WalkOf<FORM>& walk = s.walk[warp];
+  const Entry<FORM>& en = walk.en;
   // who walks: a whole warp with the same values, or the one lane that issues the products
   const uint32_t walkers = warp == kMmaWarp ? 1u << lane : 0xffffffffu;
+  if constexpr (kIsPrefix) {
+    if (lane == 0) {
+      walk.en = *first_one();
+      walk.e = s.first_entry;
+      walk.chunk() = chunk;
+      walk.x = x0;
+      walk.x1 = one_each ? x0 + 1 : stretch_begin(total, ctas, blockIdx.x + 1);
+      walk.first_piece(ca.kv_heads, s.first_prefix);
+    }
+    __syncwarp();
+  }
   auto next = [&](bool first) {
+    if (kIsPrefix && first) return true;
     if (first) {
-      if (FORMS && prefix) walk.chunk() = chunk;
       walk.x = whole ? 0 : x0;
       walk.x1 = whole ? s.given : stretch_begin(total, ctas, blockIdx.x + 1);
     }
-    return walk_next<FORMS>(&walk, p, group, whole ? s.units : nullptr, first ? s.first_entry : -1, s.first_prefix, walkers);
+    return walk_next<FORM>(&walk, p, group, whole ? s.units : nullptr, first ? s.first_entry : -1, s.first_prefix, walkers);
   };
 
   if (warp == kLoadWarp) {
@@ -645,7 +713,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     auto find = [&](int j) {
       Ahead f = {-1, 0, {0.f, 0.f, 0.f, 0}};
       const int key = en.tile_at(walk.tile + j) * kKeys + 8 * (lane & 15);
-      if (j < walk.n && key < en.end && ((key & ~(p.box - 1)) + p.box > en.lo || (FORMS && (key & ~(p.box - 1)) < sinks))) {
+      if (j < walk.n && key < en.end && ((key & ~(p.box - 1)) + p.box > en.lo || (FORM == kSinks && (key & ~(p.box - 1)) < sinks))) {
         const int page_at = key / ca.page_size;
         f.off = key - page_at * ca.page_size;
         f.page = a.block_table[static_cast<int64_t>(en.b) * a.table_width + page_at];
@@ -843,7 +911,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
             };
             clean(c.x), clean(c.y), clean(c.z), clean(c.w);
             const int key = key0 + it * kStep, at = tile * kKeys + key;
-            nan |= seen != 0 && (at >= en.lo || (FORMS && at < sinks)) && at < en.end && info[key >> 3].valid;      // some row sees it
+            nan |= seen != 0 && (at >= en.lo || (FORM == kSinks && at < sinks)) && at < en.end && info[key >> 3].valid;      // some row sees it
             put(it, c);
           }
         }
@@ -858,55 +926,34 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           mbar_arrive(&s.full[slot]);
         }
         if (j == 0) {
-          // The queries, which the TMA has put where the A operand goes: bf16
-          // rows become float16 in place, a power of two taken out of each.
+          // The queries, which the TMA has put where the A operand goes.
           good = wait(&s.q_raw, units & 1);
           if (!good) break;
           // the rows have begun the unit before, so they are done with the one before that
           if (lane == 0) s.nan_count[units & 1][w] = 0;
-          if constexpr (!MAPPED) {
-            load_queries<T, DP, FORMS>(a, en, walk.head, group, smem + L::kQ, 32 * w + lane);
-            fence_proxy_async_shared();
-            __syncwarp();
-          }
-          if constexpr (kBf16) {
-#pragma unroll 1
-            for (int row = 32 * w + lane; row < kCtaRows; row += 128) {
-              uint8_t* at = smem + L::kQ + row * 128;      // half h of row r: (2 h + r / 128) * 128 rows + r % 128
-              auto chunk = [&](int c) { return reinterpret_cast<uint4*>(at + 2 * (c / 8) * L::kHalfBytes + (((c & 7) ^ (row & 7)) * 16)); };
-              uint32_t amax = 0;                           // of the magnitudes' bits, which order as they do
-#pragma unroll 4
-              for (int c = 0; c < DP / 8; ++c) {
-                const uint4 u = *chunk(c);
-                amax = __vmaxu2(amax, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
-              }
-              const int ex = query_exponent(static_cast<int>(max(amax & 0xFFFF, amax >> 16) >> 7) - 127);
-              s.q_exponent[row] = static_cast<int8_t>(ex);
-              float inv = power_of_two(-ex);
-              if (a.scale < 0.f) inv = -inv;               // the sign goes into q, so that a larger score is a larger weight
-#pragma unroll 4
-              for (int c = 0; c < DP / 8; ++c) {
-                uint4 u = *chunk(c);
-                auto turn = [&](uint32_t v) {
-                  return f32x2_to_f16x2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xFFFF0000u) * inv);
-                };
-                u = make_uint4(turn(u.x), turn(u.y), turn(u.z), turn(u.w));
-                *chunk(c) = u;
-              }
+          if constexpr (!kIsPrefix) {
+            if constexpr (!MAPPED) {
+              load_queries<T, DP, FORM>(a, en, walk.head, group, smem + L::kQ, 32 * w + lane, kTileRows);
+              fence_proxy_async_shared();
+              __syncwarp();
             }
-            fence_proxy_async_shared();
-            __syncwarp();
-          } else if (MAPPED && a.scale < 0.f) {
+            if constexpr (kBf16) {
 #pragma unroll 1
-            for (int c = 32 * w + lane; c < L::kQBytes / 16; c += 128) {
-              uint4* at = reinterpret_cast<uint4*>(smem + L::kQ) + c;
-              const uint4 u = *at;
-              *at = make_uint4(u.x ^ 0x80008000u, u.y ^ 0x80008000u, u.z ^ 0x80008000u, u.w ^ 0x80008000u);
+              for (int row = 32 * w + lane; row < kCtaRows; row += 128) s.q_exponent[row] = static_cast<int8_t>(queries_to_f16<DP>(smem + L::kQ, row, a.scale));
+              fence_proxy_async_shared();
+              __syncwarp();
+            } else if (MAPPED && a.scale < 0.f) {
+#pragma unroll 1
+              for (int c = 32 * w + lane; c < L::kQBytes / 16; c += 128) {
+                uint4* at = reinterpret_cast<uint4*>(smem + L::kQ) + c;
+                const uint4 u = *at;
+                *at = make_uint4(u.x ^ 0x80008000u, u.y ^ 0x80008000u, u.z ^ 0x80008000u, u.w ^ 0x80008000u);
+              }
+              fence_proxy_async_shared();
+              __syncwarp();
             }
-            fence_proxy_async_shared();
-            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.q_full);
           }
-          if (lane == 0) mbar_arrive(&s.q_full);
         }
       }
     }
@@ -921,8 +968,32 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     for (bool more = next(true); more; more = next(false), ++units) {
       // after a timeout a unit's rows are left as they are, but its part in the
       // join is still played, so that the counters end at zero
-      good = good && wait(&s.q_full, units & 1);
-      const float row_scale = kBf16 ? power_of_two(s.q_exponent[row]) : 1.f;
+      float row_scale = 1.f;
+      if constexpr (kIsPrefix) {
+        // There is little to do before a piece's first scores, so a row's thread
+        // makes its queries float16: 1.0 us, 2.2 in the converting warps, which
+        // have their first keys to convert meanwhile.
+        good = good && wait(&s.q_raw, units & 1);
+        if (good) {
+          if constexpr (!MAPPED) load_queries<T, DP, FORM>(a, en, walk.head, group, smem + L::kQ, row, kCtaRows);
+          if constexpr (kBf16) {
+            row_scale = power_of_two(queries_to_f16<DP>(smem + L::kQ, row, a.scale));
+          } else if (MAPPED && a.scale < 0.f) {
+#pragma unroll 4
+            for (int c = 0; c < DP / 8; ++c) {
+              uint4* at = reinterpret_cast<uint4*>(smem + L::kQ + row * 128 + 2 * (c / 8) * L::kHalfBytes + (c & 7) * 16);
+              const uint4 u = *at;
+              *at = make_uint4(u.x ^ 0x80008000u, u.y ^ 0x80008000u, u.z ^ 0x80008000u, u.w ^ 0x80008000u);
+            }
+          }
+          fence_proxy_async_shared();
+        }
+        __syncwarp();
+        if (good && lane == 0) mbar_arrive(&s.q_full);
+      } else {
+        good = good && wait(&s.q_full, units & 1);
+        if (kBf16) row_scale = power_of_two(s.q_exponent[row]);
+      }
       // Only now may the next unit's queries come: a unit of one tile has its
       // last scores before its rows' warps have begun it, and two of them
       // would carry q_full past the phase that they wait for.
@@ -936,7 +1007,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       }
       // the CTAs that have parts of the unit, here and not where the result waits
       int cta0 = 0, pieces = 1;
-      if (walk.n != en.count && !prefix) {
+      if (!kIsPrefix && walk.n != en.count) {
         const int first_at = walk.u0 + kUnitCost;
         cta0 = stretch_of(total, ctas, first_at);
         pieces = stretch_of(total, ctas, first_at + en.count - 1) - cta0 + 1;
@@ -970,7 +1041,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           tmem_wait(ra);
           tmem_wait(rb);
           const bool all = __all_sync(0xffffffffu, info[lane & 7].valid) && key0 + kHalf - 1 <= pos_lo &&
-                           (a.window == 0 || key0 > pos_hi || (FORMS && key0 + kHalf <= sinks));
+                           (a.window == 0 || key0 > pos_hi || (FORM == kSinks && key0 + kHalf <= sinks));
           float top = -INFINITY;
           auto exponents = [&](uint32_t (&r)[32], int c) {
 #pragma unroll
@@ -987,7 +1058,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
               // which of the 32 keys this row sees, a bit each: [first, last]
               const int first = a.window > 0 ? pos - a.window + 1 - key0 - 32 * c : 0, last = pos - key0 - 32 * c;
               uint32_t mask = first <= 0 ? 0xffffffffu : first > 31 ? 0u : ~((1u << first) - 1u);
-              if constexpr (FORMS) {
+              if constexpr (FORM == kSinks) {
                 const int stay = sinks - key0 - 32 * c;
                 mask |= stay <= 0 ? 0u : stay > 31 ? 0xffffffffu : (1u << stay) - 1u;
               }
@@ -1102,7 +1173,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
             const int k0 = max(tile * kKeys, a.window > 0 ? pos - a.window + 1 : 0), k1 = min(min(pos, en.end - 1), tile * kKeys + kKeys - 1);
             uint4 bits = nan_columns(a, en.b, walk.head, k0, k1);
             nan[0] |= bits.x, nan[1] |= bits.y, nan[2] |= bits.z, nan[3] |= bits.w;
-            if constexpr (FORMS) {
+            if constexpr (FORM == kSinks) {
               bits = nan_columns(a, en.b, walk.head, tile * kKeys, min(sinks - 1, k1));
               nan[0] |= bits.x, nan[1] |= bits.y, nan[2] |= bits.z, nan[3] |= bits.w;
             }
@@ -1115,17 +1186,15 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       T* dst = static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head;
       const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // whole sectors at a time
       auto put = [&](int d, const float (&v)[32], float inv) {        // columns [d, d + 32)
-        if constexpr (FORMS) {
-          if (prefix) {
-            float* sums = p.f.sums + (walk.piece() * p.f.rows + static_cast<int64_t>(tok) * a.Hq + h) * ca.head_dim + d;
+        if constexpr (kIsPrefix) {
+          float* sums = p.f.sums + (walk.piece() * p.f.rows + static_cast<int64_t>(tok) * a.Hq + h) * ca.head_dim + d;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              if (d + e < ca.head_dim)
-                asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(sums + e), "f"(v[e]), "f"(v[e + 1]), "f"(v[e + 2]),
-                             "f"(v[e + 3]), "f"(v[e + 4]), "f"(v[e + 5]), "f"(v[e + 6]), "f"(v[e + 7])
-                             : "memory");
-            return;
-          }
+          for (int e = 0; e < 32; e += 8)
+            if (d + e < ca.head_dim)
+              asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(sums + e), "f"(v[e]), "f"(v[e + 1]), "f"(v[e + 2]),
+                           "f"(v[e + 3]), "f"(v[e + 4]), "f"(v[e + 5]), "f"(v[e + 6]), "f"(v[e + 7])
+                           : "memory");
+          return;
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 16) {
@@ -1145,12 +1214,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         }
       };
       auto put_lse = [&](float mm, float ll) {
-        if constexpr (FORMS) {
-          if (prefix) {
-            p.f.refs[walk.piece() * p.f.rows + static_cast<int64_t>(tok) * a.Hq + h] = make_float2(mm, ll);
-            if (gr == 0 && walk.head == 0 && walk.piece() == 0) p.f.pieces[walk.e / p.row_tiles] = pieces_of(en.count, walk.chunk());
-            return;
-          }
+        if constexpr (kIsPrefix) {
+          p.f.refs[walk.piece() * p.f.rows + static_cast<int64_t>(tok) * a.Hq + h] = make_float2(mm, ll);
+          if (gr == 0 && walk.head == 0 && walk.piece() == 0) p.f.pieces[walk.e / p.row_tiles] = pieces_of(en.count, walk.chunk());
+          return;
         }
         if (a.lse != nullptr) a.lse[static_cast<int64_t>(tok) * a.Hq + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
       };
@@ -1171,7 +1238,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
             if ((bits >> e) & 1) v[e] = __uint_as_float(0x7FC00000u);
         }
       };
-      if (walk.n == en.count || prefix) {
+      if (kIsPrefix || walk.n == en.count) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int d = 0; d < DP; d += 32) {
@@ -1298,12 +1365,12 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   }
 }
 
-template <typename T, int DP, bool MAPPED, bool FORMS>
+template <typename T, int DP, bool MAPPED, int FORM>
 int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t stream) {
   CUtensorMap q_map = {}, k_map, v_map;
-  typename LaunchOf<FORMS>::type p = {};
+  typename LaunchOf<FORM>::type p = {};
   p.a = a;
-  if constexpr (FORMS) p.f = *forms;
+  if constexpr (FORM != kPlain) p.f = *forms;
   p.workspace = static_cast<uint8_t*>(a.workspace) + decode_attention_workspace_bytes();
   p.box = 8;
   while (p.box < kKeys && a.cache.page_size % (2 * p.box) == 0) p.box *= 2;
@@ -1312,8 +1379,8 @@ int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t s
   if (!encode_cache_map(&k_map, a.cache, false, p.box) || !encode_cache_map(&v_map, a.cache, true, p.box) ||
       (MAPPED && !encode_query_map(&q_map, a, std::is_same<T, __half>::value, group, kCtaRows / group)))
     return MOE_ERR_CUDA;
-  auto kernel = prefill_attention_kernel<T, DP, MAPPED, FORMS>;
-  constexpr int bytes = Layout<DP>::template kBytes<FORMS>;
+  auto kernel = prefill_attention_kernel<T, DP, MAPPED, FORM>;
+  constexpr int bytes = Layout<DP>::template kBytes<FORM>;
   if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes) != cudaSuccess) return MOE_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
@@ -1337,20 +1404,21 @@ cudaError_t clear_prefill_counters(void* workspace, cudaStream_t s) {
 }
 
 namespace {
-template <typename T, bool FORMS>
+template <typename T, int FORM>
 int launch_type(const AttentionParams& p, const AttentionForms* forms, cudaStream_t s) {
   const bool mapped = p.q_token > 0 && p.q_head > 0;
-  if (p.cache.head_dim <= 64) return mapped ? launch<T, 64, true, FORMS>(p, forms, s) : launch<T, 64, false, FORMS>(p, forms, s);
-  return mapped ? launch<T, 128, true, FORMS>(p, forms, s) : launch<T, 128, false, FORMS>(p, forms, s);
+  if (p.cache.head_dim <= 64) return mapped ? launch<T, 64, true, FORM>(p, forms, s) : launch<T, 64, false, FORM>(p, forms, s);
+  return mapped ? launch<T, 128, true, FORM>(p, forms, s) : launch<T, 128, false, FORM>(p, forms, s);
 }
-template <bool FORMS>
+template <int FORM>
 int launch_forms(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s) {
-  return dtype == MOE_DTYPE_F16 ? launch_type<__half, FORMS>(p, forms, s) : launch_type<__nv_bfloat16, FORMS>(p, forms, s);
+  return dtype == MOE_DTYPE_F16 ? launch_type<__half, FORM>(p, forms, s) : launch_type<__nv_bfloat16, FORM>(p, forms, s);
 }
 }  // namespace
 
 int launch_prefill_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s) {
-  return forms != nullptr ? launch_forms<true>(p, forms, dtype, s) : launch_forms<false>(p, forms, dtype, s);
+  if (forms == nullptr) return launch_forms<kPlain>(p, forms, dtype, s);
+  return forms->pass == kPrefixPass ? launch_forms<kPrefix>(p, forms, dtype, s) : launch_forms<kSinks>(p, forms, dtype, s);
 }
 
 }  // namespace moe
