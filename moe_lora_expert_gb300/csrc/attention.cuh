@@ -329,10 +329,10 @@ struct AttentionParams {
 // all see the prefix's keys, through the block table's row of the group's first
 // sequence.  It cuts the keys in pieces and leaves each piece's unnormalised
 // sums with their references.  The own pass (the kernel for few rows) takes
-// each sequence's other keys and joins all of them: it has more CTAs, with few
-// rows each, and so joins faster than the prefix pass could.  A sequence that
-// begins inside the prefix, or whose tokens are not all among the group's first
-// max_tokens, takes no part and reads its keys itself.
+// each sequence's other keys, beside it on the SMs that it leaves free, and
+// leaves the same as one more piece; a third kernel joins them.  A sequence
+// that begins inside the prefix, or whose tokens are not all among the group's
+// first max_tokens, takes no part: the own pass reads all of its keys.
 enum AttentionPass { kWholePass, kPrefixPass, kOwnPass };
 struct AttentionForms {
   int sinks;
@@ -341,8 +341,8 @@ struct AttentionForms {
   const int32_t *seqs, *lens;
   int most_pieces, own_row_tiles; // row tiles of a sequence in the own pass
   int64_t rows;                 // N * Hq
-  float* sums;                  // [most_pieces][rows][head_dim]
-  float2* refs;                 // [most_pieces][rows]: reference and denominator
+  float* sums;                  // [most_pieces + 1][rows][head_dim], the last of the own pass
+  float2* refs;                 // [most_pieces + 1][rows]: reference and denominator
   int32_t* pieces;              // [groups]
 
   // Group g's sequences and their tokens; nothing, where the list is out of order.
@@ -377,6 +377,7 @@ int sm_count();
 size_t prefill_attention_workspace_bytes();
 cudaError_t clear_prefill_counters(void* workspace, cudaStream_t s);
 int launch_prefill_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s);  // a moe_status_t; forms NULL: none
+int launch_shared_join(const AttentionParams& p, const AttentionForms& forms, int dtype, cudaStream_t s);   // a moe_status_t
 size_t decode_attention_workspace_bytes();
 cudaError_t clear_decode_counters(void* workspace, cudaStream_t s);
 int launch_decode_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s);   // a moe_status_t

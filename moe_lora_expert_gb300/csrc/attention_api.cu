@@ -277,7 +277,7 @@ int moe_paged_attention_sinks(const moe_paged_attention_args_t* a, int sinks, mo
 
 size_t moe_shared_prefix_partial_size(int N, int Hq, int head_dim, int groups) {
   if (N <= 0 || Hq <= 0 || head_dim <= 0 || groups <= 0) return 0;
-  return most_pieces(N, Hq) * static_cast<size_t>(N) * Hq * (static_cast<size_t>(head_dim) * 4 + 8) + static_cast<size_t>(groups) * 4;
+  return (most_pieces(N, Hq) + 1) * static_cast<size_t>(N) * Hq * (static_cast<size_t>(head_dim) * 4 + 8) + static_cast<size_t>(groups) * 4;
 }
 
 int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_shared_prefix_t* x, moe_stream_t stream) {
@@ -302,18 +302,19 @@ int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_sh
   f.most_pieces = most_pieces(p.N, p.Hq);
   f.rows = static_cast<int64_t>(p.N) * p.Hq;
   f.sums = static_cast<float*>(x->partial);
-  f.refs = reinterpret_cast<float2*>(f.sums + f.most_pieces * f.rows * p.cache.head_dim);
-  f.pieces = reinterpret_cast<int32_t*>(f.refs + f.most_pieces * f.rows);
+  f.refs = reinterpret_cast<float2*>(f.sums + (f.most_pieces + 1) * f.rows * p.cache.head_dim);
+  f.pieces = reinterpret_cast<int32_t*>(f.refs + (f.most_pieces + 1) * f.rows);
   f.pass = moe::kPrefixPass;
   f.own_row_tiles = static_cast<int>((rows_of(p) + 15) / 16);
   AttentionParams prefix = p;
   prefix.B = x->groups;
   prefix.max_q_len = f.max_tokens;
   if (rows_of(p) > kSharedRows || rows_of(prefix) < kPrefixRows) return attend(p, nullptr, a->dtype, on);
-  const int error = moe::launch_prefill_attention(prefix, &f, a->dtype, on);
+  int error = moe::launch_prefill_attention(prefix, &f, a->dtype, on);
   if (error != MOE_OK) return error;
   f.pass = moe::kOwnPass;
-  return moe::launch_decode_attention(p, &f, a->dtype, on);
+  error = moe::launch_decode_attention(p, &f, a->dtype, on);
+  return error != MOE_OK ? error : moe::launch_shared_join(p, f, a->dtype, on);
 }
 
 }  // extern "C"

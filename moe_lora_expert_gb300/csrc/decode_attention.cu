@@ -102,16 +102,9 @@ struct Shared {
   float m[kWarps][kMaxRows], l[kWarps][kMaxRows];
   int total, longest, abort_flag, last;
 };
-// With the group of each entry.
-struct FormsShared : Shared {
-  int of[kMaxEntries];
-};
-template <bool FORMS> struct SharedOf { using type = Shared; };
-template <> struct SharedOf<true> { using type = FormsShared; };
 constexpr int kSlotBytes = 2 * 16 * kPitch;
 constexpr int kScratch(int rows) { return 2 * rows * 128 * 4; }              // two warps' sums
-template <bool FORMS>
-constexpr int kSmem(int rows) { return kWarps * kRing * kSlotBytes + kScratch(rows) + static_cast<int>(sizeof(typename SharedOf<FORMS>::type)) + 1024; }
+constexpr int kSmem(int rows) { return kWarps * kRing * kSlotBytes + kScratch(rows) + static_cast<int>(sizeof(Shared)) + 1024; }
 
 // Partial sums of a row tile: [slot][row][128] and (m, l) [slot][row][2];
 // counters [2][slots].
@@ -201,8 +194,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   extern __shared__ uint8_t raw[];
   uint8_t* const rings = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   float* const scratch = reinterpret_cast<float*>(rings + kWarps * kRing * kSlotBytes);
-  using S = typename SharedOf<FORMS>::type;
-  S& s = *reinterpret_cast<S*>(reinterpret_cast<uint8_t*>(scratch) + kScratch(8 * NT));
+  Shared& s = *reinterpret_cast<Shared*>(reinterpret_cast<uint8_t*>(scratch) + kScratch(8 * NT));
   const AttentionParams& a = p.a;
   const moe_kv_cache_t& ca = a.cache;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -221,7 +213,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     fence_mbarrier_init();
   }
   // The own pass may run beside the prefix pass, which lets it start when all
-  // that came before is done; it waits where it needs the other's sums.
+  // that came before is done.
   bool own = false;
   int sinks = 0;
   if constexpr (FORMS) {
@@ -250,7 +242,6 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       if constexpr (FORMS) {
         int g = 0;
         if (own) lo = p.f.taken(a.cu_q, en.b, en.q_first, en.q_len, en.len - en.q_len, g);
-        s.of[e] = g;
       }
       hi = max(0, pos1 + 1);
       if (hi > most) {
@@ -667,93 +658,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       float* ml = parts + kPartialBytes / 4;
       int* counters = reinterpret_cast<int*>(ml + kMlBytes / 4);
 
-      // What the prefix pass has left of a row, joined to four columns of it, by a
-      // warp: 16 pieces at a time, whose loads are on their way together.
-      int pieces_left = -1;
-      auto join_prefix = [&](int64_t at_row, int g, float& Mx, float& Lx, float (&acc)[4]) {
-        if constexpr (FORMS) {
-          if (pieces_left < 0) {
-            pdl_wait();
-            pieces_left = min(__ldcg(p.f.pieces + g), p.f.most_pieces);
-          }
-          const int col = 4 * lane;
-          const float2* refs = p.f.refs + at_row;
-          const float* sums = p.f.sums + at_row * ca.head_dim + col;
-          const int64_t step = p.f.rows * ca.head_dim;
-#pragma unroll 1
-          for (int i = 0; i < pieces_left; i += 16) {
-            float4 v[16];
-            // a lane holds one piece's reference and denominator
-            float2 z = make_float2(-INFINITY, 0.f);
-            if (lane < 16 && i + lane < pieces_left) z = __ldcg(refs + (i + lane) * p.f.rows);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              v[k] = i + k < pieces_left && col < ca.head_dim ? __ldcg(reinterpret_cast<const float4*>(sums + (i + k) * step)) : make_float4(0, 0, 0, 0);
-            float now = z.x;
-#pragma unroll
-            for (int x = 1; x < 16; x *= 2) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
-            now = fmaxf(Mx, __shfl_sync(0xffffffffu, now, 0));
-            const float base = now == -INFINITY ? 0.f : now, keep = fast_exp2(Mx - base), e = fast_exp2(z.x - base);
-            float l = z.y * e;
-#pragma unroll
-            for (int x = 1; x < 16; x *= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
-            Lx = fmaf(Lx, keep, __shfl_sync(0xffffffffu, l, 0));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[q] *= keep;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float f = __shfl_sync(0xffffffffu, e, k);
-              acc[0] = fmaf(v[k].x, f, acc[0]);
-              acc[1] = fmaf(v[k].y, f, acc[1]);
-              acc[2] = fmaf(v[k].z, f, acc[2]);
-              acc[3] = fmaf(v[k].w, f, acc[3]);
-            }
-            Mx = now;
-          }
-        }
-      };
-      if constexpr (FORMS) {
-        if (!split && taken > 0) {
-          // the row tile is whole here: all warps join and write its rows
-          if (warp == 0) {
-            __syncwarp();                  // every lane has added what the scratch held
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const int row = 8 * t + 2 * c + z;
-#pragma unroll
-                for (int j = 0; j < kTiles; j += 2) {
-                  const float v[4] = {o[t][j][z], o[t][j][2 + z], o[t][j + 1][z], o[t][j + 1][2 + z]};
-                  store_f32<float, 4>(scratch + row * 128 + (DP / 8) * g + 2 * j, v);
-                }
-                if (g == 0) {
-                  s.m[0][row] = M[t][z];
-                  s.l[0][row] = Ls[t][z];
-                }
-              }
-          }
-          __syncthreads();
-          const int col = 4 * lane;
-#pragma unroll 1
-          for (int row = warp; row < en.rows; row += kWarps) {
-            float Mx = s.m[0][row], Lx = s.l[0][row], acc[4] = {};
-            if (col < DP) load_f32<float, 4>(scratch + row * 128 + col, acc);
-            const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
-            join_prefix(static_cast<int64_t>(tok) * a.Hq + h, s.of[at.e], Mx, Lx, acc);
-            const float inv = Lx == 0.f ? 0.f : 1.f / Lx;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[q] *= inv;
-            if (col < ca.head_dim) store_f32<T, 4>(static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head + col, acc);
-            if (lane == 0 && a.lse != nullptr)
-              a.lse[static_cast<int64_t>(tok) * a.Hq + h] = Lx == 0.f ? -INFINITY : (Mx + log2f(Lx)) * kLn2;
-          }
-          __syncthreads();                 // before the next row tile's sums
-        }
-      }
-
       // A thread of warp 0 holds, for rows 2 c and 2 c + 1, columns [DP/8 g, DP/8 g + DP/8).
-      if (warp == 0 && (!FORMS || split || taken == 0)) {
+      if (warp == 0) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -762,6 +668,19 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             if (row >= en.rows) continue;
             if (!split) {
               const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
+              if constexpr (FORMS) {
+                if (taken > 0) {                          // joined to what the prefix pass leaves
+                  const int64_t at_row = p.f.most_pieces * p.f.rows + static_cast<int64_t>(tok) * a.Hq + h;
+#pragma unroll
+                  for (int j = 0; j < kTiles; j += 2) {
+                    const float v[4] = {o[t][j][z], o[t][j][2 + z], o[t][j + 1][z], o[t][j + 1][2 + z]};
+                    const int col = (DP / 8) * g + 2 * j;
+                    if (col < ca.head_dim) store_f32<float, 4>(p.f.sums + at_row * ca.head_dim + col, v);
+                  }
+                  if (g == 0) p.f.refs[at_row] = make_float2(M[t][z], Ls[t][z]);
+                  continue;
+                }
+              }
               const float inv = Ls[t][z] == 0.f ? 0.f : 1.f / Ls[t][z];
               T* dst = static_cast<T*>(a.out) + tok * a.out_token + h * a.out_head;
 #pragma unroll
@@ -856,7 +775,12 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             if (finish) {
               const int gr = en.row0 + row, tok = en.q_first + gr / group, h = at.head * group + gr % group;
               if constexpr (FORMS) {
-                if (taken > 0) join_prefix(static_cast<int64_t>(tok) * a.Hq + h, s.of[at.e], Mx, Lx, acc);
+                if (taken > 0) {
+                  const int64_t at_row = p.f.most_pieces * p.f.rows + static_cast<int64_t>(tok) * a.Hq + h;
+                  if (col < ca.head_dim) store_f32<float, 4>(p.f.sums + at_row * ca.head_dim + col, acc);
+                  if (lane == 0) p.f.refs[at_row] = make_float2(Mx, Lx);
+                  continue;
+                }
               }
               const float inv = Lx == 0.f ? 0.f : 1.f / Lx;
 #pragma unroll
@@ -881,7 +805,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     }
   }
 
-  if (FORMS) pdl_wait();                   // who waits for this kernel waits for the one before it
+  if (FORMS && blockIdx.x == 0) pdl_wait();  // who waits for this kernel waits for the prefix pass, too; one CTA does for all
   // Nothing of this warp is in flight when it ends: it has waited for every
   // tile, unless a wait ran out.
   if (*static_cast<volatile int*>(&s.abort_flag)) {
@@ -964,7 +888,7 @@ int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t s
   p.box = gcd(a.cache.page_size, 16);
   if (!encode_cache_map(&k_map, a.cache, false, p.box) || !encode_cache_map(&v_map, a.cache, true, p.box)) return MOE_ERR_CUDA;
   auto kernel = decode_attention_kernel<T, DP, NT, FORMS>;
-  constexpr int bytes = kSmem<FORMS>(8 * NT);
+  constexpr int bytes = kSmem(8 * NT);
   p.tile_rows = 8 * NT;
   if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes) != cudaSuccess) return MOE_ERR_CUDA;
   const int sms = sm_count();

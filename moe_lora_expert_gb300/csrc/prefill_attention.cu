@@ -62,8 +62,8 @@ constexpr int kMinTiles = 4;               // least length of a CTA's stretch (a
 // The prefix pass, in units of 0.1 us: what a piece takes besides its tiles, a
 // tile of one and of two row tiles; and the own pass before and after its tiles,
 // of which each of three CTAs on an SM reads one in 1 us.
-constexpr float kPrefixTime = 140.f, kOwnTime = 90.f;
-constexpr int kTileTime = 12, kPairTime = 21, kOwnKeys = 64;
+constexpr float kPrefixTime = 150.f, kOwnTime = 90.f;
+constexpr int kTileTime = 21, kPairTime = 21, kOwnKeys = 64;
 constexpr int kMinPiece = 2;               // key tiles of a piece in the prefix pass, at least
 constexpr int kMaxCtas = 160;
 constexpr int kMaxUnits = 16;              // whole units a CTA may be given (see the kernel)
