@@ -333,18 +333,34 @@ struct AttentionParams {
 // leaves the same as one more piece; a third kernel joins them.  A sequence
 // that begins inside the prefix, or whose tokens are not all among the group's
 // first max_tokens, takes no part: the own pass reads all of its keys.
+constexpr int kOwnUnit = 14;
 enum AttentionPass { kWholePass, kPrefixPass, kOwnPass };
 struct AttentionForms {
   int sinks;
   int pass;                     // AttentionPass
   int groups, sequences, max_tokens;
   const int32_t *seqs, *lens;
-  int most_pieces, own_row_tiles; // row tiles of a sequence in the own pass
+  int most_pieces;
+  int own_row_tiles, own_per_sm; // of the own pass: row tiles of a sequence, CTAs an SM
+  int sms;
   int64_t rows;                 // N * Hq
   float* sums;                  // [most_pieces + 1][rows][head_dim], the last of the own pass
   float2* refs;                 // [most_pieces + 1][rows]: reference and denominator
   int32_t* pieces;              // [groups]
 
+  // What both passes take, in us, if the prefix pass, with ``tiles`` key tiles of
+  // its units, has n SMs, and the own pass, with ``own`` key tiles of its row
+  // tiles, the others meanwhile (or all of them after it).  Both passes look for
+  // the same best n: they have times of their own before and after their tiles,
+  // so a CTA should do all it can in one go.  A row tile takes the own
+  // pass kOwnUnit tiles' time besides its own, counted in ``own``.
+  __device__ __forceinline__ float time(int n, int tiles, int own) const {
+    const int left = sms - n, ctas = own_per_sm * (left > 0 ? left : sms);
+    const float first = 15.f + 2.1f * static_cast<float>((tiles + n - 1) / n), second = 12.f + 0.85f * static_cast<float>((own + ctas - 1) / ctas);
+    return left > 0 ? fmaxf(first, second) : first + second;
+  }
+  // The time and n as one number that orders by time.
+  __device__ __forceinline__ int choice(int n, int tiles, int own) const { return static_cast<int>(fminf(8.f * time(n, tiles, own), 8.0e6f)) << 8 | n; }
   // Group g's sequences and their tokens; nothing, where the list is out of order.
   __device__ __forceinline__ void group(const int32_t* cu_q, int g, int& s0, int& s1, int& q0, int& q1) const {
     s0 = seqs == nullptr ? 0 : max(0, min(sequences, seqs[g]));

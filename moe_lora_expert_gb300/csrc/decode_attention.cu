@@ -101,6 +101,7 @@ struct Shared {
   int end[kMaxEntries];                   // end of the keys that some row of it sees
   float m[kWarps][kMaxRows], l[kWarps][kMaxRows];
   int total, longest, abort_flag, last;
+  int tiles, own, best;                   // of shared prefixes: see AttentionForms::time
 };
 constexpr int kSlotBytes = 2 * 16 * kPitch;
 constexpr int kScratch(int rows) { return 2 * rows * 128 * 4; }              // two warps' sums
@@ -210,6 +211,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 #pragma unroll 1
       for (int i = 0; i < kRing; ++i) mbar_init(&s.full[w][i], 1);
     s.abort_flag = 0;
+    s.tiles = s.own = 0;
+    s.best = 0x7fffffff;
     fence_mbarrier_init();
   }
   // The own pass may run beside the prefix pass, which lets it start when all
@@ -230,6 +233,22 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     const int before = sink_tiles(lo);
     return (FORMS && i < before ? i : lo / kKeys + i - before) * kKeys;
   };
+  if constexpr (FORMS) {
+    if (own) {
+      __syncthreads();
+#pragma unroll 1
+      for (int g = tid; g < p.f.groups; g += kThreads) {
+        int s0, s1, q0, q1;
+        const int64_t held = static_cast<int64_t>(a.table_width) * ca.page_size;
+        const int len = static_cast<int>(min(static_cast<int64_t>(p.f.lens[g]), held));
+        p.f.group(a.cu_q, g, s0, s1, q0, q1);
+        const int tokens = min(q1 - q0, p.f.max_tokens), each = 256 / group;
+        if (len <= 0 || tokens <= 0) continue;
+        atomicAdd(&s.tiles, (tokens + each - 1) / each * ((len + 127) / 128) * ca.kv_heads);
+        atomicAdd(&s.own, -(s1 - s0) * (len / kKeys));
+      }
+    }
+  }
   // The line: each entry's key tiles, one at least so that someone writes its rows.
   const int64_t most = static_cast<int64_t>(a.table_width) * ca.page_size;
 #pragma unroll 1
@@ -241,7 +260,10 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       lo = a.window > 0 && pos0 >= a.window ? pos0 + 1 - a.window : 0;
       if constexpr (FORMS) {
         int g = 0;
-        if (own) lo = p.f.taken(a.cu_q, en.b, en.q_first, en.q_len, en.len - en.q_len, g);
+        if (own) {
+          lo = p.f.taken(a.cu_q, en.b, en.q_first, en.q_len, en.len - en.q_len, g);
+          if (en.row0 == 0) atomicAdd(&s.own, (en.len + kKeys - 1) / kKeys + kOwnUnit);
+        }
       }
       hi = max(0, pos1 + 1);
       if (hi > most) {
@@ -283,13 +305,27 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     }
   }
   __syncthreads();
-  const int total = s.total, ctas = min(static_cast<int>(gridDim.x), (total + kMinTiles - 1) / kMinTiles);
+  int most_ctas = gridDim.x;
+  if constexpr (FORMS) {
+    if (own && p.B == a.B && entries * ca.kv_heads > most_ctas) {
+      // Where a CTA cannot have one row tile anyway: as many as the SMs hold
+      // that the prefix pass leaves (128 sequences on 32768 shared tokens: 151 us
+      // with all CTAs, 135 so).
+      const int work = max(0, s.own) * ca.kv_heads * p.f.own_row_tiles;
+#pragma unroll 1
+      for (int n = tid + 1; n <= p.f.sms; n += kThreads) atomicMin(&s.best, p.f.choice(n, s.tiles, work));
+      __syncthreads();
+      const int left = p.f.sms - (s.best & 255);
+      if (left > 0) most_ctas = min(most_ctas, left * ctas_per_sm(NT));
+    }
+  }
+  const int total = s.total, ctas = min(most_ctas, (total + kMinTiles - 1) / kMinTiles);
   const bool idle = static_cast<int>(blockIdx.x) >= ctas;
   int x0 = idle ? 0 : stretch_begin(total, ctas, blockIdx.x), x1 = idle ? 0 : stretch_begin(total, ctas, blockIdx.x + 1);
   if constexpr (FORMS) {
     // A row tile each, where that takes no CTA much longer than its stretch of
     // the line would with the joins that come with it.
-    if (own && entries * ca.kv_heads <= static_cast<int>(gridDim.x) && s.longest <= (total + ctas - 1) / ctas + kCutCost) {
+    if (own && entries * ca.kv_heads <= most_ctas && s.longest <= (total + ctas - 1) / ctas + kCutCost) {
       const int e = min(static_cast<int>(blockIdx.x) / ca.kv_heads, entries - 1), count = s.prefix[e + 1] - s.prefix[e];
       x0 = s.prefix[e] * ca.kv_heads + (static_cast<int>(blockIdx.x) - e * ca.kv_heads) * count;
       x1 = static_cast<int>(blockIdx.x) < entries * ca.kv_heads ? x0 + count : x0;

@@ -59,11 +59,7 @@ constexpr int kStages = 2;                 // tiles of codes, in the same order
 constexpr int kInfo = 4;                   // key tiles whose scales are held (see the copies)
 constexpr int kUnitCost = 2;               // key tiles' worth of time that a unit takes besides its tiles; 2 x 2048 tokens, cut from the line: 1 122, 2 103, 3 103, 4 105 us
 constexpr int kMinTiles = 4;               // least length of a CTA's stretch (a join costs about as much as four tiles)
-// The prefix pass, in units of 0.1 us: what a piece takes besides its tiles, a
-// tile of one and of two row tiles; and the own pass before and after its tiles,
-// of which each of three CTAs on an SM reads one in 1 us.
-constexpr float kPrefixTime = 150.f, kOwnTime = 90.f;
-constexpr int kTileTime = 21, kPairTime = 21, kOwnKeys = 64;
+constexpr int kOwnKeys = 64;               // of a key tile of the own pass
 constexpr int kMinPiece = 2;               // key tiles of a piece in the prefix pass, at least
 constexpr int kMaxCtas = 160;
 constexpr int kMaxUnits = 16;              // whole units a CTA may be given (see the kernel)
@@ -535,24 +531,17 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
       if (en.row0 == 0) own -= en.sequences * (en.end / kOwnKeys);
     }
 #pragma unroll 1
-    for (int b = tid; b < p.f.sequences; b += kThreads) own += (a.seq_lens[b] + kOwnKeys - 1) / kOwnKeys;
+    for (int b = tid; b < p.f.sequences; b += kThreads) own += (a.seq_lens[b] + kOwnKeys - 1) / kOwnKeys + kOwnUnit;
     own = __reduce_add_sync(0xffffffffu, own);
     if (lane == 0) atomicAdd(&s.sums[3], own);
     __syncthreads();
     const int tiles = s.sums[0], units = s.sums[1], longest = s.sums[2];
     // How many CTAs: the other SMs are the own pass's meanwhile.  Each thread
-    // works out what a number of them would take, in units of 0.1 us.
+    // works out what a number of them would take.
     int* best = s.units;                   // not in use here
     if (tid == 0) *best = 0x7fffffff;
     __syncthreads();
-    if (tid < static_cast<int>(gridDim.x)) {
-      const int sms = gridDim.x, n = tid + 1, each = static_cast<int64_t>(a.max_q_len) * group > kTileRows ? kPairTime : kTileTime;
-      const float here = kPrefixTime + static_cast<float>(each * ((tiles + n - 1) / n));
-      const float work = static_cast<float>(max(0, s.sums[3])) * ca.kv_heads * p.f.own_row_tiles * (10.f / 3.f);
-      const float rest = work - fmaxf(0.f, here - kOwnTime) * static_cast<float>(sms - n);
-      const float time = rest <= 0.f ? here : here + kOwnTime + rest / static_cast<float>(sms);
-      atomicMin(best, static_cast<int>(fminf(time, 8.0e6f)) << 8 | n);
-    }
+    if (tid < static_cast<int>(gridDim.x)) atomicMin(best, p.f.choice(tid + 1, tiles, max(0, s.sums[3]) * ca.kv_heads * p.f.own_row_tiles));
     __syncthreads();
     most_ctas = *best & 255;
     // Pieces of a length for which there is about one for each CTA: n units of
