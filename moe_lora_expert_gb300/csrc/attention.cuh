@@ -127,39 +127,39 @@ struct RopeAxes {
 struct OneAxis {};
 // The axis of pair i.
 __device__ __forceinline__ uint32_t axis_of(const RopeAxes& axes, int i) { return axes.of_pair[i / 16] >> (2 * (i % 16)) & 3; }
-// A token's position on the axis of pair i, and whether its positions on all
-// axes are in the table.
-__device__ __forceinline__ int axis_position(const RopeAxes& axes, const int32_t* positions, int64_t t, int num_positions, int i, bool& good) {
-  const uint32_t mine = axis_of(axes, i);
-  int pos = 0;
-  good = true;
+// Whether token t's positions on all axes are in the table.
+__device__ __forceinline__ bool in_table(const RopeAxes& axes, const int32_t* positions, int64_t t, int num_positions) {
+  bool good = true;
 #pragma unroll
-  for (uint32_t a = 0; a < kMaxAxes; ++a) {
-    if (a >= static_cast<uint32_t>(axes.count)) break;
-    const int p = positions[a * axes.stride + t];
-    good &= p >= 0 && p < num_positions;
-    pos = a == mine ? p : pos;
+  for (int a = 0; a < kMaxAxes; ++a) {
+    if (a >= axes.count) break;
+    good &= static_cast<uint32_t>(positions[a * axes.stride + t]) < static_cast<uint32_t>(num_positions);
   }
-  return pos;
+  return good;
 }
 // The most tokens that ``threads`` consecutive items lie in.
 __host__ __device__ __forceinline__ uint32_t axes_tokens(uint32_t threads, uint32_t per_token) { return (threads - 2) / per_token + 2; }
 // The angles of tokens [t0, t0 + tokens) as rows of cosines and sines, each
-// pair's from its own axis's row of the table, by all threads of a CTA; good[j]:
-// whether token t0 + j has all its positions in the table.  Each angle is looked
-// up once and not by every head, and a row then serves as one of the table
-// does: 4096 tokens of 36 heads of 128 in this way XX us, each thread by itself
-// 24 (a run of pairs for each axis) and 33 (axes in turns).
+// pair's from its own axis's row of the table, by all threads of a CTA; good[j]
+// (if asked for): whether token t0 + j has all its positions in the table.  Each
+// angle is looked up once and not by every head, a thread's all of one column
+// and so of one axis; a row then serves as one of the table does.
 __device__ __forceinline__ void gather_angles(float* rows, int* good, const RopeAxes& axes, const int32_t* positions, const float* cos_sin,
                                               int64_t t0, int tokens, int R, int num_positions) {
-  const int threads = blockDim.x * blockDim.y * blockDim.z;
-  for (int j = threadIdx.x + blockDim.x * (threadIdx.y + blockDim.y * threadIdx.z); j < tokens * R; j += threads) {
-    const int token = j / R, col = j - token * R;
-    bool all;
-    const int pos = axis_position(axes, positions, t0 + token, num_positions, col < R / 2 ? col : col - R / 2, all);
-    rows[j] = all ? cos_sin[static_cast<int64_t>(pos) * R + col] : 0.f;
-    if (col == 0 && good != nullptr) good[token] = all;
+  const int threads = blockDim.x * blockDim.y * blockDim.z, tid = threadIdx.x + blockDim.x * (threadIdx.y + blockDim.y * threadIdx.z);
+  const int at_once = threads / R;                      // tokens; 0: a thread has several columns
+  const int first = at_once > 0 ? tid / R : 0, step = at_once > 0 ? at_once : 1;
+  for (int col = tid - first * R; col < R && first < step; col += threads) {
+    const int32_t* pos = positions + axis_of(axes, col < R / 2 ? col : col - R / 2) * axes.stride + t0;
+    const float* column = cos_sin + col;
+#pragma unroll 4
+    for (int j = first; j < tokens; j += step) {
+      const int p = pos[j];
+      rows[j * R + col] = static_cast<uint32_t>(p) < static_cast<uint32_t>(num_positions) ? column[static_cast<int64_t>(p) * R] : 0.f;
+    }
   }
+  if (good != nullptr)
+    for (int j = tid; j < tokens; j += threads) good[j] = in_table(axes, positions, t0 + j, num_positions);
 }
 
 // (u, w) -> (u cos - w sin, w cos + u sin), in float32.  ROUNDED: each product

@@ -88,9 +88,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) kv_append_kernel(KvAppe
       int pos = kSkipped;
       if (p.cu_q == nullptr || static_cast<int>(t) < p.cu_q[p.B]) {          // else a row of no sequence
         if constexpr (kAxes) {
-          bool good;
-          axis_position(axes, p.positions, t, p.num_positions, 0, good);
-          pos = good ? 0 : kUnturned;
+          pos = in_table(axes, p.positions, t, p.num_positions) ? 0 : kUnturned;
         } else if (p.positions != nullptr) {
           pos = p.positions[t];
         } else {

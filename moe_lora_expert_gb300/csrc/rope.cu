@@ -36,69 +36,40 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, uint32_t p
 }
 
 // The same with an axis for each pair: a token has a position on each axis.
-// Finding the angles takes more then: a CTA has whole tokens, gathers their
-// angles together, and nothing is divided: threadIdx is (stretch, head, token).
-constexpr int kAxesThreads = 256;          // of a CTA, about
-constexpr int kAxesHeads = 1;              // of a thread
-constexpr int kAxesMost = 512, kAxesCtas = 3;
+// Finding the angles takes more then, and the CTA gathers those of its tokens:
+// 4096 tokens of 36 heads of 128 take 19.9 us, whatever the axes' order (by each
+// thread for itself 24 with a run of pairs for each axis, 33 with axes in turns;
+// by each warp for its own tokens 21.9 and 23.2).  Bytes would take 11.5; half
+// of the warp slots are empty for want of registers (63 a thread, 40 in the
+// kernel above), and a warp waits for positions, angles and the others.  128
+// threads: 256 20.2, 512 21.1 us; one head a thread 25.3, four 26.7.
+constexpr int kAxesThreads = 128;
+constexpr int kAxesHeads = 2;              // of a thread
+constexpr int kAxesCtas = 8;
 template <typename T, int V>
-__global__ void __launch_bounds__(kAxesMost, kAxesCtas) rope_axes_kernel(RopeParams p, const __grid_constant__ RopeAxes axes) {
+__global__ void __launch_bounds__(kAxesThreads, kAxesCtas) rope_axes_kernel(RopeParams p, const __grid_constant__ RopeAxes axes, uint32_t per_token) {
   extern __shared__ __align__(16) float angles[];      // [tokens][R], then whether each token has any
   pdl_launch_dependents();
   pdl_wait();
-  const int t0 = blockIdx.x * blockDim.z, tokens = min(static_cast<int>(blockDim.z), p.N - t0), z = threadIdx.z;
-  const int c = threadIdx.x, heads = z < tokens ? p.q.heads + p.k.heads : 0, step = gridDim.y * blockDim.y;
-  const int h0 = blockIdx.y * blockDim.y + threadIdx.y;
-  const int64_t t = t0 + z;
-  int* good = reinterpret_cast<int*>(angles + blockDim.z * p.R);
-  Pack<T, V> ra[kAxesHeads], rb[kAxesHeads];
-  const Stretch<V> s(c, p.R, p.interleaved);
-#pragma unroll
-  for (int u = 0; u < kAxesHeads; ++u) {
-    const int h = h0 + u * step;
-    if (h >= heads) break;
-    const T* in = h < p.q.heads ? static_cast<const T*>(p.q.in) + t * p.q.in_token + h * p.q.in_head
-                                : static_cast<const T*>(p.k.in) + t * p.k.in_token + (h - p.q.heads) * p.k.in_head;
-    ra[u] = *reinterpret_cast<const Pack<T, V>*>(in + s.a);
-    rb[u] = *reinterpret_cast<const Pack<T, V>*>(in + s.b);
-  }
+  const uint32_t item0 = blockIdx.x * kAxesThreads, t0 = item0 / per_token;
+  const RotationItem<T, V, kAxesHeads> x(p.q, p.k, item0 + threadIdx.x, per_token, p.N, p.D, p.R, p.interleaved);
+  const int tokens = static_cast<int>(min((item0 + kAxesThreads - 1) / per_token + 1, static_cast<uint32_t>(p.N)) - t0);
+  int* good = reinterpret_cast<int*>(angles + axes_tokens(kAxesThreads, per_token) * p.R);
   gather_angles(angles, good, axes, p.positions, p.cos_sin, t0, tokens, p.R, p.num_positions);
   __syncthreads();
-  if (h0 >= heads) return;
-  const bool turn = s.turned && good[z];
-  if (!good[z]) set_status(p.status, MOE_ERR_BAD_POSITION);
-  float cs[V], sn[V];
-  if (turn) {
-    load_cos_sin<V>(angles + z * p.R, c, p.R, cs, sn);
-    if (p.inverse) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) sn[i] = -sn[i];
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < kAxesHeads; ++u) {
-    const int h = h0 + u * step;
-    if (h >= heads) break;
-    float a[V], b[V];
-    to_f32s<T, V>(ra[u], a);
-    to_f32s<T, V>(rb[u], b);
-    if (turn) rotate<V, false>(a, b, cs, sn, p.interleaved);
-    T* out = h < p.q.heads ? static_cast<T*>(p.q.out) + t * p.q.out_token + h * p.q.out_head
-                           : static_cast<T*>(p.k.out) + t * p.k.out_token + (h - p.q.heads) * p.k.out_head;
-    store_f32<T, V>(out + s.a, a);
-    store_f32<T, V>(out + s.b, b);
-  }
+  if (!x.live) return;
+  const int j = static_cast<int>(x.t - t0);
+  if (!good[j]) set_status(p.status, MOE_ERR_BAD_POSITION);
+  x.turn_by(p.q, p.k, good[j] ? angles + j * p.R : nullptr, p.R, p.interleaved, p.inverse);
 }
 
 template <typename T, int V>
 cudaError_t launch_axes(const RopeParams& p, const RopeAxes& axes, cudaStream_t s) {
-  const uint32_t across = p.D / (2 * V);                                       // 512 at most
-  const uint32_t heads = (p.q.heads + p.k.heads + kAxesHeads - 1) / kAxesHeads;
-  const uint32_t most = kAxesMost / across, ctas = (heads + most - 1) / most, rows = (heads + ctas - 1) / ctas;
-  uint32_t tokens = kAxesThreads / (across * rows);
-  tokens = tokens < 1 ? 1 : tokens > 64 ? 64 : tokens;
-  const dim3 grid((static_cast<uint32_t>(p.N) + tokens - 1) / tokens, ctas);
-  return launch_pdl(rope_axes_kernel<T, V>, grid, dim3(across, rows, tokens), static_cast<size_t>(tokens) * (p.R + 1) * 4, s, p, axes);
+  const uint32_t per_token = rotation_items<V>(p.q.heads + p.k.heads, kAxesHeads, p.D);
+  const int64_t ctas = (static_cast<int64_t>(p.N) * per_token + kAxesThreads - 1) / kAxesThreads;
+  // at most 17 KB: a token has R / 2V stretches at least, or one
+  const size_t bytes = static_cast<size_t>(axes_tokens(kAxesThreads, per_token)) * (p.R + 1) * 4;
+  return launch_pdl(rope_axes_kernel<T, V>, dim3(static_cast<unsigned>(ctas)), dim3(kAxesThreads), bytes, s, p, axes, per_token);
 }
 
 template <typename T, int V>
