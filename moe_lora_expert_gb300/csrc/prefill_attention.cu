@@ -516,19 +516,20 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   const int from = min(tid * per, entries), to = min(from + per, entries);
   int mine = 0;
   [[maybe_unused]] int chunk = 0, most_ctas = gridDim.x;
+  [[maybe_unused]] Entry<FORM> held;       // the prefix pass: a thread's entry, if it has one at most
   if constexpr (kIsPrefix) {
     if (tid < 4) s.sums[tid] = 0;
     __syncthreads();
     int own = 0;                           // key tiles of the own pass, a head's
-    Entry<FORM> en;
+    held.count = 0;
 #pragma unroll 1
     for (int e = from; e < to; ++e) {
-      en.load(p, e, group);
-      if (en.count == 0) continue;
-      atomicAdd(&s.sums[0], en.count * ca.kv_heads);
+      held.load(p, e, group);
+      if (held.count == 0) continue;
+      atomicAdd(&s.sums[0], held.count * ca.kv_heads);
       atomicAdd(&s.sums[1], ca.kv_heads);
-      atomicMax(&s.sums[2], en.count);
-      if (en.row0 == 0) own -= en.sequences * (en.end / kOwnKeys);
+      atomicMax(&s.sums[2], held.count);
+      if (held.row0 == 0) own -= held.sequences * (held.end / kOwnKeys);
     }
 #pragma unroll 1
     for (int b = tid; b < p.f.sequences; b += kThreads) own += (a.seq_lens[b] + kOwnKeys - 1) / kOwnKeys + kOwnUnit;
@@ -554,7 +555,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
 #pragma unroll 1
   for (int e = from; e < to; ++e) {
     Entry<FORM> en;
-    en.load(p, e, group);
+    if (kIsPrefix && per == 1) en = held; else en.load(p, e, group);
     if (en.count > 0) mine += kIsPrefix ? pieces_of(en.count, chunk) : en.count + kUnitCost;
   }
   int incl = mine;
@@ -633,7 +634,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
 #pragma unroll 1
     for (int e = from; e < to; ++e) {
       Entry<FORM> en;
-      en.load(p, e, group);
+      if (kIsPrefix && per == 1) en = held; else en.load(p, e, group);
       const int places = en.count == 0 ? 0 : kIsPrefix ? pieces_of(en.count, chunk) : en.count + kUnitCost;
       if (x0 < (before + places) * ca.kv_heads) {
         s.first_entry = e;
