@@ -699,9 +699,9 @@ int moe_paged_attention_sinks(const moe_paged_attention_args_t* args, int sinks,
  *   max_tokens: at least the most new tokens of one group; it sizes the launch.
  *   partial: device scratch of the call, moe_shared_prefix_partial_size bytes,
  *     32-byte aligned, of any contents.
- * Sequences of many rows (new tokens times query heads of a key head, by
- * max_q_len) fill the tiles of a product by themselves: for more than 128 the
- * call does as moe_paged_attention does.
+ * Where sharing would not pay, by the sizes that the host has (max_q_len,
+ * max_tokens, max_seq_len), the call does as moe_paged_attention does: few rows
+ * in a group, many in each sequence, short contexts.
  * ------------------------------------------------------------------------- */
 typedef struct {
   uint32_t struct_size;           /* sizeof(moe_shared_prefix_t) */

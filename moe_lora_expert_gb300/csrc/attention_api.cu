@@ -33,9 +33,21 @@ inline int element_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 // one long context (on 8 key heads 77%: 109 / 62).
 bool few_rows(int64_t rows, int64_t pairs) { return rows <= 32 || (rows <= 96 && pairs <= 16); }
 
-// The prefix of a group is read once for all its sequences where these have at
-// most so many rows each, and all of a group together at least so many.
-constexpr int64_t kSharedRows = 128, kPrefixRows = 17;
+// Whether a prefix is read once for a group, by the rows that a sequence and
+// the largest group have for a key head and the bound on the lengths.  Shared /
+// by each sequence, in us (4 key heads of 128, 8 query heads each, about 300 own
+// keys a sequence):
+//   group of 16 rows (2 sequences): 4096 shared keys 17.9 / 19.1, 65536 46 / 39; 16 such groups 61 / 33, 544 / 253;
+//   32 rows: 256 keys 17.8 / 14.4, 1024 18.1 / 16.4, 4096 18.9 / 20.9, 65536 47 / 57; 8 such groups of 4096 35 / 32, 65536 222 / 256;
+//   64 rows: 1024 17.7 / 16.8, 16384 26.7 / 34.6, 65536 49 / 92;
+//   16 sequences of 32 rows: 256 21.9 / 22.2, 4096 30 / 41, 65536 92 / 354;
+//     of 64: 1024 36 / 33, 4096 43 / 53, 65536 138 / 412;  of 128: 1024 65 / 34, 16384 125 / 124, 65536 281 / 413;
+//     of 256: 4096 171 / 59, 16384 305 / 140.
+// Sequences of many rows fill the products' tiles by themselves, and their own
+// keys are then in the kernel that is made for few.
+bool shares(int64_t rows, int64_t group_rows, int64_t longest) {
+  return group_rows >= 32 && rows <= 128 && longest >= 2048 && (rows <= 32 || rows * rows <= longest);
+}
 // How many pieces the prefix pass may leave for a row: with one group whose
 // rows fill 256-row units, twice as many as give each SM one of them.
 int most_pieces(int N, int Hq) {
@@ -311,8 +323,9 @@ int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_sh
   AttentionParams prefix = p;
   prefix.B = x->groups;
   prefix.max_q_len = f.max_tokens;
-  if (rows_of(p) > kSharedRows || rows_of(prefix) < kPrefixRows) return attend(p, nullptr, a->dtype, on);
+  if (!shares(rows_of(p), rows_of(prefix), p.max_seq_len)) return attend(p, nullptr, a->dtype, on);
   int error = moe::launch_prefill_attention(prefix, &f, a->dtype, on);
+  if (error == MOE_ERR_UNSUPPORTED) return attend(p, nullptr, a->dtype, on);    // too many groups for one line
   if (error != MOE_OK) return error;
   f.pass = moe::kOwnPass;
   error = moe::launch_decode_attention(p, &f, a->dtype, on);

@@ -158,6 +158,9 @@ def test_nan_in_many_sinks():
 
 # ------------------------------------------------------------- shared prefixes
 
+LONG = 1 << 20   # a bound on the lengths that makes sharing worth while, whatever the lengths
+
+
 class Shared(Batch):
     """Sequences whose first tokens are those of their group's first one:
     ``held`` own tokens before the new ones, after the group's lens (a sequence
@@ -219,12 +222,12 @@ def test_shared(dtype, new, held, seqs, shared, strays, Hkv, Hq, P, D, bound):
     decode = all(n == 1 for n in new)
     most = max(sum(new[a:b]) for a, b in zip(seqs, seqs[1:])) if bound else N
     # sequences of many rows, and groups of few, are not worth the sharing: then each table row is looked at
-    alone = max(new) * (Hq // Hkv) > 128 or most * (Hq // Hkv) < 17
+    alone = max(new) * (Hq // Hkv) > 128 or most * (Hq // Hkv) < 32
     del_me = torch.full((N * Hq * (4 * D + 8) // 4,), float("nan"), device="cuda")       # what the partial sums' memory may hold
     del del_me
     out, lse = batch.cache.attend(tensor(q, dtype, (1, 8) if bound else None), tensor(batch.table, "int32") if alone else batch.dev["block_table"],
                                   batch.dev["seq_lens"], cu_q=None if decode else batch.cu_dev, max_q_len=max(new), return_lse=True,
-                                  max_shared_q=most if bound else None, **batch.groups)
+                                  max_shared_q=most if bound else None, max_seq_len=LONG, **batch.groups)
     compare(out, lse, batch, q, dtype)
     assert batch.cache.device_status() == m.MOE_OK
 
@@ -235,9 +238,9 @@ def test_shared_by_all_and_by_none():
     torch = torch_mod()
     rng = np.random.default_rng(60)
     batch = Shared(rng, [1] * 6, [1, 0, 30, 4, 100, 2], [0, 6], [90], 2, 16, 64, std=0.5)
-    q = rounded(rng, (6, 8, 64), "bfloat16")
+    q = rounded(rng, (6, 16, 64), "bfloat16")
     qt, lens = tensor(q, "bfloat16"), batch.groups["shared_lens"]
-    out, lse = batch.cache.attend(qt, **batch.dev, shared_lens=lens, return_lse=True)
+    out, lse = batch.cache.attend(qt, **batch.dev, shared_lens=lens, return_lse=True, max_seq_len=LONG)
     compare(out, lse, batch, q, "bfloat16")
     table = tensor(batch.table, "int32")
     none = dict(shared_lens=lens[:0], shared_seqs=batch.groups["shared_seqs"][:1])
@@ -257,9 +260,9 @@ def test_shared_empty_slots():
     batch = Shared(rng, [1] * 7, [1, 0, 30, 4, 100, 2, 5], [0, 4, 7], [90, 33], 2, 16, 64, std=0.5)
     for b in (0, 2, 6):
         batch.lens[b] = 0
-    q = rounded(rng, (7, 8, 64), "bfloat16")
+    q = rounded(rng, (7, 16, 64), "bfloat16")
     out, lse = batch.cache.attend(tensor(q, "bfloat16"), batch.dev["block_table"], tensor(np.array(batch.lens, np.int32), "int32"), return_lse=True,
-                                  **batch.groups)
+                                  max_seq_len=LONG, **batch.groups)
     compare(out, lse, batch, q, "bfloat16")
     assert (f64(out)[[0, 2, 6]] == 0).all() and batch.cache.device_status() == m.MOE_OK
 
@@ -270,9 +273,9 @@ def test_shared_past_the_bound(most):
     keys themselves."""
     rng = np.random.default_rng(62)
     batch = Shared(rng, [3, 2, 4, 3], [1, 0, 30, 4], [0, 4], [90], 2, 16, 64, std=0.5)
-    q = rounded(rng, (12, 8, 64), "bfloat16")
+    q = rounded(rng, (12, 16, 64), "bfloat16")
     out, lse = batch.cache.attend(tensor(q, "bfloat16"), tensor(batch.table, "int32"), batch.dev["seq_lens"], cu_q=batch.cu_dev, max_q_len=4,
-                                  return_lse=True, max_shared_q=most, **batch.groups)
+                                  return_lse=True, max_shared_q=most, max_seq_len=LONG, **batch.groups)
     compare(out, lse, batch, q, "bfloat16")
 
 
@@ -283,10 +286,11 @@ def test_shared_bad_pages_and_groups():
     torch = torch_mod()
     rng = np.random.default_rng(63)
     batch = Shared(rng, [1] * 6, [1, 0, 30, 4, 100, 2], [0, 6], [90], 2, 16, 64, std=0.5)
-    q = rounded(rng, (6, 8, 64), "bfloat16")
+    q = rounded(rng, (6, 16, 64), "bfloat16")
     table = batch.blind.copy()
     table[0, 2] = batch.pages
-    out, lse = batch.cache.attend(tensor(q, "bfloat16"), tensor(table, "int32"), batch.dev["seq_lens"], return_lse=True, **batch.groups)
+    out, lse = batch.cache.attend(tensor(q, "bfloat16"), tensor(table, "int32"), batch.dev["seq_lens"], return_lse=True, max_seq_len=LONG,
+                                  **batch.groups)
     assert batch.cache.device_status() == m.MOE_ERR_BAD_PAGE
     left = batch.table.copy()
     left[:, 2] = batch.pages                           # its keys are left out for all
@@ -295,15 +299,15 @@ def test_shared_bad_pages_and_groups():
     want = batch.cache.attend(qt, table, batch.dev["seq_lens"])
     for seqs, lens in (([0, -3], [90]), ([9, 12], [90]), ([0, 6], [1 << 30]), ([-5, -1, 0], [3, 3]), ([7, 0, 6], [3, 0])):
         got = batch.cache.attend(qt, table, batch.dev["seq_lens"], shared_seqs=tensor(np.array(seqs, np.int32), "int32"),
-                                 shared_lens=tensor(np.array(lens, np.int32), "int32"))
+                                 shared_lens=tensor(np.array(lens, np.int32), "int32"), max_seq_len=LONG)
         assert (got.float() - want.float()).abs().max() <= 2.0 ** -6 * want.abs().max()
         batch.cache.device_status()
 
 
-@pytest.mark.parametrize("B,Hkv,Hq,D,shared", [(40, 1, 8, 128, 20001), (6, 2, 8, 64, 30000), (17, 4, 32, 128, 5000)])
+@pytest.mark.parametrize("B,Hkv,Hq,D,shared", [(40, 1, 8, 128, 20001), (8, 2, 8, 64, 30000), (17, 4, 32, 128, 5000)])
 def test_shared_long_prefixes(B, Hkv, Hq, D, shared):
-    """Prefixes that many CTAs have parts of, by both kernels, twice with the
-    same bits, and against the same call without sharing."""
+    """Prefixes that many CTAs have parts of, twice with the same bits, and
+    against the same call without sharing."""
     torch = torch_mod()
     gen = torch.Generator(device="cuda").manual_seed(64)
     P, own = 64, 130
@@ -347,13 +351,13 @@ def test_shared_rows_one_part_dominates():
     for big in (0, 1):
         rng = np.random.default_rng(65 + big)
         batch = Shared(rng, [1] * 5, [1, 0, 30, 4, 100], [0, 5], [90], 1, 16, 64, std=0.5)
-        q = rounded(rng, (5, 4, 64), "bfloat16")
+        q = rounded(rng, (5, 8, 64), "bfloat16")
         batch.codes[0][...] = np.where(batch.codes[0] == 0x7F, 0x7F, ao.e4m3_encode(np.full(64, 0.25)))
         j = 40 if big == 0 else 90                     # a key of the prefix, or each sequence's first own one
         for b in range(5):
             batch.codes[0][batch.table[b, j // 16], :, j % 16] = ao.e4m3_encode(np.sign(q[b, 0]) * 448)
         batch.cache.k.copy_(tensor(batch.codes[0], torch.uint8))
-        out, lse = batch.cache.attend(tensor(q, "bfloat16"), **batch.dev, scale=4.0, return_lse=True, **batch.groups)
+        out, lse = batch.cache.attend(tensor(q, "bfloat16"), **batch.dev, scale=4.0, return_lse=True, max_seq_len=LONG, **batch.groups)
         compare(out, lse, batch, q, "bfloat16", scale=4.0)
 
 
@@ -366,12 +370,12 @@ def test_forms_in_graphs():
         rng = np.random.default_rng(seed)
         half = B // 2
         a = Shared(rng, [1] * B, [5 + b % 7 for b in range(B)], [0, half, B], [90, 200], 2, 16, 64, std=0.5)
-        q = tensor(rounded(rng, (B, 8, 64), "bfloat16"), "bfloat16")
+        q = tensor(rounded(rng, (B, 16, 64), "bfloat16"), "bfloat16")
         table, lens = tensor(a.table, "int32"), a.dev["seq_lens"]
         n, seqs = a.groups["shared_lens"], a.groups["shared_seqs"]
 
         def call(a=a, q=q, table=table, lens=lens, n=n, seqs=seqs):
-            return [*a.cache.attend(q, table, lens, return_lse=True, shared_lens=n, shared_seqs=seqs),
+            return [*a.cache.attend(q, table, lens, return_lse=True, shared_lens=n, shared_seqs=seqs, max_seq_len=LONG),
                     *a.cache.attend(q, table, lens, return_lse=True, window=20, sinks=9)]
         call()
         graph = torch.cuda.CUDAGraph()
@@ -401,6 +405,7 @@ def test_forms_on_a_given_stream():
     rng = np.random.default_rng(72)
     batch = Shared(rng, [1] * 12, [5] * 12, [0, 12], [400], 2, 16, 64, std=0.5)
     q = torch.randn((12, 8, 64), device="cuda").to(torch.bfloat16)
+    batch.groups["max_seq_len"] = LONG
     want = batch.cache.attend(q, **batch.dev, **batch.groups)
     want_sinks = batch.cache.attend(q, tensor(batch.table, "int32"), batch.dev["seq_lens"], window=30, sinks=4)
     side = torch.cuda.Stream()
@@ -410,7 +415,7 @@ def test_forms_on_a_given_stream():
     with torch.cuda.stream(side):
         torch.cuda._sleep(50_000_000)
     table, lens = tensor(batch.table, "int32"), batch.groups["shared_lens"].clone()
-    out = batch.cache.attend(q, table, batch.dev["seq_lens"], shared_lens=lens, stream=side)
+    out = batch.cache.attend(q, table, batch.dev["seq_lens"], shared_lens=lens, stream=side, max_seq_len=LONG)
     sinks = batch.cache.attend(q, table, batch.dev["seq_lens"], window=30, sinks=4, stream=side)
     held = (table.data_ptr(), lens.data_ptr())
     del table, lens
@@ -420,17 +425,86 @@ def test_forms_on_a_given_stream():
     assert torch.equal(out, want) and torch.equal(sinks, want_sinks)
 
 
-@pytest.mark.parametrize("form", ["sinks", "shared few", "shared many"])
+@pytest.mark.parametrize("form", ["sinks", "shared", "shared many"])
 def test_forms_whose_wait_runs_out(form):
     """No key tile comes: the status says so, and the next call is right."""
     rng = np.random.default_rng(73)
-    B = 40 if form == "shared many" else 3
+    B = 40 if form == "shared many" else 8
     batch = Shared(rng, [1] * B, [5] * B, [0, B], [400], 2, 16, 64, std=0.5)
     q = rounded(rng, (B, 8, 64), "bfloat16")
-    kw = dict(window=30, sinks=4) if form == "sinks" else batch.groups
+    kw = dict(window=30, sinks=4) if form == "sinks" else {**batch.groups, "max_seq_len": LONG}
     args = dict(block_table=tensor(batch.table, "int32"), seq_lens=batch.dev["seq_lens"], **kw)
     batch.cache.attend(tensor(q, "bfloat16"), **args, wait_timeout_ms=20, debug_flags=m.MOE_DEBUG_STALL_ATTENTION)
     assert batch.cache.device_status() == m.MOE_ERR_DEVICE_TIMEOUT
     out, lse = batch.cache.attend(tensor(q, "bfloat16"), **args, return_lse=True)
     assert batch.cache.device_status() == m.MOE_OK
     compare(out, lse, batch, q, "bfloat16", **(kw if form == "sinks" else {}))
+
+
+@pytest.mark.parametrize("where", ["key", "value", "own key", "own value", "query"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 2, 64), (40, 1, 128)])
+def test_shared_nan(where, Hq, Hkv, D):
+    """NaN codes in the prefix's last, partly filled tile and in a sequence's
+    own keys, and a NaN query: what sees them has NaN, in the columns it should."""
+    torch = torch_mod()
+    rng = np.random.default_rng(75)
+    batch = Shared(rng, [1] * 6, [1, 0, 30, 4, 100, 2], [0, 6], [150], Hkv, 16, D, std=0.5)
+    q = rounded(rng, (6, Hq, D), "bfloat16")
+    codes = batch.codes[0 if "key" in where else 1]
+    if where == "query":
+        q[3, 1, 5] = np.nan
+    elif "own" in where:
+        codes[batch.table[4, 170 // 16], 0, 170 % 16, 7] = 0x7F      # one of sequence 4's own
+    else:
+        for b in range(6):                                          # one that all share, in its page's copies too
+            codes[batch.table[b, 145 // 16], 0, 145 % 16, 7] = 0xFF
+    for t, c in zip((batch.cache.k, batch.cache.v), batch.codes):
+        t.copy_(tensor(c, torch.uint8))
+    out, lse = batch.cache.attend(tensor(q, "bfloat16"), **batch.dev, return_lse=True, max_seq_len=LONG, **batch.groups)
+    with np.errstate(invalid="ignore"):
+        ref, lref = ao.attend(q, *batch.codes, *batch.scales, batch.table, batch.lens, batch.cu, D ** -0.5)[:2]
+    assert np.isnan(ref).any()
+    np.testing.assert_array_equal(np.isnan(f64(out)), np.isnan(ref))
+    np.testing.assert_array_equal(np.isnan(f64(lse)), np.isnan(lref))
+    good = ~np.isnan(ref)
+    assert (np.abs(f64(out) - ref)[good] < 0.05 * np.nanmax(np.abs(ref), initial=0.0)).all()
+
+
+def test_forms_of_nothing():
+    """No tokens, no sequences."""
+    torch = torch_mod()
+    rng = np.random.default_rng(76)
+    batch = Batch(rng, [1], [20], 2, 16, 64)
+    q = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    none = torch.empty((0,), dtype=torch.int32, device="cuda")
+    table = torch.empty((0, 4), dtype=torch.int32, device="cuda")
+    n = torch.ones((1,), dtype=torch.int32, device="cuda")
+    for kw in (dict(window=5, sinks=3), dict(shared_lens=n), dict(shared_lens=n, shared_seqs=torch.zeros(2, dtype=torch.int32, device="cuda"))):
+        out, lse = batch.cache.attend(q, table, none, return_lse=True, **kw)
+        assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    assert batch.cache.device_status() == m.MOE_OK
+
+
+def test_shared_of_many_sequences_and_groups():
+    """More sequences than one launch of the own pass takes, in many groups."""
+    torch = torch_mod()
+    gen = torch.Generator(device="cuda").manual_seed(77)
+    B, P, Hkv, Hq, D, each = 600, 16, 1, 8, 64, 8
+    groups = B // each
+    shared, own, width = 96, 40, 9
+    shape = (groups * shared // P + B * 3, Hkv, P, D)
+    k, v = ((torch.randn(shape, generator=gen, device="cuda") * 40).to(torch.float8_e4m3fn).view(torch.uint8) for _ in range(2))
+    cache = m.PagedKVCache(k, v, *[torch.full(shape[:2], 2.0 ** -6, device="cuda") for _ in range(2)])
+    order = torch.randperm(shape[0], generator=gen, device="cuda").to(torch.int32)
+    first = order[:groups * 6].view(groups, 1, 6).expand(groups, each, 6).reshape(B, 6)
+    table = torch.cat([first, order[groups * 6:].view(B, 3)], dim=1).contiguous()
+    assert table.shape[1] == width
+    lens = shared + 1 + torch.randint(0, own, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    q = torch.randn((B, Hq, D), generator=gen, device="cuda").to(torch.bfloat16)
+    want, want_lse = cache.attend(q, table, lens, return_lse=True)
+    seqs = torch.arange(0, B + 1, each, dtype=torch.int32, device="cuda")
+    n = torch.full((groups,), shared, dtype=torch.int32, device="cuda")
+    got = [cache.attend(q, table, lens, return_lse=True, shared_lens=n, shared_seqs=seqs, max_seq_len=LONG, max_shared_q=most) for most in (None, each)]
+    for out, lse in got:
+        assert (out.float() - want.float()).abs().max() <= 0.02 * want.abs().max() and (lse - want_lse).abs().max() < 1e-3
+    assert cache.device_status() == m.MOE_OK
