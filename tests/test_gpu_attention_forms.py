@@ -5,6 +5,9 @@ Bounds as in test_gpu_attention (weights round to float16, scores are float32
 sums).  A joined row adds factors 2^(m - m') of the two parts, each off by 2^-22
 relative, which the 2^-17 of the probabilities' errors holds many times.
 """
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 
@@ -508,3 +511,57 @@ def test_shared_of_many_sequences_and_groups():
     for out, lse in got:
         assert (out.float() - want.float()).abs().max() <= 0.02 * want.abs().max() and (lse - want_lse).abs().max() < 1e-3
     assert cache.device_status() == m.MOE_OK
+
+
+def test_answers_to_one_prompt():
+    """Positions of several axes, a shared prompt, a window with lasting first
+    tokens and the routed MoE together, as the example serves them."""
+    torch = torch_mod()
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_layer.py")
+    spec = importlib.util.spec_from_file_location("decoder_layer_answers", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    worst, out, status = example.answers()
+    # two orders of summing the same keys, rounded to bf16 between layers' parts
+    assert worst < 2e-2 and status == [m.MOE_OK, m.MOE_OK] and torch.isfinite(out).all()
+
+
+def test_a_decode_step_in_a_graph():
+    """append with axes, attend with a shared prefix and attend with sinks in one
+    captured step, replayed as lengths and positions move on."""
+    torch = torch_mod()
+    rng = np.random.default_rng(80)
+    B, Hkv, Hq, P, D = 8, 2, 16, 16, 64
+    batch = Shared(rng, [1] * B, [20 + b for b in range(B)], [0, B], [96], Hkv, P, D, std=0.5)
+    table, lens, axes = tensor(batch.table, "int32"), batch.dev["seq_lens"], m.rope_axes([12, 10, 10], turns=True)
+    cos_sin, n = m.rope_table(400, D, device="cuda"), batch.groups["shared_lens"]
+    k, v = (tensor(rounded(rng, (B, Hkv, D), "bfloat16"), "bfloat16") for _ in range(2))
+    q = tensor(rounded(rng, (B, Hq, D), "bfloat16"), "bfloat16")
+    pos = tensor(np.stack([np.array(batch.lens) - 1] * 3).astype(np.int32), "int32")
+
+    def step():
+        turned = batch.cache.append(k, v, table, lens, q=q, cos_sin=cos_sin, positions=pos, axes=axes)
+        return (turned, batch.cache.attend(turned, table, lens, shared_lens=n, max_seq_len=LONG), batch.cache.attend(turned, table, lens, window=30, sinks=5),
+                batch.cache.attend(turned, table, lens))
+    parts = (batch.cache.k, batch.cache.v, batch.cache.k_scale, batch.cache.v_scale)
+    saved = [x.clone() for x in parts]
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for i in range(3):
+        want = None
+        for _ in range(2):                             # once eagerly, once replayed, from the same cache
+            for x, s in zip(parts, saved):
+                x.copy_(s)
+            if want is None:
+                want = [o.clone() for o in step()]
+            else:
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+        assert (want[1].float() - want[3].float()).abs().max() <= 2.0 ** -6 * want[3].abs().max()
+        saved = [x.clone() for x in parts]
+        lens.add_(1)
+        pos.add_(torch.tensor([[1], [2], [0]], dtype=torch.int32, device="cuda"))
+    assert batch.cache.device_status() == m.MOE_OK
