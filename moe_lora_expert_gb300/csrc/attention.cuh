@@ -348,7 +348,8 @@ struct AttentionForms {
   float2* refs;                 // [most_pieces + 1][rows]: reference and denominator
   int32_t* pieces;              // [groups]
 
-  // What both passes take, in us, if the prefix pass, with ``tiles`` key tiles of
+  // What both passes take, in us (as measured: a CTA's time before and after its
+  // tiles, and a tile's), if the prefix pass, with ``tiles`` key tiles of
   // its units, has n SMs, and the own pass, with ``own`` key tiles of its row
   // tiles, the others meanwhile (or all of them after it).  Both passes look for
   // the same best n: they have times of their own before and after their tiles,

@@ -35,6 +35,17 @@
 // 1, 6 and 12: 176, 176 and 179 us, 175 each without the fall; falling in any
 // tile under 2^0, to 2^8: 177, 204 and 206.)
 //
+// Sinks (the first keys stay visible in a window) are tiles before those of the
+// window; the pages between are not looked up.  One token with a window of 4096
+// and 4 sinks at the end of 262140 keys: 15.7 us, chain of latencies; 64
+// sequences in windows of 8192 with 64 sinks: 100.5 us, 5.4 TB/s, 80% of the copy
+// rate (98.1 without sinks).
+//
+// Sequences whose first keys the prefix pass takes (AttentionForms) begin after
+// them here and leave their sums for the join.  64 sequences of up to 1023 own
+// keys are 256 row tiles of 17 tiles at most: one for each CTA, since a cut costs
+// more than a tile of waiting (31 us cut evenly, 17 so).
+//
 // What bounds it: one pass over the cache's bytes.  64 sequences of up to
 // 32768 keys (8 query heads of 128 on each of 4 key heads) take 214 us, 6.3
 // TB/s, 92% of the copy rate; one token on 262140 keys 57 us (40 at the copy
@@ -224,7 +235,11 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     sinks = p.f.sinks;
   }
   pdl_launch_dependents();
-  if (!FORMS || !own || p.b0 > 0) pdl_wait();          // a further launch for one call uses the first one's workspace
+  if (!FORMS || !own || p.b0 > 0) {
+    pdl_wait();                            // a further launch for one call uses the first one's workspace
+  } else {
+    fence_proxy_async_global();            // what kernels before the prefix pass have written is read by copies here
+  }
 
   // The tiles before those of the window that hold keys which stay visible, and
   // the first key of tile i of an entry that begins at ``lo``.

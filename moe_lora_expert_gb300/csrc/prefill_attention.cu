@@ -37,6 +37,21 @@
 // that falls as well costs nothing on scores of standard deviation 1 and 3
 // (91 and 99 us), 1% on 6 and 2% on 12 there; 1, 1, 5 and 12% on chunks of 1000
 // with heads of 64.
+//
+// Sinks: the tiles of a sequence's first keys before those of its window.  2 x
+// 2048 tokens in a window of 1024 with 4 sinks: 88 us (82 without: a tile more
+// for each unit's 9.2), 587 TFLOP/s of what the mask leaves; ragged chunks of up
+// to 1000 on 8191 keys, window 3001, 131 sinks, heads of 64: 103 us (97).
+//
+// The prefix pass (AttentionForms) takes the new tokens of a group of sequences
+// as one unit's rows against the keys that all of them begin with.  All rows see
+// all keys, and a unit is cut in as many pieces as there are CTAs for it, whose
+// sums are joined by another kernel: joined here, 19 pieces of 256 rows in two
+// steps, 64 sequences on 8192 keys took 54 us instead of 30.  A piece takes 10 us
+// to its first scores (lengths, plan, pages, copies, conversion, each about one),
+// 2 us a key tile, and 5 to write its 128 KB.  Two softmax warps for 32 rows, or
+// both row tiles on the same rows of a small group, took longer: the schedulers
+// are busy half of the time and the conversion has no time to spare.
 #include <cuda.h>
 
 #include <type_traits>
@@ -1240,7 +1255,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         tc_fence_before_sync();
         continue;
       }
-
+      if constexpr (!kIsPrefix) {
       // A part of the unit: pieces of it are in consecutive CTAs.  Eight at a
       // time are joined by whoever finishes last among them, then those
       // results likewise.  Who finds all others done need not write its own.
@@ -1339,6 +1354,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
         step *= kJoin;
       }
       tc_fence_before_sync();
+      }
     }
   }
   __syncthreads();
