@@ -319,7 +319,8 @@ int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_sh
   f.pass = moe::kPrefixPass;
   f.own_row_tiles = static_cast<int>((rows_of(p) + 15) / 16);
   f.own_per_sm = rows_of(p) <= 8 ? 3 : 2;               // of decode_attention.cu
-  f.sms = moe::sm_count() < 255 ? moe::sm_count() : 255;
+  const int sms = moe::sm_count();
+  f.sms = sms < 255 ? sms : 255;
   AttentionParams prefix = p;
   prefix.B = x->groups;
   prefix.max_q_len = f.max_tokens;

@@ -64,6 +64,7 @@
 // weights and sums a key).
 #include <cuda.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "attention.cuh"
@@ -885,10 +886,16 @@ int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
 }  // namespace
 
+// Of the current device; looked up once for each (host threads may race to the same value).
 int sm_count() {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> counts[kMaxDevices] = {};
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  n = counts[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  counts[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
