@@ -565,3 +565,69 @@ def test_a_decode_step_in_a_graph():
         lens.add_(1)
         pos.add_(torch.tensor([[1], [2], [0]], dtype=torch.int32, device="cuda"))
     assert batch.cache.device_status() == m.MOE_OK
+
+
+@pytest.mark.parametrize("dtype,scale", [("bfloat16", -0.2), ("float16", -0.2), ("float16", 0.2)])
+@pytest.mark.parametrize("form", ["few", "many", "sinks few", "sinks many"])
+def test_forms_with_queries_of_any_strides(dtype, scale, form):
+    """Negative scales; queries that are one for all heads or tokens give the
+    bits of a copy of them, and the copy's are right."""
+    torch = torch_mod()
+    rng = np.random.default_rng(81)
+    B, Hq, Hkv = (40 if "many" in form else 8), 16, 2
+    new = [1] * B if "sinks" not in form or "few" in form else [5] * B
+    batch = Shared(rng, new, [b % 7 for b in range(B)], [0, B], [140], Hkv, 16, 80, std=0.5)
+    N = sum(new)
+    kw = dict(block_table=tensor(batch.table, "int32"), seq_lens=batch.dev["seq_lens"], cu_q=batch.cu_dev, max_q_len=max(new), scale=scale, return_lse=True)
+    seen = dict(window=20, sinks=9) if "sinks" in form else {}
+    kw.update(seen or {**batch.groups, "max_seq_len": LONG})
+    one_head = tensor(rounded(rng, (N, 1, 80), dtype), dtype).expand(N, Hq, 80)
+    one_token = tensor(rounded(rng, (1, Hq, 80), dtype), dtype).expand(N, Hq, 80)
+    for q in (one_head, one_token):
+        out, lse = batch.cache.attend(q, **kw)
+        want, want_lse = batch.cache.attend(q.contiguous(), **kw)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        compare_signed(out, lse, batch, f64(q), dtype, scale, **seen)
+
+
+def compare_signed(out, lse, batch, q, dtype, scale, **seen):
+    """The oracle's error terms take a positive scale: the sign goes into q."""
+    compare(out, lse, batch, q * np.sign(scale), dtype, scale=abs(scale), **seen)
+
+
+@pytest.mark.parametrize("B", [8, 40])
+def test_shared_leaves_other_rows(B):
+    """Rows behind the last sequence and past max_q_len are left as they were."""
+    torch = torch_mod()
+    rng = np.random.default_rng(82)
+    new = [3 if b == 1 else 2 for b in range(B)]
+    batch = Shared(rng, new, [b % 5 for b in range(B)], [0, B], [140], 2, 16, 64, std=0.5)
+    N = sum(new) + 4
+    q = rounded(rng, (N, 16, 64), "bfloat16")
+    out, lse = torch.full((N, 16, 64), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((N, 16), 7.0, device="cuda")
+    batch.cache.attend(tensor(q, "bfloat16"), **batch.dev, cu_q=batch.cu_dev, max_q_len=2, out=out, lse=lse, max_seq_len=LONG, **batch.groups)
+    left = np.ones(N, bool)
+    for a, n in zip(batch.cu, new):
+        left[a:a + min(n, 2)] = False
+    assert (f64(out)[left] == 7).all() and (f64(lse)[left] == 7).all() and not (f64(lse)[~left] == 7).any()
+    full, full_lse = batch.cache.attend(tensor(q[:N - 4], "bfloat16"), **batch.dev, cu_q=batch.cu_dev, max_q_len=3, return_lse=True, max_seq_len=LONG,
+                                        **batch.groups)
+    compare(full, full_lse, batch, q[:N - 4], "bfloat16")
+    assert np.abs(f64(lse)[~left] - f64(full_lse)[~left[:N - 4]]).max() < 1e-3
+
+
+def test_shared_scales_of_any_size():
+    """Pages whose key and value scales differ by many powers of two, and value
+    scales of zero: each part's reference follows its own."""
+    torch = torch_mod()
+    rng = np.random.default_rng(83)
+    batch = Shared(rng, [1] * 8, [30 + b for b in range(8)], [0, 8], [300], 2, 16, 64, std=0.5)
+    for part in batch.scales:
+        part *= np.exp2(rng.integers(-6, 7, part.shape)).astype(np.float32)
+        part[batch.table[1:, 300 // 16]] = part[batch.table[0, 300 // 16]]     # the copies of the page in which the prefix ends
+    batch.scales[1][batch.table[0, 3]] = 0.0           # one of the shared pages
+    for t, s in zip((batch.cache.k_scale, batch.cache.v_scale), batch.scales):
+        t.copy_(tensor(s, "float32"))
+    q = rounded(rng, (8, 16, 64), "bfloat16")
+    out, lse = batch.cache.attend(tensor(q, "bfloat16"), **batch.dev, scale=0.02, return_lse=True, max_seq_len=LONG, **batch.groups)
+    compare(out, lse, batch, q, "bfloat16", scale=0.02)
