@@ -349,7 +349,7 @@ struct AttentionForms {
   int32_t* pieces;              // [groups]
 
   // What both passes take, in us (as measured: a CTA's time before and after its
-  // tiles, and a tile's), if the prefix pass, with ``tiles`` key tiles of
+  // tiles, and a tile's with the other pass beside it), if the prefix pass, with ``tiles`` key tiles of
   // its units, has n SMs, and the own pass, with ``own`` key tiles of its row
   // tiles, the others meanwhile (or all of them after it).  Both passes look for
   // the same best n: they have times of their own before and after their tiles,
@@ -357,7 +357,7 @@ struct AttentionForms {
   // pass kOwnUnit tiles' time besides its own, counted in ``own``.
   __device__ __forceinline__ float time(int n, int tiles, int own) const {
     const int left = sms - n, ctas = own_per_sm * (left > 0 ? left : sms);
-    const float first = 15.f + 2.1f * static_cast<float>((tiles + n - 1) / n), second = 12.f + 0.85f * static_cast<float>((own + ctas - 1) / ctas);
+    const float first = 15.f + 2.6f * static_cast<float>((tiles + n - 1) / n), second = 12.f + 0.85f * static_cast<float>((own + ctas - 1) / ctas);
     return left > 0 ? fmaxf(first, second) : first + second;
   }
   // The time and n as one number that orders by time.

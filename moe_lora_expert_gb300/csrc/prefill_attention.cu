@@ -738,10 +738,28 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
 #pragma unroll 1
     for (bool more = next(true); more && !stop; more = next(false)) {
       if (en.position(en.rows - 1, group) >= static_cast<int64_t>(a.table_width) * ca.page_size) set_status(a.status, MOE_ERR_BAD_PAGE);
+      auto issue_queries = [&] {
+        if (!MAPPED) {
+          if (lane == 0) mbar_arrive(&s.q_raw);
+        } else if (lane == 0) {
+          mbar_arrive_expect_tx(&s.q_raw, L::kHalves * p.unit_rows * 128);
+#pragma unroll 1
+          for (int h = 0; h < L::kHalves; ++h)
+            tma_load_3d(smem_u32(smem + L::kQ + 2 * h * L::kHalfBytes), &q_map, &s.q_raw, 64 * h, walk.head * group,
+                        en.q_first + en.row0 / group);
+        }
+        ++units;
+      };
+      // In the prefix pass most CTAs have one piece, whose beginning counts: its
+      // queries come before the keys' pages are looked up, its first keys before
+      // the next ones' pages are.
+      const bool early = kIsPrefix && units == 0;
+      if (early) issue_queries();
       Ahead now = find(0);
 #pragma unroll 1
       for (int j = 0; j < walk.n && !stop; ++j) {
-        const Ahead later = find(j + 1);
+        Ahead later;
+        if (!kIsPrefix) later = find(j + 1);
         const int t = issued / 2;
         const bool issues = lane < 16 && now.page >= 0 && (8 * lane) % p.box == 0;
         const unsigned boxes = __ballot_sync(0xffffffffu, issues);
@@ -763,23 +781,15 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
             tma_load_4d(smem_u32(smem + L::kCode + st * L::kCodeBytes) + 8 * lane * 128, v == 0 ? &k_map : &v_map,
                         &s.code_full[st], now.off, walk.head, now.page);
           ++issued;
-          if (j == 0 && v == 0) {                                    // the unit's queries, after its first keys
+          if (j == 0 && v == 0 && !early) {                          // the unit's queries, after its first keys
             if (units > 0 && !wait(&s.q_empty, (units - 1) & 1)) {
               stop = true;
               break;
             }
-            if (!MAPPED) {
-              if (lane == 0) mbar_arrive(&s.q_raw);
-            } else if (lane == 0) {
-              mbar_arrive_expect_tx(&s.q_raw, L::kHalves * p.unit_rows * 128);
-#pragma unroll 1
-              for (int h = 0; h < L::kHalves; ++h)
-                tma_load_3d(smem_u32(smem + L::kQ + 2 * h * L::kHalfBytes), &q_map, &s.q_raw, 64 * h, walk.head * group,
-                            en.q_first + en.row0 / group);
-            }
-            ++units;
+            issue_queries();
           }
         }
+        if (kIsPrefix) later = find(j + 1);
         now = later;
       }
     }
