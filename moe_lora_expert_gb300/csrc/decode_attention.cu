@@ -44,7 +44,7 @@
 // Sequences whose first keys the prefix pass takes (AttentionForms) begin after
 // them here and leave their sums for the join.  64 sequences of up to 1023 own
 // keys are 256 row tiles of 17 tiles at most: one for each CTA, since a cut costs
-// more than a tile of waiting (31 us cut evenly, 17 so).
+// more than a tile of waiting (cut evenly the call takes 50.5 us, so 35.5).
 //
 // What bounds it: one pass over the cache's bytes.  64 sequences of up to
 // 32768 keys (8 query heads of 128 on each of 4 key heads) take 214 us, 6.3
@@ -89,7 +89,7 @@ constexpr int kMaxEntries = 512;          // (sequence, row tile) pairs of one l
 constexpr int kMinTiles = 2;              // a CTA's stretch of the line is at least so long; one token on 1022 keys: 1 13.0, 2 11.3, 4 12.7 us
 constexpr int kJoin = 16;                 // pieces that are joined at a time; 16 sequences of up to 4096 keys: 8 27.6, 16 24.5 us
 constexpr int kPitch = 128;               // bytes of a key in shared memory
-constexpr int kCutCost = 16;              // tiles' worth of time that a row tile which is cut takes
+constexpr int kCutCost = 16;              // tiles' worth of time that a row tile which is cut takes; drafts for 20 requests: 4 63, 16 51 us
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMost = 15.9f, kNew = 7.f;// a weight past 2^15.9 makes the reference rise, so that it becomes 2^7;
@@ -326,7 +326,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     if (own && p.B == a.B && entries * ca.kv_heads > most_ctas) {
       // Where a CTA cannot have one row tile anyway: as many as the SMs hold
       // that the prefix pass leaves (128 sequences on 32768 shared tokens: 151 us
-      // with all CTAs, 135 so).
+      // with all CTAs, 135 so; without the form 633).
       const int work = max(0, s.own) * ca.kv_heads * p.f.own_row_tiles;
 #pragma unroll 1
       for (int n = tid + 1; n <= p.f.sms; n += kThreads) atomicMin(&s.best, p.f.choice(n, s.tiles, work));

@@ -47,9 +47,11 @@
 // as one unit's rows against the keys that all of them begin with.  All rows see
 // all keys, and a unit is cut in as many pieces as there are CTAs for it, whose
 // sums are joined by another kernel: joined here, 19 pieces of 256 rows in two
-// steps, 64 sequences on 8192 keys took 54 us instead of 30.  A piece takes 10 us
+// steps, 64 sequences on 8192 keys took 54 us instead of 30.  A piece takes 9 us
 // to its first scores (lengths, plan, pages, copies, conversion, each about one),
-// 2 us a key tile, and 5 to write its 128 KB.  Two softmax warps for 32 rows, or
+// 2 us a key tile, and 3 to 5 to write its 128 KB (by way of shared memory, in
+// whole lines, the call takes as long).  With the own pass beside it that call
+// is 36 us, 128 sequences on 32768 keys 133.  Two softmax warps for 32 rows, or
 // both row tiles on the same rows of a small group, took longer: the schedulers
 // are busy half of the time and the conversion has no time to spare.
 #include <cuda.h>

@@ -4,7 +4,8 @@
 // With piece i's reference m_i, denominator l_i and sums O_i (relative to 2^m_i),
 //   out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i.
 // A warp a row, a lane four columns; 16 pieces' loads are on their way together.
-// What bounds it: the pieces' bytes, from the second-level cache.
+// What bounds it: the pieces' bytes, from the second-level cache.  2048 rows of
+// 8 pieces take 3 us of a call, 8 by themselves from cold caches.
 #include "attention.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
