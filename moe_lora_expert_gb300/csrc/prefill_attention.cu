@@ -77,7 +77,7 @@ constexpr int kInfo = 4;                   // key tiles whose scales are held (s
 constexpr int kUnitCost = 2;               // key tiles' worth of time that a unit takes besides its tiles; 2 x 2048 tokens, cut from the line: 1 122, 2 103, 3 103, 4 105 us
 constexpr int kMinTiles = 4;               // least length of a CTA's stretch (a join costs about as much as four tiles)
 constexpr int kOwnKeys = 64;               // of a key tile of the own pass
-constexpr int kMinPiece = 2;               // key tiles of a piece in the prefix pass, at least
+constexpr int kMinPiece = 2;               // key tiles of a piece in the prefix pass, about; a unit of an odd number has pieces of one, too
 constexpr int kMaxCtas = 160;
 constexpr int kMaxUnits = 16;              // whole units a CTA may be given (see the kernel)
 constexpr int kJoinCost = 8;               // key tiles' worth of time that cutting the line may cost a CTA: part of a unit written, another joined
@@ -519,7 +519,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     }
     mbar_init(&s.q_raw, 1);
     mbar_init(&s.q_full, kIsPrefix ? 8 : 4);
-    mbar_init(&s.q_empty, 1 + 2 * kTileRows / 32);   // the last scores, and every row's thread has its exponent
+    // the last scores, and every row's thread has its exponent; in the prefix
+    // pass the converting warps too have seen that the queries came
+    mbar_init(&s.q_empty, 1 + 2 * kTileRows / 32 + (kIsPrefix ? 4 : 0));
     mbar_init(&s.drained, 1);
     s.abort_flag = 0;
     fence_mbarrier_init();
@@ -948,7 +950,13 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
           if (!good) break;
           // the rows have begun the unit before, so they are done with the one before that
           if (lane == 0) s.nan_count[units & 1][w] = 0;
-          if constexpr (!kIsPrefix) {
+          if constexpr (kIsPrefix) {
+            // Without this word a piece of one tile could end, and the next
+            // one's queries come, before this warp has looked for these: it
+            // would then wait for those of the one after.  (Elsewhere the word
+            // is q_full's.)
+            if (lane == 0) mbar_arrive(&s.q_empty);
+          } else {
             if constexpr (!MAPPED) {
               load_queries<T, DP, FORM>(a, en, walk.head, group, smem + L::kQ, 32 * w + lane, kTileRows);
               fence_proxy_async_shared();

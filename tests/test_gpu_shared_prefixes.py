@@ -1,0 +1,96 @@
+"""Shared prefixes where the passes take their less common ways, against plain
+sums in float64 on the GPU.
+
+Bounds as in test_gpu_attention: weights round to float16 (2^-11 of what they
+sum), scores are float32 sums of 128 products (es), outputs round once.
+"""
+import numpy as np
+import pytest
+
+import moe_lora_expert_gb300 as m
+from test_gpu_attention import torch_mod
+
+pytestmark = pytest.mark.gpu
+
+LONG = 1 << 20   # a bound on the lengths that makes sharing worth while, whatever the lengths
+HALF_STEP = {"bfloat16": 2.0 ** -8, "float16": 2.0 ** -11}
+SCALE = 2.0 ** -6
+
+
+class Prefixes:
+    """Groups of sequences, each with a prefix of ``shared[g]`` tokens whose whole
+    pages the group's table rows have in common and whose last page, where the
+    prefix ends inside one, each has as a copy; ``own[b]`` tokens follow, the
+    last ``new[b]`` of them new."""
+
+    def __init__(self, seed, sizes, shared, own, new, Hkv, Hq, D, P=64, dtype="bfloat16", std=40.0):
+        torch = torch_mod()
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        B, rng = sum(sizes), np.random.default_rng(seed)
+        self.new, self.Hkv, self.Hq, self.D, self.P, self.dtype = new, Hkv, Hq, D, P, dtype
+        of = np.repeat(np.arange(len(sizes)), sizes)
+        self.seqs = np.cumsum([0] + list(sizes)).astype(np.int32)
+        self.lens = np.array([shared[of[b]] + own[b] for b in range(B)], np.int32)
+        table, pages, copies = np.full((B, int(-(-self.lens.max() // P)) + 1), 1 << 30, np.int64), 0, []
+        for b in range(B):
+            g = of[b]
+            lead, need, same = self.seqs[g], -(-int(self.lens[b]) // P), 0
+            if b != lead:
+                same = shared[g] // P
+                table[b, :same] = table[lead, :same]
+                if shared[g] % P:
+                    copies.append((lead, b, same))
+            table[b, same:need] = np.arange(pages, pages + need - same)
+            pages += need - same
+        order = rng.permutation(pages)
+        real = table < pages
+        table[real] = order[table[real]]
+        shape = (pages, Hkv, P, D)
+        self.k, self.v = ((torch.randn(shape, generator=gen, device="cuda") * std).to(torch.float8_e4m3fn).view(torch.uint8) for _ in range(2))
+        for lead, b, at in copies:
+            for x in (self.k, self.v):
+                x[table[b, at]] = x[table[lead, at]]
+        self.cache = m.PagedKVCache(self.k, self.v, *[torch.full(shape[:2], SCALE, device="cuda") for _ in range(2)])
+        self.table = torch.from_numpy(table.astype(np.int32)).cuda()
+        self.cu = np.cumsum([0] + list(new)).astype(np.int32)
+        self.q = torch.randn((int(self.cu[-1]), Hq, D), generator=gen, device="cuda").to(getattr(torch, dtype))
+        self.args = dict(q=self.q, block_table=self.table, seq_lens=torch.from_numpy(self.lens).cuda(),
+                         cu_q=None if max(new) == min(new) == 1 else torch.from_numpy(self.cu).cuda(), max_q_len=max(new), return_lse=True)
+        self.groups = dict(shared_lens=torch.tensor(list(shared), dtype=torch.int32, device="cuda"), shared_seqs=torch.from_numpy(self.seqs).cuda(),
+                           max_shared_q=int(max(sum(new[a:b]) for a, b in zip(self.seqs, self.seqs[1:]))))
+
+    def attend(self, **over):
+        return self.cache.attend(**{**self.args, **self.groups, "max_seq_len": LONG, **over})
+
+    def check(self, out, lse, sequences=None):
+        torch = torch_mod()
+        G = self.Hq // self.Hkv
+        for b in range(len(self.new)) if sequences is None else sequences:
+            e, n = int(self.lens[b]), self.new[b]
+            pg = self.table[b, :-(-e // self.P)].long()
+            kk, vv = (x[pg].view(torch.float8_e4m3fn).double().transpose(0, 1).flatten(1, 2)[:, :e] * SCALE for x in (self.k, self.v))
+            row = slice(int(self.cu[b]), int(self.cu[b]) + n)
+            q = self.q[row].double().view(n, self.Hkv, G, self.D).permute(1, 2, 0, 3)                 # [Hkv, G, n, D]
+            hidden = torch.arange(e, device="cuda")[None] > torch.arange(e - n, e, device="cuda")[:, None]
+            s = (torch.einsum("hgnd,hkd->hgnk", q, kk) * self.D ** -0.5).masked_fill(hidden, -np.inf)
+            es = 128 * 2.0 ** -22 * self.D ** -0.5 * torch.einsum("hgnd,hkd->hgnk", q.abs(), kk.abs()).amax(-1, keepdim=True)
+            p = torch.softmax(s, -1)
+            ref, spread = torch.einsum("hgnk,hkd->hgnd", p, vv), torch.einsum("hgnk,hkd->hgnd", p, vv.abs())
+            bound = (2.0 ** -11 + 4 * es + 2.0 ** -17) * spread + 2.0 ** -22 * 448 * SCALE + 1.01 * HALF_STEP[self.dtype] * ref.abs()
+            got = out[row].double().view(n, self.Hkv, G, self.D).permute(1, 2, 0, 3)
+            assert ((got - ref).abs() <= bound).all(), (b, float(((got - ref).abs() - bound).max()))
+            want, got = torch.logsumexp(s, -1), lse[row].double().view(n, self.Hkv, G).permute(1, 2, 0)
+            assert ((got - want).abs() <= es[..., 0] + 2.0 ** -20 * (1 + want.abs())).all(), b
+
+
+@pytest.mark.parametrize("shared", [[100] * 40, [1 + 7 * g for g in range(40)]])
+def test_more_units_than_ctas(shared):
+    """Pieces of one key tile or a few, several to a CTA, and more row tiles of
+    the own pass than CTAs in one launch."""
+    torch = torch_mod()
+    sizes = [8] * 40
+    batch = Prefixes(1, sizes, shared, [1 + (37 * b) % 90 for b in range(320)], [1] * 320, 4, 32, 64, P=16)
+    out, lse = batch.attend()
+    batch.check(out, lse)
+    again = batch.attend()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and batch.cache.device_status() == m.MOE_OK
