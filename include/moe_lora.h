@@ -690,7 +690,8 @@ int moe_paged_attention_sinks(const moe_paged_attention_args_t* args, int sinks,
  * parts are joined in float32).  The shared keys are read through the table
  * row of the group's first sequence, whatever its seq_lens says (a slot without
  * a sequence may come first if its row has the prefix's pages); a prefix may end
- * inside a page.  A sequence whose new tokens begin before lens[g], or that is
+ * inside a page.  They are not looked up where no sequence of the group takes
+ * part.  A sequence whose new tokens begin before lens[g], or that is
  * in no group, or whose tokens are not all among the first max_tokens of its
  * group's, reads all of its keys itself.
  *   args: as in moe_paged_attention, with window = 0 (MOE_ERR_UNSUPPORTED).

@@ -369,6 +369,26 @@ struct AttentionForms {
     q0 = cu_q == nullptr ? s0 : cu_q[s0];
     q1 = cu_q == nullptr ? s1 : cu_q[s1];
   }
+  // Whether a sequence whose rows are tokens [q_first, q_first + q_len) and begin
+  // at position ``start`` takes part in a prefix of n tokens of the group with
+  // tokens [q0, q1).
+  __device__ __forceinline__ bool takes_part(int n, int q0, int q1, int q_first, int q_len, int start) const {
+    return n > 0 && start >= n && q_first >= q0 && q_first + q_len <= min(q1, q0 + max_tokens);
+  }
+  // Whether some row of a group's sequences [s0, s1) does.  Where none does,
+  // nobody has to have the prefix's pages yet.
+  __device__ __forceinline__ bool some_take_part(const int32_t* cu_q, const int32_t* seq_lens, int n, int s0, int s1, int q0, int q1) const {
+    bool some = false;
+#pragma unroll 1
+    for (int s = s0; s < s1 && !some; s += 4) {          // nearly always the first one does
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = min(s + i, s1 - 1), q_first = cu_q == nullptr ? b : cu_q[b], q_len = cu_q == nullptr ? 1 : cu_q[b + 1] - q_first;
+        some |= q_len > 0 && takes_part(n, q0, q1, q_first, q_len, seq_lens[b] - q_len);
+      }
+    }
+    return some;
+  }
   // How many keys of sequence b, whose rows are tokens [q_first, q_first +
   // q_len) and begin at position ``start``, the prefix pass has taken, and in
   // which group.
@@ -385,7 +405,7 @@ struct AttentionForms {
     const int n = lens[g];
     int s0, s1, q0, q1;
     group(cu_q, g, s0, s1, q0, q1);
-    return n > 0 && start >= n && q_first >= q0 && q_first + q_len <= min(q1, q0 + max_tokens) ? n : 0;
+    return takes_part(n, q0, q1, q_first, q_len, start) ? n : 0;
   }
 };
 bool encode_cache_map(CUtensorMap* map, const moe_kv_cache_t& c, bool values, int rows);

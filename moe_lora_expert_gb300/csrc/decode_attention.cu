@@ -259,7 +259,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         const int len = static_cast<int>(min(static_cast<int64_t>(p.f.lens[g]), held));
         p.f.group(a.cu_q, g, s0, s1, q0, q1);
         const int tokens = min(q1 - q0, p.f.max_tokens), each = 256 / group;
-        if (len <= 0 || tokens <= 0) continue;
+        if (len <= 0 || tokens <= 0 || !p.f.some_take_part(a.cu_q, a.seq_lens, p.f.lens[g], s0, s1, q0, q1)) continue;
         atomicAdd(&s.tiles, (tokens + each - 1) / each * ((len + 127) / 128) * ca.kv_heads);
         atomicAdd(&s.own, -(s1 - s0) * (len / kKeys));
       }

@@ -247,7 +247,7 @@ struct Entry : EntryForms<FORM> {
       int s1, q_end;
       len = p.f.lens[b];
       p.f.group(a.cu_q, b, b, s1, q_first, q_end);
-      q_len = len > 0 ? q_end - q_first : 0;
+      q_len = p.f.some_take_part(a.cu_q, a.seq_lens, len, b, s1, q_first, q_end) ? q_end - q_first : 0;
       this->sequences = s1 - b;
     } else {
       q_first = a.cu_q == nullptr ? b : a.cu_q[b];

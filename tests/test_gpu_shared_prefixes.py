@@ -94,3 +94,21 @@ def test_more_units_than_ctas(shared):
     batch.check(out, lse)
     again = batch.attend()
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and batch.cache.device_status() == m.MOE_OK
+
+
+@pytest.mark.parametrize("chunk", [1, 3])
+def test_prefixes_that_nobody_has_yet(chunk):
+    """Sequences that are still in their first chunks: the rest of the prefix has
+    no pages yet, which is no error, and a group that has it is served as ever."""
+    torch = torch_mod()
+    batch = Prefixes(2, [6, 6], [300, 300], [20] * 12, [chunk] * 12, 2, 32, 64, P=16)
+    lens = batch.lens.copy()
+    lens[:6] = [40, 16, 17, 3, 299, 60]
+    batch.lens = lens
+    table = batch.table.cpu().numpy()
+    for b in range(6):
+        table[b, -(-int(lens[b]) // 16):] = 1 << 30
+    batch.table = torch.from_numpy(table).cuda()
+    out, lse = batch.attend(block_table=batch.table, seq_lens=torch.from_numpy(lens).cuda())
+    batch.check(out, lse)
+    assert batch.cache.device_status() == m.MOE_OK
