@@ -325,8 +325,10 @@ int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_sh
   prefix.B = x->groups;
   prefix.max_q_len = f.max_tokens;
   if (!shares(rows_of(p), rows_of(prefix), p.max_seq_len)) return attend(p, nullptr, a->dtype, on);
+  // where one of the three kernels cannot take the call, the plain one still may
+  if (!moe::decode_attention_fits(p) || !moe::shared_join_fits(p)) return attend(p, nullptr, a->dtype, on);
   int error = moe::launch_prefill_attention(prefix, &f, a->dtype, on);
-  if (error == MOE_ERR_UNSUPPORTED) return attend(p, nullptr, a->dtype, on);    // too many groups for one line
+  if (error == MOE_ERR_UNSUPPORTED) return attend(p, nullptr, a->dtype, on);    // too many groups for one line; nothing has been launched
   if (error != MOE_OK) return error;
   f.pass = moe::kOwnPass;
   error = moe::launch_decode_attention(p, &f, a->dtype, on);

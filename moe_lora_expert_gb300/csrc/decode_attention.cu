@@ -937,6 +937,17 @@ cudaError_t clear_decode_counters(void* workspace, cudaStream_t s) {
 
 namespace {
 
+// Row tiles of a sequence, and whether the line of one launch can count its key tiles.
+int64_t row_tiles_of(const AttentionParams& a, int tile_rows) {
+  return (static_cast<int64_t>(a.max_q_len) * (a.Hq / a.cache.kv_heads) + tile_rows - 1) / tile_rows;
+}
+bool fits(const AttentionParams& a, int64_t row_tiles) {
+  const int64_t entries = row_tiles * a.B < kMaxEntries ? row_tiles * a.B : kMaxEntries;
+  const int64_t line = (static_cast<int64_t>(a.table_width) * a.cache.page_size / kKeys + 1) * entries * a.cache.kv_heads;
+  return row_tiles <= kMaxEntries && line <= 0x7fffffff;
+}
+int tile_rows_of(const AttentionParams& a) { return static_cast<int64_t>(a.max_q_len) * (a.Hq / a.cache.kv_heads) <= 8 ? 8 : 16; }
+
 template <typename T, int DP, int NT, bool FORMS>
 int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t stream) {
   CUtensorMap k_map, v_map;
@@ -951,11 +962,8 @@ int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t s
   if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes) != cudaSuccess) return MOE_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
-  const int group = a.Hq / a.cache.kv_heads;
-  const int64_t row_tiles = (static_cast<int64_t>(a.max_q_len) * group + 8 * NT - 1) / (8 * NT);
-  const int64_t entries = row_tiles * a.B < kMaxEntries ? row_tiles * a.B : kMaxEntries;
-  const int64_t line = (static_cast<int64_t>(a.table_width) * a.cache.page_size / kKeys + 1) * entries * a.cache.kv_heads;
-  if (row_tiles > kMaxEntries || line > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  const int64_t row_tiles = row_tiles_of(a, 8 * NT);
+  if (!fits(a, row_tiles)) return MOE_ERR_UNSUPPORTED;
   p.row_tiles = static_cast<int>(row_tiles);
   const int per_launch = kMaxEntries / p.row_tiles;
   const int64_t longest = a.max_seq_len > 0 ? a.max_seq_len : 1;
@@ -975,7 +983,7 @@ int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t s
 
 template <typename T, bool FORMS>
 int launch_rows(const AttentionParams& p, const AttentionForms* forms, cudaStream_t s) {
-  const bool few = static_cast<int64_t>(p.max_q_len) * (p.Hq / p.cache.kv_heads) <= 8;
+  const bool few = tile_rows_of(p) == 8;
   if (p.cache.head_dim <= 64) return few ? launch<T, 64, 1, FORMS>(p, forms, s) : launch<T, 64, 2, FORMS>(p, forms, s);
   return few ? launch<T, 128, 1, FORMS>(p, forms, s) : launch<T, 128, 2, FORMS>(p, forms, s);
 }
@@ -986,6 +994,7 @@ int launch_type(const AttentionParams& p, const AttentionForms* forms, int dtype
 }
 }  // namespace
 
+bool decode_attention_fits(const AttentionParams& p) { return fits(p, row_tiles_of(p, tile_rows_of(p))); }
 int launch_decode_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s) {
   return forms != nullptr ? launch_type<true>(p, forms, dtype, s) : launch_type<false>(p, forms, dtype, s);
 }

@@ -80,9 +80,16 @@ __global__ void __launch_bounds__(32 * kWarps) shared_join_kernel(const __grid_c
 
 }  // namespace
 
+namespace {
+int64_t rows_each_of(const AttentionParams& p) { return static_cast<int64_t>(p.max_q_len) * p.Hq; }
+int64_t ctas_of(const AttentionParams& p) { return (rows_each_of(p) * p.B + kWarps - 1) / kWarps; }
+}  // namespace
+
+bool shared_join_fits(const AttentionParams& p) { return ctas_of(p) <= 0x7fffffff / kWarps; }
+
 int launch_shared_join(const AttentionParams& p, const AttentionForms& forms, int dtype, cudaStream_t s) {
-  const int64_t rows_each = static_cast<int64_t>(p.max_q_len) * p.Hq, ctas = (rows_each * p.B + kWarps - 1) / kWarps;
-  if (ctas > 0x7fffffff / kWarps) return MOE_ERR_UNSUPPORTED;
+  if (!shared_join_fits(p)) return MOE_ERR_UNSUPPORTED;
+  const int64_t rows_each = rows_each_of(p), ctas = ctas_of(p);
   const dim3 grid(static_cast<unsigned>(ctas)), block(32 * kWarps);
   const cudaError_t e = dtype == MOE_DTYPE_F16
                             ? launch_pdl(shared_join_kernel<__half>, grid, block, 0, s, p, forms, static_cast<uint32_t>(rows_each))

@@ -112,3 +112,18 @@ def test_prefixes_that_nobody_has_yet(chunk):
     out, lse = batch.attend(block_table=batch.table, seq_lens=torch.from_numpy(lens).cuda())
     batch.check(out, lse)
     assert batch.cache.device_status() == m.MOE_OK
+
+
+def test_a_table_too_wide_for_the_own_pass():
+    """A call whose own keys the kernel for few rows cannot count in one line, and
+    the plain call can: it does as that one."""
+    torch = torch_mod()
+    batch = Prefixes(3, [128], [250], [64] * 128, [64] * 128, 64, 64, 16, P=256)
+    wide = torch.full((128, 16384), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :batch.table.shape[1]] = batch.table
+    batch.table = wide
+    out, lse = batch.attend(block_table=wide)
+    want, want_lse = batch.cache.attend(**{**batch.args, "block_table": wide})
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    batch.check(out, lse, [0, 77, 127])
+    assert batch.cache.device_status() == m.MOE_OK
