@@ -249,8 +249,10 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     const int before = sink_tiles(lo);
     return (FORMS && i < before ? i : lo / kKeys + i - before) * kKeys;
   };
+  // Where a CTA cannot have one row tile anyway, the CTAs share the SMs with the prefix pass by its plan.
+  const bool planned = FORMS && own && p.B == a.B && entries * ca.kv_heads > static_cast<int>(gridDim.x);
   if constexpr (FORMS) {
-    if (own) {
+    if (planned) {
       __syncthreads();
 #pragma unroll 1
       for (int g = tid; g < p.f.groups; g += kThreads) {
@@ -278,7 +280,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         int g = 0;
         if (own) {
           lo = p.f.taken(a.cu_q, en.b, en.q_first, en.q_len, en.len - en.q_len, g);
-          if (en.row0 == 0) atomicAdd(&s.own, (en.len + kKeys - 1) / kKeys + kOwnUnit);
+          if (planned && en.row0 == 0) atomicAdd(&s.own, (en.len + kKeys - 1) / kKeys + kOwnUnit);
         }
       }
       hi = max(0, pos1 + 1);
@@ -323,9 +325,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   __syncthreads();
   int most_ctas = gridDim.x;
   if constexpr (FORMS) {
-    if (own && p.B == a.B && entries * ca.kv_heads > most_ctas) {
-      // Where a CTA cannot have one row tile anyway: as many as the SMs hold
-      // that the prefix pass leaves (128 sequences on 32768 shared tokens: 151 us
+    if (planned) {
+      // As many as the SMs hold that the prefix pass leaves (128 sequences on 32768 shared tokens: 151 us
       // with all CTAs, 135 so; without the form 633).
       const int work = max(0, s.own) * ca.kv_heads * p.f.own_row_tiles;
 #pragma unroll 1
