@@ -698,11 +698,13 @@ int moe_paged_attention_sinks(const moe_paged_attention_args_t* args, int sinks,
  *   seqs [groups + 1] int32, device, not decreasing, or NULL with groups = 1:
  *     all sequences.  lens [groups] int32, device; 0 or less: nothing shared.
  *   max_tokens: at least the most new tokens of one group; it sizes the launch.
- *   partial: device scratch of the call, moe_shared_prefix_partial_size bytes,
- *     32-byte aligned, of any contents.
+ *   partial: device scratch of the call, of any contents, 32-byte aligned:
+ *     moe_paged_attention_shared_partial_size bytes of the same arguments
+ *     (partial's own are not read), or the moe_shared_prefix_partial_size bytes
+ *     that hold for whatever bounds; NULL and 0 bytes where the first is 0.
  * Where sharing would not pay, by the sizes that the host has (max_q_len,
  * max_tokens, max_seq_len), the call does as moe_paged_attention does: few rows
- * in a group, many in each sequence, short contexts.
+ * in a group, many in each sequence, short contexts.  It then needs no scratch.
  * ------------------------------------------------------------------------- */
 typedef struct {
   uint32_t struct_size;           /* sizeof(moe_shared_prefix_t) */
@@ -713,6 +715,7 @@ typedef struct {
   size_t partial_bytes;
 } moe_shared_prefix_t;
 size_t moe_shared_prefix_partial_size(int N, int Hq, int head_dim, int groups);
+size_t moe_paged_attention_shared_partial_size(const moe_paged_attention_args_t* args, const moe_shared_prefix_t* shared);
 int moe_paged_attention_shared(const moe_paged_attention_args_t* args, const moe_shared_prefix_t* shared, moe_stream_t stream);
 
 #ifdef __cplusplus

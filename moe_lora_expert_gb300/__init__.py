@@ -50,6 +50,7 @@ EXPORTED_SYMBOLS = [
     "moe_paged_attention", "moe_paged_attention_workspace_init", "moe_stream_capture_id",
     "moe_rope_axes", "moe_kv_append_axes", "moe_paged_attention_sinks", "moe_paged_attention_shared",
     "moe_shared_prefix_partial_size",
+    "moe_paged_attention_shared_partial_size",
 ]
 
 
@@ -145,6 +146,8 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = [ctypes.c_char_p, ctypes.c_char_p, vp]    # two structs' bytes, stream
         L.moe_paged_attention_sinks.restype = i32
         L.moe_paged_attention_sinks.argtypes = [ctypes.c_char_p, i32, vp]
+        L.moe_paged_attention_shared_partial_size.restype = sz
+        L.moe_paged_attention_shared_partial_size.argtypes = [ctypes.c_char_p, ctypes.c_char_p]
         L.moe_shared_prefix_partial_size.restype = sz
         L.moe_shared_prefix_partial_size.argtypes = [i32, i32, i32, i32]
         L.moe_paged_attention_workspace_size.restype = sz

@@ -115,7 +115,7 @@ def _bind():
     _empty_like, _capturing = torch.empty_like, torch.cuda.is_current_stream_capturing
     _current_device = torch._C._cuda_getDevice
     _rope_axes_fn, _append_axes_fn = L.moe_rope_axes, L.moe_kv_append_axes
-    _sinks_fn, _shared_fn, _partial_size = L.moe_paged_attention_sinks, L.moe_paged_attention_shared, L.moe_shared_prefix_partial_size
+    _sinks_fn, _shared_fn, _partial_size = L.moe_paged_attention_sinks, L.moe_paged_attention_shared, L.moe_paged_attention_shared_partial_size
     _rope_fn, _torch = L.moe_rope, torch
 
 
@@ -539,7 +539,7 @@ class PagedKVCache:
         elif return_lse:
             lse = _empty((N, Hq), _float32_type, self.device, stream)
         B, width, bt, sl, cu, longest = self._batch(N, block_table, seq_lens, cu_q, max_q_len)
-        fn, more, partial = _attend_fn, (), None
+        fn, more = _attend_fn, ()
         if sinks:
             fn, more = _sinks_fn, (min(sinks, 1 << 30),)        # ctypes drops what an int does not hold
         if shared_lens is not None:
@@ -550,9 +550,8 @@ class PagedKVCache:
                 raise ValueError("without shared_seqs there is one group, of all sequences")
             lens = _int32(shared_lens, G, "shared_lens", index)
             seqs = 0 if shared_seqs is None else _int32(shared_seqs, G + 1, "shared_seqs", index)
-            partial = _empty((_partial_size(N, Hq, D, G),), _torch.uint8, self.device, stream)
-            fn, more = _shared_fn, (_SHARED.pack(48, G, N if max_shared_q is None else max_shared_q, seqs, lens, partial.data_ptr(),
-                                                 partial.shape[0]),)
+            named = (48, G, N if max_shared_q is None else max_shared_q, seqs, lens)
+            fn, more = _shared_fn, (_SHARED.pack(*named, 0, 0),)
         elif shared_seqs is not None:
             raise ValueError("shared_seqs goes with shared_lens")
         here = _current_device() == index
@@ -565,11 +564,16 @@ class PagedKVCache:
             qp, op, 0 if lse is None else lse.data_ptr(), q0, q1, o0, o1, bt, sl, cu, self._status_ptr, ws[0], ws[1],
             N, B, Hq, width, longest, width * self.page_size if max_seq_len is None else max_seq_len, window,
             wait_timeout_ms, D ** -0.5 if scale is None else scale, debug_flags)
+        if shared_lens is not None:
+            n = _partial_size(args, *more)
+            if n:                                                  # else the call is the plain one
+                partial = _empty((n,), _torch.uint8, self.device, stream)
+                more = (_SHARED.pack(*named, partial.data_ptr(), n),)
         if stream is not None:
             _record(stream, q, out, lse, block_table, seq_lens, cu_q, shared_lens, shared_seqs, *self._tensors)
         error = fn(args, *more, handle) if here else _elsewhere(index, fn, args, *more, handle)
         if error:
-            _raise(error, "moe_paged_attention" + ("_sinks" if sinks else "_shared" if partial is not None else ""))
+            _raise(error, "moe_paged_attention" + ("_sinks" if sinks else "" if shared_lens is None else "_shared"))
         return out if lse is None else (out, lse)
 
     def device_status(self) -> int:

@@ -413,12 +413,13 @@ bool encode_query_map(CUtensorMap* map, const AttentionParams& a, bool f16, int 
 int sm_count();
 size_t prefill_attention_workspace_bytes();
 cudaError_t clear_prefill_counters(void* workspace, cudaStream_t s);
+bool prefill_attention_fits(const AttentionParams& p);  // else the launch is MOE_ERR_UNSUPPORTED
 int launch_prefill_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s);  // a moe_status_t; forms NULL: none
 bool shared_join_fits(const AttentionParams& p);     // whether its grid can be launched
 int launch_shared_join(const AttentionParams& p, const AttentionForms& forms, int dtype, cudaStream_t s);   // a moe_status_t
 size_t decode_attention_workspace_bytes();
 cudaError_t clear_decode_counters(void* workspace, cudaStream_t s);
-bool decode_attention_fits(const AttentionParams& p);   // else the launch is MOE_ERR_UNSUPPORTED
+bool decode_attention_fits(const AttentionParams& p);   // likewise
 int launch_decode_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s);   // a moe_status_t
 
 }  // namespace moe

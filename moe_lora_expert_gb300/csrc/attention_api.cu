@@ -45,7 +45,7 @@ bool few_rows(int64_t rows, int64_t pairs) { return rows <= 32 || (rows <= 96 &&
 //     of 256: 4096 171 / 59, 16384 305 / 140.
 // Sequences of many rows fill the products' tiles by themselves, and their own
 // keys are then in the kernel that is made for few.
-bool shares(int64_t rows, int64_t group_rows, int64_t longest) {
+bool pays(int64_t rows, int64_t group_rows, int64_t longest) {
   return group_rows >= 32 && rows <= 128 && longest >= 2048 && (rows <= 32 || rows * rows <= longest);
 }
 // How many pieces the prefix pass may leave for a row: with one group whose
@@ -53,6 +53,10 @@ bool shares(int64_t rows, int64_t group_rows, int64_t longest) {
 int most_pieces(int N, int Hq) {
   const int64_t rows = static_cast<int64_t>(N) * Hq, n = 2ll * 160 * 256 / rows;
   return n < 2 ? 2 : n > 32 ? 32 : static_cast<int>(n);
+}
+
+size_t partial_bytes(int pieces, int64_t rows, int head_dim, int groups) {
+  return (pieces + 1) * static_cast<size_t>(rows) * (static_cast<size_t>(head_dim) * 4 + 8) + static_cast<size_t>(groups) * 4;
 }
 
 // Elements a thread may move at once, of 8, 4 and 1: V elements of a type
@@ -237,6 +241,25 @@ int attend(const AttentionParams& p, const AttentionForms* forms, int dtype, cud
   return moe::launch_prefill_attention(p, forms, dtype, on);
 }
 
+int check_shared(const moe_paged_attention_args_t* a, const moe_shared_prefix_t* x) {
+  if (x == nullptr) return MOE_ERR_NULL;
+  if (x->struct_size != sizeof(*x)) return MOE_ERR_UNSUPPORTED;
+  if (x->groups < 0 || x->max_tokens < 0) return MOE_ERR_SHAPE;
+  return a->window != 0 ? MOE_ERR_UNSUPPORTED : MOE_OK;   // with a window its rows would see different parts of a prefix
+}
+
+// Whether a call's prefixes are read for their groups, and then what the prefix
+// pass is given; else the call is the plain one.  All three kernels have to take
+// it, which is known before the first is launched.
+bool shares(const AttentionParams& p, const moe_shared_prefix_t* x, AttentionParams& prefix) {
+  if (p.N == 0 || x->groups == 0 || x->max_tokens == 0) return false;
+  prefix = p;
+  prefix.B = x->groups;
+  prefix.max_q_len = x->max_tokens < p.N ? x->max_tokens : p.N;
+  return pays(rows_of(p), rows_of(prefix), p.max_seq_len) && moe::prefill_attention_fits(prefix) && moe::decode_attention_fits(p) &&
+         moe::shared_join_fits(p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -289,27 +312,32 @@ int moe_paged_attention_sinks(const moe_paged_attention_args_t* a, int sinks, mo
 
 size_t moe_shared_prefix_partial_size(int N, int Hq, int head_dim, int groups) {
   if (N <= 0 || Hq <= 0 || head_dim <= 0 || groups <= 0) return 0;
-  return (most_pieces(N, Hq) + 1) * static_cast<size_t>(N) * Hq * (static_cast<size_t>(head_dim) * 4 + 8) + static_cast<size_t>(groups) * 4;
+  return partial_bytes(most_pieces(N, Hq), static_cast<int64_t>(N) * Hq, head_dim, groups);
+}
+
+size_t moe_paged_attention_shared_partial_size(const moe_paged_attention_args_t* a, const moe_shared_prefix_t* x) {
+  AttentionParams p, prefix;
+  if (x == nullptr || check_attention(a, p) != MOE_OK || check_shared(a, x) != MOE_OK || !shares(p, x, prefix)) return 0;
+  return moe_shared_prefix_partial_size(p.N, p.Hq, p.cache.head_dim, x->groups);
 }
 
 int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_shared_prefix_t* x, moe_stream_t stream) {
-  AttentionParams p;
-  const int st = check_attention(a, p);
-  if (st != MOE_OK) return st;
-  if (x == nullptr) return MOE_ERR_NULL;
-  if (x->struct_size != sizeof(*x)) return MOE_ERR_UNSUPPORTED;
-  if (x->groups < 0 || x->max_tokens < 0) return MOE_ERR_SHAPE;
-  if (a->window != 0) return MOE_ERR_UNSUPPORTED;       // its rows would see different parts of a prefix
-  if (p.N == 0) return MOE_OK;
+  AttentionParams p, prefix;
+  int st = check_attention(a, p);
+  if (st == MOE_OK) st = check_shared(a, x);
+  if (st != MOE_OK || p.N == 0) return st;
   (void)cudaGetLastError();
   const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
   if (x->groups == 0 || x->max_tokens == 0) return attend(p, nullptr, a->dtype, on);
   if (x->lens == nullptr || (x->seqs == nullptr && x->groups != 1)) return MOE_ERR_NULL;
-  const size_t need = moe_shared_prefix_partial_size(p.N, p.Hq, p.cache.head_dim, x->groups);
-  if (x->partial == nullptr || !aligned(x->partial, 32) || x->partial_bytes < need) return MOE_ERR_WORKSPACE;
+  const bool some = x->partial != nullptr || x->partial_bytes != 0, whole = shares(p, x, prefix);
+  if (some ? x->partial == nullptr || !aligned(x->partial, 32) || x->partial_bytes < moe_shared_prefix_partial_size(p.N, p.Hq, p.cache.head_dim, x->groups)
+           : whole)
+    return MOE_ERR_WORKSPACE;
+  if (!whole) return attend(p, nullptr, a->dtype, on);
   AttentionForms f = {};
   f.groups = x->groups, f.sequences = p.B;
-  f.max_tokens = x->max_tokens < p.N ? x->max_tokens : p.N;
+  f.max_tokens = prefix.max_q_len;
   f.seqs = x->seqs, f.lens = x->lens;
   f.most_pieces = most_pieces(p.N, p.Hq);
   f.rows = static_cast<int64_t>(p.N) * p.Hq;
@@ -321,14 +349,7 @@ int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_sh
   f.own_per_sm = rows_of(p) <= 8 ? 3 : 2;               // of decode_attention.cu
   const int sms = moe::sm_count();
   f.sms = sms < 255 ? sms : 255;
-  AttentionParams prefix = p;
-  prefix.B = x->groups;
-  prefix.max_q_len = f.max_tokens;
-  if (!shares(rows_of(p), rows_of(prefix), p.max_seq_len)) return attend(p, nullptr, a->dtype, on);
-  // where one of the three kernels cannot take the call, the plain one still may
-  if (!moe::decode_attention_fits(p) || !moe::shared_join_fits(p)) return attend(p, nullptr, a->dtype, on);
   int error = moe::launch_prefill_attention(prefix, &f, a->dtype, on);
-  if (error == MOE_ERR_UNSUPPORTED) return attend(p, nullptr, a->dtype, on);    // too many groups for one line; nothing has been launched
   if (error != MOE_OK) return error;
   f.pass = moe::kOwnPass;
   error = moe::launch_decode_attention(p, &f, a->dtype, on);

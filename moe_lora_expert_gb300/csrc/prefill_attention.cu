@@ -1391,6 +1391,19 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
   }
 }
 
+// Units of a sequence (or group) and key head.
+int64_t row_tiles_of(const AttentionParams& a) {
+  const int group = a.Hq / a.cache.kv_heads, unit_rows = kCtaRows / group * group;
+  return (static_cast<int64_t>(a.max_q_len) * group + unit_rows - 1) / unit_rows;
+}
+}  // namespace
+
+bool prefill_attention_fits(const AttentionParams& a) {
+  const int64_t tiles = static_cast<int64_t>(a.table_width) * a.cache.page_size / kKeys + 1 + kUnitCost;
+  return row_tiles_of(a) * a.B * tiles * a.cache.kv_heads <= 0x7fffffff;
+}
+
+namespace {
 template <typename T, int DP, bool MAPPED, int FORM>
 int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t stream) {
   CUtensorMap q_map = {}, k_map, v_map;
@@ -1410,9 +1423,8 @@ int launch(const AttentionParams& a, const AttentionForms* forms, cudaStream_t s
   if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes) != cudaSuccess) return MOE_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
-  const int64_t row_tiles = (static_cast<int64_t>(a.max_q_len) * group + p.unit_rows - 1) / p.unit_rows;
-  const int64_t line = row_tiles * a.B * ((static_cast<int64_t>(a.table_width) * a.cache.page_size) / kKeys + 1 + kUnitCost) * a.cache.kv_heads;
-  if (line > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  const int64_t row_tiles = row_tiles_of(a);
+  if (!prefill_attention_fits(a)) return MOE_ERR_UNSUPPORTED;
   p.row_tiles = static_cast<int>(row_tiles);
   int64_t grid = sms < kMaxCtas ? sms : kMaxCtas;
   const int64_t units = row_tiles * a.B * a.cache.kv_heads * ((a.max_seq_len + kKeys - 1) / kKeys + 1);

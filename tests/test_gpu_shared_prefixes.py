@@ -127,3 +127,25 @@ def test_a_table_too_wide_for_the_own_pass():
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     batch.check(out, lse, [0, 77, 127])
     assert batch.cache.device_status() == m.MOE_OK
+
+
+def test_scratch_is_taken_where_it_is_used(monkeypatch):
+    """A call that is the plain one allocates what that one does; one that shares
+    gives the same with the scratch that holds for whatever bounds."""
+    torch = torch_mod()
+    from moe_lora_expert_gb300 import attention as A
+    many = Prefixes(4, [2], [64], [1024] * 2, [1024] * 2, 4, 32, 128)
+    out, lse = torch.empty_like(many.q), torch.empty((2048, 32), device="cuda")
+
+    def growth(**over):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        many.cache.attend(**{**many.args, "return_lse": False, "out": out, "lse": lse, **over})
+        return torch.cuda.max_memory_allocated() - before
+    growth()                                            # the stream's workspace
+    assert growth(**many.groups) == growth() == 0
+    few = Prefixes(5, [8], [5000], [20] * 8, [1] * 8, 4, 32, 128)
+    want = few.attend()
+    monkeypatch.setattr(A, "_partial_size", lambda args, x: m.lib().moe_shared_prefix_partial_size(8, 32, 128, 1))
+    assert all(torch.equal(a, b) for a, b in zip(few.attend(), want))

@@ -1,0 +1,41 @@
+"""Which calls over shared prefixes are the plain call, by the sizes that the host
+has, and the scratch that the others need, without a GPU."""
+import pytest
+
+import moe_lora_expert_gb300 as m
+from test_attention_forms_host import shared
+from test_attention_host import FAKE, attend_args, lib  # noqa: F401
+
+
+def scratch(lib, over=None, more=None, cache=None):  # noqa: F811
+    """Bytes for a call of 4 sequences on 4 key heads with 8 query heads each and
+    contexts of up to 8192 tokens, or what differs from it."""
+    args = attend_args(lib, cache_over=cache, **{"max_seq_len": 8192, "table_width": 512, **(over or {})})
+    return lib.moe_paged_attention_shared_partial_size(bytes(args), shared(lib, **{"groups": 1, "seqs": None, **(more or {})}))
+
+
+def test_scratch_of_a_call_that_shares(lib):  # noqa: F811
+    want = lib.moe_shared_prefix_partial_size(4, 32, 128, 1)
+    assert scratch(lib) == want > 0
+    assert scratch(lib, more={"partial": None, "partial_bytes": 0}) == want        # its own are not read
+
+
+@pytest.mark.parametrize("over,more", [
+    ({"max_seq_len": 128}, {}),                                                    # short contexts
+    ({"N": 2, "B": 2}, {}), ({}, {"max_tokens": 3}),                               # few rows in a group
+    ({"N": 4096, "max_q_len": 1024, "cu_q": FAKE}, {"max_tokens": 4096}),          # many in each sequence
+    ({}, {"groups": 0}), ({}, {"max_tokens": 0}), ({"N": 0, "B": 0}, {}),
+    ({"table_width": 1 << 30}, {}),                                                # tables past what the kernels count
+    ({"q": None}, {}), ({"window": 5}, {}), ({}, {"struct_size": 8}), ({}, {"groups": -1})])   # refused by the call
+def test_no_scratch_for_the_plain_call(lib, over, more):  # noqa: F811
+    assert scratch(lib, over, more) == 0
+
+
+def test_no_scratch_without_arguments(lib):  # noqa: F811
+    assert lib.moe_paged_attention_shared_partial_size(None, shared(lib)) == lib.moe_paged_attention_shared_partial_size(bytes(attend_args(lib)), None) == 0
+
+
+@pytest.mark.parametrize("more", [dict(partial=None, partial_bytes=0), dict(partial=None), dict(partial=FAKE + 16), dict(partial_bytes=64)])
+def test_a_call_that_shares_is_refused_without_scratch(lib, more):  # noqa: F811
+    args = attend_args(lib, max_seq_len=8192, table_width=512)
+    assert lib.moe_paged_attention_shared(bytes(args), shared(lib, groups=1, seqs=None, **more), None) == m.MOE_ERR_WORKSPACE
