@@ -349,19 +349,24 @@ struct AttentionForms {
   int32_t* pieces;              // [groups]
 
   // What both passes take, in us (as measured: a CTA's time before and after its
-  // tiles, and a tile's with the other pass beside it), if the prefix pass, with ``tiles`` key tiles of
-  // its units, has n SMs, and the own pass, with ``own`` key tiles of its row
-  // tiles, the others meanwhile (or all of them after it).  Both passes look for
-  // the same best n: they have times of their own before and after their tiles,
-  // so a CTA should do all it can in one go.  A row tile takes the own
-  // pass kOwnUnit tiles' time besides its own, counted in ``own``.
-  __device__ __forceinline__ float time(int n, int tiles, int own) const {
+  // tiles, and a tile's with the other pass beside it), if the prefix pass, with
+  // ``tiles`` key tiles of its units in pieces of ``least`` or more, has n SMs,
+  // and the own pass, with ``own`` key tiles of its row tiles, the others
+  // meanwhile (or all of them after it).  Both passes look for the same best n:
+  // they have times of their own before and after their tiles, so a CTA should
+  // do all it can in one go.  A row tile takes the own pass kOwnUnit tiles' time
+  // besides its own, counted in ``own``.
+  __device__ __forceinline__ float time(int n, int tiles, int least, int own) const {
     const int left = sms - n, ctas = own_per_sm * (left > 0 ? left : sms);
-    const float first = 15.f + 2.6f * static_cast<float>((tiles + n - 1) / n), second = 12.f + 0.85f * static_cast<float>((own + ctas - 1) / ctas);
+    const float first = 15.f + 2.6f * static_cast<float>(max(least, (tiles + n - 1) / n)), second = 12.f + 0.85f * static_cast<float>((own + ctas - 1) / ctas);
     return left > 0 ? fmaxf(first, second) : first + second;
   }
+  // The key tiles that a piece has at least, where the longest unit has ``longest``.
+  __device__ __forceinline__ int least_piece(int longest) const { return (longest + most_pieces - 1) / most_pieces; }
   // The time and n as one number that orders by time.
-  __device__ __forceinline__ int choice(int n, int tiles, int own) const { return static_cast<int>(fminf(8.f * time(n, tiles, own), 8.0e6f)) << 8 | n; }
+  __device__ __forceinline__ int choice(int n, int tiles, int least, int own) const {
+    return static_cast<int>(fminf(8.f * time(n, tiles, least, own), 8.0e6f)) << 8 | n;
+  }
   // Group g's sequences and their tokens; nothing, where the list is out of order.
   __device__ __forceinline__ void group(const int32_t* cu_q, int g, int& s0, int& s1, int& q0, int& q1) const {
     s0 = seqs == nullptr ? 0 : max(0, min(sequences, seqs[g]));

@@ -113,7 +113,7 @@ struct Shared {
   int end[kMaxEntries];                   // end of the keys that some row of it sees
   float m[kWarps][kMaxRows], l[kWarps][kMaxRows];
   int total, longest, abort_flag, last;
-  int tiles, own, best;                   // of shared prefixes: see AttentionForms::time
+  int tiles, deepest, own, best;          // of shared prefixes: see AttentionForms::time
 };
 constexpr int kSlotBytes = 2 * 16 * kPitch;
 constexpr int kScratch(int rows) { return 2 * rows * 128 * 4; }              // two warps' sums
@@ -223,7 +223,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 #pragma unroll 1
       for (int i = 0; i < kRing; ++i) mbar_init(&s.full[w][i], 1);
     s.abort_flag = 0;
-    s.tiles = s.own = 0;
+    s.tiles = s.deepest = s.own = 0;
     s.best = 0x7fffffff;
     fence_mbarrier_init();
   }
@@ -264,6 +264,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         if (len <= 0 || tokens <= 0 || !p.f.some_take_part(a.cu_q, a.seq_lens, p.f.lens[g], s0, s1, q0, q1)) continue;
         atomicAdd(&s.tiles, (tokens + each - 1) / each * ((len + 127) / 128) * ca.kv_heads);
         atomicAdd(&s.own, -(s1 - s0) * (len / kKeys));
+        atomicMax(&s.deepest, (len + 127) / 128);
       }
     }
   }
@@ -330,7 +331,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
       // with all CTAs, 135 so; without the form 633).
       const int work = max(0, s.own) * ca.kv_heads * p.f.own_row_tiles;
 #pragma unroll 1
-      for (int n = tid + 1; n <= p.f.sms; n += kThreads) atomicMin(&s.best, p.f.choice(n, s.tiles, work));
+      for (int n = tid + 1; n <= p.f.sms; n += kThreads) atomicMin(&s.best, p.f.choice(n, s.tiles, p.f.least_piece(s.deepest), work));
       __syncthreads();
       const int left = p.f.sms - (s.best & 255);
       if (left > 0) most_ctas = min(most_ctas, left * ctas_per_sm(NT));

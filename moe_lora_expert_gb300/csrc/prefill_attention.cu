@@ -561,14 +561,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid
     int* best = s.units;                   // not in use here
     if (tid == 0) *best = 0x7fffffff;
     __syncthreads();
-    if (tid < static_cast<int>(gridDim.x)) atomicMin(best, p.f.choice(tid + 1, tiles, max(0, s.sums[3]) * ca.kv_heads * p.f.own_row_tiles));
+    if (tid < static_cast<int>(gridDim.x)) atomicMin(best, p.f.choice(tid + 1, tiles, p.f.least_piece(longest), max(0, s.sums[3]) * ca.kv_heads * p.f.own_row_tiles));
     __syncthreads();
     most_ctas = *best & 255;
     // Pieces of a length for which there is about one for each CTA: n units of
     // t tiles give at most t / chunk + n.
     const int spare = most_ctas - units;
     chunk = spare > 0 ? max(kMinPiece, (tiles + spare - 1) / spare) : longest;
-    chunk = max(max(chunk, 1), (longest + p.f.most_pieces - 1) / p.f.most_pieces);
+    chunk = max(max(chunk, 1), p.f.least_piece(longest));
     __syncthreads();
   }
 #pragma unroll 1

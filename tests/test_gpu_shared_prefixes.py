@@ -149,3 +149,16 @@ def test_scratch_is_taken_where_it_is_used(monkeypatch):
     want = few.attend()
     monkeypatch.setattr(A, "_partial_size", lambda args, x: m.lib().moe_shared_prefix_partial_size(8, 32, 128, 1))
     assert all(torch.equal(a, b) for a, b in zip(few.attend(), want))
+
+
+@pytest.mark.parametrize("shared", [20001, 29951, 29952, 29953])
+@pytest.mark.parametrize("B,Hkv,Hq,D", [(8, 1, 8, 64), (5, 1, 16, 128), (20, 2, 16, 128)])
+def test_long_prefixes_that_end_anywhere(B, Hkv, Hq, D, shared):
+    """Prefixes in over 32 pieces that end inside a page, and one short of and one
+    past a key tile; the join takes several rounds."""
+    torch = torch_mod()
+    batch = Prefixes(B + shared, [B], [shared], [1 + 11 * b for b in range(B)], [1] * B, Hkv, Hq, D)
+    out, lse = batch.attend()
+    batch.check(out, lse)
+    again = batch.attend()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and batch.cache.device_status() == m.MOE_OK
