@@ -702,9 +702,11 @@ int moe_paged_attention_sinks(const moe_paged_attention_args_t* args, int sinks,
  *     moe_paged_attention_shared_partial_size bytes of the same arguments
  *     (partial's own are not read), or the moe_shared_prefix_partial_size bytes
  *     that hold for whatever bounds; NULL and 0 bytes where the first is 0.
- * Where sharing would not pay, by the sizes that the host has (max_q_len,
- * max_tokens, max_seq_len), the call does as moe_paged_attention does: few rows
- * in a group, many in each sequence, short contexts.  It then needs no scratch.
+ * Where sharing would not pay, by the sizes that the host has (the sequences,
+ * the groups, max_q_len, max_tokens, max_seq_len), the call does as
+ * moe_paged_attention does: few rows in a group, many in each sequence, short
+ * contexts.  The lengths of the prefixes are the device's: name a prefix that is
+ * long, and bounds that are not much over what there is.  It then needs no scratch.
  * ------------------------------------------------------------------------- */
 typedef struct {
   uint32_t struct_size;           /* sizeof(moe_shared_prefix_t) */

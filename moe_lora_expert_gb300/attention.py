@@ -522,7 +522,10 @@ class PagedKVCache:
         once for the group, from the pages of its first sequence's table row.
         The result is the same up to rounding; not with a window.
         ``max_shared_q``: at least the most new tokens of one group (by default
-        N); sequences past it read their keys themselves."""
+        N); sequences past it read their keys themselves.  Whether sharing is
+        worth its launches is judged by the sequences and groups there are, this
+        bound and ``max_seq_len``: give both where the table is wide or there
+        are several groups."""
         N, Hq, D = q.shape
         dtype = q.dtype
         code, index = _dtype_code(dtype, "q"), self._index

@@ -33,20 +33,36 @@ inline int element_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 // one long context (on 8 key heads 77%: 109 / 62).
 bool few_rows(int64_t rows, int64_t pairs) { return rows <= 32 || (rows <= 96 && pairs <= 16); }
 
-// Whether a prefix is read once for a group, by the rows that a sequence and
-// the largest group have for a key head and the bound on the lengths.  Shared /
-// by each sequence, in us (4 key heads of 128, 8 query heads each, about 300 own
-// keys a sequence):
-//   group of 16 rows (2 sequences): 4096 shared keys 17.9 / 19.1, 65536 46 / 39; 16 such groups 61 / 33, 544 / 253;
-//   32 rows: 256 keys 17.8 / 14.4, 1024 18.1 / 16.4, 4096 18.9 / 20.9, 65536 47 / 57; 8 such groups of 4096 35 / 32, 65536 222 / 256;
-//   64 rows: 1024 17.7 / 16.8, 16384 26.7 / 34.6, 65536 49 / 92;
-//   16 sequences of 32 rows: 256 21.9 / 22.2, 4096 30 / 41, 65536 92 / 354;
-//     of 64: 1024 36 / 33, 4096 43 / 53, 65536 138 / 412;  of 128: 1024 65 / 34, 16384 125 / 124, 65536 281 / 413;
-//     of 256: 4096 171 / 59, 16384 305 / 140.
+// Whether prefixes are read once for their groups, by what the host has: the
+// sequences, the groups, a bound on the tokens of the largest, and a bound on the
+// lengths.  The call has three kernels then.  Outside a graph it takes the host 26
+// to 30 us, so it pays only where the plain call takes the GPU longer: where the
+// plain call's passes over the cache are 80 MB, which is 12 us of it.  And a unit
+// (256 rows of a group and key head) takes a key tile 2 us of an SM, however few
+// its rows are, which the plain call's reading for them has to outweigh.
+// Shared / plain, us a call outside graphs (query heads of 128, 8 to a key head; in
+// graphs plain calls take 0.8 less, shared ones 1 to 12):
+//   4 key heads, one group, of 4 sequences: 8192 shared tokens 26.3 / 23.2, 16384 25.6 / 28.4, 65536 45.5 / 57.2;
+//     of 8: 4096 26.1 / 21.4, 8192 26.5 / 26.0, 16384 27.6 / 34.9;  of 16: 4096 26.9 / 25.3, 8192 27.4 / 34.8, 65536 52 / 165;
+//   1 key head, 8 sequences: 16384 28.2 / 23.6, 65536 29.8 / 37.0;  8 key heads: 4096 29.1 / 25.9, 8192 29.0 / 34.5;
+//   4 key heads, groups of 2 (16 rows): 4 of 16384 38.9 / 37.9, 65536 107 / 85;  16 of 4096 61.9 / 33.2, 65536 545 / 254;
+//   groups of 4 (32 rows): 4 of 4096 27.0 / 24.3, 8192 31.0 / 31.2, 16384 41.8 / 46.9;  8 of 8192 48.5 / 47.7, 65536 223 / 257;
+//     16 of 16384 166 / 138, 65536 548 / 487;
+//   groups of 8 (64 rows): 8 of 1024 29.7 / 25.8, 4096 40.0 / 48.1;  16 of 2048 55 / 53, 4096 82 / 83, 8192 134 / 142;
+//     40 of 4096 161 / 178;  groups of 16: 16 of 2048 92 / 86, 4096 92 / 146;
+//   heads of 64: 8 sequences 8192 29.7 / 23.3, 16384 29.5 / 31.3;  4 groups of 4: 8192 29.6 / 27.6, 16384 36.9 / 39.6;
+//   16 sequences of 4 new tokens: 1024 30.3 / 25.8, 4096 29.7 / 41.4;  of 8: 1024 36 / 32, 4096 38 / 53;  of 16: 4096 66 / 53, 16384 109 / 125.
 // Sequences of many rows fill the products' tiles by themselves, and their own
-// keys are then in the kernel that is made for few.
-bool pays(int64_t rows, int64_t group_rows, int64_t longest) {
-  return group_rows >= 32 && rows <= 128 && longest >= 2048 && (rows <= 32 || rows * rows <= longest);
+// keys are then in the kernel that is made for few.  A list of groups may be
+// uneven, so with few units the bound on the largest counts and not the mean (4
+// groups of 2 or 3 sequences, 5 query heads on each of 2 key heads, and no bound: 65536 63 / 54).
+bool pays(const AttentionParams& p, int groups, int max_tokens) {
+  const int64_t heads = p.Hq / p.cache.kv_heads, rows = p.max_q_len * heads, longest = p.max_seq_len;
+  const int64_t mean_rows = (p.N + groups - 1ll) / groups * heads, units = groups * ((mean_rows + 255) / 256) * p.cache.kv_heads;
+  if (max_tokens * heads < 32 || (mean_rows < 32 && units > 8) || (mean_rows < 64 && units > 32)) return false;
+  if (rows > 128 || (rows > 32 && rows * rows > longest) || longest < 4096) return false;
+  const double plain_bytes = 2.0 * p.cache.head_dim * static_cast<double>(longest) * static_cast<double>((rows + 15) / 16 * p.B * p.cache.kv_heads);
+  return plain_bytes >= 80e6 && plain_bytes >= 8.4e6 * static_cast<double>(units);
 }
 // How many pieces the prefix pass may leave for a row: with one group whose
 // rows fill 256-row units, twice as many as give each SM one of them, and no more
@@ -262,7 +278,7 @@ bool shares(const AttentionParams& p, const moe_shared_prefix_t* x, AttentionPar
   prefix = p;
   prefix.B = x->groups;
   prefix.max_q_len = x->max_tokens < p.N ? x->max_tokens : p.N;
-  return pays(rows_of(p), rows_of(prefix), p.max_seq_len) && moe::prefill_attention_fits(prefix) && moe::decode_attention_fits(p) &&
+  return pays(p, x->groups, prefix.max_q_len) && moe::prefill_attention_fits(prefix) && moe::decode_attention_fits(p) &&
          moe::shared_join_fits(p);
 }
 

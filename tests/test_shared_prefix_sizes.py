@@ -9,8 +9,8 @@ from test_attention_host import FAKE, attend_args, lib  # noqa: F401
 
 def scratch(lib, over=None, more=None, cache=None):  # noqa: F811
     """Bytes for a call of 4 sequences on 4 key heads with 8 query heads each and
-    contexts of up to 8192 tokens, or what differs from it."""
-    args = attend_args(lib, cache_over=cache, **{"max_seq_len": 8192, "table_width": 512, **(over or {})})
+    contexts of up to 2^20 tokens, or what differs from it."""
+    args = attend_args(lib, cache_over=cache, **{"max_seq_len": 1 << 20, "table_width": 1 << 16, **(over or {})})
     return lib.moe_paged_attention_shared_partial_size(bytes(args), shared(lib, **{"groups": 1, "seqs": None, **(more or {})}))
 
 
@@ -37,7 +37,7 @@ def test_no_scratch_without_arguments(lib):  # noqa: F811
 
 @pytest.mark.parametrize("more", [dict(partial=None, partial_bytes=0), dict(partial=None), dict(partial=FAKE + 16), dict(partial_bytes=64)])
 def test_a_call_that_shares_is_refused_without_scratch(lib, more):  # noqa: F811
-    args = attend_args(lib, max_seq_len=8192, table_width=512)
+    args = attend_args(lib, max_seq_len=1 << 20, table_width=1 << 16)
     assert lib.moe_paged_attention_shared(bytes(args), shared(lib, groups=1, seqs=None, **more), None) == m.MOE_ERR_WORKSPACE
 
 
@@ -48,3 +48,19 @@ def test_few_key_heads_may_leave_a_piece_on_each_sm(lib, heads):  # noqa: F811
     size = scratch(lib, over={"Hq": 8 * heads}, cache={"kv_heads": heads})
     pieces = (size - 4) // (rows * row) - 1
     assert size == (pieces + 1) * rows * row + 4 and pieces == 160 // heads
+
+
+@pytest.mark.parametrize("B,groups,heads,most,longest,pays", [
+    (8, 1, 4, None, 2349, False), (8, 2, 4, 4, 2349, False),                  # the plain call is done before three kernels are launched
+    (8, 1, 4, None, 16685, True), (8, 1, 1, None, 16685, False), (8, 1, 1, None, 65837, True),
+    (64, 1, 4, None, 1 << 20, True), (64, 1, 4, None, 9216, True), (64, 1, 4, None, 2349, False),
+    (32, 16, 4, None, 65837, False), (32, 16, 4, 2, 65837, False),            # groups of two, with the bound and without
+    (16, 8, 4, None, 65837, False), (8, 4, 4, None, 65837, False),
+    (32, 8, 4, 4, 4397, False), (32, 8, 4, 4, 16685, True), (64, 16, 4, 4, 65837, False),
+    (64, 8, 4, 8, 1325, False), (64, 8, 4, 8, 8493, True), (320, 40, 4, 8, 8493, True),
+    (9, 4, 4, 9, 1 << 20, False), (9, 4, 2, 9, 1 << 20, True), (9, 4, 2, 3, 1 << 20, False)])   # an uneven list of few units
+def test_which_calls_share(lib, B, groups, heads, most, longest, pays):  # noqa: F811
+    """One new token a sequence, 8 query heads a key head: both sides are measured beside the rule."""
+    got = scratch(lib, over={"B": B, "N": B, "Hq": 8 * heads, "max_seq_len": longest}, cache={"kv_heads": heads},
+                  more={"groups": groups, "seqs": FAKE, "max_tokens": B if most is None else most})
+    assert (got > 0) == pays
