@@ -233,7 +233,10 @@ def _table(cos_sin, index):
 def _axis_args(axes, positions, N, R, index):
     """(pointer of the positions [axes, N], the axes' struct as bytes)."""
     if type(axes) is not bytes:
-        axes = bytes(axes)
+        try:
+            axes = bytes(list(axes))                               # bytes of a number would be so many zeros, of an array its memory
+        except TypeError:
+            raise ValueError("axes must be the axis of each pair, as rope_axes gives them") from None
     if positions is None or positions.dtype is not _int32_type or positions.get_device() != index or positions.dim() != 2:
         raise ValueError(f"positions must be an int32 tensor [axes, {N}] on cuda:{index}")
     A = positions.shape[0]
