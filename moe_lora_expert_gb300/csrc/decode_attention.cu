@@ -888,16 +888,18 @@ int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
 }  // namespace
 
-// Of the current device; looked up once for each (host threads may race to the same value).
+// Of the current device; 0 if it cannot be asked.  Kept for the first devices
+// (host threads may race to the same value), so that a call asks but once.
 int sm_count() {
-  constexpr int kMaxDevices = 64;
-  static std::atomic<int> counts[kMaxDevices] = {};
+  constexpr int kKept = 64;
+  static std::atomic<int> counts[kKept] = {};
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  n = counts[dev].load(std::memory_order_relaxed);
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const bool kept = dev >= 0 && dev < kKept;
+  if (kept) n = counts[dev].load(std::memory_order_relaxed);
   if (n > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  counts[dev].store(n, std::memory_order_relaxed);
+  if (kept) counts[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
