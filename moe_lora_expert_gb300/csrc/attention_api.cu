@@ -248,7 +248,9 @@ int check_attention(const moe_paged_attention_args_t* a, AttentionParams& p) {
   p.status = a->status;
   p.N = a->N, p.B = a->B, p.Hq = a->Hq, p.table_width = a->table_width;
   p.max_q_len = a->cu_q == nullptr ? 1 : a->max_q_len < a->N ? a->max_q_len : a->N;
-  p.window = a->window;
+  // A window past any position is cut so that a row before the first key may take it from its position.
+  const int most_window = 0x7fffffff - (a->N < 1 << 30 ? a->N : 1 << 30);
+  p.window = a->window < most_window ? a->window : most_window;
   p.max_seq_len = a->max_seq_len;
   p.scale = a->scale;
   p.workspace = a->workspace;
