@@ -343,7 +343,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   if constexpr (FORMS) {
     // A row tile each, where that takes no CTA much longer than its stretch of
     // the line would with the joins that come with it.
-    if (own && entries * ca.kv_heads <= most_ctas && s.longest <= (total + ctas - 1) / ctas + kCutCost) {
+    if (own && total > 0 && entries * ca.kv_heads <= most_ctas && s.longest <= (total + ctas - 1) / ctas + kCutCost) {
       const int e = min(static_cast<int>(blockIdx.x) / ca.kv_heads, entries - 1), count = s.prefix[e + 1] - s.prefix[e];
       x0 = s.prefix[e] * ca.kv_heads + (static_cast<int>(blockIdx.x) - e * ca.kv_heads) * count;
       x1 = static_cast<int>(blockIdx.x) < entries * ca.kv_heads ? x0 + count : x0;

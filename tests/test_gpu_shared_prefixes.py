@@ -162,3 +162,16 @@ def test_long_prefixes_that_end_anywhere(B, Hkv, Hq, D, shared):
     batch.check(out, lse)
     again = batch.attend()
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and batch.cache.device_status() == m.MOE_OK
+
+
+@pytest.mark.parametrize("N", [1, 64])
+def test_a_padded_batch_without_new_tokens(N):
+    """Rows of no sequence alone: they are left as they were."""
+    torch = torch_mod()
+    batch = Prefixes(6, [8], [300], [20] * 8, [8] * 8, 2, 64, 64, P=16)
+    q, cu = batch.q[:N], torch.zeros(9, dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((N, 64), 7.0, device="cuda")
+    batch.attend(q=q, cu_q=cu, max_q_len=4, max_shared_q=N, out=out, lse=lse)
+    assert bool((out == 7).all()) and bool((lse == 7).all()) and batch.cache.device_status() == m.MOE_OK
+    out, lse = batch.attend()
+    batch.check(out, lse)
