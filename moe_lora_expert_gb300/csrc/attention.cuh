@@ -424,6 +424,7 @@ bool shared_join_fits(const AttentionParams& p);     // whether its grid can be 
 int launch_shared_join(const AttentionParams& p, const AttentionForms& forms, int dtype, cudaStream_t s);   // a moe_status_t
 size_t decode_attention_workspace_bytes();
 cudaError_t clear_decode_counters(void* workspace, cudaStream_t s);
+void decode_attention_shape(const AttentionParams& p, int& row_tiles, int& per_sm);   // row tiles of a sequence, CTAs an SM
 bool decode_attention_fits(const AttentionParams& p);   // likewise
 int launch_decode_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s);   // a moe_status_t
 

@@ -370,8 +370,7 @@ int moe_paged_attention_shared(const moe_paged_attention_args_t* a, const moe_sh
   f.refs = reinterpret_cast<float2*>(f.sums + (f.most_pieces + 1) * f.rows * p.cache.head_dim);
   f.pieces = reinterpret_cast<int32_t*>(f.refs + (f.most_pieces + 1) * f.rows);
   f.pass = moe::kPrefixPass;
-  f.own_row_tiles = static_cast<int>((rows_of(p) + 15) / 16);
-  f.own_per_sm = rows_of(p) <= 8 ? 3 : 2;               // of decode_attention.cu
+  moe::decode_attention_shape(p, f.own_row_tiles, f.own_per_sm);
   const int sms = moe::sm_count();
   f.sms = sms < 255 ? sms : 255;
   int error = moe::launch_prefill_attention(prefix, &f, a->dtype, on);

@@ -998,6 +998,10 @@ int launch_type(const AttentionParams& p, const AttentionForms* forms, int dtype
 }
 }  // namespace
 
+void decode_attention_shape(const AttentionParams& p, int& row_tiles, int& per_sm) {
+  row_tiles = static_cast<int>(row_tiles_of(p, tile_rows_of(p)));
+  per_sm = ctas_per_sm(tile_rows_of(p) / 8);
+}
 bool decode_attention_fits(const AttentionParams& p) { return fits(p, row_tiles_of(p, tile_rows_of(p))); }
 int launch_decode_attention(const AttentionParams& p, const AttentionForms* forms, int dtype, cudaStream_t s) {
   return forms != nullptr ? launch_type<true>(p, forms, dtype, s) : launch_type<false>(p, forms, dtype, s);
