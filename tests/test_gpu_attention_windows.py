@@ -20,3 +20,19 @@ def test_a_window_past_any_position(new, lens, window, sinks):
     out, lse = batch.cache.attend(tensor(q, "bfloat16"), **batch.dev, cu_q=batch.cu_dev, max_q_len=max(new), window=window, sinks=sinks, return_lse=True)
     compare(out, lse, batch, q, "bfloat16")
     assert batch.cache.device_status() == m.MOE_OK
+
+
+@pytest.mark.parametrize("new,lens,window,sinks", [([60], [3000], 2500, 300), ([40, 3], [2600, 700], 900, 5)])
+def test_many_rows_with_sinks_whose_wait_runs_out(new, lens, window, sinks):
+    """Chunks whose units several CTAs have parts of: no key tile comes, the
+    status says so, and the joins of the calls that follow are right."""
+    rng = np.random.default_rng(sum(lens))
+    batch = Batch(rng, new, lens, 1, 16, 64, std=0.5)
+    q = rounded(rng, (sum(new), 16, 64), "bfloat16")
+    args = dict(q=tensor(q, "bfloat16"), **batch.dev, cu_q=batch.cu_dev, max_q_len=max(new), window=window, sinks=sinks)
+    batch.cache.attend(**args, wait_timeout_ms=20, debug_flags=m.MOE_DEBUG_STALL_ATTENTION)
+    assert batch.cache.device_status() == m.MOE_ERR_DEVICE_TIMEOUT
+    for _ in range(2):
+        out, lse = batch.cache.attend(**args, return_lse=True)
+        assert batch.cache.device_status() == m.MOE_OK
+        compare(out, lse, batch, q, "bfloat16", window=window, sinks=sinks)

@@ -175,3 +175,43 @@ def test_a_padded_batch_without_new_tokens(N):
     assert bool((out == 7).all()) and bool((lse == 7).all()) and batch.cache.device_status() == m.MOE_OK
     out, lse = batch.attend()
     batch.check(out, lse)
+
+
+@pytest.mark.parametrize("B,new,Hq", [(128, 1, 32), (80, 2, 32), (128, 1, 64)])
+@pytest.mark.parametrize("shared", [129, 4000])
+def test_more_row_tiles_than_ctas(B, new, Hq, shared):
+    """One launch of the own pass with more (row tile, key head) pairs than CTAs,
+    which then take the SMs that the prefix pass leaves: row tiles of 8 and of 16 rows."""
+    batch = Prefixes(B + shared, [B], [shared], [new + (53 * b) % 700 for b in range(B)], [new] * B, 4, Hq, 64)
+    out, lse = batch.attend()
+    batch.check(out, lse)
+    assert batch.cache.device_status() == m.MOE_OK
+
+
+@pytest.mark.parametrize("Hkv,Hq,D,new", [(1, 8, 64, 1), (2, 16, 128, 1), (1, 8, 128, 2), (2, 32, 64, 4)])
+@pytest.mark.parametrize("own", [[6001] + [30] * 7, [5, 2500, 40, 9, 64, 700, 1900, 4], [3000] * 2 + [5] * 6])
+def test_own_keys_of_uneven_lengths(Hkv, Hq, D, new, own):
+    """Sequences with far more keys of their own than the others: their row tiles
+    are cut, in up to 47 pieces, and leave one piece for the join."""
+    torch = torch_mod()
+    batch = Prefixes(sum(own) + D, [8], [700], own, [new if n >= new else 1 for n in own], Hkv, Hq, D)
+    out, lse = batch.attend()
+    batch.check(out, lse)
+    again = batch.attend()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and batch.cache.device_status() == m.MOE_OK
+
+
+def test_more_groups_than_threads():
+    """Over 448 units, of which a thread of the prefix pass plans several."""
+    groups = 460
+    batch = Prefixes(7, [4] * groups, [1 + (29 * g) % 300 for g in range(groups)], [1 + b % 9 for b in range(4 * groups)], [1] * (4 * groups), 1, 16, 16, P=16)
+    out, lse = batch.attend()
+    batch.check(out, lse, range(0, 4 * groups, 7))
+    assert batch.cache.device_status() == m.MOE_OK
+
+
+def test_decode_with_float16_and_wide_pages():
+    batch = Prefixes(8, [20, 12], [3001, 255], [1 + 13 * b for b in range(32)], [1] * 32, 2, 24, 112, P=256, dtype="float16")
+    out, lse = batch.attend()
+    batch.check(out, lse)
+    assert batch.cache.device_status() == m.MOE_OK
