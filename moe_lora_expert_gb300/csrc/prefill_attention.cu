@@ -291,8 +291,9 @@ struct WalkOf {
   __device__ __forceinline__ int& chunk() { return span; }
   __device__ __forceinline__ void take_piece(int each) {
     ++x;
-    tile = en.count * piece() / each;
-    n = en.count * (piece() + 1) / each - tile;
+    const uint32_t tiles = en.count, i = piece();          // 2^24 tiles in 160 pieces: 32 bits without a sign hold the products
+    tile = static_cast<int>(tiles * i / each);
+    n = static_cast<int>(tiles * (i + 1) / each) - tile;
   }
   __device__ __forceinline__ void first_piece(int heads, int first_prefix) {
     const int in = x - first_prefix * heads, each = pieces_of(en.count, chunk());
