@@ -48,4 +48,4 @@ def test_pieces_cover_a_unit_evenly(tmp_path):
     exe = tmp_path / "pieces"
     subprocess.run([cxx, "-std=c++17", "-fwrapv", str(tmp_path / "pieces.cpp"), "-o", str(exe)], check=True)
     lines = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split("\n")[:-1]
-    assert len(lines) > 30 and all(line.endswith(" 1") for line in lines), [line for line in lines if not line.endswith(" 1")]
+    assert len(lines) == 30 and all(line.endswith(" 1") for line in lines), [line for line in lines if not line.endswith(" 1")]
