@@ -38,13 +38,13 @@
 // Sinks (the first keys stay visible in a window) are tiles before those of the
 // window; the pages between are not looked up.  One token with a window of 4096
 // and 4 sinks at the end of 262140 keys: 15.7 us, chain of latencies; 64
-// sequences in windows of 8192 with 64 sinks: 100.5 us, 5.4 TB/s, 80% of the copy
-// rate (98.1 without sinks).
+// sequences in windows of 8192 with 64 sinks: 101 us, 5.4 TB/s, 79% of the copy
+// rate (98.5 without sinks).
 //
 // Sequences whose first keys the prefix pass takes (AttentionForms) begin after
 // them here and leave their sums for the join.  64 sequences of up to 1023 own
 // keys are 256 row tiles of 17 tiles at most: one for each CTA, since a cut costs
-// more than a tile of waiting (cut evenly the call takes 50.5 us, so 35.5).
+// more than a tile of waiting (cut evenly the call takes 50.5 us, so 36).
 //
 // What bounds it: one pass over the cache's bytes.  64 sequences of up to
 // 32768 keys (8 query heads of 128 on each of 4 key heads) take 214 us, 6.3
@@ -328,7 +328,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
   if constexpr (FORMS) {
     if (planned) {
       // As many as the SMs hold that the prefix pass leaves (128 sequences on 32768 shared tokens: 151 us
-      // with all CTAs, 135 so; without the form 633).
+      // with all CTAs, 135 so at the time; without the form 634).
       const int work = max(0, s.own) * ca.kv_heads * p.f.own_row_tiles;
 #pragma unroll 1
       for (int n = tid + 1; n <= p.f.sms; n += kThreads) atomicMin(&s.best, p.f.choice(n, s.tiles, p.f.least_piece(s.deepest), work));

@@ -18,8 +18,8 @@
 // thread: with 126, which held the rotated stretches, 20.5 us; 4 stretches held
 // instead of 2 the same there, 11.3 instead of 10.3 us on ragged chunks).  64
 // single tokens take 5.8 us: the chain from lengths to table to scale.  With
-// positions of three axes the 4096 tokens take 21.8 us: each row's angles are
-// gathered in shared memory first (19.4 with one axis, timed with them).
+// positions of three axes the 4096 tokens take 21.7 us: each row's angles are
+// gathered in shared memory first (17.6 with one axis, timed with them).
 #include <type_traits>
 
 #include "attention.cuh"
@@ -281,7 +281,8 @@ cudaError_t launch_heads(KvAppendParams p, const Axes& axes, cudaStream_t s) {
   size_t bytes = 0;
   const auto kernel = kv_append_kernel<T, V, HEADS, Axes>;
   if constexpr (!std::is_same<Axes, OneAxis>::value) {
-    // a row of angles and a word for each token of a page, or of a CTA's stretches of q: up to 129 KB (a page of 256, whose CTA has an SM to itself)
+    // a row of angles and a word for each token of a page, or of a CTA's stretches of q: up to 129 KB for a page of 256, and then
+    // each CTA has an SM to itself, those of q too (4096 tokens 33.9 us, on pages of 128 23.5, of 64 21.7)
     const uint32_t tokens = q_ctas > 0 ? axes_tokens(static_cast<uint32_t>(threads), p.q_items) : 1;
     bytes = (tokens > static_cast<uint32_t>(rows) ? tokens : rows) * static_cast<size_t>(p.R + 1) * 4;
     if (ensure_smem_limit(reinterpret_cast<const void*>(kernel), static_cast<int>(bytes)) != cudaSuccess) return cudaErrorInvalidValue;

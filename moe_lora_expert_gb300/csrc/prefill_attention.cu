@@ -46,14 +46,15 @@
 // The prefix pass (AttentionForms) takes the new tokens of a group of sequences
 // as one unit's rows against the keys that all of them begin with.  All rows see
 // all keys, and a unit is cut in as many pieces as there are CTAs for it, whose
-// sums are joined by another kernel: joined here, 19 pieces of 256 rows in two
-// steps, 64 sequences on 8192 keys took 54 us instead of 30.  A piece takes 9 us
-// to its first scores (lengths, plan, pages, copies, conversion, each about one),
-// 2 us a key tile, and 3 to 5 to write its 128 KB (by way of shared memory, in
-// whole lines, the call takes as long).  With the own pass beside it that call
-// is 36 us, 128 sequences on 32768 keys 133.  Two softmax warps for 32 rows, or
-// both row tiles on the same rows of a small group, took longer: the schedulers
-// are busy half of the time and the conversion has no time to spare.
+// sums are joined by another kernel: joined by the own pass, whose CTAs then held
+// their SMs until this one's end, 64 sequences on 8192 keys took 55 us and 42.5
+// so, at the time.  A piece takes 9 us to its first scores: lengths 2.3, plan and
+// place 2.9, pages 1.2, copies 1.2, conversion 0.9 and the products; then 2 us a key
+// tile, and 3 to 5 to write its 128 KB (by way of shared memory, in whole lines,
+// the call takes as long).  With the own pass beside it that call is 36 us, 128
+// sequences on 32768 keys 124.  Two softmax warps for 32 rows, or both row tiles on
+// the same rows of a small group, took longer: the schedulers are busy half of the
+// time and the conversion has no time to spare.
 #include <cuda.h>
 
 #include <type_traits>
@@ -82,7 +83,7 @@ constexpr int kMaxCtas = 160;
 constexpr int kMaxUnits = 16;              // whole units a CTA may be given (see the kernel)
 constexpr int kJoinCost = 8;               // key tiles' worth of time that cutting the line may cost a CTA: part of a unit written, another joined
 constexpr int kJoin = 8;                   // pieces that are joined at a time
-constexpr int kNanTiles = 8;               // tiles with NaN that a warp notes for a unit; hidden in part are 6 at most where all pages are there
+constexpr int kNanTiles = 8;               // tiles with NaN that a warp notes for a unit; hidden in part are 6 at most where all pages are there, 7 with sinks
 constexpr int kConvertWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
