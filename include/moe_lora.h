@@ -701,7 +701,8 @@ int moe_paged_attention_sinks(const moe_paged_attention_args_t* args, int sinks,
  *   partial: device scratch of the call, of any contents, 32-byte aligned:
  *     moe_paged_attention_shared_partial_size bytes of the same arguments
  *     (partial's own are not read), or the moe_shared_prefix_partial_size bytes
- *     that hold for whatever bounds; NULL and 0 bytes where the first is 0.
+ *     that hold for whatever bounds; NULL and 0 bytes where the first is 0.  The
+ *     first is 0, too, for arguments that the call refuses (a missing workspace).
  * Where sharing would not pay, by the sizes that the host has (the sequences,
  * the groups, max_q_len, max_tokens, max_seq_len), the call does as
  * moe_paged_attention does: few rows in a group, many in each sequence, short
